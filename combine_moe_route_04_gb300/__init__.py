@@ -16,7 +16,11 @@ __all__ = ["MoEError", "MoEShape", "MoEViews", "lib_path", "load", "shape", "cap
            "workspace_size", "alloc_workspace", "workspace_init", "workspace_views",
            "last_device_status", "check_wait_timeout", "alloc_route_outputs", "moe_route",
            "moe_grouped_gemm_up", "moe_grouped_gemm_up_rows", "moe_grouped_gemm_down", "moe_combine",
-           "moe_forward", "STATUS_NAMES", "EXPORTS", "FORWARD_KERNELS"]
+           "moe_forward", "STATUS_NAMES", "EXPORTS", "FORWARD_KERNELS",
+           "mxfp4_sizes", "alloc_mxfp4", "moe_quantize_mxfp4", "moe_quantize_weights_mxfp4",
+           "moe_dequantize_mxfp4", "moe_quantize_permute_mxfp4", "moe_grouped_gemm_up_mxfp4",
+           "moe_grouped_gemm_down_mxfp4", "mxfp4_workspace_size", "alloc_mxfp4_workspace", "moe_forward_mxfp4",
+           "balance_workspace_size", "alloc_balance_workspace", "moe_balance_loss", "moe_balance_loss_backward"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libmoe_gb300.so")
@@ -33,7 +37,10 @@ FORWARD_KERNELS = 5
 EXPORTS = ["moe_status_string", "moe_capacity", "moe_workspace_size", "moe_workspace_init",
            "moe_last_device_status", "moe_route", "moe_grouped_gemm_up", "moe_grouped_gemm_down",
            "moe_combine", "moe_forward", "moe_workspace_views", "moe_route_noalloc",
-           "moe_grouped_gemm_up_rows", "moe_check_wait_timeout"]
+           "moe_grouped_gemm_up_rows", "moe_check_wait_timeout", "moe_mxfp4_sizes", "moe_quantize_mxfp4",
+           "moe_quantize_weights_mxfp4", "moe_dequantize_mxfp4", "moe_quantize_permute_mxfp4",
+           "moe_grouped_gemm_up_mxfp4", "moe_grouped_gemm_down_mxfp4", "moe_mxfp4_workspace_size",
+           "moe_forward_mxfp4", "moe_balance_workspace_size", "moe_balance_loss", "moe_balance_loss_backward"]
 
 
 class MoEError(RuntimeError):
@@ -99,6 +106,22 @@ def load():
     lib.moe_combine.argtypes = [S] + [P] * 6
     lib.moe_forward.restype = st
     lib.moe_forward.argtypes = [S] + [P] * 8
+    I64, Z = ctypes.c_int64, ctypes.POINTER(ctypes.c_size_t)
+    for name, args in (("moe_mxfp4_sizes", [I64, I64, Z, Z]),
+                       ("moe_quantize_mxfp4", [P, I64, I64, P, P, P]),
+                       ("moe_quantize_weights_mxfp4", [P, ctypes.c_int32, I64, I64, P, P, P]),
+                       ("moe_dequantize_mxfp4", [P, P, I64, I64, P, P]),
+                       ("moe_quantize_permute_mxfp4", [S] + [P] * 6),
+                       ("moe_grouped_gemm_up_mxfp4", [S] + [P] * 11),
+                       ("moe_grouped_gemm_down_mxfp4", [S] + [P] * 9),
+                       ("moe_mxfp4_workspace_size", [S, Z]),
+                       ("moe_forward_mxfp4", [S] + [P] * 11),
+                       ("moe_balance_workspace_size", [S, Z]),
+                       ("moe_balance_loss", [S] + [P] * 9),
+                       ("moe_balance_loss_backward", [S] + [P] * 7)):
+        fn = getattr(lib, name)
+        fn.restype = st
+        fn.argtypes = args
     _lib = lib
     return lib
 
@@ -330,3 +353,175 @@ def moe_forward_raw(s, logits_ptr, x_ptr, wg_ptr, wu_ptr, wd_ptr, out_ptr, ws_pt
     s = _shape_obj(s)
     _check(load().moe_forward(ctypes.byref(s), logits_ptr, x_ptr, wg_ptr, wu_ptr, wd_ptr, out_ptr,
                               ws_ptr, stream_handle), "moe_forward")
+
+
+def mxfp4_sizes(rows: int, cols: int) -> tuple:
+    """(bytes of the codes, bytes of the scales) of an MXFP4 matrix [rows, cols]."""
+    c, z = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(load().moe_mxfp4_sizes(rows, cols, ctypes.byref(c), ctypes.byref(z)), "moe_mxfp4_sizes")
+    return c.value, z.value
+
+
+def alloc_mxfp4(rows: int, cols: int, device="cuda") -> tuple:
+    """Device buffers (codes [rows, cols / 2], scales) for an MXFP4 matrix."""
+    import torch
+    scale_bytes = mxfp4_sizes(rows, cols)[1]
+    return (torch.empty((rows, cols // 2), dtype=torch.uint8, device=device),
+            torch.empty(scale_bytes, dtype=torch.uint8, device=device))
+
+
+def _mxfp4_ptrs(codes, scales, rows, cols, name):
+    import torch
+    code_bytes, scale_bytes = mxfp4_sizes(rows, cols)
+    return [_dev_tensor(codes, torch.uint8, code_bytes, name + "codes"),
+            _dev_tensor(scales, torch.uint8, scale_bytes, name + "scales")]
+
+
+def moe_quantize_mxfp4(x, rows, cols, codes, scales, stream=None):
+    import torch
+    out = _mxfp4_ptrs(codes, scales, rows, cols, "")
+    _check(load().moe_quantize_mxfp4(_dev_tensor(x, torch.bfloat16, rows * cols, "x"), rows, cols, *out,
+                                     _stream(stream)), "moe_quantize_mxfp4")
+
+
+def moe_quantize_weights_mxfp4(w, E, K, N, codes, scales, stream=None):
+    """W [E, K, N] (K the reduction axis) to the MXFP4 matrix [E * N, K]."""
+    import torch
+    out = _mxfp4_ptrs(codes, scales, E * N, K, "")
+    _check(load().moe_quantize_weights_mxfp4(_dev_tensor(w, torch.bfloat16, E * K * N, "w"), E, K, N, *out,
+                                             _stream(stream)), "moe_quantize_weights_mxfp4")
+
+
+def moe_dequantize_mxfp4(codes, scales, rows, cols, x, stream=None):
+    import torch
+    args = _mxfp4_ptrs(codes, scales, rows, cols, "")
+    _check(load().moe_dequantize_mxfp4(*args, rows, cols, _dev_tensor(x, torch.bfloat16, rows * cols, "x"),
+                                       _stream(stream)), "moe_dequantize_mxfp4")
+
+
+def moe_quantize_permute_mxfp4(s, X, scatter_idx, codes, scales, ws, stream=None):
+    import torch
+    s = _shape_obj(s)
+    mr = capacity(s)[1]  # refuses an unsupported shape
+    args = [_dev_tensor(X, torch.bfloat16, s.T * s.H, "X"),
+            _dev_tensor(scatter_idx, torch.int32, s.T * s.k, "scatter_idx"),
+            *_mxfp4_ptrs(codes, scales, mr, s.H, ""),
+            _dev_tensor(ws, torch.uint8, 256, "ws")]
+    _check(load().moe_quantize_permute_mxfp4(ctypes.byref(s), *args, _stream(stream)), "moe_quantize_permute_mxfp4")
+
+
+def moe_grouped_gemm_up_mxfp4(s, x_codes, x_scales, counts, off_pad, wg_codes, wg_scales, wu_codes, wu_scales, h,
+                              ws, stream=None):
+    """The gate/up product on MXFP4 rows and weights; ws: an MXFP4 workspace,
+    or any uint8 buffer of at least 256 bytes, zeroed once."""
+    import torch
+    s = _shape_obj(s)
+    mr = capacity(s)[1]
+    args = [*_mxfp4_ptrs(x_codes, x_scales, mr, s.H, "x_"),
+            _dev_tensor(counts, torch.int32, s.E, "counts"),
+            _dev_tensor(off_pad, torch.int32, s.E + 1, "off_pad"),
+            *_mxfp4_ptrs(wg_codes, wg_scales, s.E * s.I, s.H, "wg_"),
+            *_mxfp4_ptrs(wu_codes, wu_scales, s.E * s.I, s.H, "wu_"),
+            _dev_tensor(h, torch.bfloat16, mr * s.I, "h"),
+            _dev_tensor(ws, torch.uint8, 256, "ws")]
+    _check(load().moe_grouped_gemm_up_mxfp4(ctypes.byref(s), *args, _stream(stream)), "moe_grouped_gemm_up_mxfp4")
+
+
+def moe_grouped_gemm_down_mxfp4(s, h_codes, h_scales, counts, off_pad, wd_codes, wd_scales, Y, ws, stream=None):
+    """The down product on MXFP4 rows and weights; ws as for the gate/up product."""
+    import torch
+    s = _shape_obj(s)
+    mr = capacity(s)[1]
+    args = [*_mxfp4_ptrs(h_codes, h_scales, mr, s.I, "h_"),
+            _dev_tensor(counts, torch.int32, s.E, "counts"),
+            _dev_tensor(off_pad, torch.int32, s.E + 1, "off_pad"),
+            *_mxfp4_ptrs(wd_codes, wd_scales, s.E * s.H, s.I, "wd_"),
+            _dev_tensor(Y, torch.bfloat16, mr * s.H, "Y"),
+            _dev_tensor(ws, torch.uint8, 256, "ws")]
+    _check(load().moe_grouped_gemm_down_mxfp4(ctypes.byref(s), *args, _stream(stream)),
+           "moe_grouped_gemm_down_mxfp4")
+
+
+def mxfp4_workspace_size(s) -> int:
+    n = ctypes.c_size_t()
+    _check(load().moe_mxfp4_workspace_size(_sp(s), ctypes.byref(n)), "moe_mxfp4_workspace_size")
+    return n.value
+
+
+def alloc_mxfp4_workspace(s, device="cuda", stream=None):
+    """A uint8 CUDA tensor of moe_mxfp4_workspace_size bytes with its status word cleared."""
+    import torch
+    ws = torch.empty(mxfp4_workspace_size(s), dtype=torch.uint8, device=device)
+    workspace_init(s, ws, stream)
+    return ws
+
+
+def moe_forward_mxfp4(s, logits, X, wg_codes, wg_scales, wu_codes, wu_scales, wd_codes, wd_scales, out, ws,
+                      stream=None):
+    """moe_forward with the experts' products in MXFP4 (weights as moe_quantize_weights_mxfp4 leaves them)."""
+    import torch
+    s = _shape_obj(s)
+    ws_bytes = mxfp4_workspace_size(s)  # refuses an unsupported shape
+    bf = torch.bfloat16
+    args = [_dev_tensor(logits, torch.float32, s.T * s.E, "logits"),
+            _dev_tensor(X, bf, s.T * s.H, "X"),
+            *_mxfp4_ptrs(wg_codes, wg_scales, s.E * s.I, s.H, "wg_"),
+            *_mxfp4_ptrs(wu_codes, wu_scales, s.E * s.I, s.H, "wu_"),
+            *_mxfp4_ptrs(wd_codes, wd_scales, s.E * s.H, s.I, "wd_"),
+            _dev_tensor(out, bf, s.T * s.H, "out"),
+            _dev_tensor(ws, torch.uint8, ws_bytes, "ws")]
+    _check(load().moe_forward_mxfp4(ctypes.byref(s), *args, _stream(stream)), "moe_forward_mxfp4")
+
+
+def balance_workspace_size(s) -> int:
+    n = ctypes.c_size_t()
+    _check(load().moe_balance_workspace_size(_sp(s), ctypes.byref(n)), "moe_balance_workspace_size")
+    return n.value
+
+
+def alloc_balance_workspace(s, device="cuda", stream=None):
+    """A uint8 CUDA tensor of moe_balance_workspace_size bytes with its counters cleared."""
+    import torch
+    ws = torch.empty(balance_workspace_size(s), dtype=torch.uint8, device=device)
+    workspace_init(s, ws, stream)
+    return ws
+
+
+def _mask_ptr(mask, n):
+    import torch
+    if mask is None:
+        return None
+    if isinstance(mask, torch.Tensor) and mask.dtype == torch.bool:
+        return _dev_tensor(mask, torch.bool, n, "mask")
+    return _dev_tensor(mask, torch.uint8, n, "mask")
+
+
+def moe_balance_loss(s, logits, topk_ids, mask, counts, num_tokens, mean_probs, losses, ws, stream=None):
+    """Per-expert counts and mean probabilities, and losses = (balance, z) of the
+    tokens whose mask (uint8 or bool [T], or None) is non-zero."""
+    import torch
+    s = _shape_obj(s)
+    ws_bytes = balance_workspace_size(s)  # refuses an unsupported shape
+    args = [_dev_tensor(logits, torch.float32, s.T * s.E, "logits"),
+            _dev_tensor(topk_ids, torch.int32, s.T * s.k, "topk_ids"),
+            _mask_ptr(mask, s.T),
+            _dev_tensor(counts, torch.int32, s.E, "counts"),
+            _dev_tensor(num_tokens, torch.int32, 1, "num_tokens"),
+            _dev_tensor(mean_probs, torch.float32, s.E, "mean_probs"),
+            _dev_tensor(losses, torch.float32, 2, "losses"),
+            _dev_tensor(ws, torch.uint8, ws_bytes, "ws")]
+    _check(load().moe_balance_loss(ctypes.byref(s), *args, _stream(stream)), "moe_balance_loss")
+
+
+def moe_balance_loss_backward(s, logits, mask, counts, num_tokens, grad_losses, dlogits, stream=None):
+    """The gradient of grad_losses[0] * balance + grad_losses[1] * z to the logits."""
+    import torch
+    s = _shape_obj(s)
+    capacity(s)  # refuses an unsupported shape
+    args = [_dev_tensor(logits, torch.float32, s.T * s.E, "logits"),
+            _mask_ptr(mask, s.T),
+            _dev_tensor(counts, torch.int32, s.E, "counts"),
+            _dev_tensor(num_tokens, torch.int32, 1, "num_tokens"),
+            _dev_tensor(grad_losses, torch.float32, 2, "grad_losses"),
+            _dev_tensor(dlogits, torch.float32, s.T * s.E, "dlogits")]
+    _check(load().moe_balance_loss_backward(ctypes.byref(s), *args, _stream(stream)), "moe_balance_loss_backward")

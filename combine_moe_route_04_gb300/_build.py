@@ -17,8 +17,9 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe_gb300.so")
-SOURCES = ["moe_api.cu", "moe_route.cu", "moe_gemm.cu", "moe_combine.cu", "moe_check.cu"]
-HEADERS = ["moe_device.cuh", "moe_internal.h"]
+SOURCES = ["moe_api.cu", "moe_route.cu", "moe_gemm.cu", "moe_combine.cu", "moe_check.cu",
+           "moe_mxfp4.cu", "moe_mxfp4_gemm.cu", "moe_balance.cu"]
+HEADERS = ["moe_device.cuh", "moe_internal.h", "moe_mxfp4.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -3,6 +3,7 @@
 // launch sequence of each step.  Host code only; it allocates no device memory.
 #include <cstdint>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 
 #include <cudaTypedefs.h>
@@ -159,6 +160,62 @@ moe_status run_down(const moe_shape& s, const uint16_t* h, const int32_t* counts
       launch_gemm_down(s, m, Y, off_pad, counts, w.status, ws_sched_down(w.status), win_done, num_sms, st));
 }
 
+// NULL or misaligned pointers of a call (the first one found decides).
+moe_status check_ptrs(std::initializer_list<const void*> ptrs) {
+  for (const void* p : ptrs) {
+    if (p == nullptr) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(p)) return MOE_ERR_MISALIGNED;
+  }
+  return MOE_OK;
+}
+
+bool mxfp4_dim(int64_t n) { return n >= 128 && n <= 32768 && n % 128 == 0; }
+moe_status check_mxfp4(int64_t rows, int64_t cols) {
+  return rows >= 1 && rows < (int64_t(1) << 31) && mxfp4_dim(cols) ? MOE_OK : MOE_ERR_UNSUPPORTED_SHAPE;
+}
+
+// Byte offsets of moe_forward_mxfp4's workspace (its first 256 bytes as in
+// every workspace).
+struct Mxfp4Layout {
+  size_t chunk_counts, topk_ids, topk_w, counts, off_pad, block_expert, num_blocks, gather_idx, scatter_idx;
+  size_t x_codes, x_scales, h_codes, h_scales, y, total;
+};
+Mxfp4Layout mxfp4_layout(const moe_shape& s) {
+  Mxfp4Layout L{};
+  const size_t T = static_cast<size_t>(s.T), E = static_cast<size_t>(s.E), k = static_cast<size_t>(s.k);
+  const size_t mr = static_cast<size_t>(max_rows_of(s)), H = static_cast<size_t>(s.H), I = static_cast<size_t>(s.I);
+  size_t off = align_up(256);
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = align_up(off + bytes);
+    return at;
+  };
+  L.chunk_counts = take(E * static_cast<size_t>(num_chunks_of(s)) * 4);
+  L.topk_ids = take(T * k * 4);
+  L.topk_w = take(T * k * 4);
+  L.counts = take(E * 4);
+  L.off_pad = take((E + 1) * 4);
+  L.block_expert = take(static_cast<size_t>(max_blocks_of(s)) * 4);
+  L.num_blocks = take(4);
+  L.gather_idx = take(mr * 4);
+  L.scatter_idx = take(T * k * 4);
+  L.x_codes = take(mr * H / 2);
+  L.x_scales = take(mr * H / 32);
+  L.h_codes = take(mr * I / 2);
+  L.h_scales = take(mr * I / 32);
+  L.y = take(mr * H * 2);
+  L.total = off;
+  return L;
+}
+
+// Tensor maps of a product: rows [max_rows][K/2], weights [E*N][K/2].
+bool mxfp4_maps(const moe_shape& s, int64_t K, int64_t N, const uint8_t* rows, const uint8_t* w0, const uint8_t* w1,
+                Mxfp4Maps* m) {
+  const uint64_t kb = static_cast<uint64_t>(K) / 2, wr = static_cast<uint64_t>(s.E) * static_cast<uint64_t>(N);
+  return encode_bytes_2d(&m->t, rows, static_cast<uint64_t>(max_rows_of(s)), kb, 32) &&
+         encode_bytes_2d(&m->w0, w0, wr, kb, 128) && encode_bytes_2d(&m->w1, w1, wr, kb, 128);
+}
+
 }  // namespace
 
 moe_status device_ready(cudaStream_t st, int* num_sms, DeviceRestore* restore) {
@@ -210,6 +267,18 @@ bool encode_bf16_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t 
   const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
                               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
+bool encode_bytes_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t bytes_per_row, uint32_t box_rows) {
+  if (g_encode == nullptr) return false;
+  cuuint64_t dims[2] = {bytes_per_row, rows};
+  cuuint64_t strides[1] = {bytes_per_row};
+  cuuint32_t box[2] = {128, box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
 
@@ -423,6 +492,189 @@ moe_status moe_forward(const moe_shape* shape, const float* logits, const moe_bf
   st = run_down(sh, v.h, v.counts, v.off_pad, W_down, v.Y, w, w.win_done, sms, s);
   if (st != MOE_OK) return st;
   return cuda_status(launch_combine(sh, v.Y, v.scatter_idx, v.topk_w, out, w.status, sms, s));
+}
+
+moe_status moe_mxfp4_sizes(int64_t rows, int64_t cols, size_t* code_bytes, size_t* scale_bytes) {
+  const moe_status st = check_mxfp4(rows, cols);
+  if (st != MOE_OK) return st;
+  if (code_bytes == nullptr || scale_bytes == nullptr) return MOE_ERR_INVALID_ARG;
+  *code_bytes = static_cast<size_t>(rows) * static_cast<size_t>(cols) / 2;
+  *scale_bytes = static_cast<size_t>((rows + 127) / 128 * 128) * static_cast<size_t>(cols) / 32;
+  return MOE_OK;
+}
+
+moe_status moe_quantize_mxfp4(const moe_bf16* x, int64_t rows, int64_t cols, uint8_t* codes, uint8_t* scales,
+                              moe_stream_t stream) {
+  moe_status st = check_mxfp4(rows, cols);
+  if (st != MOE_OK) return st;
+  st = check_ptrs({x, codes, scales});
+  if (st != MOE_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  DeviceRestore restore;
+  st = prepare_device(s, nullptr, &restore);
+  if (st != MOE_OK) return st;
+  return cuda_status(launch_quantize_rows(x, rows, cols, codes, scales, s));
+}
+
+moe_status moe_quantize_weights_mxfp4(const moe_bf16* w, int32_t E, int64_t K, int64_t N, uint8_t* codes,
+                                      uint8_t* scales, moe_stream_t stream) {
+  if (E < 1 || E > 256 || !mxfp4_dim(K) || !mxfp4_dim(N)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  moe_status st = check_ptrs({w, codes, scales});
+  if (st != MOE_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  DeviceRestore restore;
+  st = prepare_device(s, nullptr, &restore);
+  if (st != MOE_OK) return st;
+  return cuda_status(launch_quantize_weights(w, E, K, N, codes, scales, s));
+}
+
+moe_status moe_dequantize_mxfp4(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, moe_bf16* x,
+                                moe_stream_t stream) {
+  moe_status st = check_mxfp4(rows, cols);
+  if (st != MOE_OK) return st;
+  st = check_ptrs({codes, scales, x});
+  if (st != MOE_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  DeviceRestore restore;
+  st = prepare_device(s, nullptr, &restore);
+  if (st != MOE_OK) return st;
+  return cuda_status(launch_dequantize_rows(codes, scales, rows, cols, x, s));
+}
+
+moe_status moe_quantize_permute_mxfp4(const moe_shape* shape, const moe_bf16* X, const int32_t* scatter_idx,
+                                      uint8_t* codes, uint8_t* scales, void* ws, moe_stream_t stream) {
+  moe_status st = check_shape(shape);
+  if (st != MOE_OK) return st;
+  st = check_ptrs({X, scatter_idx, codes, scales, ws});
+  if (st != MOE_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  DeviceRestore restore;
+  st = prepare_device(s, nullptr, &restore);
+  if (st != MOE_OK) return st;
+  return cuda_status(launch_quantize_permute(*shape, X, scatter_idx, codes, scales, ws_status(ws), s));
+}
+
+moe_status moe_grouped_gemm_up_mxfp4(const moe_shape* shape, const uint8_t* x_codes, const uint8_t* x_scales,
+                                     const int32_t* counts, const int32_t* off_pad, const uint8_t* wg_codes,
+                                     const uint8_t* wg_scales, const uint8_t* wu_codes, const uint8_t* wu_scales,
+                                     moe_bf16* h, void* ws, moe_stream_t stream) {
+  moe_status st = check_shape(shape);
+  if (st != MOE_OK) return st;
+  st = check_ptrs({x_codes, x_scales, counts, off_pad, wg_codes, wg_scales, wu_codes, wu_scales, h, ws});
+  if (st != MOE_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int sms = 0;
+  DeviceRestore restore;
+  st = prepare_device(s, &sms, &restore);
+  if (st != MOE_OK) return st;
+  Mxfp4Maps m;
+  if (!mxfp4_maps(*shape, shape->H, shape->I, x_codes, wg_codes, wu_codes, &m)) return MOE_ERR_CUDA;
+  return cuda_status(
+      launch_mxfp4_up(*shape, m, x_scales, wg_scales, wu_scales, h, off_pad, counts, ws_status(ws), sms, s));
+}
+
+moe_status moe_grouped_gemm_down_mxfp4(const moe_shape* shape, const uint8_t* h_codes, const uint8_t* h_scales,
+                                       const int32_t* counts, const int32_t* off_pad, const uint8_t* wd_codes,
+                                       const uint8_t* wd_scales, moe_bf16* Y, void* ws, moe_stream_t stream) {
+  moe_status st = check_shape(shape);
+  if (st != MOE_OK) return st;
+  st = check_ptrs({h_codes, h_scales, counts, off_pad, wd_codes, wd_scales, Y, ws});
+  if (st != MOE_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int sms = 0;
+  DeviceRestore restore;
+  st = prepare_device(s, &sms, &restore);
+  if (st != MOE_OK) return st;
+  Mxfp4Maps m;
+  if (!mxfp4_maps(*shape, shape->I, shape->H, h_codes, wd_codes, wd_codes, &m)) return MOE_ERR_CUDA;
+  return cuda_status(launch_mxfp4_down(*shape, m, h_scales, wd_scales, Y, off_pad, counts, ws_status(ws), sms, s));
+}
+
+moe_status moe_mxfp4_workspace_size(const moe_shape* shape, size_t* bytes) {
+  const moe_status st = check_shape(shape);
+  if (st != MOE_OK) return st;
+  if (bytes == nullptr) return MOE_ERR_INVALID_ARG;
+  *bytes = mxfp4_layout(*shape).total;
+  return MOE_OK;
+}
+
+moe_status moe_forward_mxfp4(const moe_shape* shape, const float* logits, const moe_bf16* X, const uint8_t* wg_codes,
+                             const uint8_t* wg_scales, const uint8_t* wu_codes, const uint8_t* wu_scales,
+                             const uint8_t* wd_codes, const uint8_t* wd_scales, moe_bf16* out, void* ws,
+                             moe_stream_t stream) {
+  moe_status st = check_shape(shape);
+  if (st != MOE_OK) return st;
+  st = check_ptrs({logits, X, wg_codes, wg_scales, wu_codes, wu_scales, wd_codes, wd_scales, out, ws});
+  if (st != MOE_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int sms = 0;
+  DeviceRestore restore;
+  st = prepare_device(s, &sms, &restore);
+  if (st != MOE_OK) return st;
+  const moe_shape& sh = *shape;
+  const Mxfp4Layout L = mxfp4_layout(sh);
+  uint8_t* b = static_cast<uint8_t*>(ws);
+  auto i32 = [&](size_t at) { return reinterpret_cast<int32_t*>(b + at); };
+  float* topk_w = reinterpret_cast<float*>(b + L.topk_w);
+  uint16_t* Y = reinterpret_cast<uint16_t*>(b + L.y);
+  uint32_t* status = ws_status(ws);
+  Mxfp4Maps up, down;
+  if (!mxfp4_maps(sh, sh.H, sh.I, b + L.x_codes, wg_codes, wu_codes, &up) ||
+      !mxfp4_maps(sh, sh.I, sh.H, b + L.h_codes, wd_codes, wd_codes, &down))
+    return MOE_ERR_CUDA;
+  if (launch_route(sh, logits, i32(L.topk_ids), topk_w, i32(L.counts), i32(L.off_pad), i32(L.block_expert),
+                   i32(L.num_blocks), i32(L.gather_idx), i32(L.scatter_idx), i32(L.chunk_counts),
+                   ws_route_counter(ws), status, s) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  if (launch_quantize_permute(sh, X, i32(L.scatter_idx), b + L.x_codes, b + L.x_scales, status, s) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  if (launch_mxfp4_up_quantized(sh, up, b + L.x_scales, wg_scales, wu_scales, b + L.h_codes, b + L.h_scales,
+                                i32(L.off_pad), i32(L.counts), status, sms, s) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  if (launch_mxfp4_down(sh, down, b + L.h_scales, wd_scales, Y, i32(L.off_pad), i32(L.counts), status, sms, s) !=
+      cudaSuccess)
+    return MOE_ERR_CUDA;
+  return cuda_status(launch_combine(sh, Y, i32(L.scatter_idx), topk_w, out, status, sms, s));
+}
+
+moe_status moe_balance_workspace_size(const moe_shape* shape, size_t* bytes) {
+  const moe_status st = check_shape(shape);
+  if (st != MOE_OK) return st;
+  if (bytes == nullptr) return MOE_ERR_INVALID_ARG;
+  *bytes = 256 + balance_partial_bytes(*shape);
+  return MOE_OK;
+}
+
+moe_status moe_balance_loss(const moe_shape* shape, const float* logits, const int32_t* topk_ids, const uint8_t* mask,
+                            int32_t* counts, int32_t* num_tokens, float* mean_probs, float* losses, void* ws,
+                            moe_stream_t stream) {
+  moe_status st = check_shape(shape);
+  if (st != MOE_OK) return st;
+  st = check_ptrs({logits, topk_ids, counts, num_tokens, mean_probs, losses, ws});
+  if (st != MOE_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int sms = 0;
+  DeviceRestore restore;
+  st = prepare_device(s, &sms, &restore);
+  if (st != MOE_OK) return st;
+  return cuda_status(launch_balance_loss(*shape, logits, topk_ids, mask, counts, num_tokens, mean_probs, losses,
+                                         ws_status(ws) + 64, ws_balance_counter(ws), ws_status(ws), sms, s));
+}
+
+moe_status moe_balance_loss_backward(const moe_shape* shape, const float* logits, const uint8_t* mask,
+                                     const int32_t* counts, const int32_t* num_tokens, const float* grad_losses,
+                                     float* dlogits, moe_stream_t stream) {
+  moe_status st = check_shape(shape);
+  if (st != MOE_OK) return st;
+  st = check_ptrs({logits, counts, num_tokens, grad_losses, dlogits});
+  if (st != MOE_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int sms = 0;
+  DeviceRestore restore;
+  st = prepare_device(s, &sms, &restore);
+  if (st != MOE_OK) return st;
+  return cuda_status(
+      launch_balance_backward(*shape, logits, mask, counts, num_tokens, grad_losses, dlogits, sms, s));
 }
 
 }  // extern "C"

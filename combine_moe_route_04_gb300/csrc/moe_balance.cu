@@ -1,0 +1,373 @@
+// moe_balance.cu -- the router's balance loss, its per-expert counts and the
+// gradient to the logits.
+//
+// Over the n tokens that take part (mask byte non-zero, or no mask, and not
+// every logit -inf), with p = softmax(logits), f_e = counts_e / (n k) and
+// P_e = sum_t p_te / n:
+//   balance = E sum_e f_e P_e          z = sum_t logsumexp(l_t)^2 / n
+//   d/dl_te = p_te [ g0 E/n (f_e - sum_j f_j p_tj) + g1 2/n logsumexp(l_t) ]
+// (the counts are constants for the gradient).  Both kernels read the logits
+// once and are bound by memory on large batches and by launch latency on small
+// ones.
+//
+// A token's row is held by a group of G lanes (a power of two up to 32), each
+// with up to eight logits: groups of four consecutive ones (16-byte loads)
+// where E is a multiple of 4, single ones otherwise.  Sums over tokens are
+// kept per lane and joined in a fixed order (warp, CTA, then the CTA that
+// finishes last over all CTAs), so results are reproducible without
+// floating-point atomics.
+#include <cmath>
+#include <type_traits>
+#include <cstdint>
+
+#include "moe_device.cuh"
+#include "moe_internal.h"
+
+namespace moe {
+namespace {
+
+constexpr int kMaxE = 256;
+constexpr int kFwdThreads = 1024;
+constexpr int kFwdWarps = kFwdThreads / 32;
+constexpr int kBwdThreads = 256;
+
+// A lane's logits of one row: V groups of W consecutive experts, group i of
+// lane gl (its index inside its G lanes) at expert W (gl + G i).
+template <int V, int W>
+struct Row {
+  float v[V * W];
+
+  __device__ __forceinline__ static int expert(int gl, int G, int x) { return W * (gl + G * (x / W)) + x % W; }
+
+  // absent experts (and whole rows that are not `there`) read as -inf
+  __device__ __forceinline__ void load(const float* __restrict__ row, int gl, int G, int E, bool there) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int e = W * (gl + G * i);
+      const bool in = there && e < E;
+      if constexpr (W == 4) {
+        float4 q = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        if (in) q = __ldg(reinterpret_cast<const float4*>(row + e));
+        v[4 * i] = q.x;
+        v[4 * i + 1] = q.y;
+        v[4 * i + 2] = q.z;
+        v[4 * i + 3] = q.w;
+      } else {
+        v[i] = in ? __ldg(row + e) : -INFINITY;
+      }
+    }
+  }
+
+  // v becomes exp(v - max) (max taken as 0 where nothing is above -inf);
+  // returns that max and the row's sum, which is 0 only if every logit is
+  // -inf (a NaN anywhere makes it NaN).
+  __device__ __forceinline__ void exps(int G, float& top, float& sum) {
+    float m = v[0];
+#pragma unroll
+    for (int x = 1; x < V * W; ++x) m = fmaxf(m, v[x]);
+    for (int o = G >> 1; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    top = m == -INFINITY ? 0.0f : m;
+    float s = 0.0f;
+#pragma unroll
+    for (int x = 0; x < V * W; ++x) {
+      v[x] = __expf(v[x] - top);
+      s += v[x];
+    }
+    for (int o = G >> 1; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    sum = s;
+  }
+};
+
+template <int V, int W>
+__global__ void __launch_bounds__(kFwdThreads, 1)
+    balance_loss_kernel(const float* __restrict__ logits, const int32_t* __restrict__ topk_ids,
+                        const uint8_t* __restrict__ mask, int T, int E, int k, int G, int32_t* __restrict__ counts,
+                        int32_t* __restrict__ num_tokens, float* __restrict__ mean_probs, float* __restrict__ losses,
+                        uint32_t* __restrict__ partials, uint32_t* __restrict__ counter,
+                        uint32_t* __restrict__ status) {
+  __shared__ float s_p[kFwdWarps * kMaxE];
+  __shared__ int s_cnt[kMaxE];
+  __shared__ float s_z[kFwdWarps];
+  __shared__ int s_n[kFwdWarps];
+  __shared__ int s_last;
+  pdl_launch_dependents();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int gl = lane & (G - 1);
+  const int per_warp = 32 / G;
+  for (int e = tid; e < E; e += kFwdThreads) s_cnt[e] = 0;
+  __syncthreads();
+  pdl_wait();
+
+  float acc[V * W];
+#pragma unroll
+  for (int x = 0; x < V * W; ++x) acc[x] = 0.0f;
+  float z = 0.0f;
+  int n = 0;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kFwdWarps * per_warp;
+  const int64_t first = (static_cast<int64_t>(blockIdx.x) * kFwdWarps + warp) * per_warp;
+  for (int64_t t0 = first; t0 < T; t0 += stride) {  // uniform across the warp
+    const int64_t t = t0 + lane / G;
+    const bool there = t < T && (mask == nullptr || __ldg(mask + t) != 0);
+    Row<V, W> r;
+    r.load(logits + t * E, gl, G, E, there);
+    float top, sum;
+    r.exps(G, top, sum);
+    const bool takes = there && sum != 0.0f;
+    const float inv = takes ? 1.0f / sum : 0.0f;
+    if (takes) {
+#pragma unroll
+      for (int x = 0; x < V * W; ++x) acc[x] += r.v[x] * inv;
+      if (gl == 0) {
+        const float lse = top + logf(sum);
+        z += lse * lse;
+        ++n;
+      }
+      for (int j = gl; j < k; j += G) {
+        const int e = __ldg(topk_ids + t * k + j);
+        if (e >= 0 && e < E) atomicAdd(&s_cnt[e], 1);
+        else record_status(status, kStatusBounds);
+      }
+    }
+  }
+  // the warp's groups hold the same experts: join them, then the warps
+  for (int o = G; o < 32; o <<= 1) {
+#pragma unroll
+    for (int x = 0; x < V * W; ++x) acc[x] += __shfl_xor_sync(0xffffffffu, acc[x], o);
+  }
+  for (int o = 16; o > 0; o >>= 1) {
+    z += __shfl_xor_sync(0xffffffffu, z, o);
+    n += __shfl_xor_sync(0xffffffffu, n, o);
+  }
+  if (lane < G) {
+#pragma unroll
+    for (int x = 0; x < V * W; ++x) {
+      const int e = Row<V, W>::expert(gl, G, x);
+      if (e < E) s_p[warp * E + e] = acc[x];
+    }
+  }
+  if (lane == 0) {
+    s_z[warp] = z;
+    s_n[warp] = n;
+  }
+  __syncthreads();
+  float p_sum = 0.0f;  // thread e < E: this CTA's sum for expert e
+  int c_sum = 0;
+  if (tid < E) {
+    for (int w = 0; w < kFwdWarps; ++w) p_sum += s_p[w * E + tid];
+    c_sum = s_cnt[tid];
+  }
+  float z_sum = 0.0f;  // warp 0: the CTA's
+  int n_sum = 0;
+  if (warp == 0) {
+    z_sum = s_z[lane];
+    n_sum = s_n[lane];
+    for (int o = 16; o > 0; o >>= 1) {
+      z_sum += __shfl_xor_sync(0xffffffffu, z_sum, o);
+      n_sum += __shfl_xor_sync(0xffffffffu, n_sum, o);
+    }
+  }
+
+  if (gridDim.x > 1) {
+    // partials: [CTA][E] sums, [CTA][E] counts, [CTA] z, [CTA] n
+    float* part_p = reinterpret_cast<float*>(partials);
+    int32_t* part_c = reinterpret_cast<int32_t*>(partials) + static_cast<int64_t>(gridDim.x) * E;
+    float* part_z = reinterpret_cast<float*>(part_c + static_cast<int64_t>(gridDim.x) * E);
+    int32_t* part_n = reinterpret_cast<int32_t*>(part_z + gridDim.x);
+    if (tid < E) {
+      part_p[blockIdx.x * E + tid] = p_sum;
+      part_c[blockIdx.x * E + tid] = c_sum;
+    }
+    if (tid == 0) {
+      part_z[blockIdx.x] = z_sum;
+      part_n[blockIdx.x] = n_sum;
+    }
+    __syncthreads();
+    if (tid == 0) {
+      fence_acq_rel_gpu();  // release: the CTA's partials (ordered by the barrier) before the arrival
+      const uint32_t ticket = atomicAdd(counter, 1u);
+      if (ticket >= gridDim.x) record_status(status, kStatusBounds);  // the counter was not cleared
+      s_last = ticket == gridDim.x - 1 ? 1 : 0;
+      if (ticket >= gridDim.x - 1) *counter = 0u;
+      fence_acq_rel_gpu();  // acquire: every other CTA's partials
+    }
+    __syncthreads();
+    if (!s_last) return;
+    // 1024 / 256 threads share an expert's column of partials, in row order
+    // each; their sums join in a fixed order
+    const int e = tid & (kMaxE - 1), part = tid / kMaxE;
+    constexpr int kParts = kFwdThreads / kMaxE;
+    float ps = 0.0f;
+    int cs = 0;
+    if (e < E) {
+#pragma unroll 8
+      for (int b = part; b < static_cast<int>(gridDim.x); b += kParts) {
+        ps += __ldcg(part_p + b * E + e);
+        cs += __ldcg(part_c + b * E + e);
+      }
+    }
+    int* s_ci = reinterpret_cast<int*>(s_p + kParts * kMaxE);
+    s_p[part * kMaxE + e] = ps;
+    s_ci[part * kMaxE + e] = cs;
+    if (warp == 0) {
+      z_sum = 0.0f;
+      n_sum = 0;
+      for (int b = lane; b < static_cast<int>(gridDim.x); b += 32) {
+        z_sum += __ldcg(part_z + b);
+        n_sum += __ldcg(part_n + b);
+      }
+      for (int o = 16; o > 0; o >>= 1) {
+        z_sum += __shfl_xor_sync(0xffffffffu, z_sum, o);
+        n_sum += __shfl_xor_sync(0xffffffffu, n_sum, o);
+      }
+    }
+    __syncthreads();
+    if (tid < E) {
+      p_sum = 0.0f;
+      c_sum = 0;
+      for (int q = 0; q < kParts; ++q) {
+        p_sum += s_p[q * kMaxE + tid];
+        c_sum += s_ci[q * kMaxE + tid];
+      }
+    }
+    __syncthreads();
+  }
+  // the results: thread e writes its expert's; warps 0-7 form the dot product
+  if (tid == 0) s_n[0] = n_sum;
+  __syncthreads();
+  const int total_n = s_n[0];
+  const float inv_n = total_n > 0 ? 1.0f / static_cast<float>(total_n) : 0.0f;
+  float dot = 0.0f;
+  if (tid < E) {
+    const float P = p_sum * inv_n;
+    counts[tid] = c_sum;
+    mean_probs[tid] = P;
+    dot = total_n > 0 ? static_cast<float>(c_sum) / (static_cast<float>(total_n) * static_cast<float>(k)) * P : 0.0f;
+  }
+  if (warp < kMaxE / 32) {
+    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+    if (lane == 0) s_z[warp] = dot;
+  }
+  __syncthreads();
+  if (tid == 0) {
+    float d = 0.0f;
+    for (int w = 0; w < kMaxE / 32; ++w) d += s_z[w];
+    losses[0] = static_cast<float>(E) * d;
+    losses[1] = z_sum * inv_n;
+    *num_tokens = total_n;
+  }
+}
+
+template <int V, int W>
+__global__ void __launch_bounds__(kBwdThreads)
+    balance_backward_kernel(const float* __restrict__ logits, const uint8_t* __restrict__ mask, int T, int E, int k,
+                            int G, const int32_t* __restrict__ counts, const int32_t* __restrict__ num_tokens,
+                            const float* __restrict__ grad_losses, float* __restrict__ dlogits) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int gl = lane & (G - 1);
+  const int per_warp = 32 / G;
+  constexpr int kWarps = kBwdThreads / 32;
+  const int n = __ldg(num_tokens);
+  const float inv_n = n > 0 ? 1.0f / static_cast<float>(n) : 0.0f;
+  const float a = __ldg(grad_losses) * static_cast<float>(E) * inv_n;
+  const float b = __ldg(grad_losses + 1) * 2.0f * inv_n;
+  // f_e - 1/E, whose differences are the gradient's: formed from integers, so
+  // that f_e - sum f p loses nothing to cancellation (the p sum to 1)
+  float f[V * W];
+#pragma unroll
+  for (int x = 0; x < V * W; ++x) {
+    const int e = Row<V, W>::expert(gl, G, x);
+    f[x] = 0.0f;
+    if (e < E && n > 0) {
+      const int64_t nk = static_cast<int64_t>(n) * k;
+      f[x] = static_cast<float>(static_cast<int64_t>(__ldg(counts + e)) * E - nk) /
+             (static_cast<float>(nk) * static_cast<float>(E));
+    }
+  }
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kWarps * per_warp;
+  const int64_t first = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * per_warp;
+  for (int64_t t0 = first; t0 < T; t0 += stride) {
+    const int64_t t = t0 + lane / G;
+    const bool there = t < T && (mask == nullptr || __ldg(mask + t) != 0);
+    Row<V, W> r;
+    r.load(logits + t * E, gl, G, E, there);
+    float top, sum;
+    r.exps(G, top, sum);
+    const bool takes = there && sum != 0.0f;
+    const float inv = 1.0f / sum;
+    float dot = 0.0f;
+#pragma unroll
+    for (int x = 0; x < V * W; ++x) {
+      r.v[x] *= inv;
+      dot += f[x] * r.v[x];
+    }
+    for (int o = G >> 1; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+    const float c = b * (top + logf(sum)) - a * dot;
+    if (t < T) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int e = W * (gl + G * i);
+        if (e >= E) continue;
+        float d[W];
+#pragma unroll
+        for (int q = 0; q < W; ++q) d[q] = takes ? r.v[W * i + q] * fmaf(a, f[W * i + q], c) : 0.0f;
+        if constexpr (W == 4) *reinterpret_cast<float4*>(dlogits + t * E + e) = make_float4(d[0], d[1], d[2], d[3]);
+        else dlogits[t * E + e] = d[0];
+      }
+    }
+  }
+}
+
+// lanes per token: the least power of two whose V W logits each cover E
+int lanes_for(int E, int per_lane) {
+  int g = 1;
+  while (g < 32 && g * per_lane < E) g <<= 1;
+  return g;
+}
+
+// The forward and backward kernels of E experts: fn(V, W, G) with the logits
+// per lane as few as E allows (E <= 128 V, or 32 V one by one).
+template <typename F>
+cudaError_t by_experts(int E, F&& fn) {
+  using std::integral_constant;
+  if (E % 4 == 0) {
+    if (E <= 128) return fn(integral_constant<int, 1>{}, integral_constant<int, 4>{}, lanes_for(E, 4));
+    return fn(integral_constant<int, 2>{}, integral_constant<int, 4>{}, 32);
+  }
+  if (E <= 32) return fn(integral_constant<int, 1>{}, integral_constant<int, 1>{}, lanes_for(E, 1));
+  if (E <= 64) return fn(integral_constant<int, 2>{}, integral_constant<int, 1>{}, 32);
+  if (E <= 128) return fn(integral_constant<int, 4>{}, integral_constant<int, 1>{}, 32);
+  return fn(integral_constant<int, 8>{}, integral_constant<int, 1>{}, 32);
+}
+
+}  // namespace
+
+cudaError_t launch_balance_loss(const moe_shape& s, const float* logits, const int32_t* topk_ids, const uint8_t* mask,
+                                int32_t* counts, int32_t* num_tokens, float* mean_probs, float* losses,
+                                uint32_t* partials, uint32_t* counter, uint32_t* status, int num_sms,
+                                cudaStream_t st) {
+  return by_experts(s.E, [&](auto V, auto W, int G) {
+    const int64_t per_cta = static_cast<int64_t>(kFwdWarps) * (32 / G);
+    int64_t grid = (s.T + per_cta - 1) / per_cta;
+    if (grid > num_sms) grid = num_sms;
+    if (grid > kBalanceMaxCtas) grid = kBalanceMaxCtas;
+    return launch_pdl(balance_loss_kernel<V, W>, dim3(static_cast<unsigned>(grid)), dim3(kFwdThreads), 0, st, logits,
+                      topk_ids, mask, s.T, s.E, s.k, G, counts, num_tokens, mean_probs, losses, partials, counter,
+                      status);
+  });
+}
+
+cudaError_t launch_balance_backward(const moe_shape& s, const float* logits, const uint8_t* mask,
+                                    const int32_t* counts, const int32_t* num_tokens, const float* grad_losses,
+                                    float* dlogits, int num_sms, cudaStream_t st) {
+  return by_experts(s.E, [&](auto V, auto W, int G) {
+    const int64_t per_cta = static_cast<int64_t>(kBwdThreads / 32) * (32 / G);
+    int64_t grid = (s.T + per_cta - 1) / per_cta;
+    if (grid > static_cast<int64_t>(num_sms) * 8) grid = static_cast<int64_t>(num_sms) * 8;
+    return launch_pdl(balance_backward_kernel<V, W>, dim3(static_cast<unsigned>(grid)), dim3(kBwdThreads), 0, st,
+                      logits, mask, s.T, s.E, s.k, G, counts, num_tokens, grad_losses, dlogits);
+  });
+}
+
+}  // namespace moe

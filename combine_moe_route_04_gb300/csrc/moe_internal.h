@@ -84,6 +84,8 @@ constexpr int kStatusSnapshotIndex = 48;
 // the histograms; the next kernel puts it back to zero) and the mark that scan
 // leaves, two words in the same cleared 256 bytes
 inline uint32_t* ws_route_counter(void* ws) { return reinterpret_cast<uint32_t*>(ws) + 56; }
+// the balance loss's CTA counter, in the same cleared 256 bytes
+inline uint32_t* ws_balance_counter(void* ws) { return reinterpret_cast<uint32_t*>(ws) + 60; }
 
 // Launch with programmatic stream serialisation (the kernel must call
 // pdl_wait() before touching memory its predecessors use).
@@ -102,6 +104,10 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
+
+// The MXFP4 products cut an expert's c rows into ceil(c / kMxfp4WindowRows)
+// windows that start at multiples of 64 rows.
+constexpr int kMxfp4WindowRows = 192;
 
 // Launchers (asynchronous; return cudaGetLastError()).
 // route_counter: a uint32 that is zero between calls (the call leaves it so).
@@ -150,6 +156,52 @@ cudaError_t launch_gemm_down(const moe_shape& s, const GemmMaps& maps, uint16_t*
 cudaError_t launch_combine(const moe_shape& s, const uint16_t* Y, const int32_t* scatter_idx,
                            const float* topk_w, uint16_t* out, uint32_t* status, int num_sms, cudaStream_t st);
 
+// MXFP4 (codes two per byte along a row, scale bytes in tiles of 128 rows x 4
+// blocks of 32; see include/moe.h): quantisation of dense rows and of weights
+// [E][K][N] (to [E][N][K/2]), the inverse, and tokens quantised into their
+// permuted rows.
+cudaError_t launch_quantize_rows(const uint16_t* x, int64_t rows, int64_t cols, uint8_t* codes, uint8_t* scales,
+                                 cudaStream_t st);
+cudaError_t launch_dequantize_rows(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
+                                   uint16_t* x, cudaStream_t st);
+cudaError_t launch_quantize_weights(const uint16_t* w, int E, int64_t K, int64_t N, uint8_t* codes, uint8_t* scales,
+                                    cudaStream_t st);
+cudaError_t launch_quantize_permute(const moe_shape& s, const uint16_t* X, const int32_t* scatter_idx, uint8_t* codes,
+                                    uint8_t* scales, uint32_t* status, cudaStream_t st);
+
+// The grouped products on MXFP4 operands: code matrices as 128-byte-wide boxes.
+struct Mxfp4Maps {
+  CUtensorMap t;   // rows [max_rows][K/2], box 32 rows
+  CUtensorMap w0;  // weights [E*N][K/2] (gate, or down), box 128 rows
+  CUtensorMap w1;  // the up weights (down: a copy of w0)
+};
+cudaError_t launch_mxfp4_up(const moe_shape& s, const Mxfp4Maps& m, const uint8_t* x_scales, const uint8_t* wg_scales,
+                            const uint8_t* wu_scales, uint16_t* h, const int32_t* off_pad, const int32_t* counts,
+                            uint32_t* status, int num_sms, cudaStream_t st);
+// the same with h quantised to MXFP4 in the epilogue (as launch_quantize_rows
+// would from the bf16 h)
+cudaError_t launch_mxfp4_up_quantized(const moe_shape& s, const Mxfp4Maps& m, const uint8_t* x_scales,
+                                      const uint8_t* wg_scales, const uint8_t* wu_scales, uint8_t* h_codes,
+                                      uint8_t* h_scales, const int32_t* off_pad, const int32_t* counts,
+                                      uint32_t* status, int num_sms, cudaStream_t st);
+cudaError_t launch_mxfp4_down(const moe_shape& s, const Mxfp4Maps& m, const uint8_t* h_scales,
+                              const uint8_t* wd_scales, uint16_t* Y, const int32_t* off_pad, const int32_t* counts,
+                              uint32_t* status, int num_sms, cudaStream_t st);
+
+// Balance loss.  partials: the workspace region past its first 256 bytes
+// (balance_partial_bytes); counter: a uint32 that is zero between calls.
+constexpr int kBalanceMaxCtas = 256;
+inline size_t balance_partial_bytes(const moe_shape& s) {
+  return static_cast<size_t>(kBalanceMaxCtas) * (static_cast<size_t>(s.E) * 8 + 8);
+}
+cudaError_t launch_balance_loss(const moe_shape& s, const float* logits, const int32_t* topk_ids, const uint8_t* mask,
+                                int32_t* counts, int32_t* num_tokens, float* mean_probs, float* losses,
+                                uint32_t* partials, uint32_t* counter, uint32_t* status, int num_sms,
+                                cudaStream_t st);
+cudaError_t launch_balance_backward(const moe_shape& s, const float* logits, const uint8_t* mask,
+                                    const int32_t* counts, const int32_t* num_tokens, const float* grad_losses,
+                                    float* dlogits, int num_sms, cudaStream_t st);
+
 // Diagnostic: one thread waits on an mbarrier that nothing arrives on, through
 // the library's bounded wait; records kStatusTimeout after kWaitLimitNs.
 cudaError_t launch_wait_timeout(uint32_t* status, cudaStream_t st);
@@ -159,5 +211,8 @@ cudaError_t launch_wait_timeout(uint32_t* status, cudaStream_t st);
 // span equals the box's inner extent in bytes (64 or 128).
 bool encode_bf16_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows,
                     uint32_t box_cols);
+// rows x bytes_per_row bytes row-major, box 128 bytes x box_rows, 128-byte
+// swizzle.
+bool encode_bytes_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t bytes_per_row, uint32_t box_rows);
 
 }  // namespace moe

@@ -1,0 +1,497 @@
+// moe_mxfp4_gemm.cu -- grouped products of the expert layer on MXFP4 operands
+// (block-scaled tcgen05.mma, kind::mxf4).
+//
+//   up:   h = bf16(silu(X Wg[e]) * (X Wu[e])), or that h quantised to MXFP4
+//   down: Y = bf16(h Wd[e])
+// for the rows of each expert e, both operands held as e2m1 codes with one
+// e8m0 scale per 32 elements of the reduction axis; the tensor core applies
+// the scales and accumulates in float32.
+//
+// A tile is one window of up to 192 of an expert's rows times two blocks of
+// 128 output columns (up: the same 128 columns of gate and of up; down: 256
+// neighbouring columns).  The weights are the M = 128 operand and the rows the
+// N operand, so a window costs its row count rounded up to 16 and an output
+// column's gate and up values meet in one thread.  TMEM holds the two 128 x N
+// accumulators (columns 0 and 192) and each stage's scales (from column 384).
+// Windows start at multiples of 64 rows: their rows' scales then start at an
+// even TMEM column of the 128-row scale tile.
+//
+// Roles of the 10 warps: warp 0 loads (per 256-deep stage two 128 x 128-byte
+// weight boxes, the window's rows in boxes of 32, and the scale tiles), warp 1
+// copies a stage's scales to TMEM and issues its MMAs, warps 2-9 drain the
+// accumulators.  Every wait is bounded as in the bf16 GEMMs.
+#include <cstdint>
+#include <mutex>
+
+#include "moe_internal.h"
+#include "moe_mxfp4.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kMaxExperts = 256;
+constexpr int kTok = kMxfp4WindowRows;          // rows per window at most
+constexpr int kStageK = 256;                    // reduction elements per stage (128 bytes of codes)
+constexpr int kStages = 3;
+constexpr int kWBytes = 128 * 128;              // one block of 128 weight rows
+constexpr int kTBox = 32;                       // rows per token box
+constexpr int kTBoxBytes = kTBox * 128;
+constexpr int kTBytes = kTok * 128;
+constexpr int kSfBytes = 2 * 512;               // scale tiles of one 128-row block, 256 deep
+constexpr int kOffT = 2 * kWBytes;
+constexpr int kOffSf = kOffT + kTBytes;         // scales: weights 0, weights 1, rows (two 128-row blocks)
+constexpr int kStageBytes = kOffSf + 4 * kSfBytes;
+static_assert(kStageBytes % 1024 == 0, "stages start on swizzle atoms");
+
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = (2 + kEpiWarps) * 32;
+
+// TMEM columns: accumulators, then 32 columns of scales per stage
+constexpr uint32_t kAcc1 = 192;
+constexpr uint32_t kSfCol = 384;
+constexpr uint32_t kSfStageCols = 32;           // weights 0: +0, weights 1: +8, rows: +16 (8 per 128 k)
+static_assert(kSfCol + kStages * kSfStageCols <= 512, "TMEM columns");
+
+constexpr int kBarOff = kStages * kStageBytes;
+constexpr int kNumBars = 2 * kStages + 3;
+constexpr int kWinOff = kBarOff + kNumBars * 8 + 8;
+constexpr int kCntOff = kWinOff + (kMaxExperts + 1) * 4;
+constexpr int kOffpOff = kCntOff + kMaxExperts * 4;
+constexpr int kSmemBytes = kOffpOff + (kMaxExperts + 1) * 4;
+constexpr int kSmemAlloc = kSmemBytes + 1024;
+static_assert(kSmemAlloc <= 232448, "shared memory budget");
+
+enum Mode { kUpBf16 = 0, kUpMxfp4 = 1, kDown = 2 };
+
+// Untiled copy of `bytes` (a multiple of 16, both sides 16-byte aligned)
+// global -> shared, counted on `bar`.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// One 512-byte scale tile (128 rows x 4 blocks) from shared memory into four
+// TMEM columns, replicated to the four 32-lane quarters: lane i, column c
+// holds the scale word of row 32 c + i.
+__device__ __forceinline__ void sf_to_tmem(uint32_t tmem, uint32_t smem) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(smem_desc(smem, 0, 128, 0))
+               : "memory");
+}
+
+// D(tmem) (+)= A(smem) B(smem), both e2m1 with e8m0 scales per 32 elements,
+// 64 elements deep.
+__device__ __forceinline__ void mma_mxf4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
+                                         uint32_t sfb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+
+// kind::mxf4 instruction descriptor: A and B e2m1 (bits 7-9 and 10-11 = 1),
+// both K-major, N >> 3 in bits 17-22, scales e8m0 (bit 23), M >> 7 in bits
+// 27-28; `half` picks which two scales of each word a 64-deep step uses (byte
+// 0 or 2, bits 4-5 for B and 29-30 for A).
+__device__ __forceinline__ uint32_t idesc_mxf4(uint32_t N, uint32_t half) {
+  return (1u << 7) | (1u << 10) | ((N >> 3) << 17) | (1u << 23) | (1u << 27) | ((2u * half) << 4) |
+         ((2u * half) << 29);
+}
+
+struct Win {
+  int e, j, row0, rows;
+  bool ok;
+};
+
+// Tile t: expert e (windows off[e] .. off[e+1]), then column tile j, then the
+// window, so that the windows sharing a weight tile are neighbours.
+__device__ __forceinline__ Win decode(int tile, int NT, int E, const int32_t* off, const int32_t* offp,
+                                      const int32_t* cnt, int64_t max_rows) {
+  Win c{0, 0, 0, 0, false};
+  const int q = tile / NT;
+  int lo = 0, hi = E;  // last e with off[e] <= q
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (off[mid] <= q) lo = mid; else hi = mid - 1;
+  }
+  if (lo >= E) return c;
+  const int nw = off[lo + 1] - off[lo];
+  const int local = tile - NT * off[lo];
+  if (nw <= 0 || local < 0 || local >= NT * nw) return c;
+  const int w = local % nw;
+  const int n = cnt[lo];
+  const int per = ((n + nw - 1) / nw + 63) / 64 * 64;
+  c.e = lo;
+  c.j = local / nw;
+  c.row0 = offp[lo] + per * w;
+  c.rows = min(per, n - per * w);
+  const int pad_end = offp[lo + 1];
+  c.ok = c.rows > 0 && c.rows <= kTok && c.row0 >= 0 && (c.row0 & 63) == 0 && c.row0 + c.rows <= pad_end &&
+         pad_end <= max_rows && (pad_end & 127) == 0;
+  return c;
+}
+
+__device__ __forceinline__ bool vote_any(bool flag) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred pi, po;\n\t"
+      "setp.ne.u32 pi, %1, 0;\n\t"
+      "bar.red.or.pred po, 2, %2, pi;\n\t"
+      "selp.u32 %0, 1, 0, po;\n\t}"
+      : "=r"(r)
+      : "r"(flag ? 1u : 0u), "n"(kEpiWarps * 32)
+      : "memory");
+  return r != 0;
+}
+
+// silu(g) * u with the sigmoid on the SFU (a few float32 ulps; g < -88 gives
+// the limit 0, as in the bf16 GEMM).
+__device__ __forceinline__ float silu_mul(float g, float u) { return g * __fdividef(1.0f, 1.0f + __expf(-g)) * u; }
+
+template <int kMode>
+__global__ void __launch_bounds__(kThreads, 1)
+    mxfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmT, const __grid_constant__ CUtensorMap tmW0,
+                      const __grid_constant__ CUtensorMap tmW1, const uint8_t* __restrict__ sfT,
+                      const uint8_t* __restrict__ sfW0, const uint8_t* __restrict__ sfW1, void* __restrict__ D,
+                      uint8_t* __restrict__ Dsf, const int32_t* __restrict__ off_pad,
+                      const int32_t* __restrict__ counts, int E, int K, int N_out, int NT, int64_t max_rows,
+                      uint32_t* __restrict__ status) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kBarOff);
+  uint64_t* empty = full + kStages;
+  uint64_t* tfull = empty + kStages;
+  uint64_t* tempty = tfull + 1;
+  uint64_t* drain = tfull + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tfull + 3);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int32_t* s_win = reinterpret_cast<int32_t*>(smem + kWinOff);
+  int32_t* s_cnt = reinterpret_cast<int32_t*>(smem + kCntOff);
+  int32_t* s_offp = reinterpret_cast<int32_t*>(smem + kOffpOff);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+
+  pdl_launch_dependents();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(tfull, 1);
+    mbar_init(tempty, kEpiWarps);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbarrier_init();
+    prefetch_tmap(&tmT);
+    prefetch_tmap(&tmW0);
+    prefetch_tmap(&tmW1);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  pdl_wait();
+  if (warp == 2) {
+    // windows per expert -> exclusive scan (E <= 256)
+    constexpr int per = kMaxExperts / 32;
+    int loc[per];
+    int sum = 0;
+#pragma unroll
+    for (int i = 0; i < per; ++i) {
+      const int e = lane * per + i;
+      int nw = 0;
+      if (e < E) {
+        const int c = __ldg(counts + e);
+        s_cnt[e] = c;
+        nw = c > 0 ? (c - 1) / kTok + 1 : 0;
+      }
+      loc[i] = nw;
+      sum += nw;
+    }
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    int run = incl - sum;
+#pragma unroll
+    for (int i = 0; i < per; ++i) {
+      const int e = lane * per + i;
+      if (e <= E) s_win[e] = run;
+      run += loc[i];
+    }
+    if (lane == 31 && 32 * per == E) s_win[E] = incl;
+  } else if (warp == 3) {
+    for (int e = lane; e <= E; e += 32) s_offp[e] = __ldg(off_pad + e);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int total = NT * s_win[E];
+  const int KS = (K + kStageK - 1) / kStageK;
+  const int64_t kb128 = K / 128;
+
+  if (warp == 0) {
+    // ---------------------------------------------------------- loads
+    if (elect_one_sync()) {
+      const uint64_t pol_t = policy_evict_last();
+      uint32_t it = 0;
+      bool stop = false;
+      for (int tile = blockIdx.x; !stop && tile < total; tile += gridDim.x) {
+        const Win c = decode(tile, NT, E, s_win, s_offp, s_cnt, max_rows);
+        if (!c.ok) {
+          record_status(status, kStatusBounds);
+          continue;
+        }
+        // a one-window expert reads this weight tile once
+        const uint64_t pol_w = s_win[c.e + 1] - s_win[c.e] == 1 ? policy_evict_first() : policy_evict_normal();
+        const int n0 = c.j * (kMode == kDown ? 256 : 128);
+        const bool two = kMode != kDown || n0 + 128 < N_out;  // the second weight block exists
+        const int w_row = c.e * N_out + n0;                   // E * N_out < 2^31
+        const int boxes = (c.rows + kTBox - 1) / kTBox;
+        const int64_t t_block = c.row0 >> 7;
+        const bool t_two = (c.row0 & 127) + c.rows > 128;     // the window's rows span two scale blocks
+        for (int ks = 0; ks < KS; ++ks, ++it) {
+          const uint32_t s = it % kStages;
+          if (!mbar_wait(&empty[s], ((it / kStages) & 1u) ^ 1u, abort_flag, status)) {
+            stop = true;
+            break;
+          }
+          const int kt = min(2, static_cast<int>(kb128) - 2 * ks);  // 128-deep scale tiles in this stage
+          const uint32_t sfb = 512u * kt;
+          mbar_arrive_expect_tx(&full[s], (two ? 2u : 1u) * (kWBytes + sfb) + boxes * kTBoxBytes + (t_two ? 2u : 1u) * sfb);
+          uint8_t* st = smem + s * kStageBytes;
+          const int kx = ks * 128;  // bytes
+          tma_load_2d(st, &tmW0, &full[s], kx, w_row, pol_w);
+          if (two) tma_load_2d(st + kWBytes, &tmW1, &full[s], kx, kMode == kDown ? w_row + 128 : w_row, pol_w);
+          for (int b = 0; b < boxes; ++b)
+            tma_load_2d(st + kOffT + b * kTBoxBytes, &tmT, &full[s], kx, c.row0 + b * kTBox, pol_t);
+          uint8_t* sf = st + kOffSf;
+          const int64_t wsf = ((w_row >> 7) * kb128 + 2 * ks) * 512;
+          const int64_t tsf = (t_block * kb128 + 2 * ks) * 512;
+          bulk_load(sf, sfW0 + wsf, sfb, &full[s]);
+          if (two) bulk_load(sf + kSfBytes, kMode == kDown ? sfW0 + wsf + kb128 * 512 : sfW1 + wsf, sfb, &full[s]);
+          bulk_load(sf + 2 * kSfBytes, sfT + tsf, sfb, &full[s]);
+          if (t_two) bulk_load(sf + 3 * kSfBytes, sfT + tsf + kb128 * 512, sfb, &full[s]);
+        }
+      }
+      // every stage used must be consumed before the CTA may exit
+      const uint32_t nst = it < kStages ? it : kStages;
+      for (uint32_t s = 0; s < nst; ++s) {
+        const uint32_t last = s + kStages * ((it - 1 - s) / kStages);
+        int no_abort = 0;
+        mbar_wait(&empty[s], (last / kStages) & 1u, &no_abort, status);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---------------------------------------------------------- MMAs
+    if (elect_one_sync()) {
+      uint32_t it = 0;
+      uint32_t tcount = 0;
+      bool stop = false;
+      for (int tile = blockIdx.x; !stop && tile < total; tile += gridDim.x) {
+        const Win c = decode(tile, NT, E, s_win, s_offp, s_cnt, max_rows);
+        if (!c.ok) continue;
+        const bool two = kMode != kDown || c.j * 256 + 128 < N_out;
+        const uint32_t N = static_cast<uint32_t>((c.rows + 15) / 16 * 16);
+        const uint32_t id[2] = {idesc_mxf4(N, 0), idesc_mxf4(N, 1)};
+        const bool t_two = (c.row0 & 127) + c.rows > 128;
+        const uint32_t t_col = (c.row0 & 127) / 32;  // first row's column inside its scale block: 0 or 2
+        if (!mbar_wait(tempty, (tcount & 1u) ^ 1u, abort_flag, status)) break;
+        tc_fence_after();
+        for (int ks = 0; ks < KS; ++ks, ++it) {
+          const uint32_t s = it % kStages;
+          if (!mbar_wait(&full[s], (it / kStages) & 1u, abort_flag, status)) {
+            stop = true;
+            break;
+          }
+          tc_fence_after();
+          const int kt = min(2, static_cast<int>(kb128) - 2 * ks);
+          const uint32_t st = smem_u32(smem + s * kStageBytes);
+          const uint32_t sf = st + kOffSf;
+          const uint32_t tsf = tmem + kSfCol + s * kSfStageCols;  // this stage's own columns
+          for (int a = 0; a < kt; ++a) {
+            sf_to_tmem(tsf + 4 * a, sf + 512 * a);
+            if (two) sf_to_tmem(tsf + 8 + 4 * a, sf + kSfBytes + 512 * a);
+            sf_to_tmem(tsf + 16 + 8 * a, sf + 2 * kSfBytes + 512 * a);
+            if (t_two) sf_to_tmem(tsf + 16 + 8 * a + 4, sf + 3 * kSfBytes + 512 * a);
+          }
+          for (int kk = 0; kk < 2 * kt; ++kk) {
+            const uint32_t a = kk >> 1;
+            const uint64_t bd = smem_desc(st + kOffT + kk * 32, 16, 1024, kSwizzle128B);
+            const uint32_t sfb = tsf + 16 + 8 * a + t_col;
+            const uint32_t acc = (ks | kk) != 0 ? 1u : 0u;
+            mma_mxf4(tmem, smem_desc(st + kk * 32, 16, 1024, kSwizzle128B), bd, id[kk & 1], tsf + 4 * a, sfb, acc);
+            if (two)
+              mma_mxf4(tmem + kAcc1, smem_desc(st + kWBytes + kk * 32, 16, 1024, kSwizzle128B), bd, id[kk & 1],
+                       tsf + 8 + 4 * a, sfb, acc);
+          }
+          tc_commit(&empty[s]);
+        }
+        if (stop) break;
+        tc_commit(tfull);
+        ++tcount;
+      }
+      tc_commit(drain);
+      int no_abort = 0;
+      mbar_wait(drain, 0, &no_abort, status);
+    }
+    __syncwarp();
+  } else {
+    // ---------------------------------------------------------- epilogue
+    // thread = TMEM lane = output column; the two warps of a lane quarter take
+    // the window's 32-row chunks in turn
+    const int q = warp & 3;
+    const int half = (warp - 2) / 4;
+    uint32_t tcount = 0;
+    for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
+      const Win c = decode(tile, NT, E, s_win, s_offp, s_cnt, max_rows);
+      if (!c.ok) continue;
+      const bool ok = mbar_wait(tfull, tcount & 1u, abort_flag, status);
+      if (vote_any(!ok)) break;
+      ++tcount;
+      tc_fence_after();
+      const int n0 = c.j * (kMode == kDown ? 256 : 128);
+      const bool two = kMode != kDown || n0 + 128 < N_out;
+      const int col = n0 + q * 32 + lane;
+      const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16);
+#pragma unroll 1
+      for (int ch = half; ch * 32 < c.rows; ch += 2) {
+        const int64_t r0 = c.row0 + ch * 32;
+        const int left = min(32, c.rows - ch * 32);
+        uint32_t v0[32], v1[32];
+        tmem_ld_32x32b_x32(tb + ch * 32, v0);
+        if (two) tmem_ld_32x32b_x32(tb + kAcc1 + ch * 32, v1);
+        tmem_ld_wait();
+        if constexpr (kMode == kUpMxfp4) {
+          // a warp's 32 columns are one block of every row's scales: per row
+          // the block's maximum by a warp reduction of h rounded to bf16 (the
+          // codes are those of quantising the bf16 h), then eight rows' codes
+          // change places with eight columns' by three exchanges
+          uint32_t my_scale = 0u;
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            uint32_t codes = 0u;
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+              float y[2];
+#pragma unroll
+              for (int p = 0; p < 2; ++p) {
+                const int t = 8 * g + i + p;
+                const float h = silu_mul(__uint_as_float(v0[t]), __uint_as_float(v1[t]));
+                const uint32_t hb = pack_bf16x2(h, 0.0f) & 0xFFFFu;
+                const uint32_t s = scale_byte(__reduce_max_sync(0xffffffffu, hb & 0x7FFFu));
+                if (lane == t) my_scale = s;
+                y[p] = s == kScaleNan ? 0.0f : bf16lo_to_f32(hb) * scale_inverse(s);
+              }
+              uint32_t two_codes;
+              asm("{\n\t.reg .b8 b;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %2, %1;\n\tcvt.u32.u8 %0, b;\n\t}"
+                  : "=r"(two_codes)
+                  : "f"(y[0]), "f"(y[1]));
+              codes |= two_codes << (4 * i);
+            }
+            // codes: nibble i = row 8g + i of this column; transposed among
+            // groups of eight lanes: nibble i = column i of row 8g + lane % 8
+            uint32_t o = __shfl_xor_sync(0xffffffffu, codes, 4);
+            codes = (lane & 4) ? ((codes & 0xFFFF0000u) | (o >> 16)) : ((codes & 0x0000FFFFu) | (o << 16));
+            o = __shfl_xor_sync(0xffffffffu, codes, 2);
+            codes = (lane & 2) ? ((codes & 0xFF00FF00u) | ((o >> 8) & 0x00FF00FFu))
+                               : ((codes & 0x00FF00FFu) | ((o << 8) & 0xFF00FF00u));
+            o = __shfl_xor_sync(0xffffffffu, codes, 1);
+            codes = (lane & 1) ? ((codes & 0xF0F0F0F0u) | ((o >> 4) & 0x0F0F0F0Fu))
+                               : ((codes & 0x0F0F0F0Fu) | ((o << 4) & 0xF0F0F0F0u));
+            const int t = 8 * g + (lane & 7);
+            if (t < left)
+              *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(D) +
+                                           ((r0 + t) * N_out + n0 + q * 32 + (lane >> 3) * 8) / 2) = codes;
+          }
+          if (lane < left)
+            Dsf[scale_word_offset(r0 + lane, n0 / 128, N_out / 128) + q] = static_cast<uint8_t>(my_scale);
+        } else {
+          uint16_t* dst = static_cast<uint16_t*>(D) + r0 * N_out + col;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            if (i >= left) break;  // uniform across the warp
+            const float a = __uint_as_float(v0[i]), b = __uint_as_float(v1[i]);
+            if constexpr (kMode == kUpBf16) {
+              dst[static_cast<int64_t>(i) * N_out] = static_cast<uint16_t>(pack_bf16x2(silu_mul(a, b), 0.0f));
+            } else {
+              const uint32_t p = pack_bf16x2(a, b);
+              dst[static_cast<int64_t>(i) * N_out] = static_cast<uint16_t>(p);
+              if (two) dst[static_cast<int64_t>(i) * N_out + 128] = static_cast<uint16_t>(p >> 16);
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(tempty);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) {
+    __syncwarp();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int kMode>
+cudaError_t launch(const moe_shape& s, const Mxfp4Maps& m, const uint8_t* sfT, const uint8_t* sfW0,
+                   const uint8_t* sfW1, void* D, uint8_t* Dsf, const int32_t* off_pad, const int32_t* counts,
+                   uint32_t* status, int num_sms, cudaStream_t st) {
+  // the shared-memory opt-in, once per device (host threads may race here)
+  static bool done[64] = {};
+  static std::mutex mu;
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (dev >= 64 || !done[dev]) {
+      err = cudaFuncSetAttribute(mxfp4_gemm_kernel<kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAlloc);
+      if (err != cudaSuccess) return err;
+      if (dev < 64) done[dev] = true;
+    }
+  }
+  const int K = kMode == kDown ? s.I : s.H;
+  const int N_out = kMode == kDown ? s.H : s.I;
+  const int NT = kMode == kDown ? (N_out + 255) / 256 : N_out / 128;
+  const int64_t R = static_cast<int64_t>(s.T) * s.k;
+  const int64_t max_tiles = (R / kTok + (s.E < R ? s.E : R)) * NT;
+  const int grid = static_cast<int>(max_tiles < num_sms ? max_tiles : num_sms);
+  return launch_pdl(mxfp4_gemm_kernel<kMode>, dim3(grid), dim3(kThreads), kSmemAlloc, st, m.t, m.w0, m.w1, sfT, sfW0,
+                    sfW1, D, Dsf, off_pad, counts, s.E, K, N_out, NT, max_rows_of(s), status);
+}
+
+}  // namespace
+
+cudaError_t launch_mxfp4_up(const moe_shape& s, const Mxfp4Maps& m, const uint8_t* x_scales, const uint8_t* wg_scales,
+                            const uint8_t* wu_scales, uint16_t* h, const int32_t* off_pad, const int32_t* counts,
+                            uint32_t* status, int num_sms, cudaStream_t st) {
+  return launch<kUpBf16>(s, m, x_scales, wg_scales, wu_scales, h, nullptr, off_pad, counts, status, num_sms, st);
+}
+
+cudaError_t launch_mxfp4_up_quantized(const moe_shape& s, const Mxfp4Maps& m, const uint8_t* x_scales,
+                                      const uint8_t* wg_scales, const uint8_t* wu_scales, uint8_t* h_codes,
+                                      uint8_t* h_scales, const int32_t* off_pad, const int32_t* counts,
+                                      uint32_t* status, int num_sms, cudaStream_t st) {
+  return launch<kUpMxfp4>(s, m, x_scales, wg_scales, wu_scales, h_codes, h_scales, off_pad, counts, status, num_sms,
+                          st);
+}
+
+cudaError_t launch_mxfp4_down(const moe_shape& s, const Mxfp4Maps& m, const uint8_t* h_scales,
+                              const uint8_t* wd_scales, uint16_t* Y, const int32_t* off_pad, const int32_t* counts,
+                              uint32_t* status, int num_sms, cudaStream_t st) {
+  return launch<kDown>(s, m, h_scales, wd_scales, wd_scales, Y, nullptr, off_pad, counts, status, num_sms, st);
+}
+
+}  // namespace moe

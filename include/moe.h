@@ -39,6 +39,10 @@
  *   - a call makes the stream's device current for its launches and puts the
  *     calling thread's previous current device back before it returns.
  *
+ * The experts' products also run on MXFP4 operands (moe_*_mxfp4), and the
+ * router's balance loss has its gradient (moe_balance_loss*); both are
+ * described where they are declared.
+ *
  * Supported shapes (else MOE_ERR_UNSUPPORTED_SHAPE): 1 <= T <= 2^22,
  * 1 <= E <= 256, 1 <= k <= min(E, 16), 128 <= H <= 32768 and
  * 128 <= I <= 32768 with H % 128 == 0 and I % 128 == 0.
@@ -275,6 +279,130 @@ typedef struct {
 } moe_views;
 
 moe_status moe_workspace_views(const moe_shape *shape, void *ws, moe_views *views);
+
+/* ------------------------------------------------------------------ MXFP4
+ * Operands in 4 bits (OCP microscaling): a matrix [rows, cols] is cut along
+ * its rows into blocks of 32 elements with one scale each.
+ *   codes  [rows, cols/2] uint8: e2m1 elements (sign, then 0 0.5 1 1.5 2 3 4
+ *          6), element 2i in the low nibble of byte i;
+ *   scales uint8: byte s stands for 2^(s - 127), 255 for NaN, in 512-byte
+ *          tiles of 128 rows x 4 blocks: the scale of (row r, block b) is byte
+ *            ((r/128) * (cols/128) + b/4) * 512
+ *              + (r%32) * 16 + (r%128)/32 * 4 + b%4
+ *          (rows rounded up to a multiple of 128).
+ * Quantisation: s = clamp(floor(log2(max|x|)) - 2 + 127, 0, 254) over the
+ * block, codes = x * 2^(127-s) rounded to nearest even, saturated at 6.  A
+ * block of zeros gets s = 0; a block holding a NaN or an infinity gets s = 255
+ * and codes 0, so that it reads as NaN.
+ * Expert weights are quantised along their reduction axis and held with that
+ * axis contiguous: W [E, K, N] as the matrix [E*N, K].
+ *
+ * Sizes: 1 <= rows < 2^31; cols, K and N multiples of 128 from 128 to 32768;
+ * 1 <= E <= 256; else MOE_ERR_UNSUPPORTED_SHAPE. */
+
+/* Host only.  Bytes of the codes and of the scales of a [rows, cols] matrix. */
+moe_status moe_mxfp4_sizes(int64_t rows, int64_t cols, size_t *code_bytes, size_t *scale_bytes);
+
+/* Rows x [rows, cols] bf16 to codes and scales.  The scales of the rows
+ * between `rows` and the next multiple of 128 are written as 0. */
+moe_status moe_quantize_mxfp4(const moe_bf16 *x, int64_t rows, int64_t cols,
+                              uint8_t *codes, uint8_t *scales, moe_stream_t stream);
+
+/* Weights w [E, K, N] bf16 (K the reduction axis) to the codes and scales of
+ * the matrix [E*N, K]. */
+moe_status moe_quantize_weights_mxfp4(const moe_bf16 *w, int32_t E, int64_t K, int64_t N,
+                                      uint8_t *codes, uint8_t *scales, moe_stream_t stream);
+
+/* The values x [rows, cols] bf16 that codes and scales stand for (exact; past
+ * bf16's range they are infinite). */
+moe_status moe_dequantize_mxfp4(const uint8_t *codes, const uint8_t *scales, int64_t rows,
+                                int64_t cols, moe_bf16 *x, moe_stream_t stream);
+
+/* Tokens X [T, H] bf16 quantised once each and written to their k permuted
+ * rows scatter_idx [T, k]: codes and scales of the matrix [max_rows, H].
+ * Padding rows are left unwritten.  ws as for the products below. */
+moe_status moe_quantize_permute_mxfp4(const moe_shape *shape, const moe_bf16 *X,
+                                      const int32_t *scatter_idx, uint8_t *codes, uint8_t *scales,
+                                      void *ws, moe_stream_t stream);
+
+/* The grouped gate/up product on MXFP4 operands:
+ *   h[r] = bf16(silu(x_r Wg[e]) * (x_r Wu[e]))   [max_rows, I] bf16
+ * for the real rows r of every expert e (rows off_pad[e] .. off_pad[e] +
+ * counts[e]); padding rows of h are not written, and padding rows of the
+ * operands do not reach a stored result.
+ *   x_codes, x_scales: the matrix [max_rows, H] in expert order
+ *   wg_*, wu_*:        the matrices [E*I, H]
+ *   ws: moe_mxfp4_workspace_size bytes, or at least 256 bytes of which the
+ *       first 256 were cleared (the status word)
+ * The scales are applied by the tensor cores, sums are float32, h is rounded
+ * once. */
+moe_status moe_grouped_gemm_up_mxfp4(const moe_shape *shape, const uint8_t *x_codes,
+                                     const uint8_t *x_scales, const int32_t *counts,
+                                     const int32_t *off_pad, const uint8_t *wg_codes,
+                                     const uint8_t *wg_scales, const uint8_t *wu_codes,
+                                     const uint8_t *wu_scales, moe_bf16 *h, void *ws,
+                                     moe_stream_t stream);
+
+/* The grouped down product on MXFP4 operands: Y[r] = bf16(h_r Wd[e])
+ * [max_rows, H] bf16, rows as above.
+ *   h_codes, h_scales: the matrix [max_rows, I];  wd_*: the matrix [E*H, I] */
+moe_status moe_grouped_gemm_down_mxfp4(const moe_shape *shape, const uint8_t *h_codes,
+                                       const uint8_t *h_scales, const int32_t *counts,
+                                       const int32_t *off_pad, const uint8_t *wd_codes,
+                                       const uint8_t *wd_scales, moe_bf16 *Y, void *ws,
+                                       moe_stream_t stream);
+
+/* Host only.  Bytes of the workspace of moe_forward_mxfp4.  moe_workspace_init
+ * clears its counters and moe_last_device_status reads its status word, as for
+ * moe_forward's. */
+moe_status moe_mxfp4_workspace_size(const moe_shape *shape, size_t *bytes);
+
+/* The whole layer with the experts' products in MXFP4: route, quantise and
+ * permute the tokens, gate/up product with h quantised in its epilogue (to the
+ * codes that quantising the bf16 h gives), down product, combine.  Weights as
+ * moe_quantize_weights_mxfp4 leaves them; everything else as moe_forward. */
+moe_status moe_forward_mxfp4(const moe_shape *shape, const float *logits, const moe_bf16 *X,
+                             const uint8_t *wg_codes, const uint8_t *wg_scales,
+                             const uint8_t *wu_codes, const uint8_t *wu_scales,
+                             const uint8_t *wd_codes, const uint8_t *wd_scales, moe_bf16 *out,
+                             void *ws, moe_stream_t stream);
+
+/* ----------------------------------------------------------- balance loss
+ * A token takes part when its mask byte is non-zero (or mask is NULL) and not
+ * all of its logits are -inf; n tokens do.  With p = softmax(logits) over
+ * them:
+ *   counts[e]     = picks (t, j) with topk_ids[t, j] = e
+ *   mean_probs[e] = sum_t p[t, e] / n
+ *   losses[0]     = E * sum_e counts[e]/(n k) * mean_probs[e]   (balance)
+ *   losses[1]     = sum_t logsumexp(logits[t])^2 / n            (z-loss)
+ * and all of them are 0 for n = 0.  A NaN or +inf logit of a token that takes
+ * part makes the losses NaN; tokens that take no part are not looked at. */
+
+/* Host only.  Bytes of the workspace of moe_balance_loss (at most 1 MiB). */
+moe_status moe_balance_workspace_size(const moe_shape *shape, size_t *bytes);
+
+/*   logits     [T, E] float32 (-inf allowed), topk_ids [T, k] int32 (moe_route's)
+ *   mask       [T] bytes or NULL
+ *   counts     [E] int32 out, num_tokens [1] int32 out (n)
+ *   mean_probs [E] float32 out, losses [2] float32 out
+ *   ws         moe_balance_workspace_size bytes, the first 256 cleared once
+ *              (moe_workspace_init); an expert id out of range is not counted
+ *              and reported by moe_last_device_status
+ * H and I of the shape are not used. */
+moe_status moe_balance_loss(const moe_shape *shape, const float *logits, const int32_t *topk_ids,
+                            const uint8_t *mask, int32_t *counts, int32_t *num_tokens,
+                            float *mean_probs, float *losses, void *ws, moe_stream_t stream);
+
+/* The gradient to the logits, counts held constant:
+ *   dlogits[t, e] = p[t, e] * ( g0 E/n (f[e] - sum_j f[j] p[t, j])
+ *                             + g1 2/n logsumexp(logits[t]) ),  f = counts/(n k)
+ * and 0 for tokens that take no part.
+ *   counts, num_tokens: moe_balance_loss's; grad_losses [2] float32 (g0, g1),
+ *   the gradients of the two losses; dlogits [T, E] float32 out */
+moe_status moe_balance_loss_backward(const moe_shape *shape, const float *logits,
+                                     const uint8_t *mask, const int32_t *counts,
+                                     const int32_t *num_tokens, const float *grad_losses,
+                                     float *dlogits, moe_stream_t stream);
 
 #ifdef __cplusplus
 }
