@@ -149,10 +149,25 @@ def _ptr(t):
     return t.data_ptr()
 
 
+_current_stream = None
+
+
+def _raw_stream():
+    """A function giving the current stream's handle (torch's raw getter where
+    it has one: building a Stream object takes longer than a small launch)."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is None:
+        return lambda: torch.cuda.current_stream().cuda_stream
+    return lambda: raw(torch.cuda.current_device())
+
+
 def _stream(stream):
+    global _current_stream
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        if _current_stream is None:
+            _current_stream = _raw_stream()
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -372,9 +387,9 @@ def alloc_mxfp4(rows: int, cols: int, device="cuda") -> tuple:
 
 def _mxfp4_ptrs(codes, scales, rows, cols, name):
     import torch
-    code_bytes, scale_bytes = mxfp4_sizes(rows, cols)
-    return [_dev_tensor(codes, torch.uint8, code_bytes, name + "codes"),
-            _dev_tensor(scales, torch.uint8, scale_bytes, name + "scales")]
+    # the sizes of moe_mxfp4_sizes; the call itself refuses unsupported ones
+    return [_dev_tensor(codes, torch.uint8, rows * cols // 2, name + "codes"),
+            _dev_tensor(scales, torch.uint8, (rows + 127) // 128 * 4 * cols, name + "scales")]
 
 
 def moe_quantize_mxfp4(x, rows, cols, codes, scales, stream=None):

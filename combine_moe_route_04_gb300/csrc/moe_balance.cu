@@ -78,6 +78,9 @@ struct Row {
   }
 };
 
+// Rows each warp (or group of lanes) has in flight at a time.
+constexpr int kUnroll = 2;
+
 template <int V, int W>
 __global__ void __launch_bounds__(kFwdThreads, 1)
     balance_loss_kernel(const float* __restrict__ logits, const int32_t* __restrict__ topk_ids,
@@ -85,7 +88,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                         int32_t* __restrict__ num_tokens, float* __restrict__ mean_probs, float* __restrict__ losses,
                         uint32_t* __restrict__ partials, uint32_t* __restrict__ counter,
                         uint32_t* __restrict__ status) {
-  __shared__ float s_p[kFwdWarps * kMaxE];
+  __shared__ __align__(16) float s_p[kFwdWarps * kMaxE];
   __shared__ int s_cnt[kMaxE];
   __shared__ float s_z[kFwdWarps];
   __shared__ int s_n[kFwdWarps];
@@ -103,27 +106,48 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   for (int x = 0; x < V * W; ++x) acc[x] = 0.0f;
   float z = 0.0f;
   int n = 0;
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * kFwdWarps * per_warp;
-  const int64_t first = (static_cast<int64_t>(blockIdx.x) * kFwdWarps + warp) * per_warp;
-  for (int64_t t0 = first; t0 < T; t0 += stride) {  // uniform across the warp
-    const int64_t t = t0 + lane / G;
-    const bool there = t < T && (mask == nullptr || __ldg(mask + t) != 0);
-    Row<V, W> r;
-    r.load(logits + t * E, gl, G, E, there);
-    float top, sum;
-    r.exps(G, top, sum);
-    const bool takes = there && sum != 0.0f;
-    const float inv = takes ? 1.0f / sum : 0.0f;
-    if (takes) {
+  const int64_t step = static_cast<int64_t>(per_warp) * kUnroll;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kFwdWarps * step;
+  const int64_t first = (static_cast<int64_t>(blockIdx.x) * kFwdWarps + warp) * step + lane / G;
+  const int64_t warp_first = first - lane / G;
+  // the masks are read one iteration ahead of the rows they decide on
+  bool use[kUnroll];
 #pragma unroll
-      for (int x = 0; x < V * W; ++x) acc[x] += r.v[x] * inv;
+  for (int u = 0; u < kUnroll; ++u) {
+    const int64_t t = first + u * per_warp;
+    use[u] = t < T && (mask == nullptr || __ldg(mask + t) != 0);
+  }
+  for (int64_t d = 0; warp_first + d < T; d += stride) {  // uniform across the warp
+    Row<V, W> r[kUnroll];
+    int id[kUnroll];
+    bool there[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int64_t t = first + d + u * per_warp;
+      there[u] = use[u];
+      r[u].load(logits + t * E, gl, G, E, there[u]);
+      id[u] = there[u] && gl < k ? __ldg(topk_ids + t * k + gl) : 0;
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int64_t t = first + d + stride + u * per_warp;
+      use[u] = t < T && (mask == nullptr || __ldg(mask + t) != 0);
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      float top, sum;
+      r[u].exps(G, top, sum);
+      if (!there[u] || sum == 0.0f) continue;
+      const float inv = 1.0f / sum;
+#pragma unroll
+      for (int x = 0; x < V * W; ++x) acc[x] += r[u].v[x] * inv;
       if (gl == 0) {
         const float lse = top + logf(sum);
         z += lse * lse;
         ++n;
       }
       for (int j = gl; j < k; j += G) {
-        const int e = __ldg(topk_ids + t * k + j);
+        const int e = j == gl ? id[u] : __ldg(topk_ids + (first + d + u * per_warp) * k + j);
         if (e >= 0 && e < E) atomicAdd(&s_cnt[e], 1);
         else record_status(status, kStatusBounds);
       }
@@ -192,22 +216,38 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     }
     __syncthreads();
     if (!s_last) return;
-    // 1024 / 256 threads share an expert's column of partials, in row order
-    // each; their sums join in a fixed order
-    const int e = tid & (kMaxE - 1), part = tid / kMaxE;
-    constexpr int kParts = kFwdThreads / kMaxE;
-    float ps = 0.0f;
-    int cs = 0;
-    if (e < E) {
-#pragma unroll 8
-      for (int b = part; b < static_cast<int>(gridDim.x); b += kParts) {
-        ps += __ldcg(part_p + b * E + e);
-        cs += __ldcg(part_c + b * E + e);
+    // the CTAs' rows of partials go round `parts` groups of threads, a thread
+    // to W neighbouring experts; the groups' sums join in a fixed order
+    const int cols = (E + W - 1) / W;  // E % 4 == 0 where W is 4
+    const int parts = min(kFwdThreads / cols, kFwdWarps / 2);
+    const int part = tid / cols, e = tid % cols * W;
+    int* s_ci = reinterpret_cast<int*>(s_p) + kFwdWarps / 2 * kMaxE;
+    if (part < parts) {
+      float ps[W];
+      int cs[W];
+#pragma unroll
+      for (int q = 0; q < W; ++q) {
+        ps[q] = 0.0f;
+        cs[q] = 0;
+      }
+#pragma unroll 5
+      for (int b = part; b < static_cast<int>(gridDim.x); b += parts) {
+        if constexpr (W == 4) {
+          const float4 p4 = __ldcg(reinterpret_cast<const float4*>(part_p + b * E + e));
+          const int4 c4 = __ldcg(reinterpret_cast<const int4*>(part_c + b * E + e));
+          ps[0] += p4.x; ps[1] += p4.y; ps[2] += p4.z; ps[3] += p4.w;
+          cs[0] += c4.x; cs[1] += c4.y; cs[2] += c4.z; cs[3] += c4.w;
+        } else {
+          ps[0] += __ldcg(part_p + b * E + e);
+          cs[0] += __ldcg(part_c + b * E + e);
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < W; ++q) {
+        s_p[part * kMaxE + e + q] = ps[q];
+        s_ci[part * kMaxE + e + q] = cs[q];
       }
     }
-    int* s_ci = reinterpret_cast<int*>(s_p + kParts * kMaxE);
-    s_p[part * kMaxE + e] = ps;
-    s_ci[part * kMaxE + e] = cs;
     if (warp == 0) {
       z_sum = 0.0f;
       n_sum = 0;
@@ -224,7 +264,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     if (tid < E) {
       p_sum = 0.0f;
       c_sum = 0;
-      for (int q = 0; q < kParts; ++q) {
+      for (int q = 0; q < parts; ++q) {
         p_sum += s_p[q * kMaxE + tid];
         c_sum += s_ci[q * kMaxE + tid];
       }
@@ -285,33 +325,45 @@ __global__ void __launch_bounds__(kBwdThreads)
              (static_cast<float>(nk) * static_cast<float>(E));
     }
   }
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * kWarps * per_warp;
-  const int64_t first = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * per_warp;
-  for (int64_t t0 = first; t0 < T; t0 += stride) {
-    const int64_t t = t0 + lane / G;
-    const bool there = t < T && (mask == nullptr || __ldg(mask + t) != 0);
-    Row<V, W> r;
-    r.load(logits + t * E, gl, G, E, there);
-    float top, sum;
-    r.exps(G, top, sum);
-    const bool takes = there && sum != 0.0f;
-    const float inv = 1.0f / sum;
-    float dot = 0.0f;
+  // from the last token to the first: the logits that the forward pass read
+  // last are the ones that L2 still holds
+  const int64_t step = static_cast<int64_t>(per_warp) * kUnroll;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kWarps * step;
+  const int64_t tiles = (T + step - 1) / step;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kWarps + warp; i < tiles; i += stride / step) {
+    const int64_t t0 = (tiles - 1 - i) * step + lane / G;
+    Row<V, W> r[kUnroll];
+    bool there[kUnroll];
 #pragma unroll
-    for (int x = 0; x < V * W; ++x) {
-      r.v[x] *= inv;
-      dot += f[x] * r.v[x];
+    for (int u = 0; u < kUnroll; ++u) {
+      const int64_t t = t0 + u * per_warp;
+      there[u] = t < T && (mask == nullptr || __ldg(mask + t) != 0);
     }
-    for (int o = G >> 1; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-    const float c = b * (top + logf(sum)) - a * dot;
-    if (t < T) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int e = W * (gl + G * i);
+    for (int u = 0; u < kUnroll; ++u) r[u].load(logits + (t0 + u * per_warp) * E, gl, G, E, there[u]);
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int64_t t = t0 + u * per_warp;
+      float top, sum;
+      r[u].exps(G, top, sum);
+      const bool takes = there[u] && sum != 0.0f;
+      const float inv = 1.0f / sum;
+      float dot = 0.0f;
+#pragma unroll
+      for (int x = 0; x < V * W; ++x) {
+        r[u].v[x] *= inv;
+        dot += f[x] * r[u].v[x];
+      }
+      for (int o = G >> 1; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+      const float c = b * (top + logf(sum)) - a * dot;
+      if (t >= T) continue;
+#pragma unroll
+      for (int x = 0; x < V; ++x) {
+        const int e = W * (gl + G * x);
         if (e >= E) continue;
         float d[W];
 #pragma unroll
-        for (int q = 0; q < W; ++q) d[q] = takes ? r.v[W * i + q] * fmaf(a, f[W * i + q], c) : 0.0f;
+        for (int q = 0; q < W; ++q) d[q] = takes ? r[u].v[W * x + q] * fmaf(a, f[W * x + q], c) : 0.0f;
         if constexpr (W == 4) *reinterpret_cast<float4*>(dlogits + t * E + e) = make_float4(d[0], d[1], d[2], d[3]);
         else dlogits[t * E + e] = d[0];
       }
@@ -348,7 +400,7 @@ cudaError_t launch_balance_loss(const moe_shape& s, const float* logits, const i
                                 uint32_t* partials, uint32_t* counter, uint32_t* status, int num_sms,
                                 cudaStream_t st) {
   return by_experts(s.E, [&](auto V, auto W, int G) {
-    const int64_t per_cta = static_cast<int64_t>(kFwdWarps) * (32 / G);
+    const int64_t per_cta = static_cast<int64_t>(kFwdWarps) * (32 / G) * kUnroll;
     int64_t grid = (s.T + per_cta - 1) / per_cta;
     if (grid > num_sms) grid = num_sms;
     if (grid > kBalanceMaxCtas) grid = kBalanceMaxCtas;
@@ -362,7 +414,7 @@ cudaError_t launch_balance_backward(const moe_shape& s, const float* logits, con
                                     const int32_t* counts, const int32_t* num_tokens, const float* grad_losses,
                                     float* dlogits, int num_sms, cudaStream_t st) {
   return by_experts(s.E, [&](auto V, auto W, int G) {
-    const int64_t per_cta = static_cast<int64_t>(kBwdThreads / 32) * (32 / G);
+    const int64_t per_cta = static_cast<int64_t>(kBwdThreads / 32) * (32 / G) * kUnroll;
     int64_t grid = (s.T + per_cta - 1) / per_cta;
     if (grid > static_cast<int64_t>(num_sms) * 8) grid = static_cast<int64_t>(num_sms) * 8;
     return launch_pdl(balance_backward_kernel<V, W>, dim3(static_cast<unsigned>(grid)), dim3(kBwdThreads), 0, st,

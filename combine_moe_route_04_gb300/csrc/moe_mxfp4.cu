@@ -16,39 +16,36 @@ namespace {
 
 constexpr int kSegCols = 1024;  // columns per work item: 4 x (32 lanes x 8 elements)
 
-// One warp per (row, 1024-column segment): a lane holds 8 elements (16 bytes
-// in, 4 bytes of codes out), four lanes a block, sixteen lanes the four blocks
-// of a scale word.  Rows past the last one, up to a multiple of 128, get zero
-// scales so that a tile of scales is always written whole.
+// One warp per (row, 1024-column segment; blockIdx.y): a lane holds 8 elements
+// (16 bytes in, 4 bytes of codes out), four lanes a block, sixteen lanes the
+// four blocks of a scale word.  Rows past the last one, up to a multiple of
+// 128, get zero scales so that a tile of scales is always written whole.
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const uint16_t* __restrict__ x, int64_t rows, int64_t cols,
                                                             uint8_t* __restrict__ codes,
                                                             uint8_t* __restrict__ scales) {
   pdl_launch_dependents();
-  pdl_wait();
   const int lane = threadIdx.x & 31;
-  const int64_t warp0 = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-  const int64_t nwarps = (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5;
-  const int64_t segs = (cols + kSegCols - 1) / kSegCols;
-  const int64_t items = (rows + 127) / 128 * 128 * segs;
-  const int64_t kb128 = cols / 128;
-  for (int64_t item = warp0; item < items; item += nwarps) {
-    const int64_t r = item / segs;
-    const int64_t c0 = (item - r * segs) * kSegCols + lane * 8;
-    uint4 v[4];
+  const int64_t r = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const int64_t c0 = static_cast<int64_t>(blockIdx.y) * kSegCols + lane * 8;
+  const int left = static_cast<int>(cols - c0);  // a lane's piece u is there when 256 u < left
+  const uint16_t* src = x + r * cols + c0;
+  uint8_t* dst = codes + (r * cols + c0) / 2;
+  uint8_t* sc = scales + scale_word_offset(r, c0 / 128, cols / 128);
+  const bool there = r < rows;
+  pdl_wait();
+  uint4 v[4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      v[u] = make_uint4(0u, 0u, 0u, 0u);
-      if (r < rows && c0 + u * 256 < cols) v[u] = __ldg(reinterpret_cast<const uint4*>(x + r * cols + c0 + u * 256));
-    }
+  for (int u = 0; u < 4; ++u) {
+    v[u] = make_uint4(0u, 0u, 0u, 0u);
+    if (there && u * 256 < left) v[u] = __ldg(reinterpret_cast<const uint4*>(src + u * 256));
+  }
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int64_t c = c0 + u * 256;  // the sixteen lanes of a scale word are inside or outside together
-      const uint32_t s = block_scale_of_quad(v[u]);
-      const uint32_t w = scale_word_of_half(s, lane);
-      if (c < cols) {
-        if (r < rows) *reinterpret_cast<uint32_t*>(codes + (r * cols + c) / 2) = quantize_bf16x8(v[u], s);
-        if ((lane & 15) == 0) *reinterpret_cast<uint32_t*>(scales + scale_word_offset(r, c / 128, kb128)) = w;
-      }
+  for (int u = 0; u < 4; ++u) {
+    const uint32_t s = block_scale_of_quad(v[u]);
+    const uint32_t w = scale_word_of_half(s, lane);
+    if (u * 256 < left) {  // alike for the sixteen lanes of a scale word
+      if (there) *reinterpret_cast<uint32_t*>(dst + u * 128) = quantize_bf16x8(v[u], s);
+      if ((lane & 15) == 0) *reinterpret_cast<uint32_t*>(sc + u * 1024) = w;
     }
   }
 }
@@ -59,47 +56,31 @@ __global__ void __launch_bounds__(256) dequantize_rows_kernel(const uint8_t* __r
                                                               const uint8_t* __restrict__ scales, int64_t rows,
                                                               int64_t cols, uint16_t* __restrict__ x) {
   pdl_launch_dependents();
-  pdl_wait();
   const int lane = threadIdx.x & 31;
-  const int64_t warp0 = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-  const int64_t nwarps = (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5;
-  const int64_t segs = (cols + kSegCols - 1) / kSegCols;
-  const int64_t items = rows * segs;
-  const int64_t kb128 = cols / 128;
-  for (int64_t item = warp0; item < items; item += nwarps) {
-    const int64_t r = item / segs;
-    const int64_t c0 = (item - r * segs) * kSegCols + lane * 8;
-    uint32_t code[4], sb[4];
+  const int64_t r = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const int64_t c0 = static_cast<int64_t>(blockIdx.y) * kSegCols + lane * 8;
+  const int left = static_cast<int>(cols - c0);
+  const uint8_t* src = codes + (r * cols + c0) / 2;
+  const uint8_t* sc = scales + scale_word_offset(r, c0 / 128, cols / 128) + ((lane >> 2) & 3);
+  uint16_t* dst = x + r * cols + c0;
+  if (r >= rows) return;
+  pdl_wait();
+  uint32_t code[4], sb[4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int64_t c = c0 + u * 256;
-      code[u] = sb[u] = 0u;
-      if (c < cols) {
-        code[u] = __ldg(reinterpret_cast<const uint32_t*>(codes + (r * cols + c) / 2));
-        sb[u] = __ldg(scales + scale_word_offset(r, c / 128, kb128) + (c / 32) % 4);
-      }
+  for (int u = 0; u < 4; ++u) {
+    code[u] = sb[u] = 0u;
+    if (u * 256 < left) {
+      code[u] = __ldg(reinterpret_cast<const uint32_t*>(src + u * 128));
+      sb[u] = __ldg(sc + u * 1024);
     }
+  }
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int64_t c = c0 + u * 256;
-      if (c >= cols) continue;
-      const float sc = scale_value(sb[u]);
-      float f[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        // the three low bits at the top of a float's exponent and mantissa
-        // read as the e2m1 magnitude times 2^-126, its subnormal included
-        const uint32_t q = code[u] >> (4 * i);
-        const float m = __uint_as_float(((q & 7u) << 22) | ((q & 8u) << 28));
-        f[i] = m * 8.507059173023462e37f * sc;  // 2^126
-      }
-      uint4 o;
-      o.x = pack_bf16x2(f[0], f[1]);
-      o.y = pack_bf16x2(f[2], f[3]);
-      o.z = pack_bf16x2(f[4], f[5]);
-      o.w = pack_bf16x2(f[6], f[7]);
-      *reinterpret_cast<uint4*>(x + r * cols + c) = o;
-    }
+  for (int u = 0; u < 4; ++u) {
+    const uint32_t m = scale_bf16(sb[u]) * 0x10001u;
+    uint4 o;
+    dequantize_bf16x4(code[u], m, o.x, o.y);
+    dequantize_bf16x4(code[u] >> 16, m, o.z, o.w);
+    if (u * 256 < left) *reinterpret_cast<uint4*>(dst + u * 256) = o;
   }
 }
 
@@ -177,66 +158,61 @@ __global__ void __launch_bounds__(256) quantize_permute_kernel(const uint16_t* _
                                                                uint8_t* __restrict__ scales,
                                                                uint32_t* __restrict__ status) {
   pdl_launch_dependents();
-  pdl_wait();
   const int lane = threadIdx.x & 31;
-  const int64_t warp0 = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-  const int64_t nwarps = (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5;
-  const int segs = (H + kSegCols - 1) / kSegCols;
-  const int64_t items = static_cast<int64_t>(T) * segs;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const int c0 = static_cast<int>(blockIdx.y) * kSegCols + lane * 8;
   const int kb128 = H / 128;
-  for (int64_t item = warp0; item < items; item += nwarps) {
-    const int64_t t = item / segs;
-    const int c0 = static_cast<int>(item - t * segs) * kSegCols + lane * 8;
-    int my_row = -1;  // lane j < k: row of (t, j)
-    if (lane < k) {
-      const int32_t r = __ldg(scatter_idx + t * k + lane);
-      if (r >= 0 && r < max_rows) my_row = r;
-      else record_status(status, kStatusBounds);
-    }
-    uint4 v[4];
+  if (t >= T) return;  // a whole warp
+  pdl_wait();
+  int my_row = -1;  // lane j < k: row of (t, j)
+  if (lane < k) {
+    const int32_t r = __ldg(scatter_idx + t * k + lane);
+    if (r >= 0 && r < max_rows) my_row = r;
+    else record_status(status, kStatusBounds);
+  }
+  uint4 v[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    v[u] = make_uint4(0u, 0u, 0u, 0u);
+    if (c0 + u * 256 < H) v[u] = __ldg(reinterpret_cast<const uint4*>(X + t * H + c0 + u * 256));
+  }
+  uint32_t code[4], word[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const uint32_t s = block_scale_of_quad(v[u]);
+    word[u] = scale_word_of_half(s, lane);
+    code[u] = quantize_bf16x8(v[u], s);
+  }
+  for (int j = 0; j < k; ++j) {
+    const int64_t r = __shfl_sync(0xffffffffu, my_row, j);
+    if (r < 0) continue;
+    uint8_t* dst = codes + (r * H + c0) / 2;
+    uint8_t* sc = scales + scale_word_offset(r, c0 / 128, kb128);
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      v[u] = make_uint4(0u, 0u, 0u, 0u);
-      if (c0 + u * 256 < H) v[u] = __ldg(reinterpret_cast<const uint4*>(X + t * H + c0 + u * 256));
-    }
-    uint32_t code[4], word[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const uint32_t s = block_scale_of_quad(v[u]);
-      word[u] = scale_word_of_half(s, lane);
-      code[u] = quantize_bf16x8(v[u], s);
-    }
-    for (int j = 0; j < k; ++j) {
-      const int64_t r = __shfl_sync(0xffffffffu, my_row, j);
-      if (r < 0) continue;
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int c = c0 + u * 256;
-        if (c >= H) continue;
-        *reinterpret_cast<uint32_t*>(codes + (r * H + c) / 2) = code[u];
-        if ((lane & 15) == 0) *reinterpret_cast<uint32_t*>(scales + scale_word_offset(r, c / 128, kb128)) = word[u];
-      }
+      if (c0 + u * 256 >= H) continue;
+      *reinterpret_cast<uint32_t*>(dst + u * 128) = code[u];
+      if ((lane & 15) == 0) *reinterpret_cast<uint32_t*>(sc + u * 1024) = word[u];
     }
   }
 }
 
-unsigned grid_of(int64_t items) {
-  const int64_t blocks = (items + 7) / 8;  // 8 warps (items) per CTA
-  return static_cast<unsigned>(blocks < 1 ? 1 : blocks > 65536 ? 65536 : blocks);
+// one warp per row and segment, eight rows per CTA
+dim3 grid_of(int64_t rows, int64_t cols) {
+  return dim3(static_cast<unsigned>((rows + 7) / 8), static_cast<unsigned>((cols + kSegCols - 1) / kSegCols));
 }
 
 }  // namespace
 
 cudaError_t launch_quantize_rows(const uint16_t* x, int64_t rows, int64_t cols, uint8_t* codes, uint8_t* scales,
                                  cudaStream_t st) {
-  const int64_t items = (rows + 127) / 128 * 128 * ((cols + kSegCols - 1) / kSegCols);
-  return launch_pdl(quantize_rows_kernel, dim3(grid_of(items)), dim3(256), 0, st, x, rows, cols, codes, scales);
+  return launch_pdl(quantize_rows_kernel, grid_of((rows + 127) / 128 * 128, cols), dim3(256), 0, st, x, rows, cols,
+                    codes, scales);
 }
 
 cudaError_t launch_dequantize_rows(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
                                    uint16_t* x, cudaStream_t st) {
-  const int64_t items = rows * ((cols + kSegCols - 1) / kSegCols);
-  return launch_pdl(dequantize_rows_kernel, dim3(grid_of(items)), dim3(256), 0, st, codes, scales, rows, cols, x);
+  return launch_pdl(dequantize_rows_kernel, grid_of(rows, cols), dim3(256), 0, st, codes, scales, rows, cols, x);
 }
 
 cudaError_t launch_quantize_weights(const uint16_t* w, int E, int64_t K, int64_t N, uint8_t* codes, uint8_t* scales,
@@ -248,8 +224,7 @@ cudaError_t launch_quantize_weights(const uint16_t* w, int E, int64_t K, int64_t
 
 cudaError_t launch_quantize_permute(const moe_shape& s, const uint16_t* X, const int32_t* scatter_idx, uint8_t* codes,
                                     uint8_t* scales, uint32_t* status, cudaStream_t st) {
-  const int64_t items = static_cast<int64_t>(s.T) * ((s.H + kSegCols - 1) / kSegCols);
-  return launch_pdl(quantize_permute_kernel, dim3(grid_of(items)), dim3(256), 0, st, X, scatter_idx, s.T, s.H, s.k,
+  return launch_pdl(quantize_permute_kernel, grid_of(s.T, s.H), dim3(256), 0, st, X, scatter_idx, s.T, s.H, s.k,
                     max_rows_of(s), codes, scales, status);
 }
 

@@ -33,10 +33,15 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t amax) {
 // 2^(127 - s): elements are divided by their scale exactly (s <= 252 here).
 __device__ __forceinline__ float scale_inverse(uint32_t s) { return __uint_as_float((254u - s) << 23); }
 
-// 2^(s - 127) for any scale byte (s = 0 is a subnormal float, 255 is NaN).
-__device__ __forceinline__ float scale_value(uint32_t s) {
-  if (s == kScaleNan) return __uint_as_float(0x7FC00000u);
-  return s == 0u ? __uint_as_float(0x00400000u) : __uint_as_float(s << 23);
+// 2^(s - 127) as bf16 bits for any scale byte (0 is a subnormal, 255 is NaN).
+__device__ __forceinline__ uint32_t scale_bf16(uint32_t s) { return s == 0u ? 0x0040u : s == kScaleNan ? 0x7FC0u : s << 7; }
+
+// Both halves times m (bf16x2; powers of two here, so exact; subnormals are
+// kept).
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t m) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(m));
+  return r;
 }
 
 // Eight floats to eight e2m1 codes (v[0] in the low nibble), round to nearest
@@ -54,32 +59,47 @@ __device__ __forceinline__ uint32_t pack_e2m1x8(const float (&v)[8]) {
   return r;
 }
 
-// Largest magnitude (bf16 bits, sign clear) of the two bf16 in w and m.
-__device__ __forceinline__ uint32_t amax_bf16x2(uint32_t m, uint32_t w) {
-  return max(m, max(w & 0x7FFFu, (w >> 16) & 0x7FFFu));
-}
-
 // The eight bf16 in v to e2m1 codes under scale byte s (codes 0 under a NaN
 // scale).
 __device__ __forceinline__ uint32_t quantize_bf16x8(const uint4& v, uint32_t s) {
   if (s == kScaleNan) return 0u;
-  const float inv = scale_inverse(s);
-  const float f[8] = {bf16lo_to_f32(v.x) * inv, bf16hi_to_f32(v.x) * inv, bf16lo_to_f32(v.y) * inv,
-                      bf16hi_to_f32(v.y) * inv, bf16lo_to_f32(v.z) * inv, bf16hi_to_f32(v.z) * inv,
-                      bf16lo_to_f32(v.w) * inv, bf16hi_to_f32(v.w) * inv};
+  const uint32_t inv = ((254u - s) << 7) * 0x10001u;  // 2^(127 - s) in both halves
+  const uint32_t w[4] = {mul_bf16x2(v.x, inv), mul_bf16x2(v.y, inv), mul_bf16x2(v.z, inv), mul_bf16x2(v.w, inv)};
+  const float f[8] = {bf16lo_to_f32(w[0]), bf16hi_to_f32(w[0]), bf16lo_to_f32(w[1]), bf16hi_to_f32(w[1]),
+                      bf16lo_to_f32(w[2]), bf16hi_to_f32(w[2]), bf16lo_to_f32(w[3]), bf16hi_to_f32(w[3])};
   return pack_e2m1x8(f);
 }
 
+// Byte i of the result is the byte of (b:a) that nibble i of `sel` names; a
+// nibble with its top bit set gives that byte's sign bit eight times.
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
+  return r;
+}
+
+// Four codes (the low 16 bits of q) to four bf16 times the scale (bf16x2 sc):
+// the e2m1 magnitudes are bf16 whose two bytes come from eight-entry tables.
+__device__ __forceinline__ void dequantize_bf16x4(uint32_t q, uint32_t sc, uint32_t& w0, uint32_t& w1) {
+  const uint32_t sel = q & 0x7777u;
+  // the sign bit of a code is its selector's top bit: 0xFF below zero, else 0x80
+  const uint32_t neg = (prmt(0x80808080u, 0x80808080u, q) & 0x01010101u) << 7;
+  const uint32_t hi = prmt(0x3F3F3F00u, 0x40404040u, sel) | neg;
+  const uint32_t lo = prmt(0xC0800000u, 0xC0804000u, sel);
+  w0 = mul_bf16x2(prmt(lo, hi, 0x5140u), sc);
+  w1 = mul_bf16x2(prmt(lo, hi, 0x7362u), sc);
+}
+
 // Eight consecutive bf16 per lane, four lanes per block: the block's scale
-// byte, known to its four lanes.  All 32 lanes call it.
+// byte, known to its four lanes.  All 32 lanes call it.  The maxima are of the
+// magnitudes' bits, two bf16 at a time.
 __device__ __forceinline__ uint32_t block_scale_of_quad(const uint4& v) {
-  uint32_t m = amax_bf16x2(0u, v.x);
-  m = amax_bf16x2(m, v.y);
-  m = amax_bf16x2(m, v.z);
-  m = amax_bf16x2(m, v.w);
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-  return scale_byte(m);
+  constexpr uint32_t kAbs = 0x7FFF7FFFu;
+  uint32_t m = __vimax3_u16x2(v.x & kAbs, v.y & kAbs, v.z & kAbs);
+  m = __vmaxu2(m, v.w & kAbs);
+  m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  return scale_byte(max(m & 0xFFFFu, m >> 16));
 }
 
 // The scale word of the 16 lanes' four blocks (block 0 in the low byte), known
