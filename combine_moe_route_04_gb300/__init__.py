@@ -10,6 +10,7 @@ library and a compute capability 10.3 device.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 __all__ = ["MoEError", "MoEShape", "MoEViews", "lib_path", "load", "shape", "capacity",
@@ -174,6 +175,11 @@ def _stream(stream):
 
 
 def _dev_tensor(t, dtype, min_numel, name):
+    try:  # the usual case in one line; what is wrong is found below
+        if t.dtype is dtype and t.is_cuda and t.is_contiguous() and t.numel() >= min_numel:
+            return t.data_ptr()
+    except AttributeError:
+        pass
     import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch tensor" % name)
@@ -385,6 +391,27 @@ def alloc_mxfp4(rows: int, cols: int, device="cuda") -> tuple:
             torch.empty(scale_bytes, dtype=torch.uint8, device=device))
 
 
+class _Plan:
+    """A supported shape with the sizes its calls check their buffers against."""
+
+    def __init__(self, key):
+        self.shape = MoEShape(*key)
+        self.T, self.H, self.I, self.E, self.k = key
+        self.max_rows = capacity(self.shape)[1]  # refuses an unsupported shape
+        self.ref = ctypes.byref(self.shape)
+        self.mxfp4_ws = mxfp4_workspace_size(self.shape)
+        self.balance_ws = balance_workspace_size(self.shape)
+
+
+@functools.lru_cache(maxsize=256)
+def _plan_of(key):
+    return _Plan(key)
+
+
+def _plan(s) -> _Plan:
+    return _plan_of((s.T, s.H, s.I, s.E, s.k) if isinstance(s, MoEShape) else tuple(s))
+
+
 def _mxfp4_ptrs(codes, scales, rows, cols, name):
     import torch
     # the sizes of moe_mxfp4_sizes; the call itself refuses unsupported ones
@@ -416,13 +443,12 @@ def moe_dequantize_mxfp4(codes, scales, rows, cols, x, stream=None):
 
 def moe_quantize_permute_mxfp4(s, X, scatter_idx, codes, scales, ws, stream=None):
     import torch
-    s = _shape_obj(s)
-    mr = capacity(s)[1]  # refuses an unsupported shape
+    s = _plan(s)
     args = [_dev_tensor(X, torch.bfloat16, s.T * s.H, "X"),
             _dev_tensor(scatter_idx, torch.int32, s.T * s.k, "scatter_idx"),
-            *_mxfp4_ptrs(codes, scales, mr, s.H, ""),
+            *_mxfp4_ptrs(codes, scales, s.max_rows, s.H, ""),
             _dev_tensor(ws, torch.uint8, 256, "ws")]
-    _check(load().moe_quantize_permute_mxfp4(ctypes.byref(s), *args, _stream(stream)), "moe_quantize_permute_mxfp4")
+    _check(load().moe_quantize_permute_mxfp4(s.ref, *args, _stream(stream)), "moe_quantize_permute_mxfp4")
 
 
 def moe_grouped_gemm_up_mxfp4(s, x_codes, x_scales, counts, off_pad, wg_codes, wg_scales, wu_codes, wu_scales, h,
@@ -430,30 +456,28 @@ def moe_grouped_gemm_up_mxfp4(s, x_codes, x_scales, counts, off_pad, wg_codes, w
     """The gate/up product on MXFP4 rows and weights; ws: an MXFP4 workspace,
     or any uint8 buffer of at least 256 bytes, zeroed once."""
     import torch
-    s = _shape_obj(s)
-    mr = capacity(s)[1]
-    args = [*_mxfp4_ptrs(x_codes, x_scales, mr, s.H, "x_"),
+    s = _plan(s)
+    args = [*_mxfp4_ptrs(x_codes, x_scales, s.max_rows, s.H, "x_"),
             _dev_tensor(counts, torch.int32, s.E, "counts"),
             _dev_tensor(off_pad, torch.int32, s.E + 1, "off_pad"),
             *_mxfp4_ptrs(wg_codes, wg_scales, s.E * s.I, s.H, "wg_"),
             *_mxfp4_ptrs(wu_codes, wu_scales, s.E * s.I, s.H, "wu_"),
-            _dev_tensor(h, torch.bfloat16, mr * s.I, "h"),
+            _dev_tensor(h, torch.bfloat16, s.max_rows * s.I, "h"),
             _dev_tensor(ws, torch.uint8, 256, "ws")]
-    _check(load().moe_grouped_gemm_up_mxfp4(ctypes.byref(s), *args, _stream(stream)), "moe_grouped_gemm_up_mxfp4")
+    _check(load().moe_grouped_gemm_up_mxfp4(s.ref, *args, _stream(stream)), "moe_grouped_gemm_up_mxfp4")
 
 
 def moe_grouped_gemm_down_mxfp4(s, h_codes, h_scales, counts, off_pad, wd_codes, wd_scales, Y, ws, stream=None):
     """The down product on MXFP4 rows and weights; ws as for the gate/up product."""
     import torch
-    s = _shape_obj(s)
-    mr = capacity(s)[1]
-    args = [*_mxfp4_ptrs(h_codes, h_scales, mr, s.I, "h_"),
+    s = _plan(s)
+    args = [*_mxfp4_ptrs(h_codes, h_scales, s.max_rows, s.I, "h_"),
             _dev_tensor(counts, torch.int32, s.E, "counts"),
             _dev_tensor(off_pad, torch.int32, s.E + 1, "off_pad"),
             *_mxfp4_ptrs(wd_codes, wd_scales, s.E * s.H, s.I, "wd_"),
-            _dev_tensor(Y, torch.bfloat16, mr * s.H, "Y"),
+            _dev_tensor(Y, torch.bfloat16, s.max_rows * s.H, "Y"),
             _dev_tensor(ws, torch.uint8, 256, "ws")]
-    _check(load().moe_grouped_gemm_down_mxfp4(ctypes.byref(s), *args, _stream(stream)),
+    _check(load().moe_grouped_gemm_down_mxfp4(s.ref, *args, _stream(stream)),
            "moe_grouped_gemm_down_mxfp4")
 
 
@@ -475,8 +499,7 @@ def moe_forward_mxfp4(s, logits, X, wg_codes, wg_scales, wu_codes, wu_scales, wd
                       stream=None):
     """moe_forward with the experts' products in MXFP4 (weights as moe_quantize_weights_mxfp4 leaves them)."""
     import torch
-    s = _shape_obj(s)
-    ws_bytes = mxfp4_workspace_size(s)  # refuses an unsupported shape
+    s = _plan(s)
     bf = torch.bfloat16
     args = [_dev_tensor(logits, torch.float32, s.T * s.E, "logits"),
             _dev_tensor(X, bf, s.T * s.H, "X"),
@@ -484,8 +507,8 @@ def moe_forward_mxfp4(s, logits, X, wg_codes, wg_scales, wu_codes, wu_scales, wd
             *_mxfp4_ptrs(wu_codes, wu_scales, s.E * s.I, s.H, "wu_"),
             *_mxfp4_ptrs(wd_codes, wd_scales, s.E * s.H, s.I, "wd_"),
             _dev_tensor(out, bf, s.T * s.H, "out"),
-            _dev_tensor(ws, torch.uint8, ws_bytes, "ws")]
-    _check(load().moe_forward_mxfp4(ctypes.byref(s), *args, _stream(stream)), "moe_forward_mxfp4")
+            _dev_tensor(ws, torch.uint8, s.mxfp4_ws, "ws")]
+    _check(load().moe_forward_mxfp4(s.ref, *args, _stream(stream)), "moe_forward_mxfp4")
 
 
 def balance_workspace_size(s) -> int:
@@ -515,8 +538,7 @@ def moe_balance_loss(s, logits, topk_ids, mask, counts, num_tokens, mean_probs, 
     """Per-expert counts and mean probabilities, and losses = (balance, z) of the
     tokens whose mask (uint8 or bool [T], or None) is non-zero."""
     import torch
-    s = _shape_obj(s)
-    ws_bytes = balance_workspace_size(s)  # refuses an unsupported shape
+    s = _plan(s)
     args = [_dev_tensor(logits, torch.float32, s.T * s.E, "logits"),
             _dev_tensor(topk_ids, torch.int32, s.T * s.k, "topk_ids"),
             _mask_ptr(mask, s.T),
@@ -524,19 +546,18 @@ def moe_balance_loss(s, logits, topk_ids, mask, counts, num_tokens, mean_probs, 
             _dev_tensor(num_tokens, torch.int32, 1, "num_tokens"),
             _dev_tensor(mean_probs, torch.float32, s.E, "mean_probs"),
             _dev_tensor(losses, torch.float32, 2, "losses"),
-            _dev_tensor(ws, torch.uint8, ws_bytes, "ws")]
-    _check(load().moe_balance_loss(ctypes.byref(s), *args, _stream(stream)), "moe_balance_loss")
+            _dev_tensor(ws, torch.uint8, s.balance_ws, "ws")]
+    _check(load().moe_balance_loss(s.ref, *args, _stream(stream)), "moe_balance_loss")
 
 
 def moe_balance_loss_backward(s, logits, mask, counts, num_tokens, grad_losses, dlogits, stream=None):
     """The gradient of grad_losses[0] * balance + grad_losses[1] * z to the logits."""
     import torch
-    s = _shape_obj(s)
-    capacity(s)  # refuses an unsupported shape
+    s = _plan(s)
     args = [_dev_tensor(logits, torch.float32, s.T * s.E, "logits"),
             _mask_ptr(mask, s.T),
             _dev_tensor(counts, torch.int32, s.E, "counts"),
             _dev_tensor(num_tokens, torch.int32, 1, "num_tokens"),
             _dev_tensor(grad_losses, torch.float32, 2, "grad_losses"),
             _dev_tensor(dlogits, torch.float32, s.T * s.E, "dlogits")]
-    _check(load().moe_balance_loss_backward(ctypes.byref(s), *args, _stream(stream)), "moe_balance_loss_backward")
+    _check(load().moe_balance_loss_backward(s.ref, *args, _stream(stream)), "moe_balance_loss_backward")

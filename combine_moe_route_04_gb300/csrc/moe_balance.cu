@@ -17,7 +17,6 @@
 // finishes last over all CTAs), so results are reproducible without
 // floating-point atomics.
 #include <cmath>
-#include <type_traits>
 #include <cstdint>
 
 #include "moe_device.cuh"
@@ -31,29 +30,66 @@ constexpr int kFwdThreads = 1024;
 constexpr int kFwdWarps = kFwdThreads / 32;
 constexpr int kBwdThreads = 256;
 
+// e^x and ln(x) on the SFU; e^x below the smallest normal float is 0.
+__device__ __forceinline__ float fast_exp(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
+  return r;
+}
+__device__ __forceinline__ float fast_log(float x) {
+  float r;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r * 0.6931471805599453f;
+}
+__device__ __forceinline__ float fast_rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// Maximum and sum over the G lanes of a group (all 32 lanes call them).
+template <int G>
+__device__ __forceinline__ float group_max(float x) {
+  if constexpr (G == 32) {
+    float r;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+    return r;
+  } else {
+#pragma unroll
+    for (int o = G / 2; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+    return x;
+  }
+}
+template <int G>
+__device__ __forceinline__ float group_sum(float x) {
+#pragma unroll
+  for (int o = G / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
 // A lane's logits of one row: V groups of W consecutive experts, group i of
 // lane gl (its index inside its G lanes) at expert W (gl + G i).
-template <int V, int W>
+template <int V, int W, int G>
 struct Row {
   float v[V * W];
 
-  __device__ __forceinline__ static int expert(int gl, int G, int x) { return W * (gl + G * (x / W)) + x % W; }
+  __device__ __forceinline__ static int expert(int gl, int x) { return W * (gl + G * (x / W)) + x % W; }
 
-  // absent experts (and whole rows that are not `there`) read as -inf
-  __device__ __forceinline__ void load(const float* __restrict__ row, int gl, int G, int E, bool there) {
+  // `row`: the lane's first logit; absent experts (and whole rows that are
+  // not `there`) read as -inf
+  __device__ __forceinline__ void load(const float* __restrict__ row, int gl, int E, bool there) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int e = W * (gl + G * i);
-      const bool in = there && e < E;
+      const bool in = there && W * (gl + G * i) < E;
       if constexpr (W == 4) {
         float4 q = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-        if (in) q = __ldg(reinterpret_cast<const float4*>(row + e));
+        if (in) q = __ldg(reinterpret_cast<const float4*>(row + 4 * G * i));
         v[4 * i] = q.x;
         v[4 * i + 1] = q.y;
         v[4 * i + 2] = q.z;
         v[4 * i + 3] = q.w;
       } else {
-        v[i] = in ? __ldg(row + e) : -INFINITY;
+        v[i] = in ? __ldg(row + G * i) : -INFINITY;
       }
     }
   }
@@ -61,30 +97,29 @@ struct Row {
   // v becomes exp(v - max) (max taken as 0 where nothing is above -inf);
   // returns that max and the row's sum, which is 0 only if every logit is
   // -inf (a NaN anywhere makes it NaN).
-  __device__ __forceinline__ void exps(int G, float& top, float& sum) {
+  __device__ __forceinline__ void exps(float& top, float& sum) {
     float m = v[0];
 #pragma unroll
     for (int x = 1; x < V * W; ++x) m = fmaxf(m, v[x]);
-    for (int o = G >> 1; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    m = group_max<G>(m);
     top = m == -INFINITY ? 0.0f : m;
     float s = 0.0f;
 #pragma unroll
     for (int x = 0; x < V * W; ++x) {
-      v[x] = __expf(v[x] - top);
+      v[x] = fast_exp(v[x] - top);
       s += v[x];
     }
-    for (int o = G >> 1; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    sum = s;
+    sum = group_sum<G>(s);
   }
 };
 
 // Rows each warp (or group of lanes) has in flight at a time.
 constexpr int kUnroll = 2;
 
-template <int V, int W>
+template <int V, int W, int G>
 __global__ void __launch_bounds__(kFwdThreads, 1)
     balance_loss_kernel(const float* __restrict__ logits, const int32_t* __restrict__ topk_ids,
-                        const uint8_t* __restrict__ mask, int T, int E, int k, int G, int32_t* __restrict__ counts,
+                        const uint8_t* __restrict__ mask, int T, int E, int k, int32_t* __restrict__ counts,
                         int32_t* __restrict__ num_tokens, float* __restrict__ mean_probs, float* __restrict__ losses,
                         uint32_t* __restrict__ partials, uint32_t* __restrict__ counter,
                         uint32_t* __restrict__ status) {
@@ -96,7 +131,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   pdl_launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int gl = lane & (G - 1);
-  const int per_warp = 32 / G;
+  constexpr int per_warp = 32 / G;
   for (int e = tid; e < E; e += kFwdThreads) s_cnt[e] = 0;
   __syncthreads();
   pdl_wait();
@@ -118,14 +153,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     use[u] = t < T && (mask == nullptr || __ldg(mask + t) != 0);
   }
   for (int64_t d = 0; warp_first + d < T; d += stride) {  // uniform across the warp
-    Row<V, W> r[kUnroll];
+    Row<V, W, G> r[kUnroll];
     int id[kUnroll];
     bool there[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const int64_t t = first + d + u * per_warp;
       there[u] = use[u];
-      r[u].load(logits + t * E, gl, G, E, there[u]);
+      r[u].load(logits + t * E + W * gl, gl, E, there[u]);
       id[u] = there[u] && gl < k ? __ldg(topk_ids + t * k + gl) : 0;
     }
 #pragma unroll
@@ -136,20 +171,23 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       float top, sum;
-      r[u].exps(G, top, sum);
+      r[u].exps(top, sum);
       if (!there[u] || sum == 0.0f) continue;
-      const float inv = 1.0f / sum;
+      const float inv = fast_rcp(sum);
 #pragma unroll
       for (int x = 0; x < V * W; ++x) acc[x] += r[u].v[x] * inv;
       if (gl == 0) {
-        const float lse = top + logf(sum);
+        const float lse = top + fast_log(sum);
         z += lse * lse;
         ++n;
       }
-      for (int j = gl; j < k; j += G) {
-        const int e = j == gl ? id[u] : __ldg(topk_ids + (first + d + u * per_warp) * k + j);
-        if (e >= 0 && e < E) atomicAdd(&s_cnt[e], 1);
+      auto count = [&](int e) {
+        if (static_cast<unsigned>(e) < static_cast<unsigned>(E)) atomicAdd(&s_cnt[e], 1);
         else record_status(status, kStatusBounds);
+      };
+      if (gl < k) count(id[u]);
+      if constexpr (G < 16) {  // more picks than lanes
+        for (int j = gl + G; j < k; j += G) count(__ldg(topk_ids + (first + d + u * per_warp) * k + j));
       }
     }
   }
@@ -165,7 +203,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   if (lane < G) {
 #pragma unroll
     for (int x = 0; x < V * W; ++x) {
-      const int e = Row<V, W>::expert(gl, G, x);
+      const int e = Row<V, W, G>::expert(gl, x);
       if (e < E) s_p[warp * E + e] = acc[x];
     }
   }
@@ -230,7 +268,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         ps[q] = 0.0f;
         cs[q] = 0;
       }
-#pragma unroll 5
+#pragma unroll 4
       for (int b = part; b < static_cast<int>(gridDim.x); b += parts) {
         if constexpr (W == 4) {
           const float4 p4 = __ldcg(reinterpret_cast<const float4*>(part_p + b * E + e));
@@ -297,16 +335,16 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   }
 }
 
-template <int V, int W>
+template <int V, int W, int G>
 __global__ void __launch_bounds__(kBwdThreads)
     balance_backward_kernel(const float* __restrict__ logits, const uint8_t* __restrict__ mask, int T, int E, int k,
-                            int G, const int32_t* __restrict__ counts, const int32_t* __restrict__ num_tokens,
+                            const int32_t* __restrict__ counts, const int32_t* __restrict__ num_tokens,
                             const float* __restrict__ grad_losses, float* __restrict__ dlogits) {
   pdl_launch_dependents();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gl = lane & (G - 1);
-  const int per_warp = 32 / G;
+  constexpr int per_warp = 32 / G;
   constexpr int kWarps = kBwdThreads / 32;
   const int n = __ldg(num_tokens);
   const float inv_n = n > 0 ? 1.0f / static_cast<float>(n) : 0.0f;
@@ -317,7 +355,7 @@ __global__ void __launch_bounds__(kBwdThreads)
   float f[V * W];
 #pragma unroll
   for (int x = 0; x < V * W; ++x) {
-    const int e = Row<V, W>::expert(gl, G, x);
+    const int e = Row<V, W, G>::expert(gl, x);
     f[x] = 0.0f;
     if (e < E && n > 0) {
       const int64_t nk = static_cast<int64_t>(n) * k;
@@ -332,7 +370,7 @@ __global__ void __launch_bounds__(kBwdThreads)
   const int64_t tiles = (T + step - 1) / step;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * kWarps + warp; i < tiles; i += stride / step) {
     const int64_t t0 = (tiles - 1 - i) * step + lane / G;
-    Row<V, W> r[kUnroll];
+    Row<V, W, G> r[kUnroll];
     bool there[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
@@ -340,57 +378,76 @@ __global__ void __launch_bounds__(kBwdThreads)
       there[u] = t < T && (mask == nullptr || __ldg(mask + t) != 0);
     }
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) r[u].load(logits + (t0 + u * per_warp) * E, gl, G, E, there[u]);
+    for (int u = 0; u < kUnroll; ++u) r[u].load(logits + (t0 + u * per_warp) * E + W * gl, gl, E, there[u]);
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const int64_t t = t0 + u * per_warp;
       float top, sum;
-      r[u].exps(G, top, sum);
+      r[u].exps(top, sum);
       const bool takes = there[u] && sum != 0.0f;
-      const float inv = 1.0f / sum;
+      const float inv = fast_rcp(sum);
       float dot = 0.0f;
 #pragma unroll
-      for (int x = 0; x < V * W; ++x) {
-        r[u].v[x] *= inv;
-        dot += f[x] * r[u].v[x];
-      }
-      for (int o = G >> 1; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-      const float c = b * (top + logf(sum)) - a * dot;
+      for (int x = 0; x < V * W; ++x) dot = fmaf(f[x], r[u].v[x], dot);
+      dot = group_sum<G>(dot) * inv;
       if (t >= T) continue;
+      // p (a f + c) with p = v / sum
+      const float ia = a * inv;
+      const float ic = (b * (top + fast_log(sum)) - a * dot) * inv;
+      float* out = dlogits + t * E + W * gl;
 #pragma unroll
       for (int x = 0; x < V; ++x) {
-        const int e = W * (gl + G * x);
-        if (e >= E) continue;
+        if (W * (gl + G * x) >= E) continue;
         float d[W];
 #pragma unroll
-        for (int q = 0; q < W; ++q) d[q] = takes ? r[u].v[W * x + q] * fmaf(a, f[W * x + q], c) : 0.0f;
-        if constexpr (W == 4) *reinterpret_cast<float4*>(dlogits + t * E + e) = make_float4(d[0], d[1], d[2], d[3]);
-        else dlogits[t * E + e] = d[0];
+        for (int q = 0; q < W; ++q) d[q] = takes ? r[u].v[W * x + q] * fmaf(ia, f[W * x + q], ic) : 0.0f;
+        if constexpr (W == 4) *reinterpret_cast<float4*>(out + 4 * G * x) = make_float4(d[0], d[1], d[2], d[3]);
+        else out[G * x] = d[0];
       }
     }
   }
 }
 
-// lanes per token: the least power of two whose V W logits each cover E
-int lanes_for(int E, int per_lane) {
-  int g = 1;
-  while (g < 32 && g * per_lane < E) g <<= 1;
-  return g;
+// Calls fn with the row split of E experts: as few logits per lane and lanes
+// per token as cover E.
+template <int V, int W, int G>
+struct Split {};
+template <int W, int G = 1, typename F>
+cudaError_t by_lanes(int E, F&& fn) {
+  if constexpr (G < 32) {
+    if (E > W * G) return by_lanes<W, 2 * G>(E, fn);
+  }
+  return fn(Split<1, W, G>{});
 }
-
-// The forward and backward kernels of E experts: fn(V, W, G) with the logits
-// per lane as few as E allows (E <= 128 V, or 32 V one by one).
 template <typename F>
 cudaError_t by_experts(int E, F&& fn) {
-  using std::integral_constant;
-  if (E % 4 == 0) {
-    if (E <= 128) return fn(integral_constant<int, 1>{}, integral_constant<int, 4>{}, lanes_for(E, 4));
-    return fn(integral_constant<int, 2>{}, integral_constant<int, 4>{}, 32);
-  }
-  if (E <= 32) return fn(integral_constant<int, 1>{}, integral_constant<int, 1>{}, lanes_for(E, 1));
-  if (E <= 64) return fn(integral_constant<int, 2>{}, integral_constant<int, 1>{}, 32);
-  if (E <= 128) return fn(integral_constant<int, 4>{}, integral_constant<int, 1>{}, 32);
-  return fn(integral_constant<int, 8>{}, integral_constant<int, 1>{}, 32);
+  if (E % 4 == 0) return E <= 128 ? by_lanes<4>(E, fn) : fn(Split<2, 4, 32>{});
+  if (E <= 32) return by_lanes<1>(E, fn);
+  if (E <= 64) return fn(Split<2, 1, 32>{});
+  return E <= 128 ? fn(Split<4, 1, 32>{}) : fn(Split<8, 1, 32>{});
+}
+
+template <int V, int W, int G>
+cudaError_t loss_call(Split<V, W, G>, const moe_shape& s, const float* logits, const int32_t* topk_ids,
+                      const uint8_t* mask, int32_t* counts, int32_t* num_tokens, float* mean_probs, float* losses,
+                      uint32_t* partials, uint32_t* counter, uint32_t* status, int num_sms, cudaStream_t st) {
+  constexpr int kPerCta = kFwdWarps * (32 / G) * kUnroll;
+  int grid = (s.T + kPerCta - 1) / kPerCta;
+  if (grid > num_sms) grid = num_sms;
+  if (grid > kBalanceMaxCtas) grid = kBalanceMaxCtas;
+  return launch_pdl(balance_loss_kernel<V, W, G>, dim3(grid), dim3(kFwdThreads), 0, st, logits, topk_ids, mask, s.T,
+                    s.E, s.k, counts, num_tokens, mean_probs, losses, partials, counter, status);
+}
+
+template <int V, int W, int G>
+cudaError_t backward_call(Split<V, W, G>, const moe_shape& s, const float* logits, const uint8_t* mask,
+                          const int32_t* counts, const int32_t* num_tokens, const float* grad_losses, float* dlogits,
+                          int num_sms, cudaStream_t st) {
+  constexpr int kPerCta = kBwdThreads / 32 * (32 / G) * kUnroll;
+  int grid = (s.T + kPerCta - 1) / kPerCta;
+  if (grid > num_sms * 8) grid = num_sms * 8;
+  return launch_pdl(balance_backward_kernel<V, W, G>, dim3(grid), dim3(kBwdThreads), 0, st, logits, mask, s.T, s.E,
+                    s.k, counts, num_tokens, grad_losses, dlogits);
 }
 
 }  // namespace
@@ -399,26 +456,17 @@ cudaError_t launch_balance_loss(const moe_shape& s, const float* logits, const i
                                 int32_t* counts, int32_t* num_tokens, float* mean_probs, float* losses,
                                 uint32_t* partials, uint32_t* counter, uint32_t* status, int num_sms,
                                 cudaStream_t st) {
-  return by_experts(s.E, [&](auto V, auto W, int G) {
-    const int64_t per_cta = static_cast<int64_t>(kFwdWarps) * (32 / G) * kUnroll;
-    int64_t grid = (s.T + per_cta - 1) / per_cta;
-    if (grid > num_sms) grid = num_sms;
-    if (grid > kBalanceMaxCtas) grid = kBalanceMaxCtas;
-    return launch_pdl(balance_loss_kernel<V, W>, dim3(static_cast<unsigned>(grid)), dim3(kFwdThreads), 0, st, logits,
-                      topk_ids, mask, s.T, s.E, s.k, G, counts, num_tokens, mean_probs, losses, partials, counter,
-                      status);
+  return by_experts(s.E, [&](auto split) {
+    return loss_call(split, s, logits, topk_ids, mask, counts, num_tokens, mean_probs, losses, partials, counter,
+                     status, num_sms, st);
   });
 }
 
 cudaError_t launch_balance_backward(const moe_shape& s, const float* logits, const uint8_t* mask,
                                     const int32_t* counts, const int32_t* num_tokens, const float* grad_losses,
                                     float* dlogits, int num_sms, cudaStream_t st) {
-  return by_experts(s.E, [&](auto V, auto W, int G) {
-    const int64_t per_cta = static_cast<int64_t>(kBwdThreads / 32) * (32 / G) * kUnroll;
-    int64_t grid = (s.T + per_cta - 1) / per_cta;
-    if (grid > static_cast<int64_t>(num_sms) * 8) grid = static_cast<int64_t>(num_sms) * 8;
-    return launch_pdl(balance_backward_kernel<V, W>, dim3(static_cast<unsigned>(grid)), dim3(kBwdThreads), 0, st,
-                      logits, mask, s.T, s.E, s.k, G, counts, num_tokens, grad_losses, dlogits);
+  return by_experts(s.E, [&](auto split) {
+    return backward_call(split, s, logits, mask, counts, num_tokens, grad_losses, dlogits, num_sms, st);
   });
 }
 
