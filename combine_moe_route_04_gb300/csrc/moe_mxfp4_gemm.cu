@@ -16,9 +16,15 @@
 // Windows start at multiples of 64 rows: their rows' scales then start at an
 // even TMEM column of the 128-row scale tile.
 //
-// Roles of the 10 warps: warp 0 loads (per 256-deep stage two 128 x 128-byte
+// The epilogue would cost as much as the MMAs if it held the accumulators, so
+// its 12 warps take them into registers (two 32 x 32 pieces of each accumulator
+// per warp at most: the first as finished bf16, the second as it is) and hand
+// TMEM back; the rest of the arithmetic and all stores run under the next
+// tile's MMAs.
+//
+// Roles of the 14 warps: warp 0 loads (per 256-deep stage two 128 x 128-byte
 // weight boxes, the window's rows in boxes of 32, and the scale tiles), warp 1
-// copies a stage's scales to TMEM and issues its MMAs, warps 2-9 drain the
+// copies a stage's scales to TMEM and issues its MMAs, warps 2-13 drain the
 // accumulators.  Every wait is bounded as in the bf16 GEMMs.
 #include <cstdint>
 #include <mutex>
@@ -43,8 +49,15 @@ constexpr int kOffSf = kOffT + kTBytes;         // scales: weights 0, weights 1,
 constexpr int kStageBytes = kOffSf + 4 * kSfBytes;
 static_assert(kStageBytes % 1024 == 0, "stages start on swizzle atoms");
 
-constexpr int kEpiWarps = 8;
-constexpr int kThreads = (2 + kEpiWarps) * 32;
+constexpr int kEpiWarps = 12;
+constexpr int kEpiSplit = kEpiWarps / 4;         // warps sharing a lane quarter
+static_assert(2 * kEpiSplit * 32 == kTok, "two 32-row pieces of a window per warp at most");
+// staging of a piece, transposed: 32 rows of 32 columns (64 bytes, padded so
+// that eight rows start on different banks)
+constexpr int kPitch = 80;
+constexpr int kStageOutBytes = 32 * kPitch;
+constexpr int kFirstEpi = 2;
+constexpr int kThreads = (kFirstEpi + kEpiWarps) * 32;
 
 // TMEM columns: accumulators, then 32 columns of scales per stage
 constexpr uint32_t kAcc1 = 192;
@@ -57,7 +70,8 @@ constexpr int kNumBars = 2 * kStages + 3;
 constexpr int kWinOff = kBarOff + kNumBars * 8 + 8;
 constexpr int kCntOff = kWinOff + (kMaxExperts + 1) * 4;
 constexpr int kOffpOff = kCntOff + kMaxExperts * 4;
-constexpr int kSmemBytes = kOffpOff + (kMaxExperts + 1) * 4;
+constexpr int kOutOff = (kOffpOff + (kMaxExperts + 1) * 4 + 15) / 16 * 16;
+constexpr int kSmemBytes = kOutOff + kEpiWarps * kStageOutBytes;
 constexpr int kSmemAlloc = kSmemBytes + 1024;
 static_assert(kSmemAlloc <= 232448, "shared memory budget");
 
@@ -149,7 +163,51 @@ __device__ __forceinline__ bool vote_any(bool flag) {
 
 // silu(g) * u with the sigmoid on the SFU (a few float32 ulps; g < -88 gives
 // the limit 0, as in the bf16 GEMM).
-__device__ __forceinline__ float silu_mul(float g, float u) { return g * __fdividef(1.0f, 1.0f + __expf(-g)) * u; }
+__device__ __forceinline__ float silu_mul(float g, float u) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  return g * r * u;
+}
+
+// 16 TMEM lanes x 32 columns: thread i gets, for each group j of eight columns,
+// lane i / 4, columns 8 j + 2 (i % 4) and the next (v[4 j], v[4 j + 1]) and the
+// same of lane i / 4 + 8 (v[4 j + 2], v[4 j + 3]).
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+// A 32-lane x 32-column piece of an accumulator: lanes 0-15 in v[0..15], lanes
+// 16-31 in v[16..31].
+__device__ __forceinline__ void load_piece(uint32_t taddr, uint32_t (&v)[32]) {
+  tmem_ld_16x256b_x4(taddr, v);
+  tmem_ld_16x256b_x4(taddr + (16u << 16), v + 16);
+}
+
+// Four 8 x 8 bf16 matrices to shared memory, transposed: thread i's pairs lie
+// along a matrix row's neighbours 2 (i % 4), row i / 4; the address of row r of
+// matrix m comes from thread 8 m + r.
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
+               "r"(c), "r"(d)
+               : "memory");
+}
+
+// Writes a piece as bf16 to `out` (shared, [32 rows][kPitch]): packed[4 j + q]
+// holds the pair of columns 8 j + 2 (i % 4) of output column q * 8 + i / 4, so
+// matrix (j, q) lands at rows 8 j.., columns 8 q...
+__device__ __forceinline__ void stage_piece(uint32_t out, const uint32_t (&packed)[16], int lane) {
+  const uint32_t at = out + (lane & 7) * kPitch + (lane >> 3) * 16;  // thread 8 m + r: row r, columns 8 m
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    stmatrix_x4_trans(at + 8 * j * kPitch, packed[4 * j], packed[4 * j + 1], packed[4 * j + 2], packed[4 * j + 3]);
+}
 
 template <int kMode>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -345,10 +403,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else {
     // ---------------------------------------------------------- epilogue
-    // thread = TMEM lane = output column; the two warps of a lane quarter take
-    // the window's 32-row chunks in turn
+    // TMEM lane = output column, TMEM column = row of the window; the warps of
+    // a lane quarter take the window's 32-row pieces in turn
     const int q = warp & 3;
-    const int half = (warp - 2) / 4;
+    const int turn = (warp - kFirstEpi) / 4;
+    uint8_t* out = smem + kOutOff + (warp - kFirstEpi) * kStageOutBytes;
+    const uint32_t out_addr = smem_u32(out);
+    const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16);
     uint32_t tcount = 0;
     for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
       const Win c = decode(tile, NT, E, s_win, s_offp, s_cnt, max_rows);
@@ -359,79 +420,87 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const int n0 = c.j * (kMode == kDown ? 256 : 128);
       const bool two = kMode != kDown || n0 + 128 < N_out;
-      const int col = n0 + q * 32 + lane;
-      const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16);
-#pragma unroll 1
-      for (int ch = half; ch * 32 < c.rows; ch += 2) {
-        const int64_t r0 = c.row0 + ch * 32;
-        const int left = min(32, c.rows - ch * 32);
-        uint32_t v0[32], v1[32];
-        tmem_ld_32x32b_x32(tb + ch * 32, v0);
-        if (two) tmem_ld_32x32b_x32(tb + kAcc1 + ch * 32, v1);
+      const int pieces = (c.rows + 31) / 32;
+      const int mine = pieces > turn ? (pieces - turn + kEpiSplit - 1) / kEpiSplit : 0;  // 0, 1 or 2
+      uint32_t v0[32], v1[32];
+      uint32_t out0[2][16], out1[16];  // finished pieces (down: of each accumulator)
+      auto fetch = [&](int p) {
+        load_piece(tb + (turn + kEpiSplit * p) * 32, v0);
+        if (two) load_piece(tb + kAcc1 + (turn + kEpiSplit * p) * 32, v1);
         tmem_ld_wait();
-        if constexpr (kMode == kUpMxfp4) {
-          // a warp's 32 columns are one block of every row's scales: per row
-          // the block's maximum by a warp reduction of h rounded to bf16 (the
-          // codes are those of quantising the bf16 h), then eight rows' codes
-          // change places with eight columns' by three exchanges
-          uint32_t my_scale = 0u;
+      };
+      auto release = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(tempty);
+      };
+      // v0, v1 to finished bf16; entry 4 j + x: output column x * 8 + lane / 4
+      // (lanes 0-15 of the piece for x < 2), columns 8 j + 2 (lane % 4)
+      auto finish = [&](uint32_t (&a)[16], uint32_t (&b)[16]) {
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            uint32_t codes = 0u;
+        for (int j = 0; j < 4; ++j) {
 #pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-              float y[2];
-#pragma unroll
-              for (int p = 0; p < 2; ++p) {
-                const int t = 8 * g + i + p;
-                const float h = silu_mul(__uint_as_float(v0[t]), __uint_as_float(v1[t]));
-                const uint32_t hb = pack_bf16x2(h, 0.0f) & 0xFFFFu;
-                const uint32_t s = scale_byte(__reduce_max_sync(0xffffffffu, hb & 0x7FFFu));
-                if (lane == t) my_scale = s;
-                y[p] = s == kScaleNan ? 0.0f : bf16lo_to_f32(hb) * scale_inverse(s);
-              }
-              uint32_t two_codes;
-              asm("{\n\t.reg .b8 b;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %2, %1;\n\tcvt.u32.u8 %0, b;\n\t}"
-                  : "=r"(two_codes)
-                  : "f"(y[0]), "f"(y[1]));
-              codes |= two_codes << (4 * i);
-            }
-            // codes: nibble i = row 8g + i of this column; transposed among
-            // groups of eight lanes: nibble i = column i of row 8g + lane % 8
-            uint32_t o = __shfl_xor_sync(0xffffffffu, codes, 4);
-            codes = (lane & 4) ? ((codes & 0xFFFF0000u) | (o >> 16)) : ((codes & 0x0000FFFFu) | (o << 16));
-            o = __shfl_xor_sync(0xffffffffu, codes, 2);
-            codes = (lane & 2) ? ((codes & 0xFF00FF00u) | ((o >> 8) & 0x00FF00FFu))
-                               : ((codes & 0x00FF00FFu) | ((o << 8) & 0xFF00FF00u));
-            o = __shfl_xor_sync(0xffffffffu, codes, 1);
-            codes = (lane & 1) ? ((codes & 0xF0F0F0F0u) | ((o >> 4) & 0x0F0F0F0Fu))
-                               : ((codes & 0x0F0F0F0Fu) | ((o << 4) & 0xF0F0F0F0u));
-            const int t = 8 * g + (lane & 7);
-            if (t < left)
-              *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(D) +
-                                           ((r0 + t) * N_out + n0 + q * 32 + (lane >> 3) * 8) / 2) = codes;
-          }
-          if (lane < left)
-            Dsf[scale_word_offset(r0 + lane, n0 / 128, N_out / 128) + q] = static_cast<uint8_t>(my_scale);
-        } else {
-          uint16_t* dst = static_cast<uint16_t*>(D) + r0 * N_out + col;
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            if (i >= left) break;  // uniform across the warp
-            const float a = __uint_as_float(v0[i]), b = __uint_as_float(v1[i]);
-            if constexpr (kMode == kUpBf16) {
-              dst[static_cast<int64_t>(i) * N_out] = static_cast<uint16_t>(pack_bf16x2(silu_mul(a, b), 0.0f));
+          for (int x = 0; x < 4; ++x) {
+            const int i = (x >> 1) * 16 + 4 * j + (x & 1) * 2;
+            const float a0 = __uint_as_float(v0[i]), a1 = __uint_as_float(v0[i + 1]);
+            const float b0 = __uint_as_float(v1[i]), b1 = __uint_as_float(v1[i + 1]);
+            if constexpr (kMode == kDown) {
+              a[4 * j + x] = pack_bf16x2(a0, a1);
+              b[4 * j + x] = pack_bf16x2(b0, b1);
             } else {
-              const uint32_t p = pack_bf16x2(a, b);
-              dst[static_cast<int64_t>(i) * N_out] = static_cast<uint16_t>(p);
-              if (two) dst[static_cast<int64_t>(i) * N_out + 128] = static_cast<uint16_t>(p >> 16);
+              a[4 * j + x] = pack_bf16x2(silu_mul(a0, b0), silu_mul(a1, b1));
             }
           }
         }
+      };
+      // a finished piece of output columns from `col0` to the window's rows,
+      // through shared memory: four lanes a row, eight rows at a time, eight
+      // columns per lane
+      auto store = [&](int p, int col0, const uint32_t (&a)[16]) {
+        const int64_t r0 = c.row0 + (turn + kEpiSplit * p) * 32;
+        const int left = c.rows - (turn + kEpiSplit * p) * 32;
+        __syncwarp();  // the previous piece has been read
+        stage_piece(out_addr, a, lane);
+        __syncwarp();
+        const int col = col0 + q * 32 + (lane & 3) * 8;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int t = 8 * i + (lane >> 2);
+          const uint4 h = *reinterpret_cast<const uint4*>(out + t * kPitch + (lane & 3) * 16);
+          if constexpr (kMode == kUpMxfp4) {
+            // the 32 columns are one block of the row: the codes are those of
+            // quantising the bf16 h
+            const uint32_t s = block_scale_of_quad(h);
+            if (t < left) {
+              *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(D) + ((r0 + t) * N_out + col) / 2) =
+                  quantize_bf16x8(h, s);
+              if ((lane & 3) == 0)
+                Dsf[scale_word_offset(r0 + t, col0 / 128, N_out / 128) + q] = static_cast<uint8_t>(s);
+            }
+          } else {
+            if (t < left) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(D) + (r0 + t) * N_out + col) = h;
+          }
+        }
+      };
+      auto store_all = [&](int p, const uint32_t (&a)[16], const uint32_t (&b)[16]) {
+        store(p, n0, a);
+        if constexpr (kMode == kDown) {
+          if (two) store(p, n0 + 128, b);
+        }
+      };
+      if (mine == 0) {
+        release();
+      } else {
+        fetch(0);
+        if (mine == 2) {
+          finish(out0[0], out0[1]);
+          fetch(1);
+        }
+        release();  // the accumulators are this warp's no more
+        if (mine == 2) store_all(0, out0[0], out0[1]);
+        finish(out0[0], out1);
+        store_all(mine - 1, out0[0], out1);
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(tempty);
     }
   }
 
