@@ -212,8 +212,9 @@ Mxfp4Layout mxfp4_layout(const moe_shape& s) {
 bool mxfp4_maps(const moe_shape& s, int64_t K, int64_t N, const uint8_t* rows, const uint8_t* w0, const uint8_t* w1,
                 Mxfp4Maps* m) {
   const uint64_t kb = static_cast<uint64_t>(K) / 2, wr = static_cast<uint64_t>(s.E) * static_cast<uint64_t>(N);
-  return encode_bytes_2d(&m->t, rows, static_cast<uint64_t>(max_rows_of(s)), kb, 32) &&
-         encode_bytes_2d(&m->w0, w0, wr, kb, 128) && encode_bytes_2d(&m->w1, w1, wr, kb, 128);
+  for (int i = 0; i < 4; ++i)
+    if (!encode_bytes_2d(&m->t[i], rows, static_cast<uint64_t>(max_rows_of(s)), kb, mxfp4_token_box(i))) return false;
+  return encode_bytes_2d(&m->w0, w0, wr, kb, 128) && encode_bytes_2d(&m->w1, w1, wr, kb, 128);
 }
 
 }  // namespace
@@ -570,7 +571,8 @@ moe_status moe_grouped_gemm_up_mxfp4(const moe_shape* shape, const uint8_t* x_co
   Mxfp4Maps m;
   if (!mxfp4_maps(*shape, shape->H, shape->I, x_codes, wg_codes, wu_codes, &m)) return MOE_ERR_CUDA;
   return cuda_status(
-      launch_mxfp4_up(*shape, m, x_scales, wg_scales, wu_scales, h, off_pad, counts, ws_status(ws), sms, s));
+      launch_mxfp4_up(*shape, m, x_scales, wg_scales, wu_scales, h, off_pad, counts, ws_status(ws), ws_sched_up(ws),
+                      sms, s));
 }
 
 moe_status moe_grouped_gemm_down_mxfp4(const moe_shape* shape, const uint8_t* h_codes, const uint8_t* h_scales,
@@ -587,7 +589,8 @@ moe_status moe_grouped_gemm_down_mxfp4(const moe_shape* shape, const uint8_t* h_
   if (st != MOE_OK) return st;
   Mxfp4Maps m;
   if (!mxfp4_maps(*shape, shape->I, shape->H, h_codes, wd_codes, wd_codes, &m)) return MOE_ERR_CUDA;
-  return cuda_status(launch_mxfp4_down(*shape, m, h_scales, wd_scales, Y, off_pad, counts, ws_status(ws), sms, s));
+  return cuda_status(launch_mxfp4_down(*shape, m, h_scales, wd_scales, Y, off_pad, counts, ws_status(ws),
+                                       ws_sched_down(ws), sms, s));
 }
 
 moe_status moe_mxfp4_workspace_size(const moe_shape* shape, size_t* bytes) {
@@ -629,10 +632,10 @@ moe_status moe_forward_mxfp4(const moe_shape* shape, const float* logits, const 
   if (launch_quantize_permute(sh, X, i32(L.scatter_idx), b + L.x_codes, b + L.x_scales, status, s) != cudaSuccess)
     return MOE_ERR_CUDA;
   if (launch_mxfp4_up_quantized(sh, up, b + L.x_scales, wg_scales, wu_scales, b + L.h_codes, b + L.h_scales,
-                                i32(L.off_pad), i32(L.counts), status, sms, s) != cudaSuccess)
+                                i32(L.off_pad), i32(L.counts), status, ws_sched_up(ws), sms, s) != cudaSuccess)
     return MOE_ERR_CUDA;
-  if (launch_mxfp4_down(sh, down, b + L.h_scales, wd_scales, Y, i32(L.off_pad), i32(L.counts), status, sms, s) !=
-      cudaSuccess)
+  if (launch_mxfp4_down(sh, down, b + L.h_scales, wd_scales, Y, i32(L.off_pad), i32(L.counts), status,
+                        ws_sched_down(ws), sms, s) != cudaSuccess)
     return MOE_ERR_CUDA;
   return cuda_status(launch_combine(sh, Y, i32(L.scatter_idx), topk_w, out, status, sms, s));
 }

@@ -108,6 +108,9 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
 // The MXFP4 products cut an expert's c rows into ceil(c / kMxfp4WindowRows)
 // windows that start at multiples of 64 rows.
 constexpr int kMxfp4WindowRows = 192;
+// Rows of the boxes their rows are loaded in (the smallest that holds the
+// window is taken).
+__host__ __device__ constexpr int mxfp4_token_box(int i) { return i == 3 ? kMxfp4WindowRows : 32 << i; }
 
 // Launchers (asynchronous; return cudaGetLastError()).
 // route_counter: a uint32 that is zero between calls (the call leaves it so).
@@ -169,24 +172,26 @@ cudaError_t launch_quantize_weights(const uint16_t* w, int E, int64_t K, int64_t
 cudaError_t launch_quantize_permute(const moe_shape& s, const uint16_t* X, const int32_t* scatter_idx, uint8_t* codes,
                                     uint8_t* scales, uint32_t* status, cudaStream_t st);
 
+// sched: a product's tile counter and done counter, zero between launches
+// (ws_sched_up, ws_sched_down).
 // The grouped products on MXFP4 operands: code matrices as 128-byte-wide boxes.
 struct Mxfp4Maps {
-  CUtensorMap t;   // rows [max_rows][K/2], box 32 rows
+  CUtensorMap t[4];  // rows [max_rows][K/2], boxes of mxfp4_token_box(i) rows
   CUtensorMap w0;  // weights [E*N][K/2] (gate, or down), box 128 rows
   CUtensorMap w1;  // the up weights (down: a copy of w0)
 };
 cudaError_t launch_mxfp4_up(const moe_shape& s, const Mxfp4Maps& m, const uint8_t* x_scales, const uint8_t* wg_scales,
                             const uint8_t* wu_scales, uint16_t* h, const int32_t* off_pad, const int32_t* counts,
-                            uint32_t* status, int num_sms, cudaStream_t st);
+                            uint32_t* status, uint32_t* sched, int num_sms, cudaStream_t st);
 // the same with h quantised to MXFP4 in the epilogue (as launch_quantize_rows
 // would from the bf16 h)
 cudaError_t launch_mxfp4_up_quantized(const moe_shape& s, const Mxfp4Maps& m, const uint8_t* x_scales,
                                       const uint8_t* wg_scales, const uint8_t* wu_scales, uint8_t* h_codes,
                                       uint8_t* h_scales, const int32_t* off_pad, const int32_t* counts,
-                                      uint32_t* status, int num_sms, cudaStream_t st);
+                                      uint32_t* status, uint32_t* sched, int num_sms, cudaStream_t st);
 cudaError_t launch_mxfp4_down(const moe_shape& s, const Mxfp4Maps& m, const uint8_t* h_scales,
                               const uint8_t* wd_scales, uint16_t* Y, const int32_t* off_pad, const int32_t* counts,
-                              uint32_t* status, int num_sms, cudaStream_t st);
+                              uint32_t* status, uint32_t* sched, int num_sms, cudaStream_t st);
 
 // Balance loss.  partials: the workspace region past its first 256 bytes
 // (balance_partial_bytes); counter: a uint32 that is zero between calls.

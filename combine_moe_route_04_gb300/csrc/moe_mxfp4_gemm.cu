@@ -22,8 +22,9 @@
 // TMEM back; the rest of the arithmetic and all stores run under the next
 // tile's MMAs.
 //
-// Roles of the 14 warps: warp 0 loads (per 256-deep stage two 128 x 128-byte
-// weight boxes, the window's rows in boxes of 32, and the scale tiles), warp 1
+// Roles of the 14 warps: warp 0 loads (per 256-deep stage two boxes of 128
+// weight rows x 128 bytes, the window's rows in one box, and the scale tiles),
+// warp 1
 // copies a stage's scales to TMEM and issues its MMAs, warps 2-13 drain the
 // accumulators.  Every wait is bounded as in the bf16 GEMMs.
 #include <cstdint>
@@ -37,24 +38,25 @@ namespace {
 
 constexpr int kMaxExperts = 256;
 constexpr int kTok = kMxfp4WindowRows;          // rows per window at most
-constexpr int kStageK = 256;                    // reduction elements per stage (128 bytes of codes)
+constexpr int kStageK = 256;                    // reduction elements per stage
+constexpr int kAtoms = kStageK / 128;           // 128-deep scale tiles in a stage
 constexpr int kStages = 3;
-constexpr int kWBytes = 128 * 128;              // one block of 128 weight rows
-constexpr int kTBox = 32;                       // rows per token box
-constexpr int kTBoxBytes = kTBox * 128;
-constexpr int kTBytes = kTok * 128;
-constexpr int kSfBytes = 2 * 512;               // scale tiles of one 128-row block, 256 deep
+constexpr int kRowBytes = kStageK / 2;          // codes of a row in a stage (128-byte swizzle)
+constexpr int kWBytes = 128 * kRowBytes;        // one block of 128 weight rows
+constexpr int kTBytes = kTok * kRowBytes;
+constexpr int kSfBytes = 512 * kAtoms;          // scale tiles of 128 rows
 constexpr int kOffT = 2 * kWBytes;
 constexpr int kOffSf = kOffT + kTBytes;         // scales: weights 0, weights 1, rows (two 128-row blocks)
 constexpr int kStageBytes = kOffSf + 4 * kSfBytes;
 static_assert(kStageBytes % 1024 == 0, "stages start on swizzle atoms");
+static_assert(kTok % 64 == 0, "windows start at an even column of their scale tile");
 
 constexpr int kEpiWarps = 12;
 constexpr int kEpiSplit = kEpiWarps / 4;         // warps sharing a lane quarter
 static_assert(2 * kEpiSplit * 32 == kTok, "two 32-row pieces of a window per warp at most");
-// staging of a piece, transposed: 32 rows of 32 columns (64 bytes, padded so
-// that eight rows start on different banks)
-constexpr int kPitch = 80;
+// staging of 32 rows x 128 columns, written by the four warps of a turn
+// (padded so that eight rows start on different banks)
+constexpr int kPitch = 256 + 16;
 constexpr int kStageOutBytes = 32 * kPitch;
 constexpr int kFirstEpi = 2;
 constexpr int kThreads = (kFirstEpi + kEpiWarps) * 32;
@@ -62,16 +64,18 @@ constexpr int kThreads = (kFirstEpi + kEpiWarps) * 32;
 // TMEM columns: accumulators, then 32 columns of scales per stage
 constexpr uint32_t kAcc1 = 192;
 constexpr uint32_t kSfCol = 384;
-constexpr uint32_t kSfStageCols = 32;           // weights 0: +0, weights 1: +8, rows: +16 (8 per 128 k)
+constexpr uint32_t kSfStageCols = 16 * kAtoms;  // per 128 k: weights 0 +0, weights 1 +4, rows +8
 static_assert(kSfCol + kStages * kSfStageCols <= 512, "TMEM columns");
 
 constexpr int kBarOff = kStages * kStageBytes;
-constexpr int kNumBars = 2 * kStages + 3;
-constexpr int kWinOff = kBarOff + kNumBars * 8 + 8;
+constexpr int kTileRing = 4;                    // tile indices on their way from the producer
+constexpr int kNumBars = 2 * kStages + 3 + 2 * kTileRing;
+constexpr int kTileOff = kBarOff + kNumBars * 8 + 8;
+constexpr int kWinOff = kTileOff + kTileRing * 4;
 constexpr int kCntOff = kWinOff + (kMaxExperts + 1) * 4;
 constexpr int kOffpOff = kCntOff + kMaxExperts * 4;
 constexpr int kOutOff = (kOffpOff + (kMaxExperts + 1) * 4 + 15) / 16 * 16;
-constexpr int kSmemBytes = kOutOff + kEpiWarps * kStageOutBytes;
+constexpr int kSmemBytes = kOutOff + kEpiSplit * kStageOutBytes;
 constexpr int kSmemAlloc = kSmemBytes + 1024;
 static_assert(kSmemAlloc <= 232448, "shared memory budget");
 
@@ -121,7 +125,8 @@ struct Win {
 };
 
 // Tile t: expert e (windows off[e] .. off[e+1]), then column tile j, then the
-// window, so that the windows sharing a weight tile are neighbours.
+// window, so that the windows sharing a weight tile are neighbours.  All of an
+// expert's windows but the last have kTok rows.
 __device__ __forceinline__ Win decode(int tile, int NT, int E, const int32_t* off, const int32_t* offp,
                                       const int32_t* cnt, int64_t max_rows) {
   Win c{0, 0, 0, 0, false};
@@ -136,16 +141,42 @@ __device__ __forceinline__ Win decode(int tile, int NT, int E, const int32_t* of
   const int local = tile - NT * off[lo];
   if (nw <= 0 || local < 0 || local >= NT * nw) return c;
   const int w = local % nw;
-  const int n = cnt[lo];
-  const int per = ((n + nw - 1) / nw + 63) / 64 * 64;
   c.e = lo;
   c.j = local / nw;
-  c.row0 = offp[lo] + per * w;
-  c.rows = min(per, n - per * w);
+  c.row0 = offp[lo] + kTok * w;
+  c.rows = min(kTok, cnt[lo] - kTok * w);
   const int pad_end = offp[lo + 1];
   c.ok = c.rows > 0 && c.rows <= kTok && c.row0 >= 0 && (c.row0 & 63) == 0 && c.row0 + c.rows <= pad_end &&
          pad_end <= max_rows && (pad_end & 127) == 0;
   return c;
+}
+
+// Tiles are drawn from a counter in the workspace, in order (CTA b starts on
+// tile b): windows differ in rows, and CTAs that got short ones take more.  The
+// producer publishes each index to the other roles through a ring in shared
+// memory; the CTA that stops drawing last clears the counter for the next
+// launch.
+struct TileRing {
+  uint64_t* full;         // [kTileRing] one arrival (the producer)
+  uint64_t* empty;        // [kTileRing] kReaders arrivals
+  volatile int32_t* idx;  // [kTileRing]
+};
+constexpr int kReaders = 1 + kEpiWarps;  // the MMA lane and one lane of each epilogue warp
+
+__device__ __forceinline__ bool ring_put(const TileRing& r, uint32_t n, int tile, volatile int* abort,
+                                         uint32_t* status) {
+  const uint32_t slot = n % kTileRing;
+  if (!mbar_wait(&r.empty[slot], ((n / kTileRing) & 1u) ^ 1u, abort, status)) return false;
+  r.idx[slot] = tile;
+  mbar_arrive(&r.full[slot]);
+  return true;
+}
+
+// The n-th tile of this CTA, -1 when the wait gave up; the caller arrives on
+// empty[n % kTileRing] afterwards.
+__device__ __forceinline__ int ring_take(const TileRing& r, uint32_t n, volatile int* abort, uint32_t* status) {
+  const uint32_t slot = n % kTileRing;
+  return mbar_wait(&r.full[slot], (n / kTileRing) & 1u, abort, status) ? r.idx[slot] : -1;
 }
 
 __device__ __forceinline__ bool vote_any(bool flag) {
@@ -211,12 +242,11 @@ __device__ __forceinline__ void stage_piece(uint32_t out, const uint32_t (&packe
 
 template <int kMode>
 __global__ void __launch_bounds__(kThreads, 1)
-    mxfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmT, const __grid_constant__ CUtensorMap tmW0,
-                      const __grid_constant__ CUtensorMap tmW1, const uint8_t* __restrict__ sfT,
+    mxfp4_gemm_kernel(const __grid_constant__ Mxfp4Maps maps, const uint8_t* __restrict__ sfT,
                       const uint8_t* __restrict__ sfW0, const uint8_t* __restrict__ sfW1, void* __restrict__ D,
                       uint8_t* __restrict__ Dsf, const int32_t* __restrict__ off_pad,
                       const int32_t* __restrict__ counts, int E, int K, int N_out, int NT, int64_t max_rows,
-                      uint32_t* __restrict__ status) {
+                      uint32_t* __restrict__ status, uint32_t* __restrict__ sched) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + kBarOff);
@@ -224,7 +254,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* tfull = empty + kStages;
   uint64_t* tempty = tfull + 1;
   uint64_t* drain = tfull + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tfull + 3);
+  const TileRing ring{tfull + 3, tfull + 3 + kTileRing, reinterpret_cast<volatile int32_t*>(smem + kTileOff)};
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tfull + 3 + 2 * kTileRing);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int32_t* s_win = reinterpret_cast<int32_t*>(smem + kWinOff);
   int32_t* s_cnt = reinterpret_cast<int32_t*>(smem + kCntOff);
@@ -241,11 +272,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(tfull, 1);
     mbar_init(tempty, kEpiWarps);
     mbar_init(drain, 1);
+    for (int i = 0; i < kTileRing; ++i) {
+      mbar_init(&ring.full[i], 1);
+      mbar_init(&ring.empty[i], kReaders);
+    }
     *abort_flag = 0;
     fence_mbarrier_init();
-    prefetch_tmap(&tmT);
-    prefetch_tmap(&tmW0);
-    prefetch_tmap(&tmW1);
+    prefetch_tmap(&maps.t[0]);
+    prefetch_tmap(&maps.w0);
+    prefetch_tmap(&maps.w1);
   }
   if (warp == 1) {
     tmem_alloc(tmem_slot, 512);
@@ -291,52 +326,65 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const int total = NT * s_win[E];
-  const int KS = (K + kStageK - 1) / kStageK;
-  const int64_t kb128 = K / 128;
+  const int KT = K / 128;  // scale tiles along the reduction
+  const int KS = (KT + kAtoms - 1) / kAtoms;
 
   if (warp == 0) {
     // ---------------------------------------------------------- loads
     if (elect_one_sync()) {
       const uint64_t pol_t = policy_evict_last();
       uint32_t it = 0;
-      bool stop = false;
-      for (int tile = blockIdx.x; !stop && tile < total; tile += gridDim.x) {
+      int tile = blockIdx.x;
+      bool stop = !ring_put(ring, 0, tile, abort_flag, status);
+      for (uint32_t n = 0; !stop && tile < total; ++n) {
+        const uint32_t drawn = atomicAdd(sched, 1u);  // the next tile: needed after this one's loads
         const Win c = decode(tile, NT, E, s_win, s_offp, s_cnt, max_rows);
-        if (!c.ok) {
-          record_status(status, kStatusBounds);
-          continue;
-        }
+        if (!c.ok) record_status(status, kStatusBounds);
         // a one-window expert reads this weight tile once
         const uint64_t pol_w = s_win[c.e + 1] - s_win[c.e] == 1 ? policy_evict_first() : policy_evict_normal();
         const int n0 = c.j * (kMode == kDown ? 256 : 128);
         const bool two = kMode != kDown || n0 + 128 < N_out;  // the second weight block exists
         const int w_row = c.e * N_out + n0;                   // E * N_out < 2^31
-        const int boxes = (c.rows + kTBox - 1) / kTBox;
-        const int64_t t_block = c.row0 >> 7;
+        // the smallest box that holds the window (rows past it are not used)
+        const int pick = c.rows <= 32 ? 0 : c.rows <= 64 ? 1 : c.rows <= 128 ? 2 : 3;
+        const int box = mxfp4_token_box(pick);
         const bool t_two = (c.row0 & 127) + c.rows > 128;     // the window's rows span two scale blocks
-        for (int ks = 0; ks < KS; ++ks, ++it) {
+        for (int ks = 0; c.ok && ks < KS; ++ks, ++it) {
           const uint32_t s = it % kStages;
           if (!mbar_wait(&empty[s], ((it / kStages) & 1u) ^ 1u, abort_flag, status)) {
             stop = true;
             break;
           }
-          const int kt = min(2, static_cast<int>(kb128) - 2 * ks);  // 128-deep scale tiles in this stage
+          const int kt = min(kAtoms, KT - kAtoms * ks);  // scale tiles in this stage
           const uint32_t sfb = 512u * kt;
-          mbar_arrive_expect_tx(&full[s], (two ? 2u : 1u) * (kWBytes + sfb) + boxes * kTBoxBytes + (t_two ? 2u : 1u) * sfb);
+          mbar_arrive_expect_tx(&full[s],
+                                (two ? 2u : 1u) * (kWBytes + sfb) + box * kRowBytes + (t_two ? 2u : 1u) * sfb);
           uint8_t* st = smem + s * kStageBytes;
-          const int kx = ks * 128;  // bytes
-          tma_load_2d(st, &tmW0, &full[s], kx, w_row, pol_w);
-          if (two) tma_load_2d(st + kWBytes, &tmW1, &full[s], kx, kMode == kDown ? w_row + 128 : w_row, pol_w);
-          for (int b = 0; b < boxes; ++b)
-            tma_load_2d(st + kOffT + b * kTBoxBytes, &tmT, &full[s], kx, c.row0 + b * kTBox, pol_t);
+          const int kx = ks * kRowBytes;
+          tma_load_2d(st, &maps.w0, &full[s], kx, w_row, pol_w);
+          if (two)
+            tma_load_2d(st + kWBytes, kMode == kDown ? &maps.w0 : &maps.w1, &full[s], kx,
+                        kMode == kDown ? w_row + 128 : w_row, pol_w);
+          tma_load_2d(st + kOffT, &maps.t[pick], &full[s], kx, c.row0, pol_t);
           uint8_t* sf = st + kOffSf;
-          const int64_t wsf = ((w_row >> 7) * kb128 + 2 * ks) * 512;
-          const int64_t tsf = (t_block * kb128 + 2 * ks) * 512;
+          const int64_t wsf = (static_cast<int64_t>(w_row >> 7) * KT + kAtoms * ks) * 512;
+          const int64_t tsf = (static_cast<int64_t>(c.row0 >> 7) * KT + kAtoms * ks) * 512;
           bulk_load(sf, sfW0 + wsf, sfb, &full[s]);
-          if (two) bulk_load(sf + kSfBytes, kMode == kDown ? sfW0 + wsf + kb128 * 512 : sfW1 + wsf, sfb, &full[s]);
+          if (two) bulk_load(sf + kSfBytes, kMode == kDown ? sfW0 + wsf + KT * 512 : sfW1 + wsf, sfb, &full[s]);
           bulk_load(sf + 2 * kSfBytes, sfT + tsf, sfb, &full[s]);
-          if (t_two) bulk_load(sf + 3 * kSfBytes, sfT + tsf + kb128 * 512, sfb, &full[s]);
+          if (t_two) bulk_load(sf + 3 * kSfBytes, sfT + tsf + KT * 512, sfb, &full[s]);
         }
+        if (stop) break;
+        // a cleared counter gives at most total + grid - 1 here
+        const uint64_t next = static_cast<uint64_t>(gridDim.x) + drawn;
+        tile = next < static_cast<uint64_t>(total) + gridDim.x ? static_cast<int>(next) : total;
+        if (static_cast<uint64_t>(tile) != next) record_status(status, kStatusBounds);
+        stop = !ring_put(ring, n + 1, tile, abort_flag, status);
+      }
+      __threadfence();
+      if (atomicAdd(sched + 1, 1u) == gridDim.x - 1) {  // every CTA has drawn its last index
+        atomicExch(sched, 0u);
+        atomicExch(sched + 1, 0u);
       }
       // every stage used must be consumed before the CTA may exit
       const uint32_t nst = it < kStages ? it : kStages;
@@ -353,7 +401,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t it = 0;
       uint32_t tcount = 0;
       bool stop = false;
-      for (int tile = blockIdx.x; !stop && tile < total; tile += gridDim.x) {
+      for (uint32_t n = 0; !stop; ++n) {
+        const int tile = ring_take(ring, n, abort_flag, status);
+        if (tile < 0 || tile >= total) break;
+        mbar_arrive(&ring.empty[n % kTileRing]);
         const Win c = decode(tile, NT, E, s_win, s_offp, s_cnt, max_rows);
         if (!c.ok) continue;
         const bool two = kMode != kDown || c.j * 256 + 128 < N_out;
@@ -370,25 +421,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           tc_fence_after();
-          const int kt = min(2, static_cast<int>(kb128) - 2 * ks);
           const uint32_t st = smem_u32(smem + s * kStageBytes);
           const uint32_t sf = st + kOffSf;
           const uint32_t tsf = tmem + kSfCol + s * kSfStageCols;  // this stage's own columns
+          const int kt = min(kAtoms, KT - kAtoms * ks);
           for (int a = 0; a < kt; ++a) {
-            sf_to_tmem(tsf + 4 * a, sf + 512 * a);
-            if (two) sf_to_tmem(tsf + 8 + 4 * a, sf + kSfBytes + 512 * a);
-            sf_to_tmem(tsf + 16 + 8 * a, sf + 2 * kSfBytes + 512 * a);
-            if (t_two) sf_to_tmem(tsf + 16 + 8 * a + 4, sf + 3 * kSfBytes + 512 * a);
+            sf_to_tmem(tsf + 16 * a, sf + 512 * a);
+            if (two) sf_to_tmem(tsf + 16 * a + 4, sf + kSfBytes + 512 * a);
+            sf_to_tmem(tsf + 16 * a + 8, sf + 2 * kSfBytes + 512 * a);
+            if (t_two) sf_to_tmem(tsf + 16 * a + 12, sf + 3 * kSfBytes + 512 * a);
           }
-          for (int kk = 0; kk < 2 * kt; ++kk) {
-            const uint32_t a = kk >> 1;
-            const uint64_t bd = smem_desc(st + kOffT + kk * 32, 16, 1024, kSwizzle128B);
-            const uint32_t sfb = tsf + 16 + 8 * a + t_col;
+          for (int kk = 0; kk < 2 * kt; ++kk) {  // 64 deep each
+            const uint64_t bd = smem_desc(st + kOffT + kk * 32, 16, 8 * kRowBytes, kSwizzle128B);
+            const uint32_t sfc = tsf + 16 * (kk >> 1);
             const uint32_t acc = (ks | kk) != 0 ? 1u : 0u;
-            mma_mxf4(tmem, smem_desc(st + kk * 32, 16, 1024, kSwizzle128B), bd, id[kk & 1], tsf + 4 * a, sfb, acc);
+            mma_mxf4(tmem, smem_desc(st + kk * 32, 16, 8 * kRowBytes, kSwizzle128B), bd, id[kk & 1], sfc,
+                     sfc + 8 + t_col, acc);
             if (two)
-              mma_mxf4(tmem + kAcc1, smem_desc(st + kWBytes + kk * 32, 16, 1024, kSwizzle128B), bd, id[kk & 1],
-                       tsf + 8 + 4 * a, sfb, acc);
+              mma_mxf4(tmem + kAcc1, smem_desc(st + kWBytes + kk * 32, 16, 8 * kRowBytes, kSwizzle128B), bd,
+                       id[kk & 1], sfc + 4, sfc + 8 + t_col, acc);
           }
           tc_commit(&empty[s]);
         }
@@ -407,15 +458,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     // a lane quarter take the window's 32-row pieces in turn
     const int q = warp & 3;
     const int turn = (warp - kFirstEpi) / 4;
-    uint8_t* out = smem + kOutOff + (warp - kFirstEpi) * kStageOutBytes;
-    const uint32_t out_addr = smem_u32(out);
+    uint8_t* out = smem + kOutOff + turn * kStageOutBytes;
+    const uint32_t out_addr = smem_u32(out) + q * 64;  // this warp's columns
     const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16);
     uint32_t tcount = 0;
-    for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
-      const Win c = decode(tile, NT, E, s_win, s_offp, s_cnt, max_rows);
+    for (uint32_t n = 0;; ++n) {
+      const int tile = ring_take(ring, n, abort_flag, status);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ring.empty[n % kTileRing]);
+      bool ok = tile >= 0;
+      const Win c = decode(ok && tile < total ? tile : 0, NT, E, s_win, s_offp, s_cnt, max_rows);
+      if (ok && tile < total && c.ok) ok = mbar_wait(tfull, tcount & 1u, abort_flag, status);
+      if (vote_any(!ok)) break;  // every warp gives up together (they share barriers)
+      if (tile >= total) break;
       if (!c.ok) continue;
-      const bool ok = mbar_wait(tfull, tcount & 1u, abort_flag, status);
-      if (vote_any(!ok)) break;
       ++tcount;
       tc_fence_after();
       const int n0 = c.j * (kMode == kDown ? 256 : 128);
@@ -453,29 +509,30 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       };
-      // a finished piece of output columns from `col0` to the window's rows,
-      // through shared memory: four lanes a row, eight rows at a time, eight
-      // columns per lane
+      // a finished piece of the 128 output columns from `col0` to the window's
+      // rows: the turn's four warps put it together in shared memory, then
+      // write eight rows each, sixteen lanes (256 bytes) a row
       auto store = [&](int p, int col0, const uint32_t (&a)[16]) {
         const int64_t r0 = c.row0 + (turn + kEpiSplit * p) * 32;
         const int left = c.rows - (turn + kEpiSplit * p) * 32;
-        __syncwarp();  // the previous piece has been read
+        named_barrier_sync(3 + turn, 128);  // the previous piece has been read
         stage_piece(out_addr, a, lane);
-        __syncwarp();
-        const int col = col0 + q * 32 + (lane & 3) * 8;
+        named_barrier_sync(3 + turn, 128);
+        const int col = col0 + (lane & 15) * 8;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int t = 8 * i + (lane >> 2);
-          const uint4 h = *reinterpret_cast<const uint4*>(out + t * kPitch + (lane & 3) * 16);
+          const int t = 8 * q + 2 * i + (lane >> 4);
+          const uint4 h = *reinterpret_cast<const uint4*>(out + t * kPitch + (lane & 15) * 16);
           if constexpr (kMode == kUpMxfp4) {
-            // the 32 columns are one block of the row: the codes are those of
-            // quantising the bf16 h
+            // four lanes hold a block: the codes are those of quantising the
+            // bf16 h
             const uint32_t s = block_scale_of_quad(h);
+            const uint32_t w = scale_word_of_half(s, lane);
             if (t < left) {
               *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(D) + ((r0 + t) * N_out + col) / 2) =
                   quantize_bf16x8(h, s);
-              if ((lane & 3) == 0)
-                Dsf[scale_word_offset(r0 + t, col0 / 128, N_out / 128) + q] = static_cast<uint8_t>(s);
+              if ((lane & 15) == 0)
+                *reinterpret_cast<uint32_t*>(Dsf + scale_word_offset(r0 + t, col0 / 128, N_out / 128)) = w;
             }
           } else {
             if (t < left) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(D) + (r0 + t) * N_out + col) = h;
@@ -516,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int kMode>
 cudaError_t launch(const moe_shape& s, const Mxfp4Maps& m, const uint8_t* sfT, const uint8_t* sfW0,
                    const uint8_t* sfW1, void* D, uint8_t* Dsf, const int32_t* off_pad, const int32_t* counts,
-                   uint32_t* status, int num_sms, cudaStream_t st) {
+                   uint32_t* status, uint32_t* sched, int num_sms, cudaStream_t st) {
   // the shared-memory opt-in, once per device (host threads may race here)
   static bool done[64] = {};
   static std::mutex mu;
@@ -537,30 +594,30 @@ cudaError_t launch(const moe_shape& s, const Mxfp4Maps& m, const uint8_t* sfT, c
   const int64_t R = static_cast<int64_t>(s.T) * s.k;
   const int64_t max_tiles = (R / kTok + (s.E < R ? s.E : R)) * NT;
   const int grid = static_cast<int>(max_tiles < num_sms ? max_tiles : num_sms);
-  return launch_pdl(mxfp4_gemm_kernel<kMode>, dim3(grid), dim3(kThreads), kSmemAlloc, st, m.t, m.w0, m.w1, sfT, sfW0,
-                    sfW1, D, Dsf, off_pad, counts, s.E, K, N_out, NT, max_rows_of(s), status);
+  return launch_pdl(mxfp4_gemm_kernel<kMode>, dim3(grid), dim3(kThreads), kSmemAlloc, st, m, sfT, sfW0,
+                    sfW1, D, Dsf, off_pad, counts, s.E, K, N_out, NT, max_rows_of(s), status, sched);
 }
 
 }  // namespace
 
 cudaError_t launch_mxfp4_up(const moe_shape& s, const Mxfp4Maps& m, const uint8_t* x_scales, const uint8_t* wg_scales,
                             const uint8_t* wu_scales, uint16_t* h, const int32_t* off_pad, const int32_t* counts,
-                            uint32_t* status, int num_sms, cudaStream_t st) {
-  return launch<kUpBf16>(s, m, x_scales, wg_scales, wu_scales, h, nullptr, off_pad, counts, status, num_sms, st);
+                            uint32_t* status, uint32_t* sched, int num_sms, cudaStream_t st) {
+  return launch<kUpBf16>(s, m, x_scales, wg_scales, wu_scales, h, nullptr, off_pad, counts, status, sched, num_sms, st);
 }
 
 cudaError_t launch_mxfp4_up_quantized(const moe_shape& s, const Mxfp4Maps& m, const uint8_t* x_scales,
                                       const uint8_t* wg_scales, const uint8_t* wu_scales, uint8_t* h_codes,
                                       uint8_t* h_scales, const int32_t* off_pad, const int32_t* counts,
-                                      uint32_t* status, int num_sms, cudaStream_t st) {
-  return launch<kUpMxfp4>(s, m, x_scales, wg_scales, wu_scales, h_codes, h_scales, off_pad, counts, status, num_sms,
+                                      uint32_t* status, uint32_t* sched, int num_sms, cudaStream_t st) {
+  return launch<kUpMxfp4>(s, m, x_scales, wg_scales, wu_scales, h_codes, h_scales, off_pad, counts, status, sched, num_sms,
                           st);
 }
 
 cudaError_t launch_mxfp4_down(const moe_shape& s, const Mxfp4Maps& m, const uint8_t* h_scales,
                               const uint8_t* wd_scales, uint16_t* Y, const int32_t* off_pad, const int32_t* counts,
-                              uint32_t* status, int num_sms, cudaStream_t st) {
-  return launch<kDown>(s, m, h_scales, wd_scales, wd_scales, Y, nullptr, off_pad, counts, status, num_sms, st);
+                              uint32_t* status, uint32_t* sched, int num_sms, cudaStream_t st) {
+  return launch<kDown>(s, m, h_scales, wd_scales, wd_scales, Y, nullptr, off_pad, counts, status, sched, num_sms, st);
 }
 
 }  // namespace moe

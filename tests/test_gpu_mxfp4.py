@@ -158,6 +158,7 @@ def bounds(K, y, mag):
 
 COUNTS = [
     [1], [0, 1, 0], [63, 64, 65, 0], [128, 127, 129], [192, 193, 191], [0, 0, 400, 5], [257, 16, 17, 15],
+    [1025, 0, 577, 769, 1],
 ]
 
 
