@@ -105,8 +105,7 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 
-// The MXFP4 products cut an expert's c rows into ceil(c / kMxfp4WindowRows)
-// windows that start at multiples of 64 rows.
+// Most rows of a window of the MXFP4 products.
 constexpr int kMxfp4WindowRows = 192;
 // Rows of the boxes their rows are loaded in (the smallest that holds the
 // window is taken).

@@ -7,25 +7,34 @@
 // e8m0 scale per 32 elements of the reduction axis; the tensor core applies
 // the scales and accumulates in float32.
 //
-// A tile is one window of up to 192 of an expert's rows times two blocks of
-// 128 output columns (up: the same 128 columns of gate and of up; down: 256
-// neighbouring columns).  The weights are the M = 128 operand and the rows the
-// N operand, so a window costs its row count rounded up to 16 and an output
-// column's gate and up values meet in one thread.  TMEM holds the two 128 x N
-// accumulators (columns 0 and 192) and each stage's scales (from column 384).
-// Windows start at multiples of 64 rows: their rows' scales then start at an
-// even TMEM column of the 128-row scale tile.
+// A tile is one window of up to 128 or 192 (kTok) of an expert's rows times two
+// blocks of 128 output columns (up: the same 128 columns of gate and of up;
+// down: 256 neighbouring columns).  The weights are the M = 128 operand and the
+// rows the N operand, so a window costs its row count rounded up to 16 and an
+// output column's gate and up values meet in one thread.  TMEM holds the two
+// 128 x N accumulators (lane = output column, column = row) and each stage's
+// scales.  Windows start at multiples of kTok rows, so of 64: their rows' scales
+// start at an even TMEM column of the 128-row scale tile.
+//
+// What bounds it: with 8 rows per expert (4096 x 1536, 64 experts, gate/up) the
+// weights' bytes, 431 MB in 71 us = 6.1 TB/s (0.90 of the measured copy rate);
+// with 1024 (128 experts) operand delivery: the tensor cores alone would take
+// 458 us, the loads alone (8.5 GB from L2) 399 us, both together with the drain
+// take 565 us, 5.8 PFLOP/s.
 //
 // The epilogue would cost as much as the MMAs if it held the accumulators, so
-// its 12 warps take them into registers (two 32 x 32 pieces of each accumulator
-// per warp at most: the first as finished bf16, the second as it is) and hand
-// TMEM back; the rest of the arithmetic and all stores run under the next
-// tile's MMAs.
+// its warps take them into registers (as raw sums as far as registers go,
+// otherwise finished to bf16) and hand TMEM back; the rest of the arithmetic and
+// all stores run under the next tile's MMAs.  (With the accumulators held to the
+// end: 821 us where this takes 565.)
 //
-// Roles of the 14 warps: warp 0 loads (per 256-deep stage two boxes of 128
-// weight rows x 128 bytes, the window's rows in one box, and the scale tiles),
-// warp 1
-// copies a stage's scales to TMEM and issues its MMAs, warps 2-13 drain the
+// Tried and slower: clusters of four sharing weights and rows by multicast (1352
+// us: the CTAs wait for each other at every stage), CTA pairs with cta_group::2
+// (573 us, down product 468 against 383), stages 128 deep (722 us).
+//
+// Roles of the warps: warp 0 loads (per 256-deep stage two boxes of 128 weight
+// rows x 128 bytes, the window's rows in one box, and the scale tiles), warp 1
+// copies a stage's scales to TMEM and issues its MMAs, the others drain the
 // accumulators.  Every wait is bounded as in the bf16 GEMMs.
 #include <cstdint>
 #include <mutex>
@@ -37,47 +46,54 @@ namespace moe {
 namespace {
 
 constexpr int kMaxExperts = 256;
-constexpr int kTok = kMxfp4WindowRows;          // rows per window at most
-constexpr int kStageK = 256;                    // reduction elements per stage
-constexpr int kAtoms = kStageK / 128;           // 128-deep scale tiles in a stage
-constexpr int kStages = 3;
-constexpr int kRowBytes = kStageK / 2;          // codes of a row in a stage (128-byte swizzle)
-constexpr int kWBytes = 128 * kRowBytes;        // one block of 128 weight rows
-constexpr int kTBytes = kTok * kRowBytes;
-constexpr int kSfBytes = 512 * kAtoms;          // scale tiles of 128 rows
-constexpr int kOffT = 2 * kWBytes;
-constexpr int kOffSf = kOffT + kTBytes;         // scales: weights 0, weights 1, rows (two 128-row blocks)
-constexpr int kStageBytes = kOffSf + 4 * kSfBytes;
-static_assert(kStageBytes % 1024 == 0, "stages start on swizzle atoms");
-static_assert(kTok % 64 == 0, "windows start at an even column of their scale tile");
-
-constexpr int kEpiWarps = 12;
-constexpr int kEpiSplit = kEpiWarps / 4;         // warps sharing a lane quarter
-static_assert(2 * kEpiSplit * 32 == kTok, "two 32-row pieces of a window per warp at most");
+constexpr int kStageK = 256;             // reduction elements per stage
+constexpr int kAtoms = kStageK / 128;    // 128-deep scale tiles in a stage
+constexpr int kRowBytes = kStageK / 2;   // codes of a row in a stage (128-byte swizzle)
+constexpr int kWBytes = 128 * kRowBytes; // one block of 128 weight rows
+constexpr int kSfBytes = 512 * kAtoms;   // scale tiles of 128 rows
+constexpr int kFirstEpi = 2;             // epilogue warps follow the loading and the issuing one
 // staging of 32 rows x 128 columns, written by the four warps of a turn
 // (padded so that eight rows start on different banks)
 constexpr int kPitch = 256 + 16;
 constexpr int kStageOutBytes = 32 * kPitch;
-constexpr int kFirstEpi = 2;
-constexpr int kThreads = (kFirstEpi + kEpiWarps) * 32;
+constexpr int kTileRing = 4;             // tile indices on their way from the producer
 
-// TMEM columns: accumulators, then 32 columns of scales per stage
-constexpr uint32_t kAcc1 = 192;
-constexpr uint32_t kSfCol = 384;
-constexpr uint32_t kSfStageCols = 16 * kAtoms;  // per 128 k: weights 0 +0, weights 1 +4, rows +8
-static_assert(kSfCol + kStages * kSfStageCols <= 512, "TMEM columns");
-
-constexpr int kBarOff = kStages * kStageBytes;
-constexpr int kTileRing = 4;                    // tile indices on their way from the producer
-constexpr int kNumBars = 2 * kStages + 3 + 2 * kTileRing;
-constexpr int kTileOff = kBarOff + kNumBars * 8 + 8;
-constexpr int kWinOff = kTileOff + kTileRing * 4;
-constexpr int kCntOff = kWinOff + (kMaxExperts + 1) * 4;
-constexpr int kOffpOff = kCntOff + kMaxExperts * 4;
-constexpr int kOutOff = (kOffpOff + (kMaxExperts + 1) * 4 + 15) / 16 * 16;
-constexpr int kSmemBytes = kOutOff + kEpiSplit * kStageOutBytes;
-constexpr int kSmemAlloc = kSmemBytes + 1024;
-static_assert(kSmemAlloc <= 232448, "shared memory budget");
+// What depends on the most rows of a window.
+template <int kTok>
+struct Cfg {
+  static_assert(kTok == 128 || kTok == 192, "windows start at an even column of their scale tile");
+  // 64 columns of each accumulator per epilogue warp, in pieces of 32
+  static constexpr int EPI_WARPS = kTok / 16;
+  static constexpr int EPI_SPLIT = EPI_WARPS / 4;          // warps sharing a lane quarter
+  static constexpr int PIECES = kTok / 32 / EPI_SPLIT;
+  static_assert(PIECES == 2, "the epilogue's shape");
+  static constexpr int THREADS = (kFirstEpi + EPI_WARPS) * 32;
+  static constexpr int READERS = 1 + EPI_WARPS;            // of a tile index: the MMA lane, a lane of each epilogue warp
+  // Pieces that a warp may keep as raw sums until TMEM is free: 64 registers
+  // each, of 168 with ten warps, of 128 with fourteen.
+  static constexpr int RAW = kTok == 128 ? 2 : 1;
+  static constexpr int STAGES = kTok == 128 ? 4 : 3;
+  static constexpr int SF_BLOCKS = kTok == 128 ? 1 : 2;    // 128-row scale blocks that a window's rows reach
+  static constexpr int OFF_T = 2 * kWBytes;
+  static constexpr int OFF_SF = OFF_T + kTok * kRowBytes;  // scales: weights 0, weights 1, rows
+  static constexpr int STAGE_BYTES = OFF_SF + (2 + SF_BLOCKS) * kSfBytes;
+  // TMEM columns: the accumulators, then each stage's scales (per 128 k:
+  // weights 0 +0, weights 1 +4, rows +8)
+  static constexpr uint32_t ACC1 = kTok;
+  static constexpr uint32_t SF_COL = 2 * kTok;
+  static constexpr uint32_t SF_STAGE_COLS = 16 * kAtoms;
+  static constexpr int BAR_OFF = STAGES * STAGE_BYTES;
+  static constexpr int NUM_BARS = 2 * STAGES + 3 + 2 * kTileRing;
+  static constexpr int TILE_OFF = BAR_OFF + NUM_BARS * 8 + 8;
+  static constexpr int WIN_OFF = TILE_OFF + kTileRing * 4;
+  static constexpr int CNT_OFF = WIN_OFF + (kMaxExperts + 1) * 4;
+  static constexpr int OFFP_OFF = CNT_OFF + kMaxExperts * 4;
+  static constexpr int OUT_OFF = (OFFP_OFF + (kMaxExperts + 1) * 4 + 15) / 16 * 16;
+  static constexpr int ALLOC = OUT_OFF + EPI_SPLIT * kStageOutBytes + 1024;
+  static_assert(STAGE_BYTES % 1024 == 0, "stages start on swizzle atoms");
+  static_assert(SF_COL + STAGES * SF_STAGE_COLS <= 512, "TMEM columns");
+  static_assert(ALLOC <= 232448, "shared memory budget");
+};
 
 enum Mode { kUpBf16 = 0, kUpMxfp4 = 1, kDown = 2 };
 
@@ -127,6 +143,7 @@ struct Win {
 // Tile t: expert e (windows off[e] .. off[e+1]), then column tile j, then the
 // window, so that the windows sharing a weight tile are neighbours.  All of an
 // expert's windows but the last have kTok rows.
+template <int kTok>
 __device__ __forceinline__ Win decode(int tile, int NT, int E, const int32_t* off, const int32_t* offp,
                                       const int32_t* cnt, int64_t max_rows) {
   Win c{0, 0, 0, 0, false};
@@ -146,7 +163,7 @@ __device__ __forceinline__ Win decode(int tile, int NT, int E, const int32_t* of
   c.row0 = offp[lo] + kTok * w;
   c.rows = min(kTok, cnt[lo] - kTok * w);
   const int pad_end = offp[lo + 1];
-  c.ok = c.rows > 0 && c.rows <= kTok && c.row0 >= 0 && (c.row0 & 63) == 0 && c.row0 + c.rows <= pad_end &&
+  c.ok = c.rows > 0 && c.rows <= kTok && c.row0 >= 0 && (c.row0 & 63) == 0 && (kTok == 192 || (c.row0 & 127) == 0) && c.row0 + c.rows <= pad_end &&
          pad_end <= max_rows && (pad_end & 127) == 0;
   return c;
 }
@@ -158,11 +175,9 @@ __device__ __forceinline__ Win decode(int tile, int NT, int E, const int32_t* of
 // launch.
 struct TileRing {
   uint64_t* full;         // [kTileRing] one arrival (the producer)
-  uint64_t* empty;        // [kTileRing] kReaders arrivals
+  uint64_t* empty;        // [kTileRing] Cfg::READERS arrivals
   volatile int32_t* idx;  // [kTileRing]
 };
-constexpr int kReaders = 1 + kEpiWarps;  // the MMA lane and one lane of each epilogue warp
-
 __device__ __forceinline__ bool ring_put(const TileRing& r, uint32_t n, int tile, volatile int* abort,
                                          uint32_t* status) {
   const uint32_t slot = n % kTileRing;
@@ -179,6 +194,8 @@ __device__ __forceinline__ int ring_take(const TileRing& r, uint32_t n, volatile
   return mbar_wait(&r.full[slot], (n / kTileRing) & 1u, abort, status) ? r.idx[slot] : -1;
 }
 
+// OR-vote over the epilogue's threads (named barrier 2).
+template <int kCount>
 __device__ __forceinline__ bool vote_any(bool flag) {
   uint32_t r;
   asm volatile(
@@ -187,7 +204,7 @@ __device__ __forceinline__ bool vote_any(bool flag) {
       "bar.red.or.pred po, 2, %2, pi;\n\t"
       "selp.u32 %0, 1, 0, po;\n\t}"
       : "=r"(r)
-      : "r"(flag ? 1u : 0u), "n"(kEpiWarps * 32)
+      : "r"(flag ? 1u : 0u), "n"(kCount)
       : "memory");
   return r != 0;
 }
@@ -240,41 +257,42 @@ __device__ __forceinline__ void stage_piece(uint32_t out, const uint32_t (&packe
     stmatrix_x4_trans(at + 8 * j * kPitch, packed[4 * j], packed[4 * j + 1], packed[4 * j + 2], packed[4 * j + 3]);
 }
 
-template <int kMode>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int kMode, int kTok>
+__global__ void __launch_bounds__(Cfg<kTok>::THREADS, 1)
     mxfp4_gemm_kernel(const __grid_constant__ Mxfp4Maps maps, const uint8_t* __restrict__ sfT,
                       const uint8_t* __restrict__ sfW0, const uint8_t* __restrict__ sfW1, void* __restrict__ D,
                       uint8_t* __restrict__ Dsf, const int32_t* __restrict__ off_pad,
                       const int32_t* __restrict__ counts, int E, int K, int N_out, int NT, int64_t max_rows,
                       uint32_t* __restrict__ status, uint32_t* __restrict__ sched) {
+  using C = Cfg<kTok>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kBarOff);
-  uint64_t* empty = full + kStages;
-  uint64_t* tfull = empty + kStages;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);
+  uint64_t* empty = full + C::STAGES;
+  uint64_t* tfull = empty + C::STAGES;
   uint64_t* tempty = tfull + 1;
   uint64_t* drain = tfull + 2;
-  const TileRing ring{tfull + 3, tfull + 3 + kTileRing, reinterpret_cast<volatile int32_t*>(smem + kTileOff)};
+  const TileRing ring{tfull + 3, tfull + 3 + kTileRing, reinterpret_cast<volatile int32_t*>(smem + C::TILE_OFF)};
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tfull + 3 + 2 * kTileRing);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int32_t* s_win = reinterpret_cast<int32_t*>(smem + kWinOff);
-  int32_t* s_cnt = reinterpret_cast<int32_t*>(smem + kCntOff);
-  int32_t* s_offp = reinterpret_cast<int32_t*>(smem + kOffpOff);
+  int32_t* s_win = reinterpret_cast<int32_t*>(smem + C::WIN_OFF);
+  int32_t* s_cnt = reinterpret_cast<int32_t*>(smem + C::CNT_OFF);
+  int32_t* s_offp = reinterpret_cast<int32_t*>(smem + C::OFFP_OFF);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
 
   pdl_launch_dependents();
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
     mbar_init(tfull, 1);
-    mbar_init(tempty, kEpiWarps);
+    mbar_init(tempty, C::EPI_WARPS);
     mbar_init(drain, 1);
     for (int i = 0; i < kTileRing; ++i) {
       mbar_init(&ring.full[i], 1);
-      mbar_init(&ring.empty[i], kReaders);
+      mbar_init(&ring.empty[i], C::READERS);
     }
     *abort_flag = 0;
     fence_mbarrier_init();
@@ -338,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool stop = !ring_put(ring, 0, tile, abort_flag, status);
       for (uint32_t n = 0; !stop && tile < total; ++n) {
         const uint32_t drawn = atomicAdd(sched, 1u);  // the next tile: needed after this one's loads
-        const Win c = decode(tile, NT, E, s_win, s_offp, s_cnt, max_rows);
+        const Win c = decode<kTok>(tile, NT, E, s_win, s_offp, s_cnt, max_rows);
         if (!c.ok) record_status(status, kStatusBounds);
         // a one-window expert reads this weight tile once
         const uint64_t pol_w = s_win[c.e + 1] - s_win[c.e] == 1 ? policy_evict_first() : policy_evict_normal();
@@ -348,10 +366,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the smallest box that holds the window (rows past it are not used)
         const int pick = c.rows <= 32 ? 0 : c.rows <= 64 ? 1 : c.rows <= 128 ? 2 : 3;
         const int box = mxfp4_token_box(pick);
-        const bool t_two = (c.row0 & 127) + c.rows > 128;     // the window's rows span two scale blocks
+        const bool t_two = C::SF_BLOCKS > 1 && (c.row0 & 127) + c.rows > 128;  // the window's rows span two scale blocks
         for (int ks = 0; c.ok && ks < KS; ++ks, ++it) {
-          const uint32_t s = it % kStages;
-          if (!mbar_wait(&empty[s], ((it / kStages) & 1u) ^ 1u, abort_flag, status)) {
+          const uint32_t s = it % C::STAGES;
+          if (!mbar_wait(&empty[s], ((it / C::STAGES) & 1u) ^ 1u, abort_flag, status)) {
             stop = true;
             break;
           }
@@ -359,14 +377,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t sfb = 512u * kt;
           mbar_arrive_expect_tx(&full[s],
                                 (two ? 2u : 1u) * (kWBytes + sfb) + box * kRowBytes + (t_two ? 2u : 1u) * sfb);
-          uint8_t* st = smem + s * kStageBytes;
+          uint8_t* st = smem + s * C::STAGE_BYTES;
           const int kx = ks * kRowBytes;
           tma_load_2d(st, &maps.w0, &full[s], kx, w_row, pol_w);
           if (two)
             tma_load_2d(st + kWBytes, kMode == kDown ? &maps.w0 : &maps.w1, &full[s], kx,
                         kMode == kDown ? w_row + 128 : w_row, pol_w);
-          tma_load_2d(st + kOffT, &maps.t[pick], &full[s], kx, c.row0, pol_t);
-          uint8_t* sf = st + kOffSf;
+          tma_load_2d(st + C::OFF_T, &maps.t[pick], &full[s], kx, c.row0, pol_t);
+          uint8_t* sf = st + C::OFF_SF;
           const int64_t wsf = (static_cast<int64_t>(w_row >> 7) * KT + kAtoms * ks) * 512;
           const int64_t tsf = (static_cast<int64_t>(c.row0 >> 7) * KT + kAtoms * ks) * 512;
           bulk_load(sf, sfW0 + wsf, sfb, &full[s]);
@@ -387,11 +405,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         atomicExch(sched + 1, 0u);
       }
       // every stage used must be consumed before the CTA may exit
-      const uint32_t nst = it < kStages ? it : kStages;
+      const uint32_t nst = it < C::STAGES ? it : C::STAGES;
       for (uint32_t s = 0; s < nst; ++s) {
-        const uint32_t last = s + kStages * ((it - 1 - s) / kStages);
+        const uint32_t last = s + C::STAGES * ((it - 1 - s) / C::STAGES);
         int no_abort = 0;
-        mbar_wait(&empty[s], (last / kStages) & 1u, &no_abort, status);
+        mbar_wait(&empty[s], (last / C::STAGES) & 1u, &no_abort, status);
       }
     }
     __syncwarp();
@@ -405,25 +423,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int tile = ring_take(ring, n, abort_flag, status);
         if (tile < 0 || tile >= total) break;
         mbar_arrive(&ring.empty[n % kTileRing]);
-        const Win c = decode(tile, NT, E, s_win, s_offp, s_cnt, max_rows);
+        const Win c = decode<kTok>(tile, NT, E, s_win, s_offp, s_cnt, max_rows);
         if (!c.ok) continue;
         const bool two = kMode != kDown || c.j * 256 + 128 < N_out;
         const uint32_t N = static_cast<uint32_t>((c.rows + 15) / 16 * 16);
         const uint32_t id[2] = {idesc_mxf4(N, 0), idesc_mxf4(N, 1)};
-        const bool t_two = (c.row0 & 127) + c.rows > 128;
+        const bool t_two = C::SF_BLOCKS > 1 && (c.row0 & 127) + c.rows > 128;
         const uint32_t t_col = (c.row0 & 127) / 32;  // first row's column inside its scale block: 0 or 2
         if (!mbar_wait(tempty, (tcount & 1u) ^ 1u, abort_flag, status)) break;
         tc_fence_after();
         for (int ks = 0; ks < KS; ++ks, ++it) {
-          const uint32_t s = it % kStages;
-          if (!mbar_wait(&full[s], (it / kStages) & 1u, abort_flag, status)) {
+          const uint32_t s = it % C::STAGES;
+          if (!mbar_wait(&full[s], (it / C::STAGES) & 1u, abort_flag, status)) {
             stop = true;
             break;
           }
           tc_fence_after();
-          const uint32_t st = smem_u32(smem + s * kStageBytes);
-          const uint32_t sf = st + kOffSf;
-          const uint32_t tsf = tmem + kSfCol + s * kSfStageCols;  // this stage's own columns
+          const uint32_t st = smem_u32(smem + s * C::STAGE_BYTES);
+          const uint32_t sf = st + C::OFF_SF;
+          const uint32_t tsf = tmem + C::SF_COL + s * C::SF_STAGE_COLS;  // this stage's own columns
           const int kt = min(kAtoms, KT - kAtoms * ks);
           for (int a = 0; a < kt; ++a) {
             sf_to_tmem(tsf + 16 * a, sf + 512 * a);
@@ -432,13 +450,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (t_two) sf_to_tmem(tsf + 16 * a + 12, sf + 3 * kSfBytes + 512 * a);
           }
           for (int kk = 0; kk < 2 * kt; ++kk) {  // 64 deep each
-            const uint64_t bd = smem_desc(st + kOffT + kk * 32, 16, 8 * kRowBytes, kSwizzle128B);
+            const uint64_t bd = smem_desc(st + C::OFF_T + kk * 32, 16, 8 * kRowBytes, kSwizzle128B);
             const uint32_t sfc = tsf + 16 * (kk >> 1);
             const uint32_t acc = (ks | kk) != 0 ? 1u : 0u;
             mma_mxf4(tmem, smem_desc(st + kk * 32, 16, 8 * kRowBytes, kSwizzle128B), bd, id[kk & 1], sfc,
                      sfc + 8 + t_col, acc);
             if (two)
-              mma_mxf4(tmem + kAcc1, smem_desc(st + kWBytes + kk * 32, 16, 8 * kRowBytes, kSwizzle128B), bd,
+              mma_mxf4(tmem + C::ACC1, smem_desc(st + kWBytes + kk * 32, 16, 8 * kRowBytes, kSwizzle128B), bd,
                        id[kk & 1], sfc + 4, sfc + 8 + t_col, acc);
           }
           tc_commit(&empty[s]);
@@ -458,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // a lane quarter take the window's 32-row pieces in turn
     const int q = warp & 3;
     const int turn = (warp - kFirstEpi) / 4;
-    uint8_t* out = smem + kOutOff + turn * kStageOutBytes;
+    uint8_t* out = smem + C::OUT_OFF + turn * kStageOutBytes;
     const uint32_t out_addr = smem_u32(out) + q * 64;  // this warp's columns
     const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16);
     uint32_t tcount = 0;
@@ -467,9 +485,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&ring.empty[n % kTileRing]);
       bool ok = tile >= 0;
-      const Win c = decode(ok && tile < total ? tile : 0, NT, E, s_win, s_offp, s_cnt, max_rows);
+      const Win c = decode<kTok>(ok && tile < total ? tile : 0, NT, E, s_win, s_offp, s_cnt, max_rows);
       if (ok && tile < total && c.ok) ok = mbar_wait(tfull, tcount & 1u, abort_flag, status);
-      if (vote_any(!ok)) break;  // every warp gives up together (they share barriers)
+      if (vote_any<C::EPI_WARPS * 32>(!ok)) break;  // every warp gives up together (they share barriers)
       if (tile >= total) break;
       if (!c.ok) continue;
       ++tcount;
@@ -477,13 +495,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n0 = c.j * (kMode == kDown ? 256 : 128);
       const bool two = kMode != kDown || n0 + 128 < N_out;
       const int pieces = (c.rows + 31) / 32;
-      const int mine = pieces > turn ? (pieces - turn + kEpiSplit - 1) / kEpiSplit : 0;  // 0, 1 or 2
-      uint32_t v0[32], v1[32];
-      uint32_t out0[2][16], out1[16];  // finished pieces (down: of each accumulator)
-      auto fetch = [&](int p) {
-        load_piece(tb + (turn + kEpiSplit * p) * 32, v0);
-        if (two) load_piece(tb + kAcc1 + (turn + kEpiSplit * p) * 32, v1);
-        tmem_ld_wait();
+      const int mine = pieces > turn ? (pieces - turn + C::EPI_SPLIT - 1) / C::EPI_SPLIT : 0;
+      auto fetch = [&](int p, uint32_t (&v0)[32], uint32_t (&v1)[32]) {
+        load_piece(tb + (turn + C::EPI_SPLIT * p) * 32, v0);
+        if (two) load_piece(tb + C::ACC1 + (turn + C::EPI_SPLIT * p) * 32, v1);
       };
       auto release = [&]() {
         tc_fence_before();
@@ -492,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       // v0, v1 to finished bf16; entry 4 j + x: output column x * 8 + lane / 4
       // (lanes 0-15 of the piece for x < 2), columns 8 j + 2 (lane % 4)
-      auto finish = [&](uint32_t (&a)[16], uint32_t (&b)[16]) {
+      auto finish = [&](const uint32_t (&v0)[32], const uint32_t (&v1)[32], uint32_t (&a)[16], uint32_t (&b)[16]) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
 #pragma unroll
@@ -513,8 +528,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // rows: the turn's four warps put it together in shared memory, then
       // write eight rows each, sixteen lanes (256 bytes) a row
       auto store = [&](int p, int col0, const uint32_t (&a)[16]) {
-        const int64_t r0 = c.row0 + (turn + kEpiSplit * p) * 32;
-        const int left = c.rows - (turn + kEpiSplit * p) * 32;
+        const int64_t r0 = c.row0 + (turn + C::EPI_SPLIT * p) * 32;
+        const int left = c.rows - (turn + C::EPI_SPLIT * p) * 32;
         named_barrier_sync(3 + turn, 128);  // the previous piece has been read
         stage_piece(out_addr, a, lane);
         named_barrier_sync(3 + turn, 128);
@@ -545,18 +560,53 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (two) store(p, n0 + 128, b);
         }
       };
-      if (mine == 0) {
+      // finished pieces (down: of each accumulator) and raw ones
+      uint32_t a0[16], b0[16], a[16], b[16], va[C::RAW][32], vb[C::RAW][32];
+      if constexpr (C::RAW == 2 && kMode == kDown) {
+        // rounding is all there is to do (keeping raw sums: 2048 rows x 8 of
+        // 64 experts 97 us, this 73 us)
+        uint32_t pa[2][16], pb[2][16];
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          if (p < mine) {
+            fetch(p, va[0], vb[0]);
+            tmem_ld_wait();
+            finish(va[0], vb[0], pa[p], pb[p]);
+          }
+        }
+        release();
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+          if (p < mine) store_all(p, pa[p], pb[p]);
+      } else if constexpr (C::RAW == 2) {
+        // every piece is kept as it is until TMEM is free
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+          if (p < mine) fetch(p, va[p], vb[p]);
+        tmem_ld_wait();
+        release();
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          if (p < mine) {
+            finish(va[p], vb[p], a, b);
+            store_all(p, a, b);
+          }
+        }
+      } else if (mine == 0) {
         release();
       } else {
-        fetch(0);
+        // the first of two pieces is finished, the last kept as it is
+        fetch(0, va[0], vb[0]);
+        tmem_ld_wait();
         if (mine == 2) {
-          finish(out0[0], out0[1]);
-          fetch(1);
+          finish(va[0], vb[0], a0, b0);
+          fetch(1, va[0], vb[0]);
+          tmem_ld_wait();
         }
-        release();  // the accumulators are this warp's no more
-        if (mine == 2) store_all(0, out0[0], out0[1]);
-        finish(out0[0], out1);
-        store_all(mine - 1, out0[0], out1);
+        release();
+        if (mine == 2) store_all(0, a0, b0);
+        finish(va[0], vb[0], a, b);
+        store_all(mine - 1, a, b);
       }
     }
   }
@@ -570,8 +620,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int kMode>
-cudaError_t launch(const moe_shape& s, const Mxfp4Maps& m, const uint8_t* sfT, const uint8_t* sfW0,
+template <int kMode, int kTok>
+cudaError_t launch_tok(const moe_shape& s, const Mxfp4Maps& m, const uint8_t* sfT, const uint8_t* sfW0,
                    const uint8_t* sfW1, void* D, uint8_t* Dsf, const int32_t* off_pad, const int32_t* counts,
                    uint32_t* status, uint32_t* sched, int num_sms, cudaStream_t st) {
   // the shared-memory opt-in, once per device (host threads may race here)
@@ -583,7 +633,7 @@ cudaError_t launch(const moe_shape& s, const Mxfp4Maps& m, const uint8_t* sfT, c
   {
     std::lock_guard<std::mutex> lock(mu);
     if (dev >= 64 || !done[dev]) {
-      err = cudaFuncSetAttribute(mxfp4_gemm_kernel<kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAlloc);
+      err = cudaFuncSetAttribute(mxfp4_gemm_kernel<kMode, kTok>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<kTok>::ALLOC);
       if (err != cudaSuccess) return err;
       if (dev < 64) done[dev] = true;
     }
@@ -594,8 +644,21 @@ cudaError_t launch(const moe_shape& s, const Mxfp4Maps& m, const uint8_t* sfT, c
   const int64_t R = static_cast<int64_t>(s.T) * s.k;
   const int64_t max_tiles = (R / kTok + (s.E < R ? s.E : R)) * NT;
   const int grid = static_cast<int>(max_tiles < num_sms ? max_tiles : num_sms);
-  return launch_pdl(mxfp4_gemm_kernel<kMode>, dim3(grid), dim3(kThreads), kSmemAlloc, st, m, sfT, sfW0,
+  return launch_pdl(mxfp4_gemm_kernel<kMode, kTok>, dim3(grid), dim3(Cfg<kTok>::THREADS), Cfg<kTok>::ALLOC, st, m, sfT, sfW0,
                     sfW1, D, Dsf, off_pad, counts, s.E, K, N_out, NT, max_rows_of(s), status, sched);
+}
+
+// Windows of 128 rows leave shared memory for a fourth stage, and their ten
+// warps registers for the whole accumulators; windows of 192 read the weights
+// less often.  Measured (gate/up | down, us, 4096 x 1536, 64 experts): 8 rows per
+// expert 71 | 36 with 128 and 76 | 37 with 192, 256 rows 107 | 73 and 114 | 74,
+// 320 rows 125 | 85 and 121 | 80, 512 rows 173 | 121 and 164 | 110.
+constexpr int kWideRows = 256;  // rows per expert, on average, above which windows have 192
+
+template <int kMode, typename... Args>
+cudaError_t launch(const moe_shape& s, Args... args) {
+  const bool wide = static_cast<int64_t>(s.T) * s.k > static_cast<int64_t>(kWideRows) * s.E;
+  return wide ? launch_tok<kMode, 192>(s, args...) : launch_tok<kMode, 128>(s, args...);
 }
 
 }  // namespace

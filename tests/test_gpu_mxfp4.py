@@ -158,13 +158,15 @@ def bounds(K, y, mag):
 
 COUNTS = [
     [1], [0, 1, 0], [63, 64, 65, 0], [128, 127, 129], [192, 193, 191], [0, 0, 400, 5], [257, 16, 17, 15],
-    [1025, 0, 577, 769, 1],
+    [1025, 0, 577, 769, 1] + 8 * [0],
 ]
 
 
-def shape_for(counts, H, I):
-    """A shape whose capacity holds these counts (T k rows over E experts)."""
-    return (max(1, sum(counts)), H, I, len(counts), 1)
+def shape_for(counts, H, I, wide=False):
+    """A shape whose capacity holds these counts (T k rows over E experts); wide:
+    one with over 256 rows per expert, for which the products cut other windows."""
+    T = max(1, sum(counts))
+    return (max(T, 257 * len(counts)) if wide else T, H, I, len(counts), 1)
 
 
 def upload(rows, off, max_rows):
@@ -172,13 +174,13 @@ def upload(rows, off, max_rows):
     return to_dev(padded(ref.pack(c), max_rows, 0xFF)), to_dev(ref.tile(padded(s, max_rows, 255)))
 
 
-def up_call(counts, H, I, seed, rows=None):
+def up_call(counts, H, I, seed, rows=None, wide=False):
     torch = need_gpu()
     import combine_moe_route_04_gb300 as moe
     r, ws, off, real = operands(counts, H, I, 2, seed)
     if rows is not None:
         r = rows(r, off)
-    s = shape_for(counts, H, I)
+    s = shape_for(counts, H, I, wide)
     mr = moe.capacity(s)[1]
     xc, xs = upload(r, off, mr)
     h = torch.full((mr, I), -7.0, dtype=torch.bfloat16, device="cuda")
@@ -190,10 +192,11 @@ def up_call(counts, H, I, seed, rows=None):
     return to64(host_u16(h)), r, ws, off, real
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("counts", COUNTS)
 @pytest.mark.parametrize("H,I", [(128, 128), (384, 256), (1024, 384)])
-def test_up_product_against_64_bits(counts, H, I):
-    got, r, ws, off, real = up_call(counts, H, I, sum(counts) + H)
+def test_up_product_against_64_bits(counts, H, I, wide):
+    got, r, ws, off, real = up_call(counts, H, I, sum(counts) + H, wide=wide)
     g, gm = matmul64(r, ws[0], off, counts, I)
     u, um = matmul64(r, ws[1], off, counts, I)
     sig = 1.0 / (1.0 + np.exp(-g))
@@ -205,13 +208,14 @@ def test_up_product_against_64_bits(counts, H, I):
     assert np.all(got[:off[-1]][~real] == -7.0) and np.all(got[off[-1]:] == -7.0)   # padding rows stay unwritten
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("counts", COUNTS)
 @pytest.mark.parametrize("H,I", [(128, 128), (384, 256), (640, 1152)])
-def test_down_product_against_64_bits(counts, H, I):
+def test_down_product_against_64_bits(counts, H, I, wide):
     torch = need_gpu()
     import combine_moe_route_04_gb300 as moe
     r, ws, off, real = operands(counts, I, H, 1, sum(counts) + H)
-    s = shape_for(counts, H, I)
+    s = shape_for(counts, H, I, wide)
     mr = moe.capacity(s)[1]
     hc, hs = upload(r, off, mr)
     Y = torch.full((mr, H), -7.0, dtype=torch.bfloat16, device="cuda")
@@ -291,7 +295,7 @@ def steps(s, logits, X, q):
 
 
 SHAPES = [(1, 128, 128, 1, 1, 0.0), (5, 256, 128, 8, 8, 0.0), (128, 256, 512, 8, 2, 0.0), (333, 640, 384, 7, 3, 0.0),
-          (700, 384, 256, 16, 4, 3.0), (64, 1152, 640, 256, 16, 0.0)]
+          (700, 384, 256, 16, 4, 3.0), (1500, 256, 256, 4, 2, 0.5), (64, 1152, 640, 256, 16, 0.0)]
 
 
 @pytest.mark.parametrize("T,H,I,E,k,skew", SHAPES)
