@@ -257,9 +257,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     // the CTAs' rows of partials go round `parts` groups of threads, a thread
     // to W neighbouring experts; the groups' sums join in a fixed order
     const int cols = (E + W - 1) / W;  // E % 4 == 0 where W is 4
-    const int parts = min(kFwdThreads / cols, kFwdWarps / 2);
+    const int parts = min(32, min(kFwdThreads / cols, kFwdWarps * kMaxE / 2 / E));
     const int part = tid / cols, e = tid % cols * W;
-    int* s_ci = reinterpret_cast<int*>(s_p) + kFwdWarps / 2 * kMaxE;
+    int* s_ci = reinterpret_cast<int*>(s_p) + kFwdWarps * kMaxE / 2;
+    constexpr int kRows = V * W > 4 ? 3 : 5;  // in flight per thread, as registers allow
     if (part < parts) {
       float ps[W];
       int cs[W];
@@ -268,7 +269,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         ps[q] = 0.0f;
         cs[q] = 0;
       }
-#pragma unroll 4
+#pragma unroll kRows
       for (int b = part; b < static_cast<int>(gridDim.x); b += parts) {
         if constexpr (W == 4) {
           const float4 p4 = __ldcg(reinterpret_cast<const float4*>(part_p + b * E + e));
@@ -282,8 +283,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       }
 #pragma unroll
       for (int q = 0; q < W; ++q) {
-        s_p[part * kMaxE + e + q] = ps[q];
-        s_ci[part * kMaxE + e + q] = cs[q];
+        s_p[part * E + e + q] = ps[q];
+        s_ci[part * E + e + q] = cs[q];
       }
     }
     if (warp == 0) {
@@ -303,8 +304,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       p_sum = 0.0f;
       c_sum = 0;
       for (int q = 0; q < parts; ++q) {
-        p_sum += s_p[q * kMaxE + tid];
-        c_sum += s_ci[q * kMaxE + tid];
+        p_sum += s_p[q * E + tid];
+        c_sum += s_ci[q * E + tid];
       }
     }
     __syncthreads();
