@@ -230,6 +230,68 @@ def test_down_product_against_64_bits(counts, H, I, wide):
     assert np.all(got[:off[-1]][~real] == -7.0) and np.all(got[off[-1]:] == -7.0)
 
 
+@pytest.mark.parametrize("seed", range(10))
+def test_products_of_random_shapes(seed):
+    """Random expert counts (empty ones among them), sizes and windows, both products."""
+    torch = need_gpu()
+    import combine_moe_route_04_gb300 as moe
+    rng = np.random.default_rng(100 + seed)
+    E = int(rng.integers(1, 40))
+    counts = (rng.integers(0, 1 + int(np.exp(rng.uniform(0, 6.2))), E) * (rng.random(E) < 0.8)).tolist()
+    H, I = (128 * int(rng.integers(1, 7)) for _ in range(2))
+    wide = bool(rng.integers(0, 2))
+    got, r, ws, off, real = up_call(counts, H, I, seed, wide=wide)
+    g, gm = matmul64(r, ws[0], off, counts, I)
+    u, um = matmul64(r, ws[1], off, counts, I)
+    sig = 1.0 / (1.0 + np.exp(-g))
+    want = g * sig * u
+    eg, eu = bounds(H, g, gm), bounds(H, u, um)
+    tol = 1.1 * eg * np.abs(u) + np.abs(g * sig) * eu + 1.1 * eg * eu + (2.0 ** -19 + 2.0 ** -8) * np.abs(want) + 1e-30
+    assert np.all(np.abs(got[:off[-1]] - want)[real] <= tol[real])
+    assert np.all(got[:off[-1]][~real] == -7.0)
+    s = shape_for(counts, H, I, wide)
+    mr = moe.capacity(s)[1]
+    r, ws, off, real = operands(counts, I, H, 1, 50 + seed)
+    hc, hs = upload(r, off, mr)
+    Y = torch.full((mr, H), -7.0, dtype=torch.bfloat16, device="cuda")
+    status = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    args = (s, hc, hs, to_dev(np.array(counts, np.int32)), to_dev(off.astype(np.int32)), to_dev(ref.pack(ws[0][0])),
+            to_dev(ref.tile(ws[0][1])), Y, status)
+    moe.moe_grouped_gemm_down_mxfp4(*args)
+    got = to64(host_u16(Y))
+    want, mag = matmul64(r, ws[0], off, counts, H)
+    tol = bounds(I, want, mag) + 2.0 ** -8 * np.abs(want) + 1e-30
+    assert np.all(np.abs(got[:off[-1]] - want)[real] <= tol[real])
+    moe.moe_grouped_gemm_down_mxfp4(*args)
+    assert moe.last_device_status(status) == 0
+    assert np.array_equal(to64(host_u16(Y)), got)      # the same bits again
+
+
+def test_a_tile_counter_that_was_not_cleared_is_reported():
+    """As for the bf16 products: the call that finds it dirty says so, the next is sound."""
+    torch = need_gpu()
+    import combine_moe_route_04_gb300 as moe
+    counts, H, I = [300, 5, 0, 129], 256, 512
+    r, ws, off, real = operands(counts, I, H, 1, 3)
+    s = shape_for(counts, H, I)
+    mr = moe.capacity(s)[1]
+    hc, hs = upload(r, off, mr)
+    Y = torch.zeros((mr, H), dtype=torch.bfloat16, device="cuda")
+    status = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    args = (s, hc, hs, to_dev(np.array(counts, np.int32)), to_dev(off.astype(np.int32)), to_dev(ref.pack(ws[0][0])),
+            to_dev(ref.tile(ws[0][1])), Y, status)
+    moe.moe_grouped_gemm_down_mxfp4(*args)
+    assert moe.last_device_status(status) == 0
+    want = Y.clone()
+    status.view(torch.int32)[32] = 1 << 20            # the down product's counter
+    moe.moe_grouped_gemm_down_mxfp4(*args)
+    assert moe.last_device_status(status) == 7
+    Y.zero_()
+    moe.moe_grouped_gemm_down_mxfp4(*args)
+    assert moe.last_device_status(status) == 0
+    assert torch.equal(Y, want)
+
+
 def test_scales_far_apart_and_a_nan_block():
     """Every row and block with a scale of its own; one block of one row NaN:
     that row, and only it, is NaN."""
