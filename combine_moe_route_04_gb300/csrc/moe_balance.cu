@@ -145,6 +145,15 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   const int64_t stride = static_cast<int64_t>(gridDim.x) * kFwdWarps * step;
   const int64_t first = (static_cast<int64_t>(blockIdx.x) * kFwdWarps + warp) * step + lane / G;
   const int64_t warp_first = first - lane / G;
+  // Where a token has as many lanes as picks can be, lane gl counts pick gl.
+  // Otherwise the picks of a row step's per_warp tokens, per_warp k consecutive
+  // ints, go round the warp's lanes (k <= E <= W G, so at most W each): tok is
+  // the token of the step that each is of.
+  constexpr bool kSpread = G < 16;
+  constexpr int kPicks = kSpread ? W : 1;
+  int tok[kPicks];
+#pragma unroll
+  for (int q = 0; q < kPicks; ++q) tok[q] = kSpread ? (lane + 32 * q) / k : (gl < k ? lane / G : per_warp);
   // the masks are read one iteration ahead of the rows they decide on
   bool use[kUnroll];
 #pragma unroll
@@ -154,14 +163,21 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   }
   for (int64_t d = 0; warp_first + d < T; d += stride) {  // uniform across the warp
     Row<V, W, G> r[kUnroll];
-    int id[kUnroll];
+    int id[kUnroll][kPicks];
     bool there[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const int64_t t = first + d + u * per_warp;
       there[u] = use[u];
       r[u].load(logits + t * E + W * gl, gl, E, there[u]);
-      id[u] = there[u] && gl < k ? __ldg(topk_ids + t * k + gl) : 0;
+      const int64_t t0 = warp_first + d + u * per_warp;
+#pragma unroll
+      for (int q = 0; q < kPicks; ++q) {
+        if constexpr (kSpread)
+          id[u][q] = tok[q] < per_warp && t0 + tok[q] < T ? __ldg(topk_ids + t0 * k + lane + 32 * q) : 0;
+        else
+          id[u][q] = there[u] && gl < k ? __ldg(topk_ids + t * k + gl) : 0;
+      }
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
@@ -172,7 +188,16 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     for (int u = 0; u < kUnroll; ++u) {
       float top, sum;
       r[u].exps(top, sum);
-      if (!there[u] || sum == 0.0f) continue;
+      const bool takes = there[u] && sum != 0.0f;
+      const uint32_t who = kSpread ? __ballot_sync(0xffffffffu, takes) : 0u;
+#pragma unroll
+      for (int q = 0; q < kPicks; ++q) {
+        if (tok[q] >= per_warp || !(kSpread ? (who >> (tok[q] * G)) & 1u : takes)) continue;
+        const int e = id[u][q];
+        if (static_cast<unsigned>(e) < static_cast<unsigned>(E)) atomicAdd(&s_cnt[e], 1);
+        else record_status(status, kStatusBounds);
+      }
+      if (!takes) continue;
       const float inv = fast_rcp(sum);
 #pragma unroll
       for (int x = 0; x < V * W; ++x) acc[x] += r[u].v[x] * inv;
@@ -180,14 +205,6 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const float lse = top + fast_log(sum);
         z += lse * lse;
         ++n;
-      }
-      auto count = [&](int e) {
-        if (static_cast<unsigned>(e) < static_cast<unsigned>(E)) atomicAdd(&s_cnt[e], 1);
-        else record_status(status, kStatusBounds);
-      };
-      if (gl < k) count(id[u]);
-      if constexpr (G < 16) {  // more picks than lanes
-        for (int j = gl + G; j < k; j += G) count(__ldg(topk_ids + (first + d + u * per_warp) * k + j));
       }
     }
   }
