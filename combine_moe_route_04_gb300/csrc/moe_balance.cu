@@ -8,7 +8,11 @@
 //   d/dl_te = p_te [ g0 E/n (f_e - sum_j f_j p_tj) + g1 2/n logsumexp(l_t) ]
 // (the counts are constants for the gradient).  Both kernels read the logits
 // once and are bound by memory on large batches and by launch latency on small
-// ones.
+// ones: 262144 x 256 logits with 85% of the tokens taking part take 47 us
+// forward (5.0 TB/s; 6.2 past a fixed 10 us of start and of joining the CTAs'
+// sums) and 82 us backward (6.0 TB/s), 128 x 8 logits 2.8 and 2.1 us.  Until the
+// lanes per token were fixed at compile time (unrolled exchanges) and exp, log
+// and reciprocal left to the SFU they were bound by instructions (81 and 103 us).
 //
 // A token's row is held by a group of G lanes (a power of two up to 32), each
 // with up to eight logits: groups of four consecutive ones (16-byte loads)
@@ -113,7 +117,9 @@ struct Row {
   }
 };
 
-// Rows each warp (or group of lanes) has in flight at a time.
+// Rows each group of lanes has in flight at a time.  (262144 x 256 forward: one
+// 54 us, two 47 us, three or four with fewer threads for the registers 52 and
+// 63 us; rows copied ahead to shared memory 61 us.)
 constexpr int kUnroll = 2;
 
 template <int V, int W, int G>

@@ -5,7 +5,12 @@
 // and the codes e2m1(x 2^(127 - s)), rounded to nearest even and saturated at
 // 6 (the OCP microscaling rule).  Every step is exact in float32 but the
 // rounding to e2m1 itself, so the results are those of the definition to the
-// bit.  All four kernels move data once and are bound by memory.
+// bit.  All four kernels move data once and are bound by memory: 16384 x 4096
+// rows take 25.6 us (6.65 TB/s), 64 weights of 4096 x 1536 145 us (7.0 TB/s) and
+// 149 us back (6.85 TB/s); the measured copy rate is 6.7 TB/s.  On the way the
+// rows' kernel was bound by instructions (38.9 us with 64-bit divisions and
+// maxima one bf16 at a time), hence the two-dimensional grid, the 16-bit pair
+// maxima and the products by the scale in pairs of bf16.
 #include <cstdint>
 
 #include "moe_internal.h"
