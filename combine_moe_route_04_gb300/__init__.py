@@ -158,9 +158,10 @@ def _raw_stream():
     it has one: building a Stream object takes longer than a small launch)."""
     import torch
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
     if raw is None:
         return lambda: torch.cuda.current_stream().cuda_stream
-    return lambda: raw(torch.cuda.current_device())
+    return lambda: raw(device())
 
 
 def _stream(stream):
@@ -409,76 +410,89 @@ def _plan_of(key):
 
 
 def _plan(s) -> _Plan:
+    if type(s) is tuple:
+        return _plan_of(s)
     return _plan_of((s.T, s.H, s.I, s.E, s.k) if isinstance(s, MoEShape) else tuple(s))
 
 
+class _Dtypes:
+    """torch's dtypes by short names, filled at the first call (the package can
+    be imported without torch)."""
+    u8 = None
+
+
+def _dtypes():
+    if _Dtypes.u8 is None:
+        import torch
+        _Dtypes.f32, _Dtypes.bf16, _Dtypes.i32 = torch.float32, torch.bfloat16, torch.int32
+        _Dtypes.bool, _Dtypes.u8 = torch.bool, torch.uint8
+    return _Dtypes
+
+
 def _mxfp4_ptrs(codes, scales, rows, cols, name):
-    import torch
     # the sizes of moe_mxfp4_sizes; the call itself refuses unsupported ones
-    return [_dev_tensor(codes, torch.uint8, rows * cols // 2, name + "codes"),
-            _dev_tensor(scales, torch.uint8, (rows + 127) // 128 * 4 * cols, name + "scales")]
+    u8 = _dtypes().u8
+    return (_dev_tensor(codes, u8, rows * cols // 2, name + "codes"),
+            _dev_tensor(scales, u8, (rows + 127) // 128 * 4 * cols, name + "scales"))
 
 
 def moe_quantize_mxfp4(x, rows, cols, codes, scales, stream=None):
-    import torch
-    out = _mxfp4_ptrs(codes, scales, rows, cols, "")
-    _check(load().moe_quantize_mxfp4(_dev_tensor(x, torch.bfloat16, rows * cols, "x"), rows, cols, *out,
-                                     _stream(stream)), "moe_quantize_mxfp4")
+    c, z = _mxfp4_ptrs(codes, scales, rows, cols, "")
+    rc = (_lib or load()).moe_quantize_mxfp4(_dev_tensor(x, _dtypes().bf16, rows * cols, "x"), rows, cols, c, z,
+                                             _stream(stream))
+    if rc:
+        _check(rc, "moe_quantize_mxfp4")
 
 
 def moe_quantize_weights_mxfp4(w, E, K, N, codes, scales, stream=None):
     """W [E, K, N] (K the reduction axis) to the MXFP4 matrix [E * N, K]."""
-    import torch
-    out = _mxfp4_ptrs(codes, scales, E * N, K, "")
-    _check(load().moe_quantize_weights_mxfp4(_dev_tensor(w, torch.bfloat16, E * K * N, "w"), E, K, N, *out,
-                                             _stream(stream)), "moe_quantize_weights_mxfp4")
+    c, z = _mxfp4_ptrs(codes, scales, E * N, K, "")
+    rc = (_lib or load()).moe_quantize_weights_mxfp4(_dev_tensor(w, _dtypes().bf16, E * K * N, "w"), E, K, N, c, z,
+                                                     _stream(stream))
+    if rc:
+        _check(rc, "moe_quantize_weights_mxfp4")
 
 
 def moe_dequantize_mxfp4(codes, scales, rows, cols, x, stream=None):
-    import torch
-    args = _mxfp4_ptrs(codes, scales, rows, cols, "")
-    _check(load().moe_dequantize_mxfp4(*args, rows, cols, _dev_tensor(x, torch.bfloat16, rows * cols, "x"),
-                                       _stream(stream)), "moe_dequantize_mxfp4")
+    c, z = _mxfp4_ptrs(codes, scales, rows, cols, "")
+    rc = (_lib or load()).moe_dequantize_mxfp4(c, z, rows, cols, _dev_tensor(x, _dtypes().bf16, rows * cols, "x"),
+                                               _stream(stream))
+    if rc:
+        _check(rc, "moe_dequantize_mxfp4")
 
 
 def moe_quantize_permute_mxfp4(s, X, scatter_idx, codes, scales, ws, stream=None):
-    import torch
-    s = _plan(s)
-    args = [_dev_tensor(X, torch.bfloat16, s.T * s.H, "X"),
-            _dev_tensor(scatter_idx, torch.int32, s.T * s.k, "scatter_idx"),
-            *_mxfp4_ptrs(codes, scales, s.max_rows, s.H, ""),
-            _dev_tensor(ws, torch.uint8, 256, "ws")]
-    _check(load().moe_quantize_permute_mxfp4(s.ref, *args, _stream(stream)), "moe_quantize_permute_mxfp4")
+    s, d = _plan(s), _dtypes()
+    rc = (_lib or load()).moe_quantize_permute_mxfp4(
+        s.ref, _dev_tensor(X, d.bf16, s.T * s.H, "X"), _dev_tensor(scatter_idx, d.i32, s.T * s.k, "scatter_idx"),
+        *_mxfp4_ptrs(codes, scales, s.max_rows, s.H, ""), _dev_tensor(ws, d.u8, 256, "ws"), _stream(stream))
+    if rc:
+        _check(rc, "moe_quantize_permute_mxfp4")
 
 
 def moe_grouped_gemm_up_mxfp4(s, x_codes, x_scales, counts, off_pad, wg_codes, wg_scales, wu_codes, wu_scales, h,
                               ws, stream=None):
     """The gate/up product on MXFP4 rows and weights; ws: an MXFP4 workspace,
     or any uint8 buffer of at least 256 bytes, zeroed once."""
-    import torch
-    s = _plan(s)
-    args = [*_mxfp4_ptrs(x_codes, x_scales, s.max_rows, s.H, "x_"),
-            _dev_tensor(counts, torch.int32, s.E, "counts"),
-            _dev_tensor(off_pad, torch.int32, s.E + 1, "off_pad"),
-            *_mxfp4_ptrs(wg_codes, wg_scales, s.E * s.I, s.H, "wg_"),
-            *_mxfp4_ptrs(wu_codes, wu_scales, s.E * s.I, s.H, "wu_"),
-            _dev_tensor(h, torch.bfloat16, s.max_rows * s.I, "h"),
-            _dev_tensor(ws, torch.uint8, 256, "ws")]
-    _check(load().moe_grouped_gemm_up_mxfp4(s.ref, *args, _stream(stream)), "moe_grouped_gemm_up_mxfp4")
+    s, d = _plan(s), _dtypes()
+    rc = (_lib or load()).moe_grouped_gemm_up_mxfp4(
+        s.ref, *_mxfp4_ptrs(x_codes, x_scales, s.max_rows, s.H, "x_"), _dev_tensor(counts, d.i32, s.E, "counts"),
+        _dev_tensor(off_pad, d.i32, s.E + 1, "off_pad"), *_mxfp4_ptrs(wg_codes, wg_scales, s.E * s.I, s.H, "wg_"),
+        *_mxfp4_ptrs(wu_codes, wu_scales, s.E * s.I, s.H, "wu_"), _dev_tensor(h, d.bf16, s.max_rows * s.I, "h"),
+        _dev_tensor(ws, d.u8, 256, "ws"), _stream(stream))
+    if rc:
+        _check(rc, "moe_grouped_gemm_up_mxfp4")
 
 
 def moe_grouped_gemm_down_mxfp4(s, h_codes, h_scales, counts, off_pad, wd_codes, wd_scales, Y, ws, stream=None):
     """The down product on MXFP4 rows and weights; ws as for the gate/up product."""
-    import torch
-    s = _plan(s)
-    args = [*_mxfp4_ptrs(h_codes, h_scales, s.max_rows, s.I, "h_"),
-            _dev_tensor(counts, torch.int32, s.E, "counts"),
-            _dev_tensor(off_pad, torch.int32, s.E + 1, "off_pad"),
-            *_mxfp4_ptrs(wd_codes, wd_scales, s.E * s.H, s.I, "wd_"),
-            _dev_tensor(Y, torch.bfloat16, s.max_rows * s.H, "Y"),
-            _dev_tensor(ws, torch.uint8, 256, "ws")]
-    _check(load().moe_grouped_gemm_down_mxfp4(s.ref, *args, _stream(stream)),
-           "moe_grouped_gemm_down_mxfp4")
+    s, d = _plan(s), _dtypes()
+    rc = (_lib or load()).moe_grouped_gemm_down_mxfp4(
+        s.ref, *_mxfp4_ptrs(h_codes, h_scales, s.max_rows, s.I, "h_"), _dev_tensor(counts, d.i32, s.E, "counts"),
+        _dev_tensor(off_pad, d.i32, s.E + 1, "off_pad"), *_mxfp4_ptrs(wd_codes, wd_scales, s.E * s.H, s.I, "wd_"),
+        _dev_tensor(Y, d.bf16, s.max_rows * s.H, "Y"), _dev_tensor(ws, d.u8, 256, "ws"), _stream(stream))
+    if rc:
+        _check(rc, "moe_grouped_gemm_down_mxfp4")
 
 
 def mxfp4_workspace_size(s) -> int:
@@ -498,17 +512,15 @@ def alloc_mxfp4_workspace(s, device="cuda", stream=None):
 def moe_forward_mxfp4(s, logits, X, wg_codes, wg_scales, wu_codes, wu_scales, wd_codes, wd_scales, out, ws,
                       stream=None):
     """moe_forward with the experts' products in MXFP4 (weights as moe_quantize_weights_mxfp4 leaves them)."""
-    import torch
-    s = _plan(s)
-    bf = torch.bfloat16
-    args = [_dev_tensor(logits, torch.float32, s.T * s.E, "logits"),
-            _dev_tensor(X, bf, s.T * s.H, "X"),
-            *_mxfp4_ptrs(wg_codes, wg_scales, s.E * s.I, s.H, "wg_"),
-            *_mxfp4_ptrs(wu_codes, wu_scales, s.E * s.I, s.H, "wu_"),
-            *_mxfp4_ptrs(wd_codes, wd_scales, s.E * s.H, s.I, "wd_"),
-            _dev_tensor(out, bf, s.T * s.H, "out"),
-            _dev_tensor(ws, torch.uint8, s.mxfp4_ws, "ws")]
-    _check(load().moe_forward_mxfp4(s.ref, *args, _stream(stream)), "moe_forward_mxfp4")
+    s, d = _plan(s), _dtypes()
+    rc = (_lib or load()).moe_forward_mxfp4(
+        s.ref, _dev_tensor(logits, d.f32, s.T * s.E, "logits"), _dev_tensor(X, d.bf16, s.T * s.H, "X"),
+        *_mxfp4_ptrs(wg_codes, wg_scales, s.E * s.I, s.H, "wg_"),
+        *_mxfp4_ptrs(wu_codes, wu_scales, s.E * s.I, s.H, "wu_"),
+        *_mxfp4_ptrs(wd_codes, wd_scales, s.E * s.H, s.I, "wd_"), _dev_tensor(out, d.bf16, s.T * s.H, "out"),
+        _dev_tensor(ws, d.u8, s.mxfp4_ws, "ws"), _stream(stream))
+    if rc:
+        _check(rc, "moe_forward_mxfp4")
 
 
 def balance_workspace_size(s) -> int:
@@ -526,38 +538,32 @@ def alloc_balance_workspace(s, device="cuda", stream=None):
 
 
 def _mask_ptr(mask, n):
-    import torch
     if mask is None:
         return None
-    if isinstance(mask, torch.Tensor) and mask.dtype == torch.bool:
-        return _dev_tensor(mask, torch.bool, n, "mask")
-    return _dev_tensor(mask, torch.uint8, n, "mask")
+    d = _dtypes()
+    return _dev_tensor(mask, d.bool if getattr(mask, "dtype", None) is d.bool else d.u8, n, "mask")
 
 
 def moe_balance_loss(s, logits, topk_ids, mask, counts, num_tokens, mean_probs, losses, ws, stream=None):
     """Per-expert counts and mean probabilities, and losses = (balance, z) of the
     tokens whose mask (uint8 or bool [T], or None) is non-zero."""
-    import torch
-    s = _plan(s)
-    args = [_dev_tensor(logits, torch.float32, s.T * s.E, "logits"),
-            _dev_tensor(topk_ids, torch.int32, s.T * s.k, "topk_ids"),
-            _mask_ptr(mask, s.T),
-            _dev_tensor(counts, torch.int32, s.E, "counts"),
-            _dev_tensor(num_tokens, torch.int32, 1, "num_tokens"),
-            _dev_tensor(mean_probs, torch.float32, s.E, "mean_probs"),
-            _dev_tensor(losses, torch.float32, 2, "losses"),
-            _dev_tensor(ws, torch.uint8, s.balance_ws, "ws")]
-    _check(load().moe_balance_loss(s.ref, *args, _stream(stream)), "moe_balance_loss")
+    s, d = _plan(s), _dtypes()
+    rc = (_lib or load()).moe_balance_loss(
+        s.ref, _dev_tensor(logits, d.f32, s.T * s.E, "logits"), _dev_tensor(topk_ids, d.i32, s.T * s.k, "topk_ids"),
+        _mask_ptr(mask, s.T), _dev_tensor(counts, d.i32, s.E, "counts"),
+        _dev_tensor(num_tokens, d.i32, 1, "num_tokens"), _dev_tensor(mean_probs, d.f32, s.E, "mean_probs"),
+        _dev_tensor(losses, d.f32, 2, "losses"), _dev_tensor(ws, d.u8, s.balance_ws, "ws"), _stream(stream))
+    if rc:
+        _check(rc, "moe_balance_loss")
 
 
 def moe_balance_loss_backward(s, logits, mask, counts, num_tokens, grad_losses, dlogits, stream=None):
     """The gradient of grad_losses[0] * balance + grad_losses[1] * z to the logits."""
-    import torch
-    s = _plan(s)
-    args = [_dev_tensor(logits, torch.float32, s.T * s.E, "logits"),
-            _mask_ptr(mask, s.T),
-            _dev_tensor(counts, torch.int32, s.E, "counts"),
-            _dev_tensor(num_tokens, torch.int32, 1, "num_tokens"),
-            _dev_tensor(grad_losses, torch.float32, 2, "grad_losses"),
-            _dev_tensor(dlogits, torch.float32, s.T * s.E, "dlogits")]
-    _check(load().moe_balance_loss_backward(s.ref, *args, _stream(stream)), "moe_balance_loss_backward")
+    s, d = _plan(s), _dtypes()
+    rc = (_lib or load()).moe_balance_loss_backward(
+        s.ref, _dev_tensor(logits, d.f32, s.T * s.E, "logits"), _mask_ptr(mask, s.T),
+        _dev_tensor(counts, d.i32, s.E, "counts"), _dev_tensor(num_tokens, d.i32, 1, "num_tokens"),
+        _dev_tensor(grad_losses, d.f32, 2, "grad_losses"), _dev_tensor(dlogits, d.f32, s.T * s.E, "dlogits"),
+        _stream(stream))
+    if rc:
+        _check(rc, "moe_balance_loss_backward")
