@@ -208,12 +208,16 @@ Mxfp4Layout mxfp4_layout(const moe_shape& s) {
   return L;
 }
 
-// Tensor maps of a product: rows [max_rows][K/2], weights [E*N][K/2].
+// Tensor maps of a product: rows [max_rows][K/2], weights [E*N][K/2], bf16
+// output [max_rows][N] (null: the output is not bf16).
 bool mxfp4_maps(const moe_shape& s, int64_t K, int64_t N, const uint8_t* rows, const uint8_t* w0, const uint8_t* w1,
-                Mxfp4Maps* m) {
+                const uint16_t* out, Mxfp4Maps* m) {
   const uint64_t kb = static_cast<uint64_t>(K) / 2, wr = static_cast<uint64_t>(s.E) * static_cast<uint64_t>(N);
+  const uint64_t mr = static_cast<uint64_t>(max_rows_of(s));
   for (int i = 0; i < 4; ++i)
-    if (!encode_bytes_2d(&m->t[i], rows, static_cast<uint64_t>(max_rows_of(s)), kb, mxfp4_token_box(i))) return false;
+    if (!encode_bytes_2d(&m->t[i], rows, mr, kb, mxfp4_token_box(i))) return false;
+  m->out = m->t[0];
+  if (out != nullptr && !encode_bf16_2d(&m->out, out, mr, static_cast<uint64_t>(N), 32, 64)) return false;
   return encode_bytes_2d(&m->w0, w0, wr, kb, 128) && encode_bytes_2d(&m->w1, w1, wr, kb, 128);
 }
 
@@ -569,7 +573,7 @@ moe_status moe_grouped_gemm_up_mxfp4(const moe_shape* shape, const uint8_t* x_co
   st = prepare_device(s, &sms, &restore);
   if (st != MOE_OK) return st;
   Mxfp4Maps m;
-  if (!mxfp4_maps(*shape, shape->H, shape->I, x_codes, wg_codes, wu_codes, &m)) return MOE_ERR_CUDA;
+  if (!mxfp4_maps(*shape, shape->H, shape->I, x_codes, wg_codes, wu_codes, h, &m)) return MOE_ERR_CUDA;
   return cuda_status(
       launch_mxfp4_up(*shape, m, x_scales, wg_scales, wu_scales, h, off_pad, counts, ws_status(ws), ws_sched_up(ws),
                       sms, s));
@@ -588,7 +592,7 @@ moe_status moe_grouped_gemm_down_mxfp4(const moe_shape* shape, const uint8_t* h_
   st = prepare_device(s, &sms, &restore);
   if (st != MOE_OK) return st;
   Mxfp4Maps m;
-  if (!mxfp4_maps(*shape, shape->I, shape->H, h_codes, wd_codes, wd_codes, &m)) return MOE_ERR_CUDA;
+  if (!mxfp4_maps(*shape, shape->I, shape->H, h_codes, wd_codes, wd_codes, Y, &m)) return MOE_ERR_CUDA;
   return cuda_status(launch_mxfp4_down(*shape, m, h_scales, wd_scales, Y, off_pad, counts, ws_status(ws),
                                        ws_sched_down(ws), sms, s));
 }
@@ -622,8 +626,8 @@ moe_status moe_forward_mxfp4(const moe_shape* shape, const float* logits, const 
   uint16_t* Y = reinterpret_cast<uint16_t*>(b + L.y);
   uint32_t* status = ws_status(ws);
   Mxfp4Maps up, down;
-  if (!mxfp4_maps(sh, sh.H, sh.I, b + L.x_codes, wg_codes, wu_codes, &up) ||
-      !mxfp4_maps(sh, sh.I, sh.H, b + L.h_codes, wd_codes, wd_codes, &down))
+  if (!mxfp4_maps(sh, sh.H, sh.I, b + L.x_codes, wg_codes, wu_codes, nullptr, &up) ||
+      !mxfp4_maps(sh, sh.I, sh.H, b + L.h_codes, wd_codes, wd_codes, Y, &down))
     return MOE_ERR_CUDA;
   if (launch_route(sh, logits, i32(L.topk_ids), topk_w, i32(L.counts), i32(L.off_pad), i32(L.block_expert),
                    i32(L.num_blocks), i32(L.gather_idx), i32(L.scatter_idx), i32(L.chunk_counts),

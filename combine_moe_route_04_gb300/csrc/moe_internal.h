@@ -178,6 +178,7 @@ struct Mxfp4Maps {
   CUtensorMap t[4];  // rows [max_rows][K/2], boxes of mxfp4_token_box(i) rows
   CUtensorMap w0;  // weights [E*N][K/2] (gate, or down), box 128 rows
   CUtensorMap w1;  // the up weights (down: a copy of w0)
+  CUtensorMap out;  // bf16 output [max_rows][N], box 32 rows x 64 columns (unused where h is quantised)
 };
 cudaError_t launch_mxfp4_up(const moe_shape& s, const Mxfp4Maps& m, const uint8_t* x_scales, const uint8_t* wg_scales,
                             const uint8_t* wu_scales, uint16_t* h, const int32_t* off_pad, const int32_t* counts,

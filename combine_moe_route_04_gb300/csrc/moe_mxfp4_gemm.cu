@@ -52,10 +52,15 @@ constexpr int kRowBytes = kStageK / 2;   // codes of a row in a stage (128-byte 
 constexpr int kWBytes = 128 * kRowBytes; // one block of 128 weight rows
 constexpr int kSfBytes = 512 * kAtoms;   // scale tiles of 128 rows
 constexpr int kFirstEpi = 2;             // epilogue warps follow the loading and the issuing one
-// staging of 32 rows x 128 columns, written by the four warps of a turn
-// (padded so that eight rows start on different banks)
-constexpr int kPitch = 256 + 16;
-constexpr int kStageOutBytes = 32 * kPitch;
+// Staging of 32 rows x 128 bf16 columns, written by the four warps of a turn:
+// two halves of 64 columns, rows of 128 bytes, in the 128-byte swizzle of the
+// stores' tensor map (which also puts eight rows on different banks).
+constexpr int kHalfOutBytes = 32 * 128;
+constexpr int kStageOutBytes = 2 * kHalfOutBytes;
+// byte offset of row t, 16-byte chunk c (of 16) in the staging
+__device__ __forceinline__ int staged_at(int t, int c) {
+  return (c >> 3) * kHalfOutBytes + t * 128 + (((c & 7) ^ (t & 7)) << 4);
+}
 constexpr int kTileRing = 4;             // tile indices on their way from the producer
 
 // What depends on the most rows of a window.
@@ -88,7 +93,7 @@ struct Cfg {
   static constexpr int WIN_OFF = TILE_OFF + kTileRing * 4;
   static constexpr int CNT_OFF = WIN_OFF + (kMaxExperts + 1) * 4;
   static constexpr int OFFP_OFF = CNT_OFF + kMaxExperts * 4;
-  static constexpr int OUT_OFF = (OFFP_OFF + (kMaxExperts + 1) * 4 + 15) / 16 * 16;
+  static constexpr int OUT_OFF = (OFFP_OFF + (kMaxExperts + 1) * 4 + 1023) / 1024 * 1024;
   static constexpr int ALLOC = OUT_OFF + EPI_SPLIT * kStageOutBytes + 1024;
   static_assert(STAGE_BYTES % 1024 == 0, "stages start on swizzle atoms");
   static_assert(SF_COL + STAGES * SF_STAGE_COLS <= 512, "TMEM columns");
@@ -238,6 +243,25 @@ __device__ __forceinline__ void load_piece(uint32_t taddr, uint32_t (&v)[32]) {
   tmem_ld_16x256b_x4(taddr + (16u << 16), v + 16);
 }
 
+// A piece to bf16 pairs: entry 4 j + x holds the columns 8 j + 2 (i % 4) and the
+// next of TMEM lane 8 x + i / 4; rounded alone, or as silu(g) * u.
+__device__ __forceinline__ constexpr int piece_entry(int k) { return (k & 2) * 8 + (k >> 2) * 4 + (k & 1) * 2; }
+__device__ __forceinline__ void round_piece(const uint32_t (&v)[32], uint32_t (&out)[16]) {
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    const int i = piece_entry(k);
+    out[k] = pack_bf16x2(__uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+  }
+}
+__device__ __forceinline__ void gate_piece(const uint32_t (&g)[32], const uint32_t (&u)[32], uint32_t (&out)[16]) {
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    const int i = piece_entry(k);
+    out[k] = pack_bf16x2(silu_mul(__uint_as_float(g[i]), __uint_as_float(u[i])),
+                         silu_mul(__uint_as_float(g[i + 1]), __uint_as_float(u[i + 1])));
+  }
+}
+
 // Four 8 x 8 bf16 matrices to shared memory, transposed: thread i's pairs lie
 // along a matrix row's neighbours 2 (i % 4), row i / 4; the address of row r of
 // matrix m comes from thread 8 m + r.
@@ -247,14 +271,14 @@ __device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uin
                : "memory");
 }
 
-// Writes a piece as bf16 to `out` (shared, [32 rows][kPitch]): packed[4 j + q]
-// holds the pair of columns 8 j + 2 (i % 4) of output column q * 8 + i / 4, so
-// matrix (j, q) lands at rows 8 j.., columns 8 q...
-__device__ __forceinline__ void stage_piece(uint32_t out, const uint32_t (&packed)[16], int lane) {
-  const uint32_t at = out + (lane & 7) * kPitch + (lane >> 3) * 16;  // thread 8 m + r: row r, columns 8 m
+// Writes a piece as bf16 to the staging at `out`, columns 32 q..: packed[4 j + x]
+// holds the rows 8 j + 2 (i % 4) and the next of column x * 8 + i / 4, so matrix
+// (j, x) lands at rows 8 j.., columns 32 q + 8 x...
+__device__ __forceinline__ void stage_piece(uint32_t out, int q, const uint32_t (&packed)[16], int lane) {
+  const uint32_t at = out + staged_at(lane & 7, 4 * q + (lane >> 3));  // thread 8 x + r: row r, columns 8 x
 #pragma unroll
   for (int j = 0; j < 4; ++j)
-    stmatrix_x4_trans(at + 8 * j * kPitch, packed[4 * j], packed[4 * j + 1], packed[4 * j + 2], packed[4 * j + 3]);
+    stmatrix_x4_trans(at + 8 * j * 128, packed[4 * j], packed[4 * j + 1], packed[4 * j + 2], packed[4 * j + 3]);
 }
 
 template <int kMode, int kTok>
@@ -299,6 +323,7 @@ __global__ void __launch_bounds__(Cfg<kTok>::THREADS, 1)
     prefetch_tmap(&maps.t[0]);
     prefetch_tmap(&maps.w0);
     prefetch_tmap(&maps.w1);
+    if (kMode != kUpMxfp4) prefetch_tmap(&maps.out);
   }
   if (warp == 1) {
     tmem_alloc(tmem_slot, 512);
@@ -477,7 +502,7 @@ __global__ void __launch_bounds__(Cfg<kTok>::THREADS, 1)
     const int q = warp & 3;
     const int turn = (warp - kFirstEpi) / 4;
     uint8_t* out = smem + C::OUT_OFF + turn * kStageOutBytes;
-    const uint32_t out_addr = smem_u32(out) + q * 64;  // this warp's columns
+    const uint32_t out_addr = smem_u32(out);
     const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16);
     uint32_t tcount = 0;
     for (uint32_t n = 0;; ++n) {
@@ -505,39 +530,37 @@ __global__ void __launch_bounds__(Cfg<kTok>::THREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(tempty);
       };
-      // v0, v1 to finished bf16; entry 4 j + x: output column x * 8 + lane / 4
-      // (lanes 0-15 of the piece for x < 2), columns 8 j + 2 (lane % 4)
-      auto finish = [&](const uint32_t (&v0)[32], const uint32_t (&v1)[32], uint32_t (&a)[16], uint32_t (&b)[16]) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int i = (x >> 1) * 16 + 4 * j + (x & 1) * 2;
-            const float a0 = __uint_as_float(v0[i]), a1 = __uint_as_float(v0[i + 1]);
-            const float b0 = __uint_as_float(v1[i]), b1 = __uint_as_float(v1[i + 1]);
-            if constexpr (kMode == kDown) {
-              a[4 * j + x] = pack_bf16x2(a0, a1);
-              b[4 * j + x] = pack_bf16x2(b0, b1);
-            } else {
-              a[4 * j + x] = pack_bf16x2(silu_mul(a0, b0), silu_mul(a1, b1));
-            }
-          }
-        }
-      };
-      // a finished piece of the 128 output columns from `col0` to the window's
-      // rows: the turn's four warps put it together in shared memory, then
-      // write eight rows each, sixteen lanes (256 bytes) a row
+      // A finished piece of the 128 output columns from `col0` to the window's
+      // rows: the turn's four warps put it together in shared memory; 32 rows of
+      // bf16 then leave by TMA (written by the warps themselves they held up the
+      // epilogue: down product of 16384 tokens XX us, this YY us), fewer rows and
+      // quantised ones are written by the warps, eight rows each, sixteen lanes a
+      // row.
       auto store = [&](int p, int col0, const uint32_t (&a)[16]) {
         const int64_t r0 = c.row0 + (turn + C::EPI_SPLIT * p) * 32;
         const int left = c.rows - (turn + C::EPI_SPLIT * p) * 32;
+        if (kMode != kUpMxfp4 && q == 0) {
+          if (lane == 0) tma_store_wait_read<0>();
+          __syncwarp();
+        }
         named_barrier_sync(3 + turn, 128);  // the previous piece has been read
-        stage_piece(out_addr, a, lane);
+        stage_piece(out_addr, q, a, lane);
+        if (kMode != kUpMxfp4) fence_proxy_async_smem();
         named_barrier_sync(3 + turn, 128);
+        if (kMode != kUpMxfp4 && left >= 32) {  // alike for the turn's warps
+          if (q == 0 && lane == 0) {
+            tma_store_2d(&maps.out, out, col0, static_cast<int32_t>(r0));
+            tma_store_2d(&maps.out, out + kHalfOutBytes, col0 + 64, static_cast<int32_t>(r0));
+            tma_store_commit();
+          }
+          __syncwarp();
+          return;
+        }
         const int col = col0 + (lane & 15) * 8;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int t = 8 * q + 2 * i + (lane >> 4);
-          const uint4 h = *reinterpret_cast<const uint4*>(out + t * kPitch + (lane & 15) * 16);
+          const uint4 h = *reinterpret_cast<const uint4*>(out + staged_at(t, lane & 15));
           if constexpr (kMode == kUpMxfp4) {
             // four lanes hold a block: the codes are those of quantising the
             // bf16 h
@@ -560,18 +583,22 @@ __global__ void __launch_bounds__(Cfg<kTok>::THREADS, 1)
           if (two) store(p, n0 + 128, b);
         }
       };
-      // finished pieces (down: of each accumulator) and raw ones
-      uint32_t a0[16], b0[16], a[16], b[16], va[C::RAW][32], vb[C::RAW][32];
-      if constexpr (C::RAW == 2 && kMode == kDown) {
-        // rounding is all there is to do (keeping raw sums: 2048 rows x 8 of
-        // 64 experts 97 us, this 73 us)
+      uint32_t va[C::RAW][32], vb[C::RAW][32], done[16];  // raw pieces, a finished one
+      if constexpr (kMode == kDown) {
+        // rounding is all there is to do: every piece is finished as it is read
+        // (keeping raw sums, with windows of 128: 97 us for 73, T 2048)
         uint32_t pa[2][16], pb[2][16];
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
           if (p < mine) {
-            fetch(p, va[0], vb[0]);
+            load_piece(tb + (turn + C::EPI_SPLIT * p) * 32, va[0]);
             tmem_ld_wait();
-            finish(va[0], vb[0], pa[p], pb[p]);
+            round_piece(va[0], pa[p]);
+            if (two) {
+              load_piece(tb + C::ACC1 + (turn + C::EPI_SPLIT * p) * 32, va[0]);
+              tmem_ld_wait();
+              round_piece(va[0], pb[p]);
+            }
           }
         }
         release();
@@ -588,8 +615,8 @@ __global__ void __launch_bounds__(Cfg<kTok>::THREADS, 1)
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
           if (p < mine) {
-            finish(va[p], vb[p], a, b);
-            store_all(p, a, b);
+            gate_piece(va[p], vb[p], done);
+            store(p, n0, done);
           }
         }
       } else if (mine == 0) {
@@ -599,16 +626,18 @@ __global__ void __launch_bounds__(Cfg<kTok>::THREADS, 1)
         fetch(0, va[0], vb[0]);
         tmem_ld_wait();
         if (mine == 2) {
-          finish(va[0], vb[0], a0, b0);
+          gate_piece(va[0], vb[0], done);
           fetch(1, va[0], vb[0]);
           tmem_ld_wait();
         }
         release();
-        if (mine == 2) store_all(0, a0, b0);
-        finish(va[0], vb[0], a, b);
-        store_all(mine - 1, a, b);
+        if (mine == 2) store(0, n0, done);
+        gate_piece(va[0], vb[0], done);
+        store(mine - 1, n0, done);
       }
     }
+    if (kMode != kUpMxfp4 && q == 0 && lane == 0) tma_store_wait_all<0>();  // this thread's stores are written
+    __syncwarp();
   }
 
   tc_fence_before();
