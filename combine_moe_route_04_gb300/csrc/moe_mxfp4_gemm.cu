@@ -20,17 +20,18 @@
 // weights' bytes, 431 MB in 71 us = 6.1 TB/s (0.90 of the measured copy rate);
 // with 1024 (128 experts) operand delivery: the tensor cores alone would take
 // 458 us, the loads alone (8.5 GB from L2) 399 us, both together with the drain
-// take 565 us, 5.8 PFLOP/s.
+// take 559 us, 5.9 PFLOP/s (608 us where a long run meets the power cap).
 //
 // The epilogue would cost as much as the MMAs if it held the accumulators, so
 // its warps take them into registers (as raw sums as far as registers go,
 // otherwise finished to bf16) and hand TMEM back; the rest of the arithmetic and
 // all stores run under the next tile's MMAs.  (With the accumulators held to the
-// end: 821 us where this takes 565.)
+// end: 821 us where this takes 559.)
 //
 // Tried and slower: clusters of four sharing weights and rows by multicast (1352
-// us: the CTAs wait for each other at every stage), CTA pairs with cta_group::2
-// (573 us, down product 468 against 383), stages 128 deep (722 us).
+// us: the CTAs wait for each other at every stage), of two sharing weights (738
+// us), CTA pairs with cta_group::2 (573 us, down product 468 against 383), stages
+// 128 deep (722 us).
 //
 // Roles of the warps: warp 0 loads (per 256-deep stage two boxes of 128 weight
 // rows x 128 bytes, the window's rows in one box, and the scale tiles), warp 1
