@@ -34,7 +34,9 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t amax) {
 __device__ __forceinline__ float scale_inverse(uint32_t s) { return __uint_as_float((254u - s) << 23); }
 
 // 2^(s - 127) as bf16 bits for any scale byte (0 is a subnormal, 255 is NaN).
-__device__ __forceinline__ uint32_t scale_bf16(uint32_t s) { return s == 0u ? 0x0040u : s == kScaleNan ? 0x7FC0u : s << 7; }
+__device__ __forceinline__ uint32_t scale_bf16(uint32_t s) {
+  return s == 0u ? 0x0040u : s == kScaleNan ? 0x7FC0u : s << 7;
+}
 
 // Both halves times m (bf16x2; powers of two here, so exact; subnormals are
 // kept).

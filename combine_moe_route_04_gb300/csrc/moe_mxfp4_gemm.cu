@@ -74,7 +74,7 @@ struct Cfg {
   static constexpr int PIECES = kTok / 32 / EPI_SPLIT;
   static_assert(PIECES == 2, "the epilogue's shape");
   static constexpr int THREADS = (kFirstEpi + EPI_WARPS) * 32;
-  static constexpr int READERS = 1 + EPI_WARPS;            // of a tile index: the MMA lane, a lane of each epilogue warp
+  static constexpr int READERS = 1 + EPI_WARPS;  // of a tile index: the MMA lane, a lane of each epilogue warp
   // Pieces that a warp may keep as raw sums until TMEM is free: 64 registers
   // each, of 168 with ten warps, of 128 with fourteen.
   static constexpr int RAW = kTok == 128 ? 2 : 1;
@@ -166,11 +166,13 @@ __device__ __forceinline__ Win decode(int tile, int NT, int E, const int32_t* of
   const int w = local % nw;
   c.e = lo;
   c.j = local / nw;
-  c.row0 = offp[lo] + kTok * w;
+  // the window's rows lie inside the expert's 128-row blocks, and those inside
+  // the buffers, whatever the counts and offsets given
+  const int64_t first = offp[lo], row0 = first + static_cast<int64_t>(kTok) * w, pad_end = offp[lo + 1];
   c.rows = min(kTok, cnt[lo] - kTok * w);
-  const int pad_end = offp[lo + 1];
-  c.ok = c.rows > 0 && c.rows <= kTok && c.row0 >= 0 && (c.row0 & 63) == 0 && (kTok == 192 || (c.row0 & 127) == 0) && c.row0 + c.rows <= pad_end &&
-         pad_end <= max_rows && (pad_end & 127) == 0;
+  c.ok = c.rows > 0 && first >= 0 && (first & 127) == 0 && (pad_end & 127) == 0 && row0 + c.rows <= pad_end &&
+         pad_end <= max_rows;
+  c.row0 = static_cast<int>(row0);
   return c;
 }
 
@@ -341,7 +343,11 @@ __global__ void __launch_bounds__(Cfg<kTok>::THREADS, 1)
       const int e = lane * per + i;
       int nw = 0;
       if (e < E) {
-        const int c = __ldg(counts + e);
+        int c = __ldg(counts + e);
+        if (c > max_rows) {  // no buffer holds so many: no tiles for them
+          record_status(status, kStatusBounds);
+          c = 0;
+        }
         s_cnt[e] = c;
         nw = c > 0 ? (c - 1) / kTok + 1 : 0;
       }
@@ -394,7 +400,7 @@ __global__ void __launch_bounds__(Cfg<kTok>::THREADS, 1)
         // the smallest box that holds the window (rows past it are not used)
         const int pick = c.rows <= 32 ? 0 : c.rows <= 64 ? 1 : c.rows <= 128 ? 2 : 3;
         const int box = mxfp4_token_box(pick);
-        const bool t_two = C::SF_BLOCKS > 1 && (c.row0 & 127) + c.rows > 128;  // the window's rows span two scale blocks
+        const bool t_two = C::SF_BLOCKS > 1 && (c.row0 & 127) + c.rows > 128;  // its rows span two scale blocks
         for (int ks = 0; c.ok && ks < KS; ++ks, ++it) {
           const uint32_t s = it % C::STAGES;
           if (!mbar_wait(&empty[s], ((it / C::STAGES) & 1u) ^ 1u, abort_flag, status)) {
@@ -665,7 +671,8 @@ cudaError_t launch_tok(const moe_shape& s, const Mxfp4Maps& m, const uint8_t* sf
   {
     std::lock_guard<std::mutex> lock(mu);
     if (dev >= 64 || !done[dev]) {
-      err = cudaFuncSetAttribute(mxfp4_gemm_kernel<kMode, kTok>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<kTok>::ALLOC);
+      err = cudaFuncSetAttribute(mxfp4_gemm_kernel<kMode, kTok>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 Cfg<kTok>::ALLOC);
       if (err != cudaSuccess) return err;
       if (dev < 64) done[dev] = true;
     }
@@ -676,8 +683,8 @@ cudaError_t launch_tok(const moe_shape& s, const Mxfp4Maps& m, const uint8_t* sf
   const int64_t R = static_cast<int64_t>(s.T) * s.k;
   const int64_t max_tiles = (R / kTok + (s.E < R ? s.E : R)) * NT;
   const int grid = static_cast<int>(max_tiles < num_sms ? max_tiles : num_sms);
-  return launch_pdl(mxfp4_gemm_kernel<kMode, kTok>, dim3(grid), dim3(Cfg<kTok>::THREADS), Cfg<kTok>::ALLOC, st, m, sfT, sfW0,
-                    sfW1, D, Dsf, off_pad, counts, s.E, K, N_out, NT, max_rows_of(s), status, sched);
+  return launch_pdl(mxfp4_gemm_kernel<kMode, kTok>, dim3(grid), dim3(Cfg<kTok>::THREADS), Cfg<kTok>::ALLOC, st, m,
+                    sfT, sfW0, sfW1, D, Dsf, off_pad, counts, s.E, K, N_out, NT, max_rows_of(s), status, sched);
 }
 
 // Windows of 128 rows leave shared memory for a fourth stage, and their ten
@@ -705,8 +712,8 @@ cudaError_t launch_mxfp4_up_quantized(const moe_shape& s, const Mxfp4Maps& m, co
                                       const uint8_t* wg_scales, const uint8_t* wu_scales, uint8_t* h_codes,
                                       uint8_t* h_scales, const int32_t* off_pad, const int32_t* counts,
                                       uint32_t* status, uint32_t* sched, int num_sms, cudaStream_t st) {
-  return launch<kUpMxfp4>(s, m, x_scales, wg_scales, wu_scales, h_codes, h_scales, off_pad, counts, status, sched, num_sms,
-                          st);
+  return launch<kUpMxfp4>(s, m, x_scales, wg_scales, wu_scales, h_codes, h_scales, off_pad, counts, status, sched,
+                          num_sms, st);
 }
 
 cudaError_t launch_mxfp4_down(const moe_shape& s, const Mxfp4Maps& m, const uint8_t* h_scales,

@@ -38,7 +38,8 @@ def ref64(logits, ids, mask, g):
         fp = (p * f).sum(1, keepdims=True)
         d[use] = p * (g[0] * E / n * (f - fp) + g[1] * 2 / n * lse[:, None])
         c = np.abs(f - 1.0 / E)
-        mag[use] = p * (abs(g[0]) * E / n * (c + (p * c).sum(1, keepdims=True)) + abs(g[1]) * 2 / n * np.abs(lse[:, None]))
+        mag[use] = p * (abs(g[0]) * E / n * (c + (p * c).sum(1, keepdims=True))
+                        + abs(g[1]) * 2 / n * np.abs(lse[:, None]))
     return counts, n, P, losses, d, mag
 
 
@@ -85,7 +86,8 @@ def check(logits, ids, mask, g=(1e-2, 1e-3)):
     return d
 
 
-CASES = [(1, 1, 1), (1, 2, 2), (3, 5, 5), (31, 8, 2), (128, 8, 2), (97, 37, 3), (513, 64, 8), (1000, 128, 8), (333, 256, 16),
+CASES = [(1, 1, 1), (1, 2, 2), (3, 5, 5), (31, 8, 2), (128, 8, 2), (97, 37, 3), (513, 64, 8), (1000, 128, 8),
+         (333, 256, 16),
          (77, 255, 16), (2050, 100, 4), (4099, 3, 1), (6000, 16, 1), (9001, 66, 7)]
 
 
@@ -209,7 +211,8 @@ def test_after_the_layers_routing_on_a_stream_and_in_a_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(counts, bufs["counts"])
-    wc, wn, wP, wl, wd, mag = ref64(logits.cpu().numpy(), bufs["topk_ids"].cpu().numpy(), None, np.float32([1.0, 0.1]).astype(np.float64))
+    wc, wn, wP, wl, wd, mag = ref64(logits.cpu().numpy(), bufs["topk_ids"].cpu().numpy(), None,
+                                    np.float32([1.0, 0.1]).astype(np.float64))
     assert np.array_equal(counts.cpu().numpy(), wc)
     assert np.all(np.abs(losses.cpu().numpy() - wl) <= 1e-5 * wl)
 
@@ -226,7 +229,8 @@ def test_refusals():
     moe.moe_balance_loss(**good)
     for name, bad, err in (("logits", f(8, 3), ValueError), ("logits", f(8, 4).double(), TypeError),
                            ("logits", f(4, 8).t(), ValueError), ("topk_ids", i(8, 1), ValueError),
-                           ("mask", f(8), TypeError), ("mask", torch.ones(7, dtype=torch.bool, device="cuda"), ValueError),
+                           ("mask", f(8), TypeError),
+                           ("mask", torch.ones(7, dtype=torch.bool, device="cuda"), ValueError),
                            ("ws", ws[:-1], ValueError), ("losses", torch.zeros(2), ValueError)):
         with pytest.raises(err):
             moe.moe_balance_loss(**{**good, name: bad})

@@ -116,6 +116,7 @@ def test_balance_at_the_largest_shape():
     want = np.array([E * (f * p.mean(0)).sum(), (lse ** 2).mean()])
     assert np.all(np.abs(losses.cpu().numpy() - want) <= 2 * rel * want)
     wd = p * (E / T * (f - (p * f).sum(1, keepdims=True)) + 2 / T * lse[:, None])
-    mag = p * (E / T * (np.abs(f - 1 / E) + (p * np.abs(f - 1 / E)).sum(1, keepdims=True)) + 2 / T * np.abs(lse[:, None]))
+    mag = p * (E / T * (np.abs(f - 1 / E) + (p * np.abs(f - 1 / E)).sum(1, keepdims=True))
+               + 2 / T * np.abs(lse[:, None]))
     for at in (0, T // 2, T - 64):
         assert np.all(np.abs(d[at:at + 64].cpu().numpy() - wd) <= 2.0 ** -24 * 200 * mag)

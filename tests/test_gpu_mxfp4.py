@@ -50,7 +50,8 @@ def run_quantize(bits):
     return codes, scales
 
 
-@pytest.mark.parametrize("rows,cols", [(1, 128), (3, 256), (127, 1408), (128, 1024), (129, 640), (300, 2176), (5, 32768)])
+@pytest.mark.parametrize("rows,cols", [(1, 128), (3, 256), (127, 1408), (128, 1024), (129, 640), (300, 2176),
+                                       (5, 32768)])
 def test_quantize_and_back_to_the_bit(rows, cols):
     torch = need_gpu()
     import combine_moe_route_04_gb300 as moe
@@ -313,7 +314,8 @@ def test_scales_far_apart_and_a_nan_block():
     sig = 1.0 / (1.0 + np.exp(-np.clip(g, -700, 700)))
     want = g * sig * u
     eg, eu = bounds(H, g, gm), bounds(H, u, um)
-    tol = 1.1 * eg * np.abs(u) + np.abs(g * sig) * eu + 1.1 * eg * eu + (2.0 ** -18 * (1 + np.abs(g)) + 2.0 ** -8) * np.abs(want) + 1e-30
+    tol = 1.1 * eg * np.abs(u) + np.abs(g * sig) * eu + 1.1 * eg * eu \
+        + (2.0 ** -18 * (1 + np.abs(g)) + 2.0 ** -8) * np.abs(want) + 1e-30
     assert np.all(np.abs(got[:off[-1]] - want)[real] <= tol[real])
 
 
@@ -486,6 +488,12 @@ def test_counts_out_of_range_are_reported():
     moe.moe_grouped_gemm_up_mxfp4(s, xc, xs, torch.tensor([200, 1], **i32), torch.tensor([0, 128, 256], **i32), wc, wsc,
                                   wc, wsc, h, ws)
     assert moe.last_device_status(ws) == 7
+    for counts, off, want in (([60, 4], [0, 128, 128 * 64], 7), ([60, 4], [0, 100, 256], 7),
+                              ([60, 4], [128, 0, 128], 7), ([1 << 30, 4], [0, 128, 256], 7),
+                              ([-5, 4], [0, 128, 256], 0)):
+        moe.moe_grouped_gemm_up_mxfp4(s, xc, xs, torch.tensor(counts, **i32), torch.tensor(off, **i32), wc, wsc, wc,
+                                      wsc, h, ws)
+        assert moe.last_device_status(ws) == want
     moe.moe_grouped_gemm_up_mxfp4(s, xc, xs, torch.tensor([60, 4], **i32), torch.tensor([0, 128, 256], **i32), wc, wsc,
                                   wc, wsc, h, ws)
     assert moe.last_device_status(ws) == 0
