@@ -10,9 +10,16 @@
 // once and are bound by memory on large batches and by launch latency on small
 // ones: 262144 x 256 logits with 85% of the tokens taking part take 47 us
 // forward (5.0 TB/s; 6.2 past a fixed 10 us of start and of joining the CTAs'
-// sums) and 82 us backward (6.0 TB/s), 128 x 8 logits 2.8 and 2.1 us.  Until the
+// sums) and 82 us backward (6.0 TB/s), 128 x 8 logits 3.0 and 2.1 us.  Until the
 // lanes per token were fixed at compile time (unrolled exchanges) and exp, log
 // and reciprocal left to the SFU they were bound by instructions (81 and 103 us).
+//
+// What a kernel of this library wrote just before (picks, counts, partial sums)
+// is not read through the non-coherent path: under programmatic dependent launch
+// a CTA may become resident before it is written.  Picks and counts are cached in
+// L1 all the same (__ldca): every warp of the backward kernel reads all counts,
+// and past L1 its smallest calls took a quarter longer, mid-sized ones three
+// times as long.
 //
 // A token's row is held by a group of G lanes (a power of two up to 32), each
 // with up to eight logits: groups of four consecutive ones (16-byte loads)
@@ -159,7 +166,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   constexpr int kPicks = kSpread ? W : 1;
   int tok[kPicks];
 #pragma unroll
-  for (int q = 0; q < kPicks; ++q) tok[q] = kSpread ? (lane + 32 * q) / k : (gl < k ? lane / G : per_warp);
+  for (int q = 0; q < kPicks; ++q) {
+    tok[q] = per_warp;  // none
+    if (kSpread ? 32 * q < per_warp * k : gl < k) tok[q] = kSpread ? (lane + 32 * q) / k : lane / G;
+  }
   // the masks are read one iteration ahead of the rows they decide on
   bool use[kUnroll];
 #pragma unroll
@@ -179,10 +189,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       const int64_t t0 = warp_first + d + u * per_warp;
 #pragma unroll
       for (int q = 0; q < kPicks; ++q) {
+        id[u][q] = 0;
+        if (kSpread && 32 * q >= per_warp * k) break;  // uniform
         if constexpr (kSpread)
-          id[u][q] = tok[q] < per_warp && t0 + tok[q] < T ? __ldg(topk_ids + t0 * k + lane + 32 * q) : 0;
+          id[u][q] = tok[q] < per_warp && t0 + tok[q] < T ? __ldca(topk_ids + t0 * k + lane + 32 * q) : 0;
         else
-          id[u][q] = there[u] && gl < k ? __ldg(topk_ids + t * k + gl) : 0;
+          id[u][q] = there[u] && gl < k ? __ldca(topk_ids + t * k + gl) : 0;
       }
     }
 #pragma unroll
@@ -198,6 +210,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       const uint32_t who = kSpread ? __ballot_sync(0xffffffffu, takes) : 0u;
 #pragma unroll
       for (int q = 0; q < kPicks; ++q) {
+        if (kSpread && 32 * q >= per_warp * k) break;
         if (tok[q] >= per_warp || !(kSpread ? (who >> (tok[q] * G)) & 1u : takes)) continue;
         const int e = id[u][q];
         if (static_cast<unsigned>(e) < static_cast<unsigned>(E)) atomicAdd(&s_cnt[e], 1);
@@ -370,10 +383,10 @@ __global__ void __launch_bounds__(kBwdThreads)
   const int gl = lane & (G - 1);
   constexpr int per_warp = 32 / G;
   constexpr int kWarps = kBwdThreads / 32;
-  const int n = __ldg(num_tokens);
+  const int n = __ldca(num_tokens);
   const float inv_n = n > 0 ? 1.0f / static_cast<float>(n) : 0.0f;
-  const float a = __ldg(grad_losses) * static_cast<float>(E) * inv_n;
-  const float b = __ldg(grad_losses + 1) * 2.0f * inv_n;
+  const float a = __ldca(grad_losses) * static_cast<float>(E) * inv_n;
+  const float b = __ldca(grad_losses + 1) * 2.0f * inv_n;
   // f_e - 1/E, whose differences are the gradient's: formed from integers, so
   // that f_e - sum f p loses nothing to cancellation (the p sum to 1)
   float f[V * W];
@@ -383,7 +396,7 @@ __global__ void __launch_bounds__(kBwdThreads)
     f[x] = 0.0f;
     if (e < E && n > 0) {
       const int64_t nk = static_cast<int64_t>(n) * k;
-      f[x] = static_cast<float>(static_cast<int64_t>(__ldg(counts + e)) * E - nk) /
+      f[x] = static_cast<float>(static_cast<int64_t>(__ldca(counts + e)) * E - nk) /
              (static_cast<float>(nk) * static_cast<float>(E));
     }
   }

@@ -11,6 +11,8 @@
 // rows' kernel was bound by instructions (38.9 us with 64-bit divisions and
 // maxima one bf16 at a time), hence the two-dimensional grid, the 16-bit pair
 // maxima and the products by the scale in pairs of bf16.
+// Inputs may be what an earlier kernel of a chain of dependent launches wrote, so
+// they are read past L1 (__ldcg), not through the non-coherent path.
 #include <cstdint>
 
 #include "moe_internal.h"
@@ -42,7 +44,7 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const uint16_t* __re
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     v[u] = make_uint4(0u, 0u, 0u, 0u);
-    if (there && u * 256 < left) v[u] = __ldg(reinterpret_cast<const uint4*>(src + u * 256));
+    if (there && u * 256 < left) v[u] = __ldcg(reinterpret_cast<const uint4*>(src + u * 256));
   }
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
@@ -75,8 +77,8 @@ __global__ void __launch_bounds__(256) dequantize_rows_kernel(const uint8_t* __r
   for (int u = 0; u < 4; ++u) {
     code[u] = sb[u] = 0u;
     if (u * 256 < left) {
-      code[u] = __ldg(reinterpret_cast<const uint32_t*>(src + u * 128));
-      sb[u] = __ldg(sc + u * 1024);
+      code[u] = __ldcg(reinterpret_cast<const uint32_t*>(src + u * 128));
+      sb[u] = __ldcg(sc + u * 1024);
     }
   }
 #pragma unroll
@@ -115,7 +117,7 @@ __global__ void __launch_bounds__(256) quantize_weights_kernel(const uint16_t* _
     const uint16_t* src = w + (e * K + k0 + 32 * b) * N + n0 + 2 * lane;
     uint32_t v[32];
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = __ldg(reinterpret_cast<const uint32_t*>(src + i * N));
+    for (int i = 0; i < 32; ++i) v[i] = __ldcg(reinterpret_cast<const uint32_t*>(src + i * N));
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       uint32_t m = 0u;
@@ -171,7 +173,7 @@ __global__ void __launch_bounds__(256) quantize_permute_kernel(const uint16_t* _
   pdl_wait();
   int my_row = -1;  // lane j < k: row of (t, j)
   if (lane < k) {
-    const int32_t r = __ldg(scatter_idx + t * k + lane);
+    const int32_t r = __ldcg(scatter_idx + t * k + lane);
     if (r >= 0 && r < max_rows) my_row = r;
     else record_status(status, kStatusBounds);
   }
@@ -179,7 +181,7 @@ __global__ void __launch_bounds__(256) quantize_permute_kernel(const uint16_t* _
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     v[u] = make_uint4(0u, 0u, 0u, 0u);
-    if (c0 + u * 256 < H) v[u] = __ldg(reinterpret_cast<const uint4*>(X + t * H + c0 + u * 256));
+    if (c0 + u * 256 < H) v[u] = __ldcg(reinterpret_cast<const uint4*>(X + t * H + c0 + u * 256));
   }
   uint32_t code[4], word[4];
 #pragma unroll

@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(Cfg<kTok>::THREADS, 1)
       const int e = lane * per + i;
       int nw = 0;
       if (e < E) {
-        int c = __ldg(counts + e);
+        int c = __ldcg(counts + e);
         if (c > max_rows) {  // no buffer holds so many: no tiles for them
           record_status(status, kStatusBounds);
           c = 0;
@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(Cfg<kTok>::THREADS, 1)
     }
     if (lane == 31 && 32 * per == E) s_win[E] = incl;
   } else if (warp == 3) {
-    for (int e = lane; e <= E; e += 32) s_offp[e] = __ldg(off_pad + e);
+    for (int e = lane; e <= E; e += 32) s_offp[e] = __ldcg(off_pad + e);
   }
   tc_fence_before();
   __syncthreads();
