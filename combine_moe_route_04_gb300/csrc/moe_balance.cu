@@ -94,13 +94,13 @@ struct Row {
       const bool in = there && W * (gl + G * i) < E;
       if constexpr (W == 4) {
         float4 q = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-        if (in) q = __ldg(reinterpret_cast<const float4*>(row + 4 * G * i));
+        if (in) q = __ldcg(reinterpret_cast<const float4*>(row + 4 * G * i));
         v[4 * i] = q.x;
         v[4 * i + 1] = q.y;
         v[4 * i + 2] = q.z;
         v[4 * i + 3] = q.w;
       } else {
-        v[i] = in ? __ldg(row + G * i) : -INFINITY;
+        v[i] = in ? __ldcg(row + G * i) : -INFINITY;
       }
     }
   }
@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u) {
     const int64_t t = first + u * per_warp;
-    use[u] = t < T && (mask == nullptr || __ldg(mask + t) != 0);
+    use[u] = t < T && (mask == nullptr || __ldca(mask + t) != 0);
   }
   for (int64_t d = 0; warp_first + d < T; d += stride) {  // uniform across the warp
     Row<V, W, G> r[kUnroll];
@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const int64_t t = first + d + stride + u * per_warp;
-      use[u] = t < T && (mask == nullptr || __ldg(mask + t) != 0);
+      use[u] = t < T && (mask == nullptr || __ldca(mask + t) != 0);
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
@@ -412,7 +412,7 @@ __global__ void __launch_bounds__(kBwdThreads)
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const int64_t t = t0 + u * per_warp;
-      there[u] = t < T && (mask == nullptr || __ldg(mask + t) != 0);
+      there[u] = t < T && (mask == nullptr || __ldca(mask + t) != 0);
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) r[u].load(logits + (t0 + u * per_warp) * E + W * gl, gl, E, there[u]);

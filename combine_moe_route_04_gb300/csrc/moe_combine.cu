@@ -12,6 +12,8 @@
 // out.  (Measured: pieces for every shape cost the large workloads 1.5%; one
 // warp per token left decode's 64 tokens on 8 SMs, 13 us slower.)
 // No atomics: results are bitwise reproducible.
+// Y, the rows and the weights are what earlier kernels of the chain wrote, some
+// of it perhaps while this one is already resident: read past L1 (__ldcg).
 #include <cstdint>
 
 #include "moe_device.cuh"
@@ -49,8 +51,8 @@ __global__ void __launch_bounds__(256, 2) combine_kernel(const uint16_t* __restr
     int my_row = -1;
     float my_w = 0.0f;
     if (lane < k) {
-      const int64_t r = __ldg(scatter_idx + t * k + lane);
-      my_w = __ldg(topk_w + t * k + lane);
+      const int64_t r = __ldcg(scatter_idx + t * k + lane);
+      my_w = __ldcg(topk_w + t * k + lane);
       if (r >= 0 && r < max_rows) {
         my_row = static_cast<int>(r);
       } else if (status != nullptr && first == 0) {
@@ -74,7 +76,7 @@ __global__ void __launch_bounds__(256, 2) combine_kernel(const uint16_t* __restr
         for (int cc = 0; cc < CH; ++cc) {
           const int v = c0 + cc * 32 + lane;
           y[j][cc] = make_uint4(0u, 0u, 0u, 0u);
-          if (j < k && rows[j] >= 0 && v < vpr) y[j][cc] = __ldg(Y4 + static_cast<int64_t>(rows[j]) * vpr + v);
+          if (j < k && rows[j] >= 0 && v < vpr) y[j][cc] = __ldcg(Y4 + static_cast<int64_t>(rows[j]) * vpr + v);
         }
       }
 #pragma unroll

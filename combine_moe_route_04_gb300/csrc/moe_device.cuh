@@ -144,6 +144,11 @@ __device__ __forceinline__ void fence_acq_rel_gpu() { asm volatile("fence.acq_re
 // before it touches memory that an earlier kernel writes or reads; wait
 // returns when the previous grid has completed and its writes are visible.
 // Without the launch attribute both are no-ops.
+// A kernel may therefore be resident, and share an SM's L1, while an earlier
+// one still reads or writes its inputs: no device memory is read through the
+// non-coherent path (__ldg, or a plain read of a const __restrict__ pointer,
+// which the compiler may turn into one).  What is read once goes past L1
+// (__ldcg); what neighbouring warps share may stay in it (__ldca).
 __device__ __forceinline__ void pdl_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }

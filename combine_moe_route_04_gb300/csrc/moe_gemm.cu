@@ -319,6 +319,9 @@ __global__ void __launch_bounds__(S_THREADS, 1)
   if (warp == 2) {
     // windows per expert (ceil(count / 256)) -> exclusive scan, E <= 256
     constexpr int per = MAX_E / 32;
+    int cnt[per];  // all loads ahead of the first store
+#pragma unroll
+    for (int i = 0; i < per; ++i) cnt[i] = lane * per + i < E ? __ldcg(counts + lane * per + i) : 0;
     int loc[per];
     int sum = 0;
 #pragma unroll
@@ -326,9 +329,8 @@ __global__ void __launch_bounds__(S_THREADS, 1)
       const int e = lane * per + i;
       int nw = 0;
       if (e < E) {
-        const int cnt = __ldg(counts + e);
-        s_cnt[e] = cnt;  // the tile decoder's copy
-        nw = cnt > 0 ? (cnt + S_TOK - 1) / S_TOK : 0;
+        s_cnt[e] = cnt[i];  // the tile decoder's copy
+        nw = cnt[i] > 0 ? (cnt[i] + S_TOK - 1) / S_TOK : 0;
       }
       loc[i] = nw;
       sum += nw;
@@ -349,7 +351,12 @@ __global__ void __launch_bounds__(S_THREADS, 1)
     if (lane == 31 && 32 * per == E) s_win_off[E] = incl;
   } else if (warp == 3) {
     // the tile decoder's copy of the padded offsets
-    for (int e = lane; e <= E; e += 32) s_offp[e] = __ldg(off_pad + e);
+    int off[MAX_E / 32 + 1];
+#pragma unroll
+    for (int i = 0; i <= MAX_E / 32; ++i) off[i] = lane + 32 * i <= E ? __ldcg(off_pad + lane + 32 * i) : 0;
+#pragma unroll
+    for (int i = 0; i <= MAX_E / 32; ++i)
+      if (lane + 32 * i <= E) s_offp[lane + 32 * i] = off[i];
   }
   tc_fence_before();
   __syncthreads();
@@ -768,7 +775,7 @@ __global__ void scatter_rows_kernel(const uint16_t* __restrict__ X, const int32_
     const int c0 = static_cast<int>(item % nchunk) * CH;
     int my_row = -1;  // lane j < k: row of (t, j)
     if (lane < k) {
-      const int32_t r = __ldg(scatter_idx + static_cast<int64_t>(t) * k + lane);
+      const int32_t r = __ldcg(scatter_idx + static_cast<int64_t>(t) * k + lane);
       if (r >= 0 && r < max_rows) my_row = r;
       else record_status(status, kStatusBounds);
     }
@@ -778,7 +785,7 @@ __global__ void scatter_rows_kernel(const uint16_t* __restrict__ X, const int32_
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int idx = lane + 32 * u;
-      if (idx < nv) v[u] = __ldg(src + idx);
+      if (idx < nv) v[u] = __ldcg(src + idx);
     }
     for (int j = 0; j < k; ++j) {
       const int row = __shfl_sync(0xffffffffu, my_row, j);

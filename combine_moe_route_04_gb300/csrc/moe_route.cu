@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(kTopkThreads) route_topk_hist_kernel(
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
       const int e = lane + 32 * i;
-      key[i] = (e < E) ? pick_key(__ldg(row + e), e) : 0ull;
+      key[i] = (e < E) ? pick_key(__ldcg(row + e), e) : 0ull;
     }
     // this lane's keys in descending order (a small exchange network)
 #pragma unroll
@@ -347,7 +347,7 @@ __device__ __forceinline__ int64_t entry_row(int t, int e, int E, int nch, const
     record_status(status, kStatusBounds);
     return -1;
   }
-  const int64_t row = static_cast<int64_t>(s_off[e]) + __ldg(chunk_base + static_cast<int64_t>(e) * nch + t / kChunkTokens) +
+  const int64_t row = static_cast<int64_t>(s_off[e]) + __ldcg(chunk_base + static_cast<int64_t>(e) * nch + t / kChunkTokens) +
                       rank;
   if (row < 0 || row >= max_rows) {
     record_status(status, kStatusBounds);
@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(256) route_scatter_kernel(int T, int E, int k,
   const int64_t nthreads = static_cast<int64_t>(gridDim.x) * blockDim.x;
   for (int64_t i = gtid; i < static_cast<int64_t>(T) * k; i += nthreads) {
     const int t = static_cast<int>(i / k);
-    const int64_t row = entry_row(t, topk_ids[i], E, nch, s_off, chunk_base, scatter_idx[i], max_rows, status);
+    const int64_t row = entry_row(t, __ldcg(topk_ids + i), E, nch, s_off, chunk_base, scatter_idx[i], max_rows, status);
     if (row < 0) continue;
     scatter_idx[i] = static_cast<int32_t>(row);
     gather_idx[row] = t;
@@ -440,7 +440,7 @@ __global__ void __launch_bounds__(256) permute_gather_kernel(int T, int H, int E
     int my_row = -1;  // lane j < k: row of (t, j)
     if (lane < k) {
       const int64_t i = static_cast<int64_t>(t) * k + lane;
-      const int64_t row = entry_row(t, __ldg(topk_ids + i), E, nch, s_off, chunk_base, __ldg(local_rank + i),
+      const int64_t row = entry_row(t, __ldcg(topk_ids + i), E, nch, s_off, chunk_base, __ldcg(local_rank + i),
                                     max_rows, status);
       if (row >= 0) {
         my_row = static_cast<int>(row);
@@ -456,7 +456,7 @@ __global__ void __launch_bounds__(256) permute_gather_kernel(int T, int H, int E
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int idx = lane + 32 * u;
-      if (idx < nv) v[u] = __ldg(src + idx);
+      if (idx < nv) v[u] = __ldcg(src + idx);
     }
     for (int j = 0; j < k; ++j) {
       const int row = __shfl_sync(0xffffffffu, my_row, j);
