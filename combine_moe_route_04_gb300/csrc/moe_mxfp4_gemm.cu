@@ -180,7 +180,15 @@ __device__ __forceinline__ Win decode(int tile, int NT, int E, const int32_t* of
 // tile b): windows differ in rows, and CTAs that got short ones take more.  The
 // producer publishes each index to the other roles through a ring in shared
 // memory; the CTA that stops drawing last clears the counter for the next
-// launch.
+// launch.  That CTA also knows whether the launch started from a cleared
+// counter: the word behind it counts the CTAs that have stopped (bits 0-9),
+// sums their indexes plus one (bits 10-29), and gets bit 30 from the one that
+// drew 0, the first value of a cleared counter.  With anything else in either
+// word the sum comes out wrong (tiles may have been left out): an error.
+constexpr int kMaxGrid = 1023;
+__device__ __forceinline__ uint32_t stopped(uint32_t ctas, uint32_t index_sum, bool drew_zero) {
+  return ctas | (index_sum << 10) | (drew_zero ? 1u << 30 : 0u);
+}
 struct TileRing {
   uint64_t* full;         // [kTileRing] one arrival (the producer)
   uint64_t* empty;        // [kTileRing] Cfg::READERS arrivals
@@ -385,6 +393,7 @@ __global__ void __launch_bounds__(Cfg<kTok>::THREADS, 1)
       const uint64_t pol_t = policy_evict_last();
       uint32_t it = 0;
       int tile = blockIdx.x;
+      bool drew_zero = false;
       bool stop = !ring_put(ring, 0, tile, abort_flag, status);
       for (uint32_t n = 0; !stop && tile < total; ++n) {
         const uint32_t drawn = atomicAdd(sched, 1u);  // the next tile: needed after this one's loads
@@ -426,6 +435,7 @@ __global__ void __launch_bounds__(Cfg<kTok>::THREADS, 1)
           bulk_load(sf + 2 * kSfBytes, sfT + tsf, sfb, &full[s]);
           if (t_two) bulk_load(sf + 3 * kSfBytes, sfT + tsf + KT * 512, sfb, &full[s]);
         }
+        drew_zero |= drawn == 0u;
         if (stop) break;
         // a cleared counter gives at most total + grid - 1 here
         const uint64_t next = static_cast<uint64_t>(gridDim.x) + drawn;
@@ -434,7 +444,11 @@ __global__ void __launch_bounds__(Cfg<kTok>::THREADS, 1)
         stop = !ring_put(ring, n + 1, tile, abort_flag, status);
       }
       __threadfence();
-      if (atomicAdd(sched + 1, 1u) == gridDim.x - 1) {  // every CTA has drawn its last index
+      const uint32_t mine = stopped(1u, blockIdx.x + 1u, drew_zero);
+      const uint32_t seen = atomicAdd(sched + 1, mine) + mine;
+      if ((seen & 0x3FFu) == gridDim.x) {  // every CTA has drawn its last index
+        const uint32_t clean = stopped(gridDim.x, gridDim.x * (gridDim.x + 1u) / 2u, total > 0);
+        if (seen != clean) record_status(status, kStatusBounds);
         atomicExch(sched, 0u);
         atomicExch(sched + 1, 0u);
       }
@@ -682,6 +696,7 @@ cudaError_t launch_tok(const moe_shape& s, const Mxfp4Maps& m, const uint8_t* sf
   const int NT = kMode == kDown ? (N_out + 255) / 256 : N_out / 128;
   const int64_t R = static_cast<int64_t>(s.T) * s.k;
   const int64_t max_tiles = (R / kTok + (s.E < R ? s.E : R)) * NT;
+  if (num_sms > kMaxGrid) num_sms = kMaxGrid;
   const int grid = static_cast<int>(max_tiles < num_sms ? max_tiles : num_sms);
   return launch_pdl(mxfp4_gemm_kernel<kMode, kTok>, dim3(grid), dim3(Cfg<kTok>::THREADS), Cfg<kTok>::ALLOC, st, m,
                     sfT, sfW0, sfW1, D, Dsf, off_pad, counts, s.E, K, N_out, NT, max_rows_of(s), status, sched);

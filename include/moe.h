@@ -333,7 +333,9 @@ moe_status moe_quantize_permute_mxfp4(const moe_shape *shape, const moe_bf16 *X,
  *   x_codes, x_scales: the matrix [max_rows, H] in expert order
  *   wg_*, wu_*:        the matrices [E*I, H]
  *   ws: moe_mxfp4_workspace_size bytes, or at least 256 bytes of which the
- *       first 256 were cleared (the status word)
+ *       first 256 were cleared (the status word and the tile counters; a
+ *       product that finds its tile counter anything but cleared reports
+ *       MOE_ERR_DEVICE_BOUNDS, and some of its rows may not be written)
  * The scales are applied by the tensor cores, sums are float32, h is rounded
  * once. */
 moe_status moe_grouped_gemm_up_mxfp4(const moe_shape *shape, const uint8_t *x_codes,
