@@ -282,10 +282,18 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     __syncthreads();
     if (tid == 0) {
       fence_acq_rel_gpu();  // release: the CTA's partials (ordered by the barrier) before the arrival
-      const uint32_t ticket = atomicAdd(counter, 1u);
-      if (ticket >= gridDim.x) record_status(status, kStatusBounds);  // the counter was not cleared
-      s_last = ticket == gridDim.x - 1 ? 1 : 0;
-      if (ticket >= gridDim.x - 1) *counter = 0u;
+      // The word counts the CTAs that have arrived (bits 0-9) and sums their
+      // indexes plus one above.  The last one is known by the sum; c of them
+      // cannot sum to less than c (c + 1) / 2, and only the whole grid sums to
+      // `all`: anything else was in the word before the launch (a leftover that
+      // is itself the state of some CTAs' arrivals is not told from them).
+      const uint32_t mine = 1u | ((blockIdx.x + 1u) << 10);
+      const uint32_t seen = atomicAdd(counter, mine) + mine;
+      const uint32_t c = seen & 0x3FFu, sum = seen >> 10, all = gridDim.x * (gridDim.x + 1u) / 2u;
+      if (sum < c * (c + 1u) / 2u || sum > all || (sum == all) != (c == gridDim.x))
+        record_status(status, kStatusBounds);
+      s_last = sum == all ? 1 : 0;
+      if (sum >= all) *counter = 0u;
       fence_acq_rel_gpu();  // acquire: every other CTA's partials
     }
     __syncthreads();

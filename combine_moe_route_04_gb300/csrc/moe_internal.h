@@ -195,7 +195,7 @@ cudaError_t launch_mxfp4_down(const moe_shape& s, const Mxfp4Maps& m, const uint
 
 // Balance loss.  partials: the workspace region past its first 256 bytes
 // (balance_partial_bytes); counter: a uint32 that is zero between calls.
-constexpr int kBalanceMaxCtas = 256;
+constexpr int kBalanceMaxCtas = 256;  // at most 1023: the counter has ten bits for them
 inline size_t balance_partial_bytes(const moe_shape& s) {
   return static_cast<size_t>(kBalanceMaxCtas) * (static_cast<size_t>(s.E) * 8 + 8);
 }

@@ -389,7 +389,8 @@ moe_status moe_balance_workspace_size(const moe_shape *shape, size_t *bytes);
  *   mean_probs [E] float32 out, losses [2] float32 out
  *   ws         moe_balance_workspace_size bytes, the first 256 cleared once
  *              (moe_workspace_init); an expert id out of range is not counted
- *              and reported by moe_last_device_status
+ *              and reported by moe_last_device_status, as is a counter that
+ *              was not cleared (the results may then be stale)
  * H and I of the shape are not used. */
 moe_status moe_balance_loss(const moe_shape *shape, const float *logits, const int32_t *topk_ids,
                             const uint8_t *mask, int32_t *counts, int32_t *num_tokens,

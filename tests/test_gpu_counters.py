@@ -94,3 +94,73 @@ def test_a_product_without_rows_has_nothing_to_report(which):
         assert moe.last_device_status(ws) == 0
         assert bool((out == -7.0).all())
         assert not ws.any()
+
+
+@pytest.mark.parametrize("T,E,k", [(3000, 64, 4), (700, 255, 3), (50000, 8, 2)])
+def test_the_balance_loss_reports_what_its_counter_held(T, E, k):
+    torch = need_gpu()
+    import combine_moe_route_04_gb300 as moe
+    s = (T, 128, 128, E, k)
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    logits = torch.randn((T, E), generator=gen, device="cuda")
+    ids = logits.topk(k, dim=1).indices.int().contiguous()
+    counts, num = torch.zeros(E, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    P, losses = torch.zeros(E, device="cuda"), torch.zeros(2, device="cuda")
+    ws = moe.alloc_balance_workspace(s)
+    word = ws[:256].view(torch.int32)[60:61]          # the CTAs' counter
+
+    def call():
+        for t in (counts, num, P, losses):
+            t.fill_(-5)
+        moe.moe_balance_loss(s, logits, ids, None, counts, num, P, losses, ws)
+        return moe.last_device_status(ws), [t.clone() for t in (counts, num, P, losses)]
+
+    def same(a, b):
+        return all(torch.equal(x, y) for x, y in zip(a, b))
+
+    status, want = call()
+    assert status == 0 and word.item() == 0 and want[1].item() == T
+    for left in (1, 2, 5, 9):                         # in the count: reported, and no harm done
+        word.fill_(left)
+        status, got = call()
+        assert status == BOUNDS and same(got, want), left
+        assert word.item() == 0
+    for left in (1 << 10, 7 << 10, 1 << 20, 1 << 31, 0x12345678, -1):
+        word.fill_(left - (1 << 32) if left >= 1 << 31 else left)
+        assert call()[0] == BOUNDS, left
+        word.zero_()
+        status, got = call()
+        assert status == 0 and same(got, want), left
+
+
+def test_the_balance_loss_waits_for_its_slowest_cta():
+    """A leftover of one, and one CTA with nearly all of the work: the CTA before it
+    must not take itself for the last."""
+    torch = need_gpu()
+    import combine_moe_route_04_gb300 as moe
+    T, E, k = 1 << 18, 256, 4
+    s = (T, 128, 128, E, k)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    logits = torch.randn((T, E), generator=torch.Generator(device="cuda").manual_seed(1), device="cuda")
+    ids = logits.topk(k, dim=1).indices.int().contiguous()
+    mask = (torch.arange(T, device="cuda") // 64) % sms == 0      # CTA b takes the b-th 64 tokens of every 64 sms
+    counts, num = torch.zeros(E, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    P, losses = torch.zeros(E, device="cuda"), torch.zeros(2, device="cuda")
+    ws = moe.alloc_balance_workspace(s)
+    word = ws[:256].view(torch.int32)[60:61]
+    part = ws[256:]
+
+    def call():
+        for t in (counts, num, P, losses, part):
+            t.zero_()
+        moe.moe_balance_loss(s, logits, ids, mask, counts, num, P, losses, ws)
+        return moe.last_device_status(ws), [t.clone() for t in (counts, num, P, losses)]
+
+    status, want = call()
+    assert status == 0 and want[1].item() == mask.sum().item()
+    for _ in range(5):
+        word.fill_(1)
+        status, got = call()
+        assert status == BOUNDS
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert word.item() == 0
