@@ -383,7 +383,12 @@ __global__ void __launch_bounds__(Cfg<kTok>::THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int total = NT * s_win[E];
+  // windows of counts that fit the buffers: the full ones hold kTok of max_rows
+  // rows each, and an expert has one more at most (so total < 2^28).  Counts that
+  // ask for more give no tiles.
+  const bool fits = static_cast<int64_t>(s_win[E] - E) * kTok <= max_rows;
+  if (!fits && threadIdx.x == 0) record_status(status, kStatusBounds);
+  const int total = fits ? NT * s_win[E] : 0;
   const int KT = K / 128;  // scale tiles along the reduction
   const int KS = (KT + kAtoms - 1) / kAtoms;
 

@@ -164,3 +164,35 @@ def test_the_balance_loss_waits_for_its_slowest_cta():
         assert status == BOUNDS
         assert all(torch.equal(a, b) for a, b in zip(got, want))
         assert word.item() == 0
+
+
+@pytest.mark.parametrize("which", [UP, DOWN])
+@pytest.mark.parametrize("wide", [False, True])
+def test_counts_that_fit_alone_but_not_together_are_reported(which, wide):
+    """Every expert is said to fill the buffers, of a shape whose tiles would then
+    number past 32 bits.  The counts alone decide that nothing is loaded or stored
+    (every expert's padded rows are empty, too), so the buffers can be small."""
+    torch = need_gpu()
+    import ctypes
+    import combine_moe_route_04_gb300 as moe
+    H, I = (128, 32768) if which == UP else (32768, 128)
+    s = moe.shape(1 << 22, H, I, 256, 16 if wide else 1)       # 262144 or 16384 rows per expert
+    if not wide:
+        s.T = 256 * 256                                          # 256 rows per expert: the shorter windows
+    mr = moe.capacity(s)[1]
+    N = I if which == UP else H
+    tiles = 256 * ((mr - 1) // (192 if wide else 128) + 1) * (N // 128 if which == UP else -(-N // 256))
+    assert tiles >= 1 << 31 or not wide
+    counts = torch.full((256,), mr, dtype=torch.int32, device="cuda")
+    off = torch.zeros(257, dtype=torch.int32, device="cuda")
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    small = torch.full((4096,), 7, dtype=torch.uint8, device="cuda")
+    p = small.data_ptr()
+    stream = torch.cuda.current_stream().cuda_stream
+    a = [ctypes.byref(s), p, p, counts.data_ptr(), off.data_ptr()] + [p] * (4 if which == UP else 2) \
+        + [p, ws.data_ptr(), stream]
+    fn = moe.load().moe_grouped_gemm_up_mxfp4 if which == UP else moe.load().moe_grouped_gemm_down_mxfp4
+    for _ in range(2):
+        assert fn(*a) == 0
+        assert moe.last_device_status(ws) == BOUNDS
+        assert bool((small == 7).all()) and not ws.any()
