@@ -220,6 +220,11 @@ def alloc_workspace(s, device="cuda", stream=None):
 
 
 def workspace_views(s, ws) -> MoEViews:
+    """Addresses of what moe_forward left in its workspace.  A tensor too small to
+    be one is refused (moe_forward_mxfp4 lays its smaller workspace out otherwise)."""
+    size = workspace_size(s)
+    if hasattr(ws, "numel") and ws.numel() * ws.element_size() < size:
+        raise ValueError("ws holds %d bytes, moe_forward's workspace has %d" % (ws.numel() * ws.element_size(), size))
     v = MoEViews()
     _check(load().moe_workspace_views(_sp(s), _ptr(ws), ctypes.byref(v)), "moe_workspace_views")
     return v

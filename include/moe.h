@@ -263,7 +263,9 @@ moe_status moe_forward(const moe_shape *shape, const float *logits, const moe_bf
                        moe_stream_t stream);
 
 /* Device pointers to the intermediates that moe_forward leaves in `ws`
- * (valid after the forward's work on the stream has completed). */
+ * (valid after the forward's work on the stream has completed).  `ws` has
+ * moe_workspace_size bytes: the smaller workspace of moe_forward_mxfp4 is laid
+ * out otherwise, and the call cannot tell. */
 typedef struct {
     int32_t *topk_ids;
     float *topk_w;
@@ -356,7 +358,7 @@ moe_status moe_grouped_gemm_down_mxfp4(const moe_shape *shape, const uint8_t *h_
 
 /* Host only.  Bytes of the workspace of moe_forward_mxfp4.  moe_workspace_init
  * clears its counters and moe_last_device_status reads its status word, as for
- * moe_forward's. */
+ * moe_forward's; moe_workspace_views does not apply to it. */
 moe_status moe_mxfp4_workspace_size(const moe_shape *shape, size_t *bytes);
 
 /* The whole layer with the experts' products in MXFP4: route, quantise and
