@@ -652,8 +652,8 @@ __global__ void __launch_bounds__(S_THREADS, 1)
             for (int i = 0; i < 16; ++i) {
               const float g0 = __uint_as_float(gv[2 * i]), g1 = __uint_as_float(gv[2 * i + 1]);
               const float u0 = __uint_as_float(uv[2 * i]), u1 = __uint_as_float(uv[2 * i + 1]);
-              // silu(g) = g * sigmoid(g) on the SFU (a few float32 ulps, far
-              // below the bf16 rounding of h; g < -88 gives the limit 0)
+              // silu(g) = g * sigmoid(g) on the SFU (about |g| 2^-24 and a few
+              // ulps, far below the bf16 rounding of h; g < -88 gives the limit 0)
               const float h0 = g0 * __fdividef(1.0f, 1.0f + __expf(-g0)) * u0;
               const float h1 = g1 * __fdividef(1.0f, 1.0f + __expf(-g1)) * u1;
               packed[cl * 16 + i] = pack_bf16x2(h0, h1);

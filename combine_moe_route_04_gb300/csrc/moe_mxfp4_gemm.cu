@@ -225,8 +225,10 @@ __device__ __forceinline__ bool vote_any(bool flag) {
   return r != 0;
 }
 
-// silu(g) * u with the sigmoid on the SFU (a few float32 ulps; g < -88 gives
-// the limit 0, as in the bf16 GEMM).
+// silu(g) * u with the sigmoid on the SFU.  The exponent g log2 e is rounded
+// before ex2, so below zero the relative error grows with |g|, to about
+// |g| 2^-24 and a few ulps (2^-17 at g = -88, below which the result is the
+// limit 0, as in the bf16 GEMM): far under h's rounding to bf16, 2^-9.
 __device__ __forceinline__ float silu_mul(float g, float u) {
   float e, r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
