@@ -21,7 +21,10 @@ __all__ = ["MoEError", "MoEShape", "MoEViews", "lib_path", "load", "shape", "cap
            "mxfp4_sizes", "alloc_mxfp4", "moe_quantize_mxfp4", "moe_quantize_weights_mxfp4",
            "moe_dequantize_mxfp4", "moe_quantize_permute_mxfp4", "moe_grouped_gemm_up_mxfp4",
            "moe_grouped_gemm_down_mxfp4", "mxfp4_workspace_size", "alloc_mxfp4_workspace", "moe_forward_mxfp4",
-           "balance_workspace_size", "alloc_balance_workspace", "moe_balance_loss", "moe_balance_loss_backward"]
+           "balance_workspace_size", "alloc_balance_workspace", "moe_balance_loss", "moe_balance_loss_backward",
+           "moe_grouped_gemm_up_train", "moe_combine_backward", "moe_grouped_gemm_down_backward",
+           "moe_grouped_gemm_up_backward", "moe_grouped_gemm_weight_backward", "moe_permute_backward",
+           "moe_forward_train", "backward_workspace_size", "alloc_backward_workspace", "moe_backward"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libmoe_gb300.so")
@@ -41,7 +44,10 @@ EXPORTS = ["moe_status_string", "moe_capacity", "moe_workspace_size", "moe_works
            "moe_grouped_gemm_up_rows", "moe_check_wait_timeout", "moe_mxfp4_sizes", "moe_quantize_mxfp4",
            "moe_quantize_weights_mxfp4", "moe_dequantize_mxfp4", "moe_quantize_permute_mxfp4",
            "moe_grouped_gemm_up_mxfp4", "moe_grouped_gemm_down_mxfp4", "moe_mxfp4_workspace_size",
-           "moe_forward_mxfp4", "moe_balance_workspace_size", "moe_balance_loss", "moe_balance_loss_backward"]
+           "moe_forward_mxfp4", "moe_balance_workspace_size", "moe_balance_loss", "moe_balance_loss_backward",
+           "moe_grouped_gemm_up_train", "moe_combine_backward", "moe_grouped_gemm_down_backward",
+           "moe_grouped_gemm_up_backward", "moe_grouped_gemm_weight_backward", "moe_permute_backward",
+           "moe_forward_train", "moe_backward_workspace_size", "moe_backward"]
 
 
 class MoEError(RuntimeError):
@@ -119,7 +125,16 @@ def load():
                        ("moe_forward_mxfp4", [S] + [P] * 11),
                        ("moe_balance_workspace_size", [S, Z]),
                        ("moe_balance_loss", [S] + [P] * 9),
-                       ("moe_balance_loss_backward", [S] + [P] * 7)):
+                       ("moe_balance_loss_backward", [S] + [P] * 7),
+                       ("moe_grouped_gemm_up_train", [S] + [P] * 10),
+                       ("moe_combine_backward", [S] + [P] * 9),
+                       ("moe_grouped_gemm_down_backward", [S] + [P] * 10),
+                       ("moe_grouped_gemm_up_backward", [S] + [P] * 9),
+                       ("moe_grouped_gemm_weight_backward", [S] + [P] * 12),
+                       ("moe_permute_backward", [S] + [P] * 5),
+                       ("moe_forward_train", [S] + [P] * 10),
+                       ("moe_backward_workspace_size", [S, Z]),
+                       ("moe_backward", [S] + [P] * 14)):
         fn = getattr(lib, name)
         fn.restype = st
         fn.argtypes = args
@@ -407,6 +422,8 @@ class _Plan:
         self.ref = ctypes.byref(self.shape)
         self.mxfp4_ws = mxfp4_workspace_size(self.shape)
         self.balance_ws = balance_workspace_size(self.shape)
+        self.ws = workspace_size(self.shape)
+        self.backward_ws = backward_workspace_size(self.shape)
 
 
 @functools.lru_cache(maxsize=256)
@@ -572,3 +589,123 @@ def moe_balance_loss_backward(s, logits, mask, counts, num_tokens, grad_losses, 
         _stream(stream))
     if rc:
         _check(rc, "moe_balance_loss_backward")
+
+
+def moe_grouped_gemm_up_train(s, Xp, counts, off_pad, W_gate, W_up, g, u, h, ws, stream=None):
+    """moe_grouped_gemm_up_rows that also keeps g and u; ws: any workspace, or a
+    uint8 buffer of at least 256 bytes, zeroed once (as in every call below)."""
+    s, d = _plan(s), _dtypes()
+    rows, w = s.max_rows * s.I, s.E * s.H * s.I
+    rc = (_lib or load()).moe_grouped_gemm_up_train(
+        s.ref, _dev_tensor(Xp, d.bf16, s.max_rows * s.H, "Xp"), _dev_tensor(counts, d.i32, s.E, "counts"),
+        _dev_tensor(off_pad, d.i32, s.E + 1, "off_pad"), _dev_tensor(W_gate, d.bf16, w, "W_gate"),
+        _dev_tensor(W_up, d.bf16, w, "W_up"), _dev_tensor(g, d.bf16, rows, "g"), _dev_tensor(u, d.bf16, rows, "u"),
+        _dev_tensor(h, d.bf16, rows, "h"), _dev_tensor(ws, d.u8, 256, "ws"), _stream(stream))
+    if rc:
+        _check(rc, "moe_grouped_gemm_up_train")
+
+
+def moe_combine_backward(s, Y, scatter_idx, topk_ids, topk_w, dout, dY, dlogits, ws, stream=None):
+    """The gradients of the combine (dY) and of the routing weights (dlogits)."""
+    s, d = _plan(s), _dtypes()
+    rows, picks = s.max_rows * s.H, s.T * s.k
+    rc = (_lib or load()).moe_combine_backward(
+        s.ref, _dev_tensor(Y, d.bf16, rows, "Y"), _dev_tensor(scatter_idx, d.i32, picks, "scatter_idx"),
+        _dev_tensor(topk_ids, d.i32, picks, "topk_ids"), _dev_tensor(topk_w, d.f32, picks, "topk_w"),
+        _dev_tensor(dout, d.bf16, s.T * s.H, "dout"), _dev_tensor(dY, d.bf16, rows, "dY"),
+        _dev_tensor(dlogits, d.f32, s.T * s.E, "dlogits"), _dev_tensor(ws, d.u8, 256, "ws"), _stream(stream))
+    if rc:
+        _check(rc, "moe_combine_backward")
+
+
+def moe_grouped_gemm_down_backward(s, dY, counts, off_pad, W_down, g, u, dg, du, ws, stream=None):
+    """dg and du from dY: the down product's gradient with the activation's in its epilogue."""
+    s, d = _plan(s), _dtypes()
+    rows = s.max_rows * s.I
+    rc = (_lib or load()).moe_grouped_gemm_down_backward(
+        s.ref, _dev_tensor(dY, d.bf16, s.max_rows * s.H, "dY"), _dev_tensor(counts, d.i32, s.E, "counts"),
+        _dev_tensor(off_pad, d.i32, s.E + 1, "off_pad"), _dev_tensor(W_down, d.bf16, s.E * s.I * s.H, "W_down"),
+        _dev_tensor(g, d.bf16, rows, "g"), _dev_tensor(u, d.bf16, rows, "u"), _dev_tensor(dg, d.bf16, rows, "dg"),
+        _dev_tensor(du, d.bf16, rows, "du"), _dev_tensor(ws, d.u8, 256, "ws"), _stream(stream))
+    if rc:
+        _check(rc, "moe_grouped_gemm_down_backward")
+
+
+def moe_grouped_gemm_up_backward(s, dg, du, counts, off_pad, W_gate, W_up, dXp, ws, stream=None):
+    """The rows' gradient dXp = dg W_gate^T + du W_up^T."""
+    s, d = _plan(s), _dtypes()
+    rows, w = s.max_rows * s.I, s.E * s.H * s.I
+    rc = (_lib or load()).moe_grouped_gemm_up_backward(
+        s.ref, _dev_tensor(dg, d.bf16, rows, "dg"), _dev_tensor(du, d.bf16, rows, "du"),
+        _dev_tensor(counts, d.i32, s.E, "counts"), _dev_tensor(off_pad, d.i32, s.E + 1, "off_pad"),
+        _dev_tensor(W_gate, d.bf16, w, "W_gate"), _dev_tensor(W_up, d.bf16, w, "W_up"),
+        _dev_tensor(dXp, d.bf16, s.max_rows * s.H, "dXp"), _dev_tensor(ws, d.u8, 256, "ws"), _stream(stream))
+    if rc:
+        _check(rc, "moe_grouped_gemm_up_backward")
+
+
+def moe_grouped_gemm_weight_backward(s, Xp, h, dg, du, dY, counts, off_pad, dW_gate, dW_up, dW_down, ws, stream=None):
+    """The gradients of the three weights (zero for an expert without rows)."""
+    s, d = _plan(s), _dtypes()
+    wide, rows, w = s.max_rows * s.H, s.max_rows * s.I, s.E * s.H * s.I
+    rc = (_lib or load()).moe_grouped_gemm_weight_backward(
+        s.ref, _dev_tensor(Xp, d.bf16, wide, "Xp"), _dev_tensor(h, d.bf16, rows, "h"),
+        _dev_tensor(dg, d.bf16, rows, "dg"), _dev_tensor(du, d.bf16, rows, "du"), _dev_tensor(dY, d.bf16, wide, "dY"),
+        _dev_tensor(counts, d.i32, s.E, "counts"), _dev_tensor(off_pad, d.i32, s.E + 1, "off_pad"),
+        _dev_tensor(dW_gate, d.bf16, w, "dW_gate"), _dev_tensor(dW_up, d.bf16, w, "dW_up"),
+        _dev_tensor(dW_down, d.bf16, w, "dW_down"), _dev_tensor(ws, d.u8, 256, "ws"), _stream(stream))
+    if rc:
+        _check(rc, "moe_grouped_gemm_weight_backward")
+
+
+def moe_permute_backward(s, dXp, scatter_idx, dX, ws, stream=None):
+    """The row gather's gradient: the sum of a token's k rows of dXp."""
+    s, d = _plan(s), _dtypes()
+    rc = (_lib or load()).moe_permute_backward(
+        s.ref, _dev_tensor(dXp, d.bf16, s.max_rows * s.H, "dXp"),
+        _dev_tensor(scatter_idx, d.i32, s.T * s.k, "scatter_idx"), _dev_tensor(dX, d.bf16, s.T * s.H, "dX"),
+        _dev_tensor(ws, d.u8, 256, "ws"), _stream(stream))
+    if rc:
+        _check(rc, "moe_permute_backward")
+
+
+def moe_forward_train(s, logits, X, W_gate, W_up, W_down, g, u, out, ws, stream=None):
+    """moe_forward that keeps g and u [max_rows, I] for moe_backward, which also reads ws as this call leaves it."""
+    s, d = _plan(s), _dtypes()
+    rows, w = s.max_rows * s.I, s.E * s.H * s.I
+    rc = (_lib or load()).moe_forward_train(
+        s.ref, _dev_tensor(logits, d.f32, s.T * s.E, "logits"), _dev_tensor(X, d.bf16, s.T * s.H, "X"),
+        _dev_tensor(W_gate, d.bf16, w, "W_gate"), _dev_tensor(W_up, d.bf16, w, "W_up"),
+        _dev_tensor(W_down, d.bf16, w, "W_down"), _dev_tensor(g, d.bf16, rows, "g"), _dev_tensor(u, d.bf16, rows, "u"),
+        _dev_tensor(out, d.bf16, s.T * s.H, "out"), _dev_tensor(ws, d.u8, s.ws, "ws"), _stream(stream))
+    if rc:
+        _check(rc, "moe_forward_train")
+
+
+def backward_workspace_size(s) -> int:
+    n = ctypes.c_size_t()
+    _check(load().moe_backward_workspace_size(_sp(s), ctypes.byref(n)), "moe_backward_workspace_size")
+    return n.value
+
+
+def alloc_backward_workspace(s, device="cuda", stream=None):
+    """A uint8 CUDA tensor of moe_backward_workspace_size bytes with its counters cleared."""
+    import torch
+    ws = torch.empty(backward_workspace_size(s), dtype=torch.uint8, device=device)
+    workspace_init(s, ws, stream)
+    return ws
+
+
+def moe_backward(s, W_gate, W_up, W_down, g, u, dout, dX, dW_gate, dW_up, dW_down, dlogits, ws, bws, stream=None):
+    """The layer's backward pass after moe_forward_train (g, u and ws as it left them); bws: scratch."""
+    s, d = _plan(s), _dtypes()
+    rows, w, x = s.max_rows * s.I, s.E * s.H * s.I, s.T * s.H
+    rc = (_lib or load()).moe_backward(
+        s.ref, _dev_tensor(W_gate, d.bf16, w, "W_gate"), _dev_tensor(W_up, d.bf16, w, "W_up"),
+        _dev_tensor(W_down, d.bf16, w, "W_down"), _dev_tensor(g, d.bf16, rows, "g"), _dev_tensor(u, d.bf16, rows, "u"),
+        _dev_tensor(dout, d.bf16, x, "dout"), _dev_tensor(dX, d.bf16, x, "dX"),
+        _dev_tensor(dW_gate, d.bf16, w, "dW_gate"), _dev_tensor(dW_up, d.bf16, w, "dW_up"),
+        _dev_tensor(dW_down, d.bf16, w, "dW_down"), _dev_tensor(dlogits, d.f32, s.T * s.E, "dlogits"),
+        _dev_tensor(ws, d.u8, s.ws, "ws"), _dev_tensor(bws, d.u8, s.backward_ws, "bws"), _stream(stream))
+    if rc:
+        _check(rc, "moe_backward")

@@ -121,9 +121,10 @@ moe_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_E
 
 // The gate/up GEMM over rows already in expert order (Xp [max_rows][H]).
 // win_done: nullptr, or the forward's per-window counters (see launch_gemm_up).
+// g, u: nullptr, or where the training forward keeps them.
 moe_status run_up_rows(const moe_shape& s, const uint16_t* Xp, const int32_t* counts, const int32_t* off_pad,
-                       const uint16_t* Wg, const uint16_t* Wu, uint16_t* h, const Views& w, uint32_t* win_done,
-                       int num_sms, cudaStream_t st) {
+                       const uint16_t* Wg, const uint16_t* Wu, uint16_t* h, uint32_t* status, uint32_t* win_done,
+                       int num_sms, cudaStream_t st, uint16_t* g = nullptr, uint16_t* u = nullptr) {
   const uint64_t mr = static_cast<uint64_t>(max_rows_of(s));
   GemmMaps m;
   const uint64_t EH = static_cast<uint64_t>(s.E) * s.H;
@@ -131,8 +132,10 @@ moe_status run_up_rows(const moe_shape& s, const uint16_t* Xp, const int32_t* co
       !encode_bf16_2d(&m.b1, Wu, EH, s.I, 32, 64) || !encode_bf16_2d(&m.a64, Xp, mr, s.H, 64, 32) ||
       !encode_bf16_2d(&m.a80, Xp, mr, s.H, 80, 32))
     return MOE_ERR_CUDA;
-  return cuda_status(
-      launch_gemm_up(s, m, h, off_pad, counts, w.status, ws_sched_up(w.status), win_done, num_sms, st));
+  if (g != nullptr)
+    return cuda_status(
+        launch_gemm_up_train(s, m, g, u, h, off_pad, counts, status, ws_sched_up(status), win_done, num_sms, st));
+  return cuda_status(launch_gemm_up(s, m, h, off_pad, counts, status, ws_sched_up(status), win_done, num_sms, st));
 }
 
 // Row gather into the workspace's Xp (token by token: each row of X read
@@ -143,7 +146,7 @@ moe_status run_up(const moe_shape& s, const uint16_t* X, const int32_t* scatter_
                   uint16_t* h, const Views& w, uint32_t* win_done, int num_sms, cudaStream_t st) {
   cudaError_t e = launch_scatter_rows(s, X, scatter_idx, w.xp, w.status, st);
   if (e != cudaSuccess) return MOE_ERR_CUDA;
-  return run_up_rows(s, w.xp, counts, off_pad, Wg, Wu, h, w, win_done, num_sms, st);
+  return run_up_rows(s, w.xp, counts, off_pad, Wg, Wu, h, w.status, win_done, num_sms, st);
 }
 
 moe_status run_down(const moe_shape& s, const uint16_t* h, const int32_t* counts, const int32_t* off_pad,
@@ -219,6 +222,93 @@ bool mxfp4_maps(const moe_shape& s, int64_t K, int64_t N, const uint8_t* rows, c
   m->out = m->t[0];
   if (out != nullptr && !encode_bf16_2d(&m->out, out, mr, static_cast<uint64_t>(N), 32, 64)) return false;
   return encode_bytes_2d(&m->w0, w0, wr, kb, 128) && encode_bytes_2d(&m->w1, w1, wr, kb, 128);
+}
+
+// Byte offsets of moe_backward's workspace (its first 256 bytes as in every
+// workspace).
+struct BackwardLayout {
+  size_t dy, dg, du, total;
+};
+BackwardLayout backward_layout(const moe_shape& s) {
+  BackwardLayout L{};
+  const size_t mr = static_cast<size_t>(max_rows_of(s));
+  size_t off = align_up(256);
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = align_up(off + bytes);
+    return at;
+  };
+  L.dy = take(mr * static_cast<size_t>(s.H) * 2);  // later dXp
+  L.dg = take(mr * static_cast<size_t>(s.I) * 2);
+  L.du = take(mr * static_cast<size_t>(s.I) * 2);
+  L.total = off;
+  return L;
+}
+
+moe_status run_down_backward(const moe_shape& s, const uint16_t* dY, const int32_t* counts, const int32_t* off_pad,
+                             const uint16_t* Wd, const uint16_t* g, const uint16_t* u, uint16_t* dg, uint16_t* du,
+                             uint32_t* status, int num_sms, cudaStream_t st) {
+  const uint64_t mr = static_cast<uint64_t>(max_rows_of(s));
+  TrainMaps m = {};
+  bool ok = encode_bf16_2d(&m.a[0], Wd, static_cast<uint64_t>(s.E) * s.I, s.H, 128, 64) &&
+            encode_bf16_2d(&m.in[0], g, mr, s.I, 32, 64) && encode_bf16_2d(&m.in[1], u, mr, s.I, 32, 64) &&
+            encode_bf16_2d(&m.out[0], dg, mr, s.I, 32, 64) && encode_bf16_2d(&m.out[1], du, mr, s.I, 32, 64);
+  for (int i = 0; i < 4; ++i) ok = ok && encode_bf16_2d(&m.b[0][i], dY, mr, s.H, train_token_box(i), 64);
+  if (!ok) return MOE_ERR_CUDA;
+  return cuda_status(launch_down_backward(s, m, dg, du, off_pad, counts, status, ws_sched_up(status), num_sms, st));
+}
+
+moe_status run_up_backward(const moe_shape& s, const uint16_t* dg, const uint16_t* du, const int32_t* counts,
+                           const int32_t* off_pad, const uint16_t* Wg, const uint16_t* Wu, uint16_t* dXp,
+                           uint32_t* status, int num_sms, cudaStream_t st) {
+  const uint64_t mr = static_cast<uint64_t>(max_rows_of(s)), EH = static_cast<uint64_t>(s.E) * s.H;
+  TrainMaps m = {};
+  bool ok = encode_bf16_2d(&m.a[0], Wg, EH, s.I, 128, 64) && encode_bf16_2d(&m.a[1], Wu, EH, s.I, 128, 64) &&
+            encode_bf16_2d(&m.out[0], dXp, mr, s.H, 32, 64);
+  for (int i = 0; i < 4; ++i)
+    ok = ok && encode_bf16_2d(&m.b[0][i], dg, mr, s.I, train_token_box(i), 64) &&
+         encode_bf16_2d(&m.b[1][i], du, mr, s.I, train_token_box(i), 64);
+  if (!ok) return MOE_ERR_CUDA;
+  return cuda_status(launch_up_backward(s, m, dXp, off_pad, counts, status, ws_sched_down(status), num_sms, st));
+}
+
+moe_status run_weight_backward(const moe_shape& s, const uint16_t* Xp, const uint16_t* h, const uint16_t* dg,
+                               const uint16_t* du, const uint16_t* dY, const int32_t* counts, const int32_t* off_pad,
+                               uint16_t* dWg, uint16_t* dWu, uint16_t* dWd, uint32_t* status, int num_sms,
+                               cudaStream_t st) {
+  const uint64_t mr = static_cast<uint64_t>(max_rows_of(s));
+  const uint64_t EH = static_cast<uint64_t>(s.E) * s.H, EI = static_cast<uint64_t>(s.E) * s.I;
+  TrainMaps m = {};
+  if (!encode_bf16_2d(&m.a[0], dg, mr, s.I, 64, 64) || !encode_bf16_2d(&m.a[1], du, mr, s.I, 64, 64) ||
+      !encode_bf16_2d(&m.a[2], dY, mr, s.H, 64, 64) || !encode_bf16_2d(&m.b[0][0], Xp, mr, s.H, 64, 64) ||
+      !encode_bf16_2d(&m.b[1][0], h, mr, s.I, 64, 64) || !encode_bf16_2d(&m.out[0], dWg, EH, s.I, 32, 64) ||
+      !encode_bf16_2d(&m.out[1], dWu, EH, s.I, 32, 64) || !encode_bf16_2d(&m.out[2], dWd, EI, s.H, 32, 64))
+    return MOE_ERR_CUDA;
+  return cuda_status(launch_weight_backward(s, m, off_pad, counts, status, ws_sched_up(status), num_sms, st));
+}
+
+// moe_forward, or with g and u (both or neither) the training forward.
+moe_status run_forward(const moe_shape& sh, const float* logits, const uint16_t* X, const uint16_t* W_gate,
+                       const uint16_t* W_up, const uint16_t* W_down, uint16_t* g, uint16_t* u, uint16_t* out,
+                       void* ws, cudaStream_t s) {
+  int sms = 0;
+  DeviceRestore restore;
+  moe_status st = prepare_device(s, &sms, &restore);
+  if (st != MOE_OK) return st;
+  const Views w = views_of(sh, ws);
+  const moe_views& v = w.v;
+  // routing, then the permutation and the row gather in one kernel
+  if (launch_route_gather(sh, logits, X, v.topk_ids, v.topk_w, v.counts, v.off_pad, v.block_expert, v.num_blocks,
+                          v.gather_idx, v.scatter_idx, w.local_rank, w.chunk_counts, w.xp,
+                          ws_route_counter(w.status), w.win_done, forward_counters_of(sh), w.status, sms,
+                          s) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  // the down GEMM starts on each token window as soon as its h rows are in
+  st = run_up_rows(sh, w.xp, v.counts, v.off_pad, W_gate, W_up, v.h, w.status, w.win_done, sms, s, g, u);
+  if (st != MOE_OK) return st;
+  st = run_down(sh, v.h, v.counts, v.off_pad, W_down, v.Y, w, w.win_done, sms, s);
+  if (st != MOE_OK) return st;
+  return cuda_status(launch_combine(sh, v.Y, v.scatter_idx, v.topk_w, out, w.status, sms, s));
 }
 
 }  // namespace
@@ -428,7 +518,7 @@ moe_status moe_grouped_gemm_up_rows(const moe_shape* shape, const moe_bf16* Xp, 
   DeviceRestore restore;
   st = prepare_device(s, &sms, &restore);
   if (st != MOE_OK) return st;
-  return run_up_rows(*shape, Xp, counts, off_pad, W_gate, W_up, h, views_of(*shape, ws), nullptr, sms, s);
+  return run_up_rows(*shape, Xp, counts, off_pad, W_gate, W_up, h, ws_status(ws), nullptr, sms, s);
 }
 
 moe_status moe_grouped_gemm_down(const moe_shape* shape, const moe_bf16* h, const int32_t* counts,
@@ -478,25 +568,7 @@ moe_status moe_forward(const moe_shape* shape, const float* logits, const moe_bf
     if (!aligned16(p)) return MOE_ERR_MISALIGNED;
   }
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  int sms = 0;
-  DeviceRestore restore;
-  st = prepare_device(s, &sms, &restore);
-  if (st != MOE_OK) return st;
-  const moe_shape& sh = *shape;
-  const Views w = views_of(sh, ws);
-  const moe_views& v = w.v;
-  // routing, then the permutation and the row gather in one kernel
-  if (launch_route_gather(sh, logits, X, v.topk_ids, v.topk_w, v.counts, v.off_pad, v.block_expert, v.num_blocks,
-                          v.gather_idx, v.scatter_idx, w.local_rank, w.chunk_counts, w.xp,
-                          ws_route_counter(w.status), w.win_done, forward_counters_of(sh), w.status, sms,
-                          s) != cudaSuccess)
-    return MOE_ERR_CUDA;
-  // the down GEMM starts on each token window as soon as its h rows are in
-  st = run_up_rows(sh, w.xp, v.counts, v.off_pad, W_gate, W_up, v.h, w, w.win_done, sms, s);
-  if (st != MOE_OK) return st;
-  st = run_down(sh, v.h, v.counts, v.off_pad, W_down, v.Y, w, w.win_done, sms, s);
-  if (st != MOE_OK) return st;
-  return cuda_status(launch_combine(sh, v.Y, v.scatter_idx, v.topk_w, out, w.status, sms, s));
+  return run_forward(*shape, logits, X, W_gate, W_up, W_down, nullptr, nullptr, out, ws, s);
 }
 
 moe_status moe_mxfp4_sizes(int64_t rows, int64_t cols, size_t* code_bytes, size_t* scale_bytes) {
@@ -682,6 +754,151 @@ moe_status moe_balance_loss_backward(const moe_shape* shape, const float* logits
   if (st != MOE_OK) return st;
   return cuda_status(
       launch_balance_backward(*shape, logits, mask, counts, num_tokens, grad_losses, dlogits, sms, s));
+}
+
+moe_status moe_grouped_gemm_up_train(const moe_shape* shape, const moe_bf16* Xp, const int32_t* counts,
+                                     const int32_t* off_pad, const moe_bf16* W_gate, const moe_bf16* W_up,
+                                     moe_bf16* g, moe_bf16* u, moe_bf16* h, void* ws, moe_stream_t stream) {
+  moe_status st = check_shape(shape);
+  if (st != MOE_OK) return st;
+  st = check_ptrs({Xp, counts, off_pad, W_gate, W_up, g, u, h, ws});
+  if (st != MOE_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int sms = 0;
+  DeviceRestore restore;
+  st = prepare_device(s, &sms, &restore);
+  if (st != MOE_OK) return st;
+  return run_up_rows(*shape, Xp, counts, off_pad, W_gate, W_up, h, ws_status(ws), nullptr, sms, s, g, u);
+}
+
+moe_status moe_combine_backward(const moe_shape* shape, const moe_bf16* Y, const int32_t* scatter_idx,
+                                const int32_t* topk_ids, const float* topk_w, const moe_bf16* dout, moe_bf16* dY,
+                                float* dlogits, void* ws, moe_stream_t stream) {
+  moe_status st = check_shape(shape);
+  if (st != MOE_OK) return st;
+  st = check_ptrs({Y, scatter_idx, topk_ids, topk_w, dout, dY, dlogits, ws});
+  if (st != MOE_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int sms = 0;
+  DeviceRestore restore;
+  st = prepare_device(s, &sms, &restore);
+  if (st != MOE_OK) return st;
+  return cuda_status(launch_combine_backward(*shape, Y, scatter_idx, topk_ids, topk_w, dout, dY, dlogits,
+                                             ws_status(ws), sms, s));
+}
+
+moe_status moe_grouped_gemm_down_backward(const moe_shape* shape, const moe_bf16* dY, const int32_t* counts,
+                                          const int32_t* off_pad, const moe_bf16* W_down, const moe_bf16* g,
+                                          const moe_bf16* u, moe_bf16* dg, moe_bf16* du, void* ws,
+                                          moe_stream_t stream) {
+  moe_status st = check_shape(shape);
+  if (st != MOE_OK) return st;
+  st = check_ptrs({dY, counts, off_pad, W_down, g, u, dg, du, ws});
+  if (st != MOE_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int sms = 0;
+  DeviceRestore restore;
+  st = prepare_device(s, &sms, &restore);
+  if (st != MOE_OK) return st;
+  return run_down_backward(*shape, dY, counts, off_pad, W_down, g, u, dg, du, ws_status(ws), sms, s);
+}
+
+moe_status moe_grouped_gemm_up_backward(const moe_shape* shape, const moe_bf16* dg, const moe_bf16* du,
+                                        const int32_t* counts, const int32_t* off_pad, const moe_bf16* W_gate,
+                                        const moe_bf16* W_up, moe_bf16* dXp, void* ws, moe_stream_t stream) {
+  moe_status st = check_shape(shape);
+  if (st != MOE_OK) return st;
+  st = check_ptrs({dg, du, counts, off_pad, W_gate, W_up, dXp, ws});
+  if (st != MOE_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int sms = 0;
+  DeviceRestore restore;
+  st = prepare_device(s, &sms, &restore);
+  if (st != MOE_OK) return st;
+  return run_up_backward(*shape, dg, du, counts, off_pad, W_gate, W_up, dXp, ws_status(ws), sms, s);
+}
+
+moe_status moe_grouped_gemm_weight_backward(const moe_shape* shape, const moe_bf16* Xp, const moe_bf16* h,
+                                            const moe_bf16* dg, const moe_bf16* du, const moe_bf16* dY,
+                                            const int32_t* counts, const int32_t* off_pad, moe_bf16* dW_gate,
+                                            moe_bf16* dW_up, moe_bf16* dW_down, void* ws, moe_stream_t stream) {
+  moe_status st = check_shape(shape);
+  if (st != MOE_OK) return st;
+  st = check_ptrs({Xp, h, dg, du, dY, counts, off_pad, dW_gate, dW_up, dW_down, ws});
+  if (st != MOE_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int sms = 0;
+  DeviceRestore restore;
+  st = prepare_device(s, &sms, &restore);
+  if (st != MOE_OK) return st;
+  return run_weight_backward(*shape, Xp, h, dg, du, dY, counts, off_pad, dW_gate, dW_up, dW_down, ws_status(ws), sms,
+                             s);
+}
+
+moe_status moe_permute_backward(const moe_shape* shape, const moe_bf16* dXp, const int32_t* scatter_idx, moe_bf16* dX,
+                                void* ws, moe_stream_t stream) {
+  moe_status st = check_shape(shape);
+  if (st != MOE_OK) return st;
+  st = check_ptrs({dXp, scatter_idx, dX, ws});
+  if (st != MOE_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int sms = 0;
+  DeviceRestore restore;
+  st = prepare_device(s, &sms, &restore);
+  if (st != MOE_OK) return st;
+  return cuda_status(launch_combine(*shape, dXp, scatter_idx, nullptr, dX, ws_status(ws), sms, s));
+}
+
+moe_status moe_forward_train(const moe_shape* shape, const float* logits, const moe_bf16* X, const moe_bf16* W_gate,
+                             const moe_bf16* W_up, const moe_bf16* W_down, moe_bf16* g, moe_bf16* u, moe_bf16* out,
+                             void* ws, moe_stream_t stream) {
+  moe_status st = check_shape(shape);
+  if (st != MOE_OK) return st;
+  st = check_ptrs({logits, X, W_gate, W_up, W_down, g, u, out, ws});
+  if (st != MOE_OK) return st;
+  return run_forward(*shape, logits, X, W_gate, W_up, W_down, g, u, out, ws, reinterpret_cast<cudaStream_t>(stream));
+}
+
+moe_status moe_backward_workspace_size(const moe_shape* shape, size_t* bytes) {
+  const moe_status st = check_shape(shape);
+  if (st != MOE_OK) return st;
+  if (bytes == nullptr) return MOE_ERR_INVALID_ARG;
+  *bytes = backward_layout(*shape).total;
+  return MOE_OK;
+}
+
+moe_status moe_backward(const moe_shape* shape, const moe_bf16* W_gate, const moe_bf16* W_up, const moe_bf16* W_down,
+                        const moe_bf16* g, const moe_bf16* u, const moe_bf16* dout, moe_bf16* dX, moe_bf16* dW_gate,
+                        moe_bf16* dW_up, moe_bf16* dW_down, float* dlogits, const void* ws, void* bws,
+                        moe_stream_t stream) {
+  moe_status st = check_shape(shape);
+  if (st != MOE_OK) return st;
+  st = check_ptrs({W_gate, W_up, W_down, g, u, dout, dX, dW_gate, dW_up, dW_down, dlogits, ws, bws});
+  if (st != MOE_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int sms = 0;
+  DeviceRestore restore;
+  st = prepare_device(s, &sms, &restore);
+  if (st != MOE_OK) return st;
+  const moe_shape& sh = *shape;
+  const moe_views v = views_of(sh, const_cast<void*>(ws)).v;  // read only
+  const BackwardLayout L = backward_layout(sh);
+  uint8_t* b = static_cast<uint8_t*>(bws);
+  uint16_t* dY = reinterpret_cast<uint16_t*>(b + L.dy);
+  uint16_t* dg = reinterpret_cast<uint16_t*>(b + L.dg);
+  uint16_t* du = reinterpret_cast<uint16_t*>(b + L.du);
+  uint32_t* status = ws_status(bws);
+  if (launch_combine_backward(sh, v.Y, v.scatter_idx, v.topk_ids, v.topk_w, dout, dY, dlogits, status, sms, s) !=
+      cudaSuccess)
+    return MOE_ERR_CUDA;
+  st = run_down_backward(sh, dY, v.counts, v.off_pad, W_down, g, u, dg, du, status, sms, s);
+  if (st != MOE_OK) return st;
+  st = run_weight_backward(sh, v.Xp, v.h, dg, du, dY, v.counts, v.off_pad, dW_gate, dW_up, dW_down, status, sms, s);
+  if (st != MOE_OK) return st;
+  uint16_t* dXp = dY;  // every use of dY is done
+  st = run_up_backward(sh, dg, du, v.counts, v.off_pad, W_gate, W_up, dXp, status, sms, s);
+  if (st != MOE_OK) return st;
+  return cuda_status(launch_combine(sh, dXp, v.scatter_idx, nullptr, dX, status, sms, s));
 }
 
 }  // extern "C"

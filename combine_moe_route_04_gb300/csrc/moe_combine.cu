@@ -3,6 +3,7 @@
 // What it computes ("通算融合算子（一）：为什么要把通信写进 GEMM kernel 里" §4, table of
 // data-flow patterns, "GEMM + combine": the top-k weighted reduction):
 //   out[t, c] = bf16( sum_{j = 0..k-1} w[t, j] * Y[scatter_idx[t, j], c] )
+// (or, without weights, the plain sum: the gradient of the row gather)
 // with a float32 accumulator in slot order, each product and each sum rounded
 // to float32 (__fmul_rn / __fadd_rn keep the compiler from fusing them).
 //
@@ -52,7 +53,7 @@ __global__ void __launch_bounds__(256, 2) combine_kernel(const uint16_t* __restr
     float my_w = 0.0f;
     if (lane < k) {
       const int64_t r = __ldcg(scatter_idx + t * k + lane);
-      my_w = __ldcg(topk_w + t * k + lane);
+      my_w = topk_w != nullptr ? __ldcg(topk_w + t * k + lane) : 1.0f;
       if (r >= 0 && r < max_rows) {
         my_row = static_cast<int>(r);
       } else if (status != nullptr && first == 0) {

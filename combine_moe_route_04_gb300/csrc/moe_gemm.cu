@@ -247,15 +247,17 @@ __device__ __forceinline__ bool ring_put(const TileRing& r, uint32_t n, int tile
   return true;
 }
 
-template <bool kUp>
+template <bool kUp, bool kSave>
 __global__ void __launch_bounds__(S_THREADS, 1)
     grouped_gemm_window_kernel(const __grid_constant__ CUtensorMap tmT, const __grid_constant__ CUtensorMap tmT64,
                                const __grid_constant__ CUtensorMap tmT80, const __grid_constant__ CUtensorMap tmW0,
                                const __grid_constant__ CUtensorMap tmW1, uint16_t* __restrict__ D,
                                const int32_t* __restrict__ off_pad, const int32_t* __restrict__ counts, int E,
                                int K, int NT, int N_out, int64_t max_rows, uint32_t* __restrict__ status,
-                               uint32_t* __restrict__ sched, uint32_t* __restrict__ win_done, uint32_t win_target) {
+                               uint32_t* __restrict__ sched, uint32_t* __restrict__ win_done, uint32_t win_target,
+                               uint16_t* __restrict__ G, uint16_t* __restrict__ U) {
   using C = SwapCfg<kUp>;
+  static_assert(kUp || !kSave, "only the gate/up GEMM has g and u");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sStage = smem;
@@ -638,6 +640,24 @@ __global__ void __launch_bounds__(S_THREADS, 1)
       uint32_t packed[CH_PER * 16];                 // bf16 pairs (token 2i, 2i+1 of chunk cl) of this column
       uint32_t packed1[kUp ? 1 : CH_PER * 16];      // down: the second accumulator's column
       const uint32_t tbase = tmem_base + a * ACC_COLS + (static_cast<uint32_t>(q * 32) << 16);
+      // Training: g and u of a 32-token chunk leave as bf16 as they are read,
+      // in the store pattern of h below (neighbouring lanes swap tokens).
+      auto save_chunk = [&](uint16_t* S, const uint32_t (&v)[32], int ch) {
+        const int cg = c.j * C::TILE_COLS + (C::TILE_COLS / 2) * static_cast<int>(rank) + col;
+        if (cg >= N_out) return;  // uniform across the warp
+        const int odd = lane & 1;
+        uint32_t* dst = reinterpret_cast<uint32_t*>(S + static_cast<int64_t>(c.row0 + ch * 32 + odd) * N_out + (cg & ~1));
+        const int rem = c.rows - ch * 32;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          if (2 * i < rem) {  // uniform across the warp
+            const uint32_t pair = pack_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+            const uint32_t other = __shfl_xor_sync(0xffffffffu, pair, 1);
+            const uint32_t w = odd ? __byte_perm(other, pair, 0x7632) : __byte_perm(pair, other, 0x5410);
+            if (2 * i + odd < rem) dst[static_cast<int64_t>(i) * N_out] = w;  // two rows = N_out words
+          }
+        }
+      };
 #pragma unroll
       for (int cl = 0; cl < CH_PER; ++cl) {
         const int ch = half + S_EPI_SPLIT * cl;
@@ -648,6 +668,10 @@ __global__ void __launch_bounds__(S_THREADS, 1)
             tmem_ld_32x32b_x32(tbase + 256 + ch * 32, uv);
             tmem_ld_wait();
             if (cl == mine - 1) release();
+            if constexpr (kSave) {
+              save_chunk(G, gv, ch);
+              save_chunk(U, uv, ch);
+            }
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               const float g0 = __uint_as_float(gv[2 * i]), g1 = __uint_as_float(gv[2 * i + 1]);
@@ -800,10 +824,10 @@ __global__ void scatter_rows_kernel(const uint16_t* __restrict__ X, const int32_
   }
 }
 
-template <bool kUp>
+template <bool kUp, bool kSave = false>
 cudaError_t launch_gemm(const moe_shape& s, const GemmMaps& maps, uint16_t* D, const int32_t* off_pad,
                         const int32_t* counts, uint32_t* status, uint32_t* sched, uint32_t* win_done,
-                        int num_sms, cudaStream_t st) {
+                        int num_sms, cudaStream_t st, uint16_t* g = nullptr, uint16_t* u = nullptr) {
   using C = SwapCfg<kUp>;
   // the shared-memory opt-in, once per device (host threads may race here)
   static bool attr_done[64] = {};
@@ -814,8 +838,8 @@ cudaError_t launch_gemm(const moe_shape& s, const GemmMaps& maps, uint16_t* D, c
   {
     std::lock_guard<std::mutex> lock(attr_mu);
     if (dev >= 64 || !attr_done[dev]) {
-      err = cudaFuncSetAttribute(grouped_gemm_window_kernel<kUp>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 C::ALLOC);
+      err = cudaFuncSetAttribute(grouped_gemm_window_kernel<kUp, kSave>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, C::ALLOC);
       if (err != cudaSuccess) return err;
       if (dev < 64) attr_done[dev] = true;
     }
@@ -846,9 +870,9 @@ cudaError_t launch_gemm(const moe_shape& s, const GemmMaps& maps, uint16_t* D, c
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, grouped_gemm_window_kernel<kUp>, maps.a, maps.a64, maps.a80, maps.b0, maps.b1, D,
+  return cudaLaunchKernelEx(&cfg, grouped_gemm_window_kernel<kUp, kSave>, maps.a, maps.a64, maps.a80, maps.b0, maps.b1, D,
                             off_pad, counts, s.E, K, NT, kUp ? s.I : s.H, max_rows_of(s), status, sched, win_done,
-                            win_target);
+                            win_target, g, u);
 }
 
 }  // namespace
@@ -866,6 +890,12 @@ cudaError_t launch_gemm_up(const moe_shape& s, const GemmMaps& maps, uint16_t* h
                            const int32_t* counts, uint32_t* status, uint32_t* sched, uint32_t* win_done,
                            int num_sms, cudaStream_t st) {
   return launch_gemm<true>(s, maps, h, off_pad, counts, status, sched, win_done, num_sms, st);
+}
+
+cudaError_t launch_gemm_up_train(const moe_shape& s, const GemmMaps& maps, uint16_t* g, uint16_t* u, uint16_t* h,
+                                 const int32_t* off_pad, const int32_t* counts, uint32_t* status, uint32_t* sched,
+                                 uint32_t* win_done, int num_sms, cudaStream_t st) {
+  return launch_gemm<true, true>(s, maps, h, off_pad, counts, status, sched, win_done, num_sms, st, g, u);
 }
 
 cudaError_t launch_gemm_down(const moe_shape& s, const GemmMaps& maps, uint16_t* Y, const int32_t* off_pad,

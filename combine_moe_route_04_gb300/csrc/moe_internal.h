@@ -151,10 +151,15 @@ struct GemmMaps {
 cudaError_t launch_gemm_up(const moe_shape& s, const GemmMaps& maps, uint16_t* h, const int32_t* off_pad,
                            const int32_t* counts, uint32_t* status, uint32_t* sched, uint32_t* win_done,
                            int num_sms, cudaStream_t st);
+// the same that also stores g and u (bf16, [max_rows][I])
+cudaError_t launch_gemm_up_train(const moe_shape& s, const GemmMaps& maps, uint16_t* g, uint16_t* u, uint16_t* h,
+                                 const int32_t* off_pad, const int32_t* counts, uint32_t* status, uint32_t* sched,
+                                 uint32_t* win_done, int num_sms, cudaStream_t st);
 cudaError_t launch_gemm_down(const moe_shape& s, const GemmMaps& maps, uint16_t* Y, const int32_t* off_pad,
                              const int32_t* counts, uint32_t* status, uint32_t* sched, uint32_t* win_done,
                              int num_sms, cudaStream_t st);
 
+// topk_w may be null: weights of one (the gradient of the row gather)
 cudaError_t launch_combine(const moe_shape& s, const uint16_t* Y, const int32_t* scatter_idx,
                            const float* topk_w, uint16_t* out, uint32_t* status, int num_sms, cudaStream_t st);
 
@@ -192,6 +197,29 @@ cudaError_t launch_mxfp4_up_quantized(const moe_shape& s, const Mxfp4Maps& m, co
 cudaError_t launch_mxfp4_down(const moe_shape& s, const Mxfp4Maps& m, const uint8_t* h_scales,
                               const uint8_t* wd_scales, uint16_t* Y, const int32_t* off_pad, const int32_t* counts,
                               uint32_t* status, uint32_t* sched, int num_sms, cudaStream_t st);
+
+// The experts' backward products.  b: token rows in boxes of train_token_box(i)
+// rows x 64 (down: dY; up: dg, du), or X and h in boxes of 64 x 64 (weights).
+__host__ __device__ constexpr int train_token_box(int i) { return 16 << i; }
+struct TrainMaps {
+  CUtensorMap a[3];     // down: W_down; up: W_gate, W_up (box 128 x 64); weights: dg, du, dY (box 64 x 64)
+  CUtensorMap b[2][4];
+  CUtensorMap in[2];    // down: g, u, box 32 x 64
+  CUtensorMap out[3];   // down: dg, du; up: dX; weights: dW_gate, dW_up, dW_down; box 32 x 64
+};
+cudaError_t launch_down_backward(const moe_shape& s, const TrainMaps& m, uint16_t* dg, uint16_t* du,
+                                 const int32_t* off_pad, const int32_t* counts, uint32_t* status, uint32_t* sched,
+                                 int num_sms, cudaStream_t st);
+cudaError_t launch_up_backward(const moe_shape& s, const TrainMaps& m, uint16_t* dx, const int32_t* off_pad,
+                               const int32_t* counts, uint32_t* status, uint32_t* sched, int num_sms,
+                               cudaStream_t st);
+cudaError_t launch_weight_backward(const moe_shape& s, const TrainMaps& m, const int32_t* off_pad,
+                                   const int32_t* counts, uint32_t* status, uint32_t* sched, int num_sms,
+                                   cudaStream_t st);
+// The combine's gradients: dY[row] = w dout, and the router's dlogits.
+cudaError_t launch_combine_backward(const moe_shape& s, const uint16_t* Y, const int32_t* scatter_idx,
+                                    const int32_t* topk_ids, const float* topk_w, const uint16_t* dout, uint16_t* dY,
+                                    float* dlogits, uint32_t* status, int num_sms, cudaStream_t st);
 
 // Balance loss.  partials: the workspace region past its first 256 bytes
 // (balance_partial_bytes); counter: a uint32 that is zero between calls.

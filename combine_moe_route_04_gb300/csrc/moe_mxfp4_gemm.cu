@@ -42,6 +42,7 @@
 
 #include "moe_internal.h"
 #include "moe_mxfp4.cuh"
+#include "moe_transpose.cuh"
 
 namespace moe {
 namespace {
@@ -53,15 +54,6 @@ constexpr int kRowBytes = kStageK / 2;   // codes of a row in a stage (128-byte 
 constexpr int kWBytes = 128 * kRowBytes; // one block of 128 weight rows
 constexpr int kSfBytes = 512 * kAtoms;   // scale tiles of 128 rows
 constexpr int kFirstEpi = 2;             // epilogue warps follow the loading and the issuing one
-// Staging of 32 rows x 128 bf16 columns, written by the four warps of a turn:
-// two halves of 64 columns, rows of 128 bytes, in the 128-byte swizzle of the
-// stores' tensor map (which also puts eight rows on different banks).
-constexpr int kHalfOutBytes = 32 * 128;
-constexpr int kStageOutBytes = 2 * kHalfOutBytes;
-// byte offset of row t, 16-byte chunk c (of 16) in the staging
-__device__ __forceinline__ int staged_at(int t, int c) {
-  return (c >> 3) * kHalfOutBytes + t * 128 + (((c & 7) ^ (t & 7)) << 4);
-}
 constexpr int kTileRing = 4;             // tile indices on their way from the producer
 
 // What depends on the most rows of a window.
@@ -95,7 +87,7 @@ struct Cfg {
   static constexpr int CNT_OFF = WIN_OFF + (kMaxExperts + 1) * 4;
   static constexpr int OFFP_OFF = CNT_OFF + kMaxExperts * 4;
   static constexpr int OUT_OFF = (OFFP_OFF + (kMaxExperts + 1) * 4 + 1023) / 1024 * 1024;
-  static constexpr int ALLOC = OUT_OFF + EPI_SPLIT * kStageOutBytes + 1024;
+  static constexpr int ALLOC = OUT_OFF + EPI_SPLIT * kPieceBytes + 1024;
   static_assert(STAGE_BYTES % 1024 == 0, "stages start on swizzle atoms");
   static_assert(SF_COL + STAGES * SF_STAGE_COLS <= 512, "TMEM columns");
   static_assert(ALLOC <= 232448, "shared memory budget");
@@ -236,36 +228,7 @@ __device__ __forceinline__ float silu_mul(float g, float u) {
   return g * r * u;
 }
 
-// 16 TMEM lanes x 32 columns: thread i gets, for each group j of eight columns,
-// lane i / 4, columns 8 j + 2 (i % 4) and the next (v[4 j], v[4 j + 1]) and the
-// same of lane i / 4 + 8 (v[4 j + 2], v[4 j + 3]).
-__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t* v) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
-        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-      : "r"(taddr)
-      : "memory");
-}
-
-// A 32-lane x 32-column piece of an accumulator: lanes 0-15 in v[0..15], lanes
-// 16-31 in v[16..31].
-__device__ __forceinline__ void load_piece(uint32_t taddr, uint32_t (&v)[32]) {
-  tmem_ld_16x256b_x4(taddr, v);
-  tmem_ld_16x256b_x4(taddr + (16u << 16), v + 16);
-}
-
-// A piece to bf16 pairs: entry 4 j + x holds the columns 8 j + 2 (i % 4) and the
-// next of TMEM lane 8 x + i / 4; rounded alone, or as silu(g) * u.
-__device__ __forceinline__ constexpr int piece_entry(int k) { return (k & 2) * 8 + (k >> 2) * 4 + (k & 1) * 2; }
-__device__ __forceinline__ void round_piece(const uint32_t (&v)[32], uint32_t (&out)[16]) {
-#pragma unroll
-  for (int k = 0; k < 16; ++k) {
-    const int i = piece_entry(k);
-    out[k] = pack_bf16x2(__uint_as_float(v[i]), __uint_as_float(v[i + 1]));
-  }
-}
+// The same of silu(g) * u.
 __device__ __forceinline__ void gate_piece(const uint32_t (&g)[32], const uint32_t (&u)[32], uint32_t (&out)[16]) {
 #pragma unroll
   for (int k = 0; k < 16; ++k) {
@@ -273,25 +236,6 @@ __device__ __forceinline__ void gate_piece(const uint32_t (&g)[32], const uint32
     out[k] = pack_bf16x2(silu_mul(__uint_as_float(g[i]), __uint_as_float(u[i])),
                          silu_mul(__uint_as_float(g[i + 1]), __uint_as_float(u[i + 1])));
   }
-}
-
-// Four 8 x 8 bf16 matrices to shared memory, transposed: thread i's pairs lie
-// along a matrix row's neighbours 2 (i % 4), row i / 4; the address of row r of
-// matrix m comes from thread 8 m + r.
-__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
-               "r"(c), "r"(d)
-               : "memory");
-}
-
-// Writes a piece as bf16 to the staging at `out`, columns 32 q..: packed[4 j + x]
-// holds the rows 8 j + 2 (i % 4) and the next of column x * 8 + i / 4, so matrix
-// (j, x) lands at rows 8 j.., columns 32 q + 8 x...
-__device__ __forceinline__ void stage_piece(uint32_t out, int q, const uint32_t (&packed)[16], int lane) {
-  const uint32_t at = out + staged_at(lane & 7, 4 * q + (lane >> 3));  // thread 8 x + r: row r, columns 8 x
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    stmatrix_x4_trans(at + 8 * j * 128, packed[4 * j], packed[4 * j + 1], packed[4 * j + 2], packed[4 * j + 3]);
 }
 
 template <int kMode, int kTok>
@@ -531,7 +475,7 @@ __global__ void __launch_bounds__(Cfg<kTok>::THREADS, 1)
     // a lane quarter take the window's 32-row pieces in turn
     const int q = warp & 3;
     const int turn = (warp - kFirstEpi) / 4;
-    uint8_t* out = smem + C::OUT_OFF + turn * kStageOutBytes;
+    uint8_t* out = smem + C::OUT_OFF + turn * kPieceBytes;
     const uint32_t out_addr = smem_u32(out);
     const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16);
     uint32_t tcount = 0;
@@ -580,7 +524,7 @@ __global__ void __launch_bounds__(Cfg<kTok>::THREADS, 1)
         if (kMode != kUpMxfp4 && left >= 32) {  // alike for the turn's warps
           if (q == 0 && lane == 0) {
             tma_store_2d(&maps.out, out, col0, static_cast<int32_t>(r0));
-            tma_store_2d(&maps.out, out + kHalfOutBytes, col0 + 64, static_cast<int32_t>(r0));
+            tma_store_2d(&maps.out, out + kPieceBytes / 2, col0 + 64, static_cast<int32_t>(r0));
             tma_store_commit();
           }
           __syncwarp();

@@ -39,9 +39,10 @@
  *   - a call makes the stream's device current for its launches and puts the
  *     calling thread's previous current device back before it returns.
  *
- * The experts' products also run on MXFP4 operands (moe_*_mxfp4), and the
- * router's balance loss has its gradient (moe_balance_loss*); both are
- * described where they are declared.
+ * The experts' products also run on MXFP4 operands (moe_*_mxfp4), the router's
+ * balance loss has its gradient (moe_balance_loss*), and the layer has its
+ * backward pass (moe_forward_train, moe_*backward); each is described where it
+ * is declared.
  *
  * Supported shapes (else MOE_ERR_UNSUPPORTED_SHAPE): 1 <= T <= 2^22,
  * 1 <= E <= 256, 1 <= k <= min(E, 16), 128 <= H <= 32768 and
@@ -408,6 +409,96 @@ moe_status moe_balance_loss_backward(const moe_shape *shape, const float *logits
                                      const uint8_t *mask, const int32_t *counts,
                                      const int32_t *num_tokens, const float *grad_losses,
                                      float *dlogits, moe_stream_t stream);
+
+/* --------------------------------------------------------------- training
+ * The backward pass of the experts' gated feed-forward and of the layer around
+ * it.  Per expert, over its rows,
+ *   g = x Wg, u = x Wu, s = sigmoid(g), h = g s u, Y = h Wd
+ *   dh = dY Wd^T, dg = dh u s (1 + g (1 - s)), du = dh g s
+ *   dx = dg Wg^T + du Wu^T, dWg = x^T dg, dWu = x^T du, dWd = h^T dY
+ * with float32 sums, and g, u, h, dg, du and every result rounded once to bf16.
+ * One expert that takes every token (E = k = 1, counts[0] = T) is a dense gated
+ * feed-forward.
+ *
+ * Buffers in expert order have max_rows rows, as above; padding rows are not
+ * written, and what they hold does not reach a result.  ws: any workspace, or
+ * at least 256 bytes whose first 256 were cleared (the status word and the tile
+ * counters; a product that finds its counter anything but cleared reports
+ * MOE_ERR_DEVICE_BOUNDS).  Outputs may not overlap inputs or one another. */
+
+/* moe_grouped_gemm_up_rows that also keeps g and u, [max_rows, I] bf16 (h is
+ * formed from the float32 sums: the same bits). */
+moe_status moe_grouped_gemm_up_train(const moe_shape *shape, const moe_bf16 *Xp,
+                                     const int32_t *counts, const int32_t *off_pad,
+                                     const moe_bf16 *W_gate, const moe_bf16 *W_up, moe_bf16 *g,
+                                     moe_bf16 *u, moe_bf16 *h, void *ws, moe_stream_t stream);
+
+/* Gradients of the combine and of the routing weights:
+ *   dY[row(t, j)] = topk_w[t, j] dout[t]                     [max_rows, H] bf16
+ *   dlogits[t, e] = sum over j with topk_ids[t, j] = e of
+ *                   w_j (dw_j - sum_l w_l dw_l),  dw_j = <dout[t], Y[row(t, j)]>
+ * [T, E] float32 (zero where nothing was picked), which is the gradient of the
+ * softmax, top-k and renormalisation with the picks held.  A row or an id out of
+ * range takes no part and is reported.
+ *   Y, scatter_idx, topk_ids, topk_w: the forward's; dout [T, H] bf16 */
+moe_status moe_combine_backward(const moe_shape *shape, const moe_bf16 *Y,
+                                const int32_t *scatter_idx, const int32_t *topk_ids,
+                                const float *topk_w, const moe_bf16 *dout, moe_bf16 *dY,
+                                float *dlogits, void *ws, moe_stream_t stream);
+
+/* dg and du [max_rows, I] from dY [max_rows, H]; the activation's derivative is
+ * formed in the product's epilogue, from the float32 dh. */
+moe_status moe_grouped_gemm_down_backward(const moe_shape *shape, const moe_bf16 *dY,
+                                          const int32_t *counts, const int32_t *off_pad,
+                                          const moe_bf16 *W_down, const moe_bf16 *g,
+                                          const moe_bf16 *u, moe_bf16 *dg, moe_bf16 *du, void *ws,
+                                          moe_stream_t stream);
+
+/* dXp [max_rows, H] from dg and du: both products in one sum. */
+moe_status moe_grouped_gemm_up_backward(const moe_shape *shape, const moe_bf16 *dg,
+                                        const moe_bf16 *du, const int32_t *counts,
+                                        const int32_t *off_pad, const moe_bf16 *W_gate,
+                                        const moe_bf16 *W_up, moe_bf16 *dXp, void *ws,
+                                        moe_stream_t stream);
+
+/* The gradients of the three weights, [E, H, I], [E, H, I] and [E, I, H] bf16,
+ * from the rows and their gradients; zero for an expert without rows. */
+moe_status moe_grouped_gemm_weight_backward(const moe_shape *shape, const moe_bf16 *Xp,
+                                            const moe_bf16 *h, const moe_bf16 *dg,
+                                            const moe_bf16 *du, const moe_bf16 *dY,
+                                            const int32_t *counts, const int32_t *off_pad,
+                                            moe_bf16 *dW_gate, moe_bf16 *dW_up, moe_bf16 *dW_down,
+                                            void *ws, moe_stream_t stream);
+
+/* The gradient of the row gather: dX[t] = bf16(sum_j dXp[scatter_idx[t, j]]),
+ * a float32 sum in slot order. */
+moe_status moe_permute_backward(const moe_shape *shape, const moe_bf16 *dXp,
+                                const int32_t *scatter_idx, moe_bf16 *dX, void *ws,
+                                moe_stream_t stream);
+
+/* moe_forward (the same output, bit for bit) that keeps g and u [max_rows, I]
+ * for the backward pass, which also reads the routing, Xp, h and Y left in
+ * `ws`: one workspace per layer whose backward pass is still to come. */
+moe_status moe_forward_train(const moe_shape *shape, const float *logits, const moe_bf16 *X,
+                             const moe_bf16 *W_gate, const moe_bf16 *W_up, const moe_bf16 *W_down,
+                             moe_bf16 *g, moe_bf16 *u, moe_bf16 *out, void *ws,
+                             moe_stream_t stream);
+
+/* Host only.  Bytes of the scratch of moe_backward, which layers may share;
+ * moe_workspace_init clears its counters and moe_last_device_status reads its
+ * status word. */
+moe_status moe_backward_workspace_size(const moe_shape *shape, size_t *bytes);
+
+/* The layer's backward pass: dout [T, H] bf16 to dX [T, H], the gradients of
+ * the three weights, and dlogits [T, E] float32 (of the routing weights alone:
+ * moe_balance_loss_backward's adds to it).
+ *   g, u, ws: as moe_forward_train left them (read, not changed)
+ *   bws:      moe_backward_workspace_size bytes */
+moe_status moe_backward(const moe_shape *shape, const moe_bf16 *W_gate, const moe_bf16 *W_up,
+                        const moe_bf16 *W_down, const moe_bf16 *g, const moe_bf16 *u,
+                        const moe_bf16 *dout, moe_bf16 *dX, moe_bf16 *dW_gate, moe_bf16 *dW_up,
+                        moe_bf16 *dW_down, float *dlogits, const void *ws, void *bws,
+                        moe_stream_t stream);
 
 #ifdef __cplusplus
 }
