@@ -24,7 +24,10 @@ __all__ = ["MoEError", "MoEShape", "MoEViews", "lib_path", "load", "shape", "cap
            "balance_workspace_size", "alloc_balance_workspace", "moe_balance_loss", "moe_balance_loss_backward",
            "moe_grouped_gemm_up_train", "moe_combine_backward", "moe_grouped_gemm_down_backward",
            "moe_grouped_gemm_up_backward", "moe_grouped_gemm_weight_backward", "moe_permute_backward",
-           "moe_forward_train", "backward_workspace_size", "alloc_backward_workspace", "moe_backward"]
+           "moe_forward_train", "backward_workspace_size", "alloc_backward_workspace", "moe_backward",
+           "alloc_int8", "moe_quantize_int8", "moe_quantize_weights_int8", "moe_dequantize_int8",
+           "moe_quantize_permute_int8", "moe_grouped_gemm_up_int8", "moe_grouped_gemm_down_int8",
+           "int8_workspace_size", "alloc_int8_workspace", "moe_forward_int8"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libmoe_gb300.so")
@@ -47,7 +50,10 @@ EXPORTS = ["moe_status_string", "moe_capacity", "moe_workspace_size", "moe_works
            "moe_forward_mxfp4", "moe_balance_workspace_size", "moe_balance_loss", "moe_balance_loss_backward",
            "moe_grouped_gemm_up_train", "moe_combine_backward", "moe_grouped_gemm_down_backward",
            "moe_grouped_gemm_up_backward", "moe_grouped_gemm_weight_backward", "moe_permute_backward",
-           "moe_forward_train", "moe_backward_workspace_size", "moe_backward"]
+           "moe_forward_train", "moe_backward_workspace_size", "moe_backward",
+           "moe_quantize_int8", "moe_quantize_weights_int8", "moe_dequantize_int8",
+           "moe_quantize_permute_int8", "moe_grouped_gemm_up_int8", "moe_grouped_gemm_down_int8",
+           "moe_int8_workspace_size", "moe_forward_int8"]
 
 
 class MoEError(RuntimeError):
@@ -134,7 +140,15 @@ def load():
                        ("moe_permute_backward", [S] + [P] * 5),
                        ("moe_forward_train", [S] + [P] * 10),
                        ("moe_backward_workspace_size", [S, Z]),
-                       ("moe_backward", [S] + [P] * 14)):
+                       ("moe_backward", [S] + [P] * 14),
+                       ("moe_quantize_int8", [P, I64, I64, P, P, P]),
+                       ("moe_quantize_weights_int8", [P, ctypes.c_int32, I64, I64, P, P, P]),
+                       ("moe_dequantize_int8", [P, P, I64, I64, P, P]),
+                       ("moe_quantize_permute_int8", [S] + [P] * 6),
+                       ("moe_grouped_gemm_up_int8", [S] + [P] * 11),
+                       ("moe_grouped_gemm_down_int8", [S] + [P] * 9),
+                       ("moe_int8_workspace_size", [S, Z]),
+                       ("moe_forward_int8", [S] + [P] * 11)):
         fn = getattr(lib, name)
         fn.restype = st
         fn.argtypes = args
@@ -423,6 +437,7 @@ class _Plan:
         self.mxfp4_ws = mxfp4_workspace_size(self.shape)
         self.balance_ws = balance_workspace_size(self.shape)
         self.ws = workspace_size(self.shape)
+        self.int8_ws = int8_workspace_size(self.shape)
         self.backward_ws = backward_workspace_size(self.shape)
 
 
@@ -447,7 +462,7 @@ def _dtypes():
     if _Dtypes.u8 is None:
         import torch
         _Dtypes.f32, _Dtypes.bf16, _Dtypes.i32 = torch.float32, torch.bfloat16, torch.int32
-        _Dtypes.bool, _Dtypes.u8 = torch.bool, torch.uint8
+        _Dtypes.bool, _Dtypes.i8, _Dtypes.u8 = torch.bool, torch.int8, torch.uint8
     return _Dtypes
 
 
@@ -709,3 +724,101 @@ def moe_backward(s, W_gate, W_up, W_down, g, u, dout, dX, dW_gate, dW_up, dW_dow
         _dev_tensor(ws, d.u8, s.ws, "ws"), _dev_tensor(bws, d.u8, s.backward_ws, "bws"), _stream(stream))
     if rc:
         _check(rc, "moe_backward")
+
+
+def alloc_int8(rows: int, cols: int, device="cuda") -> tuple:
+    """Device buffers (codes [rows, cols] int8, scales [rows] float32) for a matrix in 8-bit integers."""
+    import torch
+    return (torch.empty((rows, cols), dtype=torch.int8, device=device),
+            torch.empty(rows, dtype=torch.float32, device=device))
+
+
+def _int8_ptrs(codes, scales, rows, cols, name):
+    # the call itself refuses unsupported sizes
+    d = _dtypes()
+    return _dev_tensor(codes, d.i8, rows * cols, name + "codes"), _dev_tensor(scales, d.f32, rows, name + "scales")
+
+
+def moe_quantize_int8(x, rows, cols, codes, scales, stream=None):
+    c, z = _int8_ptrs(codes, scales, rows, cols, "")
+    rc = (_lib or load()).moe_quantize_int8(_dev_tensor(x, _dtypes().bf16, rows * cols, "x"), rows, cols, c, z,
+                                            _stream(stream))
+    if rc:
+        _check(rc, "moe_quantize_int8")
+
+
+def moe_quantize_weights_int8(w, E, K, N, codes, scales, stream=None):
+    """W [E, K, N] (K the reduction axis) to the 8-bit matrix [E * N, K]."""
+    c, z = _int8_ptrs(codes, scales, E * N, K, "")
+    rc = (_lib or load()).moe_quantize_weights_int8(_dev_tensor(w, _dtypes().bf16, E * K * N, "w"), E, K, N, c, z,
+                                                    _stream(stream))
+    if rc:
+        _check(rc, "moe_quantize_weights_int8")
+
+
+def moe_dequantize_int8(codes, scales, rows, cols, x, stream=None):
+    c, z = _int8_ptrs(codes, scales, rows, cols, "")
+    rc = (_lib or load()).moe_dequantize_int8(c, z, rows, cols, _dev_tensor(x, _dtypes().bf16, rows * cols, "x"),
+                                              _stream(stream))
+    if rc:
+        _check(rc, "moe_dequantize_int8")
+
+
+def moe_quantize_permute_int8(s, X, scatter_idx, codes, scales, ws, stream=None):
+    s, d = _plan(s), _dtypes()
+    rc = (_lib or load()).moe_quantize_permute_int8(
+        s.ref, _dev_tensor(X, d.bf16, s.T * s.H, "X"), _dev_tensor(scatter_idx, d.i32, s.T * s.k, "scatter_idx"),
+        *_int8_ptrs(codes, scales, s.max_rows, s.H, ""), _dev_tensor(ws, d.u8, 256, "ws"), _stream(stream))
+    if rc:
+        _check(rc, "moe_quantize_permute_int8")
+
+
+def moe_grouped_gemm_up_int8(s, x_codes, x_scales, counts, off_pad, wg_codes, wg_scales, wu_codes, wu_scales, h, ws,
+                             stream=None):
+    """The gate/up product on rows and weights in 8-bit integers; ws: any
+    workspace, or a uint8 buffer of at least 256 bytes, zeroed once."""
+    s, d = _plan(s), _dtypes()
+    rc = (_lib or load()).moe_grouped_gemm_up_int8(
+        s.ref, *_int8_ptrs(x_codes, x_scales, s.max_rows, s.H, "x_"), _dev_tensor(counts, d.i32, s.E, "counts"),
+        _dev_tensor(off_pad, d.i32, s.E + 1, "off_pad"), *_int8_ptrs(wg_codes, wg_scales, s.E * s.I, s.H, "wg_"),
+        *_int8_ptrs(wu_codes, wu_scales, s.E * s.I, s.H, "wu_"), _dev_tensor(h, d.bf16, s.max_rows * s.I, "h"),
+        _dev_tensor(ws, d.u8, 256, "ws"), _stream(stream))
+    if rc:
+        _check(rc, "moe_grouped_gemm_up_int8")
+
+
+def moe_grouped_gemm_down_int8(s, h_codes, h_scales, counts, off_pad, wd_codes, wd_scales, Y, ws, stream=None):
+    """The down product on rows and weights in 8-bit integers; ws as for the gate/up product."""
+    s, d = _plan(s), _dtypes()
+    rc = (_lib or load()).moe_grouped_gemm_down_int8(
+        s.ref, *_int8_ptrs(h_codes, h_scales, s.max_rows, s.I, "h_"), _dev_tensor(counts, d.i32, s.E, "counts"),
+        _dev_tensor(off_pad, d.i32, s.E + 1, "off_pad"), *_int8_ptrs(wd_codes, wd_scales, s.E * s.H, s.I, "wd_"),
+        _dev_tensor(Y, d.bf16, s.max_rows * s.H, "Y"), _dev_tensor(ws, d.u8, 256, "ws"), _stream(stream))
+    if rc:
+        _check(rc, "moe_grouped_gemm_down_int8")
+
+
+def int8_workspace_size(s) -> int:
+    n = ctypes.c_size_t()
+    _check(load().moe_int8_workspace_size(_sp(s), ctypes.byref(n)), "moe_int8_workspace_size")
+    return n.value
+
+
+def alloc_int8_workspace(s, device="cuda", stream=None):
+    """A uint8 CUDA tensor of moe_int8_workspace_size bytes with its counters cleared."""
+    import torch
+    ws = torch.empty(int8_workspace_size(s), dtype=torch.uint8, device=device)
+    workspace_init(s, ws, stream)
+    return ws
+
+
+def moe_forward_int8(s, logits, X, wg_codes, wg_scales, wu_codes, wu_scales, wd_codes, wd_scales, out, ws, stream=None):
+    """moe_forward with the experts' products in 8-bit integers (weights as moe_quantize_weights_int8 leaves them)."""
+    s, d = _plan(s), _dtypes()
+    rc = (_lib or load()).moe_forward_int8(
+        s.ref, _dev_tensor(logits, d.f32, s.T * s.E, "logits"), _dev_tensor(X, d.bf16, s.T * s.H, "X"),
+        *_int8_ptrs(wg_codes, wg_scales, s.E * s.I, s.H, "wg_"), *_int8_ptrs(wu_codes, wu_scales, s.E * s.I, s.H, "wu_"),
+        *_int8_ptrs(wd_codes, wd_scales, s.E * s.H, s.I, "wd_"), _dev_tensor(out, d.bf16, s.T * s.H, "out"),
+        _dev_tensor(ws, d.u8, s.int8_ws, "ws"), _stream(stream))
+    if rc:
+        _check(rc, "moe_forward_int8")

@@ -172,9 +172,10 @@ moe_status check_ptrs(std::initializer_list<const void*> ptrs) {
   return MOE_OK;
 }
 
-bool mxfp4_dim(int64_t n) { return n >= 128 && n <= 32768 && n % 128 == 0; }
-moe_status check_mxfp4(int64_t rows, int64_t cols) {
-  return rows >= 1 && rows < (int64_t(1) << 31) && mxfp4_dim(cols) ? MOE_OK : MOE_ERR_UNSUPPORTED_SHAPE;
+// the sizes a quantised matrix may have
+bool matrix_dim(int64_t n) { return n >= 128 && n <= 32768 && n % 128 == 0; }
+moe_status check_matrix(int64_t rows, int64_t cols) {
+  return rows >= 1 && rows < (int64_t(1) << 31) && matrix_dim(cols) ? MOE_OK : MOE_ERR_UNSUPPORTED_SHAPE;
 }
 
 // Byte offsets of moe_forward_mxfp4's workspace (its first 256 bytes as in
@@ -243,6 +244,53 @@ BackwardLayout backward_layout(const moe_shape& s) {
   L.du = take(mr * static_cast<size_t>(s.I) * 2);
   L.total = off;
   return L;
+}
+
+// Byte offsets of moe_forward_int8's workspace (its first 256 bytes as in every
+// workspace).
+struct Int8Layout {
+  size_t chunk_counts, topk_ids, topk_w, counts, off_pad, block_expert, num_blocks, gather_idx, scatter_idx;
+  size_t x_codes, x_scales, h, h_codes, h_scales, y, total;
+};
+Int8Layout int8_layout(const moe_shape& s) {
+  Int8Layout L{};
+  const size_t T = static_cast<size_t>(s.T), E = static_cast<size_t>(s.E), k = static_cast<size_t>(s.k);
+  const size_t mr = static_cast<size_t>(max_rows_of(s)), H = static_cast<size_t>(s.H), I = static_cast<size_t>(s.I);
+  size_t off = align_up(256);
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = align_up(off + bytes);
+    return at;
+  };
+  L.chunk_counts = take(E * static_cast<size_t>(num_chunks_of(s)) * 4);
+  L.topk_ids = take(T * k * 4);
+  L.topk_w = take(T * k * 4);
+  L.counts = take(E * 4);
+  L.off_pad = take((E + 1) * 4);
+  L.block_expert = take(static_cast<size_t>(max_blocks_of(s)) * 4);
+  L.num_blocks = take(4);
+  L.gather_idx = take(mr * 4);
+  L.scatter_idx = take(T * k * 4);
+  L.x_codes = take(mr * H);
+  L.x_scales = take(mr * 4);
+  L.h = take(mr * I * 2);
+  L.h_codes = take(mr * I);
+  L.h_scales = take(mr * 4);
+  L.y = take(mr * H * 2);
+  L.total = off;
+  return L;
+}
+
+// Tensor maps of a product: rows [max_rows][K], weights [E*N][K], bf16 output
+// [max_rows][N].
+bool int8_maps(const moe_shape& s, int64_t K, int64_t N, const int8_t* rows, const int8_t* w0, const int8_t* w1,
+               const uint16_t* out, Int8Maps* m) {
+  const uint64_t kb = static_cast<uint64_t>(K), wr = static_cast<uint64_t>(s.E) * static_cast<uint64_t>(N);
+  const uint64_t mr = static_cast<uint64_t>(max_rows_of(s));
+  for (int i = 0; i < 3; ++i)
+    if (!encode_bytes_2d(&m->t[i], rows, mr, kb, int8_token_box(i))) return false;
+  return encode_bf16_2d(&m->out, out, mr, static_cast<uint64_t>(N), 32, 64) &&
+         encode_bytes_2d(&m->w0, w0, wr, kb, 128) && encode_bytes_2d(&m->w1, w1, wr, kb, 128);
 }
 
 moe_status run_down_backward(const moe_shape& s, const uint16_t* dY, const int32_t* counts, const int32_t* off_pad,
@@ -572,7 +620,7 @@ moe_status moe_forward(const moe_shape* shape, const float* logits, const moe_bf
 }
 
 moe_status moe_mxfp4_sizes(int64_t rows, int64_t cols, size_t* code_bytes, size_t* scale_bytes) {
-  const moe_status st = check_mxfp4(rows, cols);
+  const moe_status st = check_matrix(rows, cols);
   if (st != MOE_OK) return st;
   if (code_bytes == nullptr || scale_bytes == nullptr) return MOE_ERR_INVALID_ARG;
   *code_bytes = static_cast<size_t>(rows) * static_cast<size_t>(cols) / 2;
@@ -582,7 +630,7 @@ moe_status moe_mxfp4_sizes(int64_t rows, int64_t cols, size_t* code_bytes, size_
 
 moe_status moe_quantize_mxfp4(const moe_bf16* x, int64_t rows, int64_t cols, uint8_t* codes, uint8_t* scales,
                               moe_stream_t stream) {
-  moe_status st = check_mxfp4(rows, cols);
+  moe_status st = check_matrix(rows, cols);
   if (st != MOE_OK) return st;
   st = check_ptrs({x, codes, scales});
   if (st != MOE_OK) return st;
@@ -595,7 +643,7 @@ moe_status moe_quantize_mxfp4(const moe_bf16* x, int64_t rows, int64_t cols, uin
 
 moe_status moe_quantize_weights_mxfp4(const moe_bf16* w, int32_t E, int64_t K, int64_t N, uint8_t* codes,
                                       uint8_t* scales, moe_stream_t stream) {
-  if (E < 1 || E > 256 || !mxfp4_dim(K) || !mxfp4_dim(N)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (E < 1 || E > 256 || !matrix_dim(K) || !matrix_dim(N)) return MOE_ERR_UNSUPPORTED_SHAPE;
   moe_status st = check_ptrs({w, codes, scales});
   if (st != MOE_OK) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -607,7 +655,7 @@ moe_status moe_quantize_weights_mxfp4(const moe_bf16* w, int32_t E, int64_t K, i
 
 moe_status moe_dequantize_mxfp4(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, moe_bf16* x,
                                 moe_stream_t stream) {
-  moe_status st = check_mxfp4(rows, cols);
+  moe_status st = check_matrix(rows, cols);
   if (st != MOE_OK) return st;
   st = check_ptrs({codes, scales, x});
   if (st != MOE_OK) return st;
@@ -899,6 +947,147 @@ moe_status moe_backward(const moe_shape* shape, const moe_bf16* W_gate, const mo
   st = run_up_backward(sh, dg, du, v.counts, v.off_pad, W_gate, W_up, dXp, status, sms, s);
   if (st != MOE_OK) return st;
   return cuda_status(launch_combine(sh, dXp, v.scatter_idx, nullptr, dX, status, sms, s));
+}
+
+moe_status moe_quantize_int8(const moe_bf16* x, int64_t rows, int64_t cols, int8_t* codes, float* scales,
+                             moe_stream_t stream) {
+  moe_status st = check_matrix(rows, cols);
+  if (st != MOE_OK) return st;
+  st = check_ptrs({x, codes, scales});
+  if (st != MOE_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  DeviceRestore restore;
+  st = prepare_device(s, nullptr, &restore);
+  if (st != MOE_OK) return st;
+  return cuda_status(launch_quantize_rows_int8(x, rows, cols, codes, scales, s));
+}
+
+moe_status moe_quantize_weights_int8(const moe_bf16* w, int32_t E, int64_t K, int64_t N, int8_t* codes, float* scales,
+                                     moe_stream_t stream) {
+  if (E < 1 || E > 256 || !matrix_dim(K) || !matrix_dim(N)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  moe_status st = check_ptrs({w, codes, scales});
+  if (st != MOE_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  DeviceRestore restore;
+  st = prepare_device(s, nullptr, &restore);
+  if (st != MOE_OK) return st;
+  return cuda_status(launch_quantize_weights_int8(w, E, K, N, codes, scales, s));
+}
+
+moe_status moe_dequantize_int8(const int8_t* codes, const float* scales, int64_t rows, int64_t cols, moe_bf16* x,
+                               moe_stream_t stream) {
+  moe_status st = check_matrix(rows, cols);
+  if (st != MOE_OK) return st;
+  st = check_ptrs({codes, scales, x});
+  if (st != MOE_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  DeviceRestore restore;
+  st = prepare_device(s, nullptr, &restore);
+  if (st != MOE_OK) return st;
+  return cuda_status(launch_dequantize_rows_int8(codes, scales, rows, cols, x, s));
+}
+
+moe_status moe_quantize_permute_int8(const moe_shape* shape, const moe_bf16* X, const int32_t* scatter_idx,
+                                     int8_t* codes, float* scales, void* ws, moe_stream_t stream) {
+  moe_status st = check_shape(shape);
+  if (st != MOE_OK) return st;
+  st = check_ptrs({X, scatter_idx, codes, scales, ws});
+  if (st != MOE_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  DeviceRestore restore;
+  st = prepare_device(s, nullptr, &restore);
+  if (st != MOE_OK) return st;
+  return cuda_status(launch_quantize_permute_int8(*shape, X, scatter_idx, codes, scales, ws_status(ws), s));
+}
+
+moe_status moe_grouped_gemm_up_int8(const moe_shape* shape, const int8_t* x_codes, const float* x_scales,
+                                    const int32_t* counts, const int32_t* off_pad, const int8_t* wg_codes,
+                                    const float* wg_scales, const int8_t* wu_codes, const float* wu_scales,
+                                    moe_bf16* h, void* ws, moe_stream_t stream) {
+  moe_status st = check_shape(shape);
+  if (st != MOE_OK) return st;
+  st = check_ptrs({x_codes, x_scales, counts, off_pad, wg_codes, wg_scales, wu_codes, wu_scales, h, ws});
+  if (st != MOE_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int sms = 0;
+  DeviceRestore restore;
+  st = prepare_device(s, &sms, &restore);
+  if (st != MOE_OK) return st;
+  Int8Maps m;
+  if (!int8_maps(*shape, shape->H, shape->I, x_codes, wg_codes, wu_codes, h, &m)) return MOE_ERR_CUDA;
+  return cuda_status(launch_int8_up(*shape, m, x_scales, wg_scales, wu_scales, h, off_pad, counts, ws_status(ws),
+                                    ws_sched_up(ws_status(ws)), sms, s));
+}
+
+moe_status moe_grouped_gemm_down_int8(const moe_shape* shape, const int8_t* h_codes, const float* h_scales,
+                                      const int32_t* counts, const int32_t* off_pad, const int8_t* wd_codes,
+                                      const float* wd_scales, moe_bf16* Y, void* ws, moe_stream_t stream) {
+  moe_status st = check_shape(shape);
+  if (st != MOE_OK) return st;
+  st = check_ptrs({h_codes, h_scales, counts, off_pad, wd_codes, wd_scales, Y, ws});
+  if (st != MOE_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int sms = 0;
+  DeviceRestore restore;
+  st = prepare_device(s, &sms, &restore);
+  if (st != MOE_OK) return st;
+  Int8Maps m;
+  if (!int8_maps(*shape, shape->I, shape->H, h_codes, wd_codes, wd_codes, Y, &m)) return MOE_ERR_CUDA;
+  return cuda_status(launch_int8_down(*shape, m, h_scales, wd_scales, Y, off_pad, counts, ws_status(ws),
+                                      ws_sched_down(ws_status(ws)), sms, s));
+}
+
+moe_status moe_int8_workspace_size(const moe_shape* shape, size_t* bytes) {
+  const moe_status st = check_shape(shape);
+  if (st != MOE_OK) return st;
+  if (bytes == nullptr) return MOE_ERR_INVALID_ARG;
+  *bytes = int8_layout(*shape).total;
+  return MOE_OK;
+}
+
+moe_status moe_forward_int8(const moe_shape* shape, const float* logits, const moe_bf16* X, const int8_t* wg_codes,
+                            const float* wg_scales, const int8_t* wu_codes, const float* wu_scales,
+                            const int8_t* wd_codes, const float* wd_scales, moe_bf16* out, void* ws,
+                            moe_stream_t stream) {
+  moe_status st = check_shape(shape);
+  if (st != MOE_OK) return st;
+  st = check_ptrs({logits, X, wg_codes, wg_scales, wu_codes, wu_scales, wd_codes, wd_scales, out, ws});
+  if (st != MOE_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int sms = 0;
+  DeviceRestore restore;
+  st = prepare_device(s, &sms, &restore);
+  if (st != MOE_OK) return st;
+  const moe_shape& sh = *shape;
+  const Int8Layout L = int8_layout(sh);
+  uint8_t* b = static_cast<uint8_t*>(ws);
+  auto i32 = [&](size_t at) { return reinterpret_cast<int32_t*>(b + at); };
+  auto f32 = [&](size_t at) { return reinterpret_cast<float*>(b + at); };
+  auto i8 = [&](size_t at) { return reinterpret_cast<int8_t*>(b + at); };
+  uint16_t* h = reinterpret_cast<uint16_t*>(b + L.h);
+  uint16_t* Y = reinterpret_cast<uint16_t*>(b + L.y);
+  uint32_t* status = ws_status(ws);
+  Int8Maps up, down;
+  if (!int8_maps(sh, sh.H, sh.I, i8(L.x_codes), wg_codes, wu_codes, h, &up) ||
+      !int8_maps(sh, sh.I, sh.H, i8(L.h_codes), wd_codes, wd_codes, Y, &down))
+    return MOE_ERR_CUDA;
+  if (launch_route(sh, logits, i32(L.topk_ids), f32(L.topk_w), i32(L.counts), i32(L.off_pad), i32(L.block_expert),
+                   i32(L.num_blocks), i32(L.gather_idx), i32(L.scatter_idx), i32(L.chunk_counts),
+                   ws_route_counter(ws), status, s) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  if (launch_quantize_permute_int8(sh, X, i32(L.scatter_idx), i8(L.x_codes), f32(L.x_scales), status, s) !=
+      cudaSuccess)
+    return MOE_ERR_CUDA;
+  if (launch_int8_up(sh, up, f32(L.x_scales), wg_scales, wu_scales, h, i32(L.off_pad), i32(L.counts), status,
+                     ws_sched_up(status), sms, s) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  if (launch_quantize_expert_rows_int8(sh, h, sh.I, i32(L.gather_idx), i32(L.num_blocks), i8(L.h_codes),
+                                       f32(L.h_scales), s) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  if (launch_int8_down(sh, down, f32(L.h_scales), wd_scales, Y, i32(L.off_pad), i32(L.counts), status,
+                       ws_sched_down(status), sms, s) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  return cuda_status(launch_combine(sh, Y, i32(L.scatter_idx), f32(L.topk_w), out, status, sms, s));
 }
 
 }  // extern "C"

@@ -1,0 +1,302 @@
+// moe_int8.cu -- quantisation to 8-bit integers with one scale per row, and back.
+//
+// A row x gets the scale s = amax / 127 (float32, amax = max |x|) and the codes
+//   q = 127 x / amax, rounded to the nearest integer, ties to even,
+// and stands for q s.  The quotient is rounded as if it were exact: 127 x / amax
+// of two bf16 values (8-bit significands) is either a tie n + 1/2 or at least
+// 2^-17 of its power of two away from one, so it is formed as x * (127 / amax)
+// (off by less than 2^-22), rounded to 19 bits behind the leading one, which
+// restores a tie and crosses none, and then to an integer.
+//
+// Everything moves data once and is bound by memory; the weights' kernel reads
+// its columns twice, the second time from L2.
+// Inputs may be what an earlier kernel of a chain of dependent launches wrote, so
+// they are read past L1 (__ldcg), not through the non-coherent path.
+#include <cstdint>
+
+#include "moe_device.cuh"
+#include "moe_internal.h"
+
+namespace moe {
+namespace {
+
+constexpr uint32_t kInfBits = 0x7F80u;  // bf16 magnitudes from here on are infinite or NaN
+
+// the larger of the magnitudes of two pairs of bf16, per half
+__device__ __forceinline__ uint32_t max_magnitude(uint32_t m, uint32_t v) { return __vmaxu2(m, v & 0x7FFF7FFFu); }
+__device__ __forceinline__ uint32_t max_magnitude(uint32_t m, const uint4& v) {
+  return max_magnitude(max_magnitude(max_magnitude(max_magnitude(m, v.x), v.y), v.z), v.w);
+}
+
+// What a row's largest magnitude (bf16 bits) makes of its elements: the code of
+// x is rint(pre * x * mul), the scale `scale`.
+struct RowScale {
+  float pre, mul, scale;
+};
+__device__ __forceinline__ RowScale row_scale(uint32_t amax_bits) {
+  const float amax = __uint_as_float(amax_bits << 16);
+  RowScale r;
+  // far below one, 127 / amax would overflow: both are raised by 2^64 (exact)
+  r.pre = amax < 0x1p-64f ? 0x1p64f : 1.0f;
+  r.mul = __fdiv_rn(127.0f, amax * r.pre);
+  r.scale = __fdiv_rn(amax, 127.0f);
+  if (amax_bits == 0u) r.mul = 0.0f;
+  if (amax_bits >= kInfBits) {  // a NaN or an infinity: the row reads as NaN
+    r.mul = 0.0f;
+    r.scale = __uint_as_float(0x7FC00000u);
+  }
+  return r;
+}
+// (x may be a NaN or infinite only where mul = 0; the conversion gives 0 for the
+// NaN that comes out)
+__device__ __forceinline__ uint32_t code_of(float x, const RowScale& r) {
+  const float y = x * r.pre * r.mul;
+  const float z = __uint_as_float((__float_as_uint(y) + 8u) & ~15u);
+  return static_cast<uint32_t>(__float2int_rn(z));
+}
+// four codes of the bf16 pairs a, b
+__device__ __forceinline__ uint32_t codes4(uint32_t a, uint32_t b, const RowScale& r) {
+  const uint32_t lo = __byte_perm(code_of(bf16lo_to_f32(a), r), code_of(bf16hi_to_f32(a), r), 0x0040);
+  const uint32_t hi = __byte_perm(code_of(bf16lo_to_f32(b), r), code_of(bf16hi_to_f32(b), r), 0x0040);
+  return __byte_perm(lo, hi, 0x5410);
+}
+
+constexpr int kRowVecs = 4;  // 16-byte vectors of a row that a lane keeps
+
+// Row t of x to row(s) of codes: row t itself, or (scatter_idx) the token's k
+// permuted rows; with gather_idx, only rows of x that hold a token (x is then in
+// expert order).  A row is taken by a group of 1, 2, 4 or 8 warps, enough to keep
+// 8192 columns in registers between the maximum and the codes; further columns
+// are read twice.
+__global__ void __launch_bounds__(256) quantize_rows_kernel(const uint16_t* __restrict__ x, int64_t rows, int cols,
+                                                            const int32_t* __restrict__ scatter_idx, int k,
+                                                            int64_t max_rows, const int32_t* __restrict__ gather_idx,
+                                                            const int32_t* __restrict__ num_blocks, int group,
+                                                            int8_t* __restrict__ codes, float* __restrict__ scales,
+                                                            uint32_t* __restrict__ status) {
+  __shared__ uint32_t s_max[8];
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5;
+  const int part = warp & (group - 1);
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * (8 / group) + warp / group;
+  pdl_wait();
+  bool there = t < rows;
+  if (there && gather_idx != nullptr)
+    there = t < static_cast<int64_t>(__ldcg(num_blocks)) * kRowBlock && __ldcg(gather_idx + t) >= 0;
+  int64_t my_row = -1;  // lane j: the j-th row to write
+  if (there) {
+    if (scatter_idx == nullptr) {
+      my_row = t;
+    } else if (lane < k) {
+      const int32_t r = __ldcg(scatter_idx + t * k + lane);
+      if (r >= 0 && r < max_rows) my_row = r;
+      else if (part == 0) record_status(status, kStatusBounds);
+    }
+  }
+  const int vpr = cols / 8;
+  const uint4* src = reinterpret_cast<const uint4*>(x) + t * vpr;
+  const int first = part * 32 + lane, step = group * 32;
+  uint4 v[kRowVecs];
+  uint32_t m = 0u;
+#pragma unroll
+  for (int i = 0; i < kRowVecs; ++i) {
+    v[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (there && first + i * step < vpr) v[i] = __ldcg(src + first + i * step);
+  }
+#pragma unroll
+  for (int i = 0; i < kRowVecs; ++i) m = max_magnitude(m, v[i]);
+  if (there)
+    for (int c = first + kRowVecs * step; c < vpr; c += step) m = max_magnitude(m, __ldcg(src + c));
+  m = max(m & 0xFFFFu, m >> 16);
+  m = __reduce_max_sync(0xffffffffu, m);
+  if (group > 1) {
+    if (lane == 0) s_max[warp] = m;
+    __syncthreads();
+    m = 0u;
+    for (int i = 0; i < group; ++i) m = max(m, s_max[warp - part + i]);
+  }
+  if (!there) return;
+  const RowScale r = row_scale(m);
+  uint2* dst = reinterpret_cast<uint2*>(codes);
+  for (int c0 = part * 32; c0 < vpr; c0 += kRowVecs * step) {  // alike for the warp's lanes
+    uint2 q[kRowVecs];
+#pragma unroll
+    for (int i = 0; i < kRowVecs; ++i) {
+      const int c = c0 + lane + i * step;
+      if (c0 != part * 32 && c < vpr) v[i] = __ldcg(src + c);
+      q[i] = make_uint2(codes4(v[i].x, v[i].y, r), codes4(v[i].z, v[i].w, r));
+    }
+    for (int j = 0; j < k; ++j) {
+      const int64_t row = __shfl_sync(0xffffffffu, my_row, j);
+      if (row < 0) continue;
+#pragma unroll
+      for (int i = 0; i < kRowVecs; ++i)
+        if (c0 + lane + i * step < vpr) dst[row * vpr + c0 + lane + i * step] = q[i];
+    }
+  }
+  if (part == 0 && my_row >= 0 && lane < k) scales[my_row] = r.scale;
+}
+
+// Values bf16(q s): a thread takes 16 codes.
+__global__ void __launch_bounds__(256) dequantize_rows_kernel(const int8_t* __restrict__ codes,
+                                                              const float* __restrict__ scales, int64_t n16,
+                                                              int vecs_per_row, uint16_t* __restrict__ x) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+  if (i >= n16) return;
+  const uint4 q = __ldcg(reinterpret_cast<const uint4*>(codes) + i);
+  const float s = __ldcg(scales + i / vecs_per_row);
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+  uint32_t o[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t b = w[j >> 1] >> (16 * (j & 1));
+    o[j] = pack_bf16x2(static_cast<float>(static_cast<int8_t>(b)) * s,
+                       static_cast<float>(static_cast<int8_t>(b >> 8)) * s);
+  }
+  uint4* dst = reinterpret_cast<uint4*>(x) + 2 * i;
+  dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+  dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
+// Weights w [E][K][N] to codes [E][N][K], the reduction axis K contiguous, and a
+// scale per (e, n).  A CTA takes 64 columns of one expert: a first pass over
+// their K rows (128 bytes each) for the maxima, a second one in steps of kWk rows
+// for the codes, which cross shared memory once so that each column's 128 bytes
+// leave together.
+constexpr int kWn = 64;
+constexpr int kWeightThreads = 1024;
+constexpr int kWk = kWeightThreads / 8 * 4;  // four rows x eight columns per thread
+
+__global__ void __launch_bounds__(kWeightThreads) quantize_weights_kernel(const uint16_t* __restrict__ w, int K, int N,
+                                                                          int8_t* __restrict__ codes,
+                                                                          float* __restrict__ scales) {
+  __shared__ __align__(16) uint32_t s_codes[kWn * kWk / 4];
+  __shared__ uint4 s_max[kWeightThreads / 32][8];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int cg = threadIdx.x & 7;   // columns 8 cg..
+  const int kr = threadIdx.x >> 3;  // row of the thread, or group of four rows
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t e = blockIdx.y;
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * kWn;
+  const uint4* src = reinterpret_cast<const uint4*>(w + e * K * N + n0) + cg;
+  const int64_t pitch = N / 8;
+  uint4 m = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 8
+  for (int k = kr; k < K; k += kWeightThreads / 8) {
+    const uint4 v = __ldcg(src + k * pitch);
+    m.x = max_magnitude(m.x, v.x);
+    m.y = max_magnitude(m.y, v.y);
+    m.z = max_magnitude(m.z, v.z);
+    m.w = max_magnitude(m.w, v.w);
+  }
+#pragma unroll
+  for (int o = 8; o < 32; o <<= 1) {  // the warp's four rows
+    m.x = __vmaxu2(m.x, __shfl_xor_sync(0xffffffffu, m.x, o));
+    m.y = __vmaxu2(m.y, __shfl_xor_sync(0xffffffffu, m.y, o));
+    m.z = __vmaxu2(m.z, __shfl_xor_sync(0xffffffffu, m.z, o));
+    m.w = __vmaxu2(m.w, __shfl_xor_sync(0xffffffffu, m.w, o));
+  }
+  if (lane < 8) s_max[warp][lane] = m;
+  __syncthreads();
+  m = s_max[0][cg];
+  for (int i = 1; i < kWeightThreads / 32; ++i) {
+    const uint4 v = s_max[i][cg];
+    m.x = __vmaxu2(m.x, v.x);
+    m.y = __vmaxu2(m.y, v.y);
+    m.z = __vmaxu2(m.z, v.z);
+    m.w = __vmaxu2(m.w, v.w);
+  }
+  RowScale r[8];
+  const uint32_t mw[4] = {m.x, m.y, m.z, m.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    r[i] = row_scale((mw[i >> 1] >> (16 * (i & 1))) & 0xFFFFu);
+    if (kr == 0) scales[e * N + n0 + 8 * cg + i] = r[i].scale;
+  }
+  for (int k0 = 0; k0 < K; k0 += kWk) {
+    const int k = k0 + 4 * kr;
+    if (k < K) {  // K is a multiple of 128
+      uint4 v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = __ldcg(src + (k + i) * pitch);
+      const uint32_t a[4][4] = {{v[0].x, v[0].y, v[0].z, v[0].w}, {v[1].x, v[1].y, v[1].z, v[1].w},
+                                {v[2].x, v[2].y, v[2].z, v[2].w}, {v[3].x, v[3].y, v[3].z, v[3].w}};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {  // column 8 cg + i: its four k's are one word
+        uint32_t q[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          q[j] = code_of(i & 1 ? bf16hi_to_f32(a[j][i >> 1]) : bf16lo_to_f32(a[j][i >> 1]), r[i]);
+        // 16-byte chunks of a column are permuted by its group, which spreads
+        // both accesses over all banks
+        const int chunk = (kr >> 2) ^ cg;
+        s_codes[(8 * cg + i) * (kWk / 4) + chunk * 4 + (kr & 3)] =
+            __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
+      }
+    }
+    __syncthreads();
+    const int left = min(kWk, K - k0) / 16;  // 16-byte chunks of a column
+    for (int i = threadIdx.x; i < kWn * (kWk / 16); i += kWeightThreads) {
+      const int n = i / (kWk / 16), c = i % (kWk / 16);
+      if (c < left)
+        *reinterpret_cast<uint4*>(codes + (e * N + n0 + n) * K + k0 + c * 16) =
+            *reinterpret_cast<const uint4*>(s_codes + n * (kWk / 4) + (c ^ (n >> 3)) * 4);
+    }
+    __syncthreads();
+  }
+}
+
+int group_of(int64_t cols) {
+  int group = 1;
+  while (group < 8 && cols > 32 * 8 * kRowVecs * group) group *= 2;
+  return group;
+}
+
+}  // namespace
+
+cudaError_t launch_quantize_rows_int8(const uint16_t* x, int64_t rows, int64_t cols, int8_t* codes, float* scales,
+                                      cudaStream_t st) {
+  const int group = group_of(cols);
+  const int64_t per = 8 / group;
+  return launch_pdl(quantize_rows_kernel, dim3(static_cast<unsigned>((rows + per - 1) / per)), dim3(256), 0, st, x,
+                    rows, static_cast<int>(cols), nullptr, 1, rows, nullptr, nullptr, group, codes, scales, nullptr);
+}
+
+cudaError_t launch_quantize_expert_rows_int8(const moe_shape& s, const uint16_t* x, int64_t cols,
+                                             const int32_t* gather_idx, const int32_t* num_blocks, int8_t* codes,
+                                             float* scales, cudaStream_t st) {
+  const int group = group_of(cols);
+  const int64_t per = 8 / group, rows = max_rows_of(s);
+  return launch_pdl(quantize_rows_kernel, dim3(static_cast<unsigned>((rows + per - 1) / per)), dim3(256), 0, st, x,
+                    rows, static_cast<int>(cols), nullptr, 1, rows, gather_idx, num_blocks, group, codes, scales,
+                    nullptr);
+}
+
+cudaError_t launch_quantize_permute_int8(const moe_shape& s, const uint16_t* X, const int32_t* scatter_idx,
+                                         int8_t* codes, float* scales, uint32_t* status, cudaStream_t st) {
+  const int group = group_of(s.H);
+  const int64_t per = 8 / group;
+  return launch_pdl(quantize_rows_kernel, dim3(static_cast<unsigned>((s.T + per - 1) / per)), dim3(256), 0, st, X,
+                    static_cast<int64_t>(s.T), s.H, scatter_idx, s.k, max_rows_of(s), nullptr, nullptr, group, codes,
+                    scales, status);
+}
+
+cudaError_t launch_dequantize_rows_int8(const int8_t* codes, const float* scales, int64_t rows, int64_t cols,
+                                        uint16_t* x, cudaStream_t st) {
+  const int64_t n16 = rows * (cols / 16);
+  return launch_pdl(dequantize_rows_kernel, dim3(static_cast<unsigned>((n16 + 255) / 256)), dim3(256), 0, st, codes,
+                    scales, n16, static_cast<int>(cols / 16), x);
+}
+
+cudaError_t launch_quantize_weights_int8(const uint16_t* w, int E, int64_t K, int64_t N, int8_t* codes, float* scales,
+                                         cudaStream_t st) {
+  const dim3 grid(static_cast<unsigned>(N / kWn), static_cast<unsigned>(E));
+  return launch_pdl(quantize_weights_kernel, grid, dim3(kWeightThreads), 0, st, w, static_cast<int>(K),
+                    static_cast<int>(N), codes, scales);
+}
+
+}  // namespace moe

@@ -221,6 +221,37 @@ cudaError_t launch_combine_backward(const moe_shape& s, const uint16_t* Y, const
                                     const int32_t* topk_ids, const float* topk_w, const uint16_t* dout, uint16_t* dY,
                                     float* dlogits, uint32_t* status, int num_sms, cudaStream_t st);
 
+// 8-bit integers (codes int8 [rows][cols], a float32 scale per row; see
+// include/moe.h): quantisation of dense rows, of the real rows of a buffer in
+// expert order, of tokens into their permuted rows, and of weights [E][K][N] (to
+// [E][N][K]); the inverse.
+cudaError_t launch_quantize_rows_int8(const uint16_t* x, int64_t rows, int64_t cols, int8_t* codes, float* scales,
+                                      cudaStream_t st);
+cudaError_t launch_quantize_expert_rows_int8(const moe_shape& s, const uint16_t* x, int64_t cols,
+                                             const int32_t* gather_idx, const int32_t* num_blocks, int8_t* codes,
+                                             float* scales, cudaStream_t st);
+cudaError_t launch_quantize_permute_int8(const moe_shape& s, const uint16_t* X, const int32_t* scatter_idx,
+                                         int8_t* codes, float* scales, uint32_t* status, cudaStream_t st);
+cudaError_t launch_quantize_weights_int8(const uint16_t* w, int E, int64_t K, int64_t N, int8_t* codes, float* scales,
+                                         cudaStream_t st);
+cudaError_t launch_dequantize_rows_int8(const int8_t* codes, const float* scales, int64_t rows, int64_t cols,
+                                        uint16_t* x, cudaStream_t st);
+
+// The grouped products on 8-bit integers: code matrices as 128-byte-wide boxes.
+struct Int8Maps {
+  CUtensorMap t[3];  // rows [max_rows][K], boxes of int8_token_box(i) rows
+  CUtensorMap w0;    // weights [E*N][K] (gate, or down), box 128 rows
+  CUtensorMap w1;    // the up weights (down: a copy of w0)
+  CUtensorMap out;   // bf16 output [max_rows][N], box 32 rows x 64 columns
+};
+__host__ __device__ constexpr int int8_token_box(int i) { return 32 << i; }
+cudaError_t launch_int8_up(const moe_shape& s, const Int8Maps& m, const float* x_scales, const float* wg_scales,
+                           const float* wu_scales, uint16_t* h, const int32_t* off_pad, const int32_t* counts,
+                           uint32_t* status, uint32_t* sched, int num_sms, cudaStream_t st);
+cudaError_t launch_int8_down(const moe_shape& s, const Int8Maps& m, const float* h_scales, const float* wd_scales,
+                             uint16_t* Y, const int32_t* off_pad, const int32_t* counts, uint32_t* status,
+                             uint32_t* sched, int num_sms, cudaStream_t st);
+
 // Balance loss.  partials: the workspace region past its first 256 bytes
 // (balance_partial_bytes); counter: a uint32 that is zero between calls.
 constexpr int kBalanceMaxCtas = 256;  // at most 1023: the counter has ten bits for them

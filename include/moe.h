@@ -39,10 +39,10 @@
  *   - a call makes the stream's device current for its launches and puts the
  *     calling thread's previous current device back before it returns.
  *
- * The experts' products also run on MXFP4 operands (moe_*_mxfp4), the router's
- * balance loss has its gradient (moe_balance_loss*), and the layer has its
- * backward pass (moe_forward_train, moe_*backward); each is described where it
- * is declared.
+ * The experts' products also run on MXFP4 operands (moe_*_mxfp4) and on 8-bit
+ * integers (moe_*_int8), the router's balance loss has its gradient
+ * (moe_balance_loss*), and the layer has its backward pass (moe_forward_train,
+ * moe_*backward); each is described where it is declared.
  *
  * Supported shapes (else MOE_ERR_UNSUPPORTED_SHAPE): 1 <= T <= 2^22,
  * 1 <= E <= 256, 1 <= k <= min(E, 16), 128 <= H <= 32768 and
@@ -371,6 +371,74 @@ moe_status moe_forward_mxfp4(const moe_shape *shape, const float *logits, const 
                              const uint8_t *wu_codes, const uint8_t *wu_scales,
                              const uint8_t *wd_codes, const uint8_t *wd_scales, moe_bf16 *out,
                              void *ws, moe_stream_t stream);
+
+/* --------------------------------------------------------- 8-bit integers
+ * A matrix [rows, cols] in 8 bits: codes q [rows, cols] int8 and one float32
+ * scale per row, s = amax / 127 with amax = max |x| of the row; it stands for
+ * q s.  Quantisation: q = 127 x / amax rounded to the nearest integer, ties to
+ * even (-127 .. 127), exactly.  A row of zeros gets s = 0; a row holding a NaN
+ * or an infinity gets s = NaN and codes 0, so that it reads as NaN.  Expert
+ * weights get a scale per output column: W [E, K, N] as the matrix [E*N, K].
+ * The products also take the code -128.
+ *
+ * Sizes as for MXFP4. */
+
+/* Rows x [rows, cols] bf16 to codes and scales. */
+moe_status moe_quantize_int8(const moe_bf16 *x, int64_t rows, int64_t cols, int8_t *codes,
+                             float *scales, moe_stream_t stream);
+
+/* Weights w [E, K, N] bf16 (K the reduction axis) to the codes and scales of
+ * the matrix [E*N, K]. */
+moe_status moe_quantize_weights_int8(const moe_bf16 *w, int32_t E, int64_t K, int64_t N,
+                                     int8_t *codes, float *scales, moe_stream_t stream);
+
+/* The values bf16(q s) [rows, cols] that codes and scales stand for. */
+moe_status moe_dequantize_int8(const int8_t *codes, const float *scales, int64_t rows, int64_t cols,
+                               moe_bf16 *x, moe_stream_t stream);
+
+/* Tokens X [T, H] bf16 quantised once each and written to their k permuted
+ * rows scatter_idx [T, k]: codes and scales of the matrix [max_rows, H].
+ * Padding rows are left unwritten.  ws as for the products below. */
+moe_status moe_quantize_permute_int8(const moe_shape *shape, const moe_bf16 *X,
+                                     const int32_t *scatter_idx, int8_t *codes, float *scales,
+                                     void *ws, moe_stream_t stream);
+
+/* The grouped gate/up product on 8-bit integers:
+ *   h[r] = bf16(silu(g) u),  g = x_scales[r] wg_scales[n] <x_codes[r], wg_codes[n]>
+ * and u alike with wu, [max_rows, I] bf16, for the real rows r of every expert;
+ * padding rows as for the MXFP4 product.
+ *   x_codes, x_scales: the matrix [max_rows, H] in expert order
+ *   wg_*, wu_*:        the matrices [E*I, H]
+ *   ws: any workspace, or at least 256 bytes whose first 256 were cleared
+ * Products of codes are exact and their float32 sums too while they are below
+ * 2^24 (whatever the codes for H <= 1024). */
+moe_status moe_grouped_gemm_up_int8(const moe_shape *shape, const int8_t *x_codes,
+                                    const float *x_scales, const int32_t *counts,
+                                    const int32_t *off_pad, const int8_t *wg_codes,
+                                    const float *wg_scales, const int8_t *wu_codes,
+                                    const float *wu_scales, moe_bf16 *h, void *ws,
+                                    moe_stream_t stream);
+
+/* The grouped down product on 8-bit integers: Y [max_rows, H] bf16, rows as above.
+ *   h_codes, h_scales: the matrix [max_rows, I];  wd_*: the matrix [E*H, I] */
+moe_status moe_grouped_gemm_down_int8(const moe_shape *shape, const int8_t *h_codes,
+                                      const float *h_scales, const int32_t *counts,
+                                      const int32_t *off_pad, const int8_t *wd_codes,
+                                      const float *wd_scales, moe_bf16 *Y, void *ws,
+                                      moe_stream_t stream);
+
+/* Host only.  Bytes of the workspace of moe_forward_int8; moe_workspace_init and
+ * moe_last_device_status serve it, moe_workspace_views does not. */
+moe_status moe_int8_workspace_size(const moe_shape *shape, size_t *bytes);
+
+/* The whole layer with the experts' products on 8-bit integers: route, quantise
+ * and permute the tokens, gate/up product, h quantised row by row, down product,
+ * combine.  Weights as moe_quantize_weights_int8 leaves them; everything else as
+ * moe_forward. */
+moe_status moe_forward_int8(const moe_shape *shape, const float *logits, const moe_bf16 *X,
+                            const int8_t *wg_codes, const float *wg_scales, const int8_t *wu_codes,
+                            const float *wu_scales, const int8_t *wd_codes, const float *wd_scales,
+                            moe_bf16 *out, void *ws, moe_stream_t stream);
 
 /* ----------------------------------------------------------- balance loss
  * A token takes part when its mask byte is non-zero (or mask is NULL) and not
