@@ -44,44 +44,31 @@ constexpr int kTileN = 256;               // most output rows per tile
 constexpr int kOperandBytes = 128 * kStageK * 2;  // 128 m (or n) x 64 k
 constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kBoxBytes = kStageK * 128;  // 64 k x 64 columns (weight backward)
+constexpr int kStages = 6;
 constexpr int kEpiWarps = 8;              // two per TMEM lane quarter, taking 32-row pieces in turn
 constexpr int kTurns = kEpiWarps / 4;
-constexpr int kTileRing = 8;              // tile indices on their way from the scheduler
+constexpr int kSlots = 2;                 // pieces in a turn's staging
+constexpr int kTileRing = 4;              // tiles on their way from the scheduler
 constexpr uint32_t kTmemCols = 512;
+// warps: loads, MMAs, epilogue, scheduler, clearing (weight backward)
+constexpr int kSchedWarp = 2 + kEpiWarps;
+constexpr int kOutOff = kStages * kStageBytes;
+constexpr int kRingOff = kOutOff + kTurns * kSlots * kPieceBytes;
+constexpr int kBarOff = kRingOff + kTileRing * 16;
+// full, empty, tail, cleared [kStages]; tfull, tempty [2]; inputs [kTurns]; drain;
+// ring full, empty [kTileRing]
+constexpr int kNumBars = 4 * kStages + 4 + kTurns + 1 + 2 * kTileRing;
+constexpr int kSlotOff = kBarOff + kNumBars * 8;
+constexpr int kSmem = kSlotOff + 16 + 1024;
+static_assert(kSmem <= 232448, "shared memory budget");
 
 template <int kMode>
 struct Cfg {
   static constexpr int FIX_WARPS = kMode == kWeightBwd ? 1 : 0;
-  static constexpr int THREADS = (2 + kEpiWarps + FIX_WARPS) * 32;
-  // readers of a tile index: CTA 0's MMA lane and CTA 1's producer lane, both
-  // CTAs' epilogue (and clearing) warps
-  static constexpr int READERS = 2 + 2 * (kEpiWarps + FIX_WARPS);
-  static constexpr int STAGES = kMode == kDownBwd ? 5 : 6;
-  // staging per turn: dg and du (32 rows x 128 columns each), or one output piece
-  static constexpr int PIECES = kMode == kDownBwd ? 2 : 1;
-  static constexpr int OUT_OFF = STAGES * kStageBytes;
-  static constexpr int BAR_OFF = OUT_OFF + kTurns * PIECES * kPieceBytes;
-  // full, empty, tail, cleared [STAGES]; tfull, tempty [2]; inputs [kTurns];
-  // drain; ring full, empty [kTileRing]
-  static constexpr int NUM_BARS = 4 * STAGES + 4 + kTurns + 1 + 2 * kTileRing;
-  static constexpr int SLOT_OFF = BAR_OFF + NUM_BARS * 8;
-  static constexpr int TILE_OFF = SLOT_OFF + 16;
-  static constexpr int WIN_OFF = TILE_OFF + kTileRing * 4;
-  static constexpr int CNT_OFF = WIN_OFF + (kMaxExperts + 1) * 4;
-  static constexpr int OFFP_OFF = CNT_OFF + kMaxExperts * 4;
-  static constexpr int BYTES = OFFP_OFF + (kMaxExperts + 1) * 4;
-  static constexpr int ALLOC = BYTES + 1024;
-  static_assert(ALLOC <= 232448, "shared memory budget");
-};
-
-struct Tile {
-  int e;     // expert
-  int mat;   // weight backward: gate, up, down
-  int m0;    // first output column of the pair
-  int n0;    // first row: of the window, or of the expert's gradient matrix
-  int n;     // real rows (1..256)
-  int k;     // length of the reduction
-  bool ok;
+  static constexpr int THREADS = (3 + kEpiWarps + FIX_WARPS) * 32;
+  // readers of a tile: CTA 0's MMA lane, both CTAs' loading lanes, epilogue and
+  // clearing warps
+  static constexpr int READERS = 3 + 2 * (kEpiWarps + FIX_WARPS);
 };
 
 struct Problem {
@@ -89,96 +76,206 @@ struct Problem {
   int64_t max_rows;
 };
 
-// Down and up backward: an expert's c rows are cut into nw = ceil(c / 256)
-// windows of equal size (rounded up to 16), so that those which share a weight
-// tile run in step; tile = expert, then column tile, then window.
-// Weight backward: tile = expert, then gate / up / down, then row tile, then
-// column tile.
-template <int kMode>
-__device__ __forceinline__ Tile decode(int tile, const Problem& p, const int32_t* win, const int32_t* offp,
-                                       const int32_t* cnt) {
-  Tile c{0, 0, 0, 0, 0, 0, false};
-  if constexpr (kMode == kWeightBwd) {
-    const int ti = (p.I + 255) / 256, th = (p.H + 255) / 256;
-    const int per = ti * th;
-    c.e = tile / (3 * per);
-    if (c.e >= p.E) return c;
-    const int rem = tile - c.e * 3 * per;
-    c.mat = rem / per;
-    const int at = rem - c.mat * per;
-    const int tm = c.mat == 2 ? th : ti;  // column tiles
-    c.m0 = at % tm * kTileM;
-    c.n0 = at / tm * kTileN;
-    c.n = min(kTileN, (c.mat == 2 ? p.I : p.H) - c.n0);
-    c.k = cnt[c.e];
-  } else {
-    const int nt = ((kMode == kDownBwd ? p.I : p.H) + 255) / 256;
-    const int q = tile / nt;
-    int lo = 0, hi = p.E;  // last e with win[e] <= q
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (win[mid] <= q) lo = mid; else hi = mid - 1;
-    }
-    if (lo >= p.E) return c;
-    const int nw = win[lo + 1] - win[lo];
-    const int local = tile - nt * win[lo];
-    if (nw <= 0 || local < 0 || local >= nt * nw) return c;
-    const int w = local % nw;
-    const int size = ((cnt[lo] + nw - 1) / nw + 15) / 16 * 16;
-    c.e = lo;
-    c.m0 = local / nw * kTileM;
-    c.n = min(size, cnt[lo] - size * w);
-    c.n0 = size * w;  // relative to the expert's first row until checked
-    c.k = kMode == kDownBwd ? p.H : 2 * p.I;
-  }
-  // the expert's rows lie inside its 128-row blocks, and those inside the buffers
-  const int64_t first = offp[c.e], end = offp[c.e + 1];
-  const int rows = cnt[c.e];
-  c.ok = c.n > 0 && c.n <= kTileN && rows >= 0 && first >= 0 && first + rows <= end && end <= p.max_rows;
-  if (kMode != kWeightBwd) c.n0 += static_cast<int>(first);
+// A tile as the scheduler hands it out.
+struct Tile {
+  int e;    // expert
+  int mat;  // weight backward: gate, up, down; else: 1 where the expert has one window
+  int m0;   // first output column of the pair
+  int n0;   // weight backward: first row in the expert's gradient matrix
+  int n;    // output rows (1..256)
+  int row;  // first row of the window, or (weight backward) of the expert
+  int k;    // length of the reduction
+  bool ok, last;
+};
+__device__ __forceinline__ int4 pack_tile(const Tile& c) {
+  return make_int4(c.n | (c.ok ? 1 << 9 : 0) | (c.last ? 1 << 10 : 0) | (c.mat << 11) | (c.e << 13),
+                   (c.m0 / kTileM) | (c.n0 / kTileN << 16), c.row, c.k);
+}
+__device__ __forceinline__ Tile unpack_tile(const int4& v) {
+  Tile c;
+  c.n = v.x & 511;
+  c.ok = (v.x >> 9) & 1;
+  c.last = (v.x >> 10) & 1;
+  c.mat = (v.x >> 11) & 3;
+  c.e = v.x >> 13;
+  c.m0 = (v.y & 0xFFFF) * kTileM;
+  c.n0 = (v.y >> 16) * kTileN;
+  c.row = v.z;
+  c.k = v.w;
   return c;
 }
 
-// Tiles are drawn from a counter in the workspace, in order: cluster b starts
-// on tile b, and CTA 0's producer lane publishes every later index to both CTAs
-// a whole tile before it is needed.  The cluster that stops drawing last clears
-// the counter, and knows whether the launch started from a cleared one: the word
-// behind it counts the clusters that have stopped (bits 0-9), sums their indexes
-// plus one (bits 10-29), and gets bit 30 from the one that drew 0.  With anything
-// else in either word the sum comes out wrong (tiles may have been left out).
+// Tiles go to the clusters in order: cluster b starts on tile b, and a warp of its
+// CTA 0 draws every later index from a counter in the workspace, finds the tile
+// and hands it to all roles of both CTAs through a ring.  The cluster that stops
+// drawing last clears the counter, and knows whether the launch started from a
+// cleared one: the word behind it counts the clusters that have stopped (bits
+// 0-9), sums their indexes plus one (bits 10-29), and gets bit 30 from the one
+// that drew 0.  With anything else in either word the sum comes out wrong (tiles
+// may have been left out).
+// (Each role finding its tile from the index by itself, with three divisions and
+// a search, took 860 of the 6800 cycles that a weight tile of 8 rows had.)
 constexpr int kMaxClusters = 1023;
 __device__ __forceinline__ uint32_t stopped(uint32_t clusters, uint32_t index_sum, bool drew_zero) {
   return clusters | (index_sum << 10) | (drew_zero ? 1u << 30 : 0u);
 }
 struct TileRing {
-  uint64_t* full;         // [kTileRing], this CTA: one arrival (the scheduler)
-  uint64_t* empty;        // [kTileRing], used in CTA 0: READERS arrivals
-  volatile int32_t* idx;  // [kTileRing], this CTA
+  uint64_t* full;   // [kTileRing], this CTA: one arrival (the scheduler)
+  uint64_t* empty;  // [kTileRing], used in CTA 0: READERS arrivals
+  int4* tile;       // [kTileRing], this CTA
 };
-__device__ __forceinline__ bool ring_put(const TileRing& r, uint32_t n, int tile, volatile int* abort,
+__device__ __forceinline__ bool ring_put(const TileRing& r, uint32_t n, const Tile& c, volatile int* abort,
                                          uint32_t* status) {
   const uint32_t slot = n % kTileRing;
   if (!mbar_wait<true>(&r.empty[slot], ((n / kTileRing) & 1u) ^ 1u, abort, status)) return false;
-  r.idx[slot] = tile;
+  const int4 v = pack_tile(c);
+  *const_cast<volatile int*>(&r.tile[slot].x) = v.x;
+  *const_cast<volatile int*>(&r.tile[slot].y) = v.y;
+  *const_cast<volatile int*>(&r.tile[slot].z) = v.z;
+  *const_cast<volatile int*>(&r.tile[slot].w) = v.w;
   mbar_arrive(&r.full[slot]);
-  const uint32_t there = map_to_cta(const_cast<int32_t*>(&r.idx[slot]), 1);
-  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(there), "r"(tile) : "memory");
+  asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(map_to_cta(&r.tile[slot], 1)), "r"(v.x),
+               "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
   mbar_arrive_cluster(map_to_cta(&r.full[slot], 1));
   return true;
 }
-// The n-th tile of this cluster, -1 when the wait gave up; released at once.
-__device__ __forceinline__ int ring_peek(const TileRing& r, uint32_t n, uint32_t rank, volatile int* abort,
+// The n-th tile of this cluster; false when the wait gave up.
+__device__ __forceinline__ bool ring_get(const TileRing& r, uint32_t n, uint32_t rank, Tile& c, volatile int* abort,
                                          uint32_t* status) {
   const uint32_t slot = n % kTileRing;
   const uint32_t ph = (n / kTileRing) & 1u;
   const bool ok = rank == 0 ? mbar_wait<false>(&r.full[slot], ph, abort, status)
                             : mbar_wait<true>(&r.full[slot], ph, abort, status);
-  return ok ? r.idx[slot] : -1;
+  if (!ok) return false;
+  const volatile int* w = reinterpret_cast<const volatile int*>(&r.tile[slot]);
+  c = unpack_tile(make_int4(w[0], w[1], w[2], w[3]));
+  return true;
 }
 __device__ __forceinline__ void ring_release(const TileRing& r, uint32_t n, uint32_t rank, uint32_t empty0) {
   const uint32_t slot = n % kTileRing;
   if (rank == 0) mbar_arrive(&r.empty[slot]);
   else mbar_arrive_cluster(empty0 + 8u * slot);
+}
+
+// The scheduler: one warp, a lane knowing eight experts.
+//   down and up backward: an expert's c rows are cut into ceil(c / 256) windows of
+//   equal size (rounded up to 16), so that those which share a weight tile run in
+//   step; tiles in the order expert, column tile, window.
+//   weight backward: expert, then gate / up / down, then row tile, column tile.
+template <int kMode>
+__device__ __forceinline__ void schedule(const TileRing& ring, const Problem& p, const int32_t* off_pad,
+                                         const int32_t* counts, uint32_t cluster, uint32_t nclusters, int lane,
+                                         volatile int* abort, uint32_t* status, uint32_t* sched) {
+  constexpr int per = kMaxExperts / 32;
+  const uint32_t all = 0xffffffffu;
+  const int ti = (p.I + kTileM - 1) / kTileM, th = (p.H + kTileM - 1) / kTileM;
+  const int col_tiles = kMode == kDownBwd ? ti : th;
+  int cnt[per], off[per + 1], nw[per];
+  int sum = 0;
+#pragma unroll
+  for (int i = 0; i <= per; ++i) {
+    const int e = lane * per + i;
+    off[i] = e <= p.E ? __ldcg(off_pad + e) : 0;
+    if (i < per) cnt[i] = e < p.E ? __ldcg(counts + e) : 0;
+  }
+#pragma unroll
+  for (int i = 0; i < per; ++i) {
+    const int e = lane * per + i;
+    // an expert whose rows do not lie inside its blocks and the buffers gets no rows
+    const int64_t first = off[i], end = off[i + 1];
+    if (e < p.E && (cnt[i] < 0 || first < 0 || first + cnt[i] > end || end > p.max_rows)) {
+      record_status(status, kStatusBounds);
+      cnt[i] = kMode == kWeightBwd ? -1 : 0;
+    }
+    nw[i] = cnt[i] > 0 ? (cnt[i] - 1) / kTileN + 1 : 0;
+    sum += nw[i];
+  }
+  int incl = sum;  // windows up to this lane's last expert
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(all, incl, o);
+    if (lane >= o) incl += y;
+  }
+  const int windows = __shfl_sync(all, incl, 31);
+  // windows of counts that fit the buffers: nw of them hold more than 256 (nw - 1) rows
+  const bool fits = static_cast<int64_t>(windows - p.E) * kTileN <= p.max_rows;
+  if (!fits && lane == 0) record_status(status, kStatusBounds);
+  const int total = kMode == kWeightBwd ? p.E * 3 * ti * th : fits ? col_tiles * windows : 0;
+
+  uint32_t drawn = 0;
+  if (lane == 0) drawn = atomicAdd(sched, 1u);
+  bool drew_zero = false;
+  int tile = static_cast<int>(cluster);
+  for (uint32_t n = 0;; ++n) {
+    Tile c{0, 0, 0, 0, 0, 0, 0, false, tile >= total};
+    int owner = 0;  // the lane that knows the tile's expert
+    if (tile < total) {
+      if constexpr (kMode == kWeightBwd) {
+        const int e = tile / (3 * ti * th);
+        int at = tile - e * 3 * ti * th;
+        owner = e / per;
+        c.e = e;
+        c.mat = at / (ti * th);
+        at -= c.mat * ti * th;
+        const int tm = c.mat == 2 ? th : ti;  // column tiles
+        const int tn = at / tm;
+        c.m0 = (at - tn * tm) * kTileM;
+        c.n0 = tn * kTileN;
+        c.n = min(kTileN, (c.mat == 2 ? p.I : p.H) - c.n0);
+#pragma unroll
+        for (int i = 0; i < per; ++i) {
+          if (i == e % per) {
+            c.row = off[i];
+            c.k = cnt[i];
+          }
+        }
+        c.ok = c.k >= 0;
+      } else {
+        const int q = tile / col_tiles;  // (all column tiles of a window's expert lie together)
+        owner = __ffs(__ballot_sync(all, incl > q)) - 1;
+        int base = incl - sum;  // windows before this lane's first expert
+#pragma unroll
+        for (int i = 0; i < per; ++i) {
+          if (q >= base && q < base + nw[i]) {
+            const int local = tile - col_tiles * base;
+            const int j = local / nw[i];
+            const int w = local - j * nw[i];
+            const int size = ((cnt[i] + nw[i] - 1) / nw[i] + 15) / 16 * 16;
+            c.e = lane * per + i;
+            c.mat = nw[i] == 1 ? 1 : 0;
+            c.m0 = j * kTileM;
+            c.n = min(size, cnt[i] - size * w);
+            c.row = off[i] + size * w;
+            c.k = kMode == kDownBwd ? p.H : 2 * p.I;
+            c.ok = c.n > 0;
+          }
+          base += nw[i];
+        }
+      }
+    }
+    bool put = true;
+    if (lane == owner) put = ring_put(ring, n, c, abort, status);
+    if (__any_sync(all, !put) || tile >= total) break;
+    const uint32_t d = __shfl_sync(all, drawn, 0);
+    drew_zero |= d == 0u;
+    // a cleared counter gives less than total + 2 clusters here
+    const uint64_t next = static_cast<uint64_t>(nclusters) + d;
+    if (next >= static_cast<uint64_t>(total) + 2u * nclusters && lane == 0) record_status(status, kStatusBounds);
+    tile = next < static_cast<uint64_t>(total) ? static_cast<int>(next) : total;
+    if (lane == 0) drawn = atomicAdd(sched, 1u);
+  }
+  if (lane == 0) {
+    drew_zero |= drawn == 0u;
+    __threadfence();
+    const uint32_t mine = stopped(1u, cluster + 1u, drew_zero);
+    const uint32_t seen = atomicAdd(sched + 1, mine) + mine;
+    if ((seen & 0x3FFu) == nclusters) {  // every cluster has drawn its last index
+      if (seen != stopped(nclusters, nclusters * (nclusters + 1u) / 2u, true)) record_status(status, kStatusBounds);
+      atomicExch(sched, 0u);
+      atomicExch(sched + 1, 0u);
+    }
+  }
 }
 
 // OR-vote over the epilogue's threads (named barrier 2).
@@ -213,27 +310,24 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
   using C = Cfg<kMode>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);
-  uint64_t* empty = full + C::STAGES;
-  uint64_t* tail = empty + C::STAGES;      // this CTA's loads of a stage that is to be cleared
-  uint64_t* cleared = tail + C::STAGES;    // used in CTA 0: CTA 1 has cleared its part
-  uint64_t* tfull = cleared + C::STAGES;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kBarOff);
+  uint64_t* empty = full + kStages;
+  uint64_t* tail = empty + kStages;      // this CTA's loads of a stage that is to be cleared
+  uint64_t* cleared = tail + kStages;    // used in CTA 0: CTA 1 has cleared its part
+  uint64_t* tfull = cleared + kStages;
   uint64_t* tempty = tfull + 2;
-  uint64_t* inbar = tempty + 2;            // [kTurns] g and u of a piece
+  uint64_t* inbar = tempty + 2;          // [kTurns] g and u of a piece
   uint64_t* drain = inbar + kTurns;
-  const TileRing ring{drain + 1, drain + 1 + kTileRing, reinterpret_cast<volatile int32_t*>(smem + C::TILE_OFF)};
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::SLOT_OFF);
+  const TileRing ring{drain + 1, drain + 1 + kTileRing, reinterpret_cast<int4*>(smem + kRingOff)};
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kSlotOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int32_t* s_win = reinterpret_cast<int32_t*>(smem + C::WIN_OFF);
-  int32_t* s_cnt = reinterpret_cast<int32_t*>(smem + C::CNT_OFF);
-  int32_t* s_offp = reinterpret_cast<int32_t*>(smem + C::OFFP_OFF);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_ctarank();  // 0: draws the tiles and issues the MMAs
+  const uint32_t rank = cluster_ctarank();  // 0: schedules and issues the MMAs
 
   pdl_launch_dependents();
   if (threadIdx.x == 0) {
-    for (int s = 0; s < C::STAGES; ++s) {
+    for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
       mbar_init(&tail[s], 1);
@@ -260,61 +354,11 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
     tmem_alloc_pair(tmem_slot, kTmemCols);
     tmem_relinquish_pair();
   }
-  pdl_wait();
-  if (warp == 2) {
-    // windows per expert -> exclusive scan (E <= 256)
-    constexpr int per = kMaxExperts / 32;
-    int loc[per];
-    int sum = 0;
-#pragma unroll
-    for (int i = 0; i < per; ++i) {
-      const int e = lane * per + i;
-      int nw = 0;
-      if (e < p.E) {
-        int c = __ldcg(counts + e);
-        if (c > p.max_rows) {  // no buffer holds so many: no tiles for them
-          record_status(status, kStatusBounds);
-          c = kMode == kWeightBwd ? -1 : 0;
-        }
-        s_cnt[e] = c;
-        nw = c > 0 ? (c - 1) / kTileN + 1 : 0;
-      }
-      loc[i] = nw;
-      sum += nw;
-    }
-    int incl = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
-    }
-    int run = incl - sum;
-#pragma unroll
-    for (int i = 0; i < per; ++i) {
-      const int e = lane * per + i;
-      if (e <= p.E) s_win[e] = run;
-      run += loc[i];
-    }
-    if (lane == 31 && 32 * per == p.E) s_win[p.E] = incl;
-  } else if (warp == 3) {
-    for (int e = lane; e <= p.E; e += 32) s_offp[e] = __ldcg(off_pad + e);
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  int total;
-  if constexpr (kMode == kWeightBwd) {
-    total = p.E * 3 * ((p.I + 255) / 256) * ((p.H + 255) / 256);
-  } else {
-    // windows of counts that fit the buffers (see the check of each window):
-    // nw windows hold more than 256 (nw - 1) rows
-    const bool fits = static_cast<int64_t>(s_win[p.E] - p.E) * kTileN <= p.max_rows;
-    if (!fits && threadIdx.x == 0) record_status(status, kStatusBounds);
-    total = fits ? ((kMode == kDownBwd ? p.I : p.H) + 255) / 256 * s_win[p.E] : 0;
-  }
-  const uint32_t nclusters = gridDim.x >> 1;
-  const uint32_t cluster = blockIdx.x >> 1;
+  pdl_wait();
   const uint32_t full0 = map_to_cta(full, 0);
   const uint32_t tempty0 = map_to_cta(tempty, 0);
   const uint32_t rempty0 = map_to_cta(ring.empty, 0);
@@ -329,33 +373,11 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
       const uint64_t pol_normal = policy_evict_normal();
       const uint64_t pol_once = policy_evict_first();
       uint32_t it = 0;
-      bool drew_zero = false;
       bool stop = false;
-      int tile = static_cast<int>(cluster);
-      uint32_t drawn = 0;
-      if (rank == 0) {
-        drawn = atomicAdd(sched, 1u);  // tile 1's index
-        stop = !ring_put(ring, 0, tile, abort_flag, status);
-      } else {
-        tile = ring_peek(ring, 0, rank, abort_flag, status);
-        if (tile >= 0) ring_release(ring, 0, rank, rempty0);
-      }
-      for (uint32_t n = 0; !stop && tile >= 0 && tile < total; ++n) {
-        int next = total;
-        if (rank == 0) {
-          drew_zero |= drawn == 0u;
-          // a cleared counter gives less than total + 2 clusters here
-          const uint64_t t = static_cast<uint64_t>(nclusters) + drawn;
-          if (t < static_cast<uint64_t>(total)) next = static_cast<int>(t);
-          else if (t >= static_cast<uint64_t>(total) + 2u * nclusters) record_status(status, kStatusBounds);
-          if (!ring_put(ring, n + 1, next, abort_flag, status)) {
-            stop = true;
-            break;
-          }
-          drawn = atomicAdd(sched, 1u);
-        }
-        const Tile c = decode<kMode>(tile, p, s_win, s_offp, s_cnt);
-        if (!c.ok) record_status(status, kStatusBounds);
+      Tile c;
+      for (uint32_t n = 0; !stop && ring_get(ring, n, rank, c, abort_flag, status); ++n) {
+        if (c.last) break;
+        ring_release(ring, n, rank, rempty0);
         const int nk = c.ok ? stages_of(c.k) : 0;
         const int n_half = (c.n + 15) / 16 * 8;  // output rows this CTA supplies
         const int m_first = c.m0 + 128 * static_cast<int>(rank);
@@ -365,8 +387,8 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
           const int n_first = c.n0 + n_half * static_cast<int>(rank);  // 64 or 128 columns
           const uint32_t mine = static_cast<uint32_t>(2 + n_half / 64) * kBoxBytes;
           for (int kb = 0; kb < nk; ++kb, ++it) {
-            const uint32_t s = it % C::STAGES;
-            if (!mbar_wait(&empty[s], ((it / C::STAGES) & 1u) ^ 1u, abort_flag, status)) {
+            const uint32_t s = it % kStages;
+            if (!mbar_wait(&empty[s], ((it / kStages) & 1u) ^ 1u, abort_flag, status)) {
               stop = true;
               break;
             }
@@ -375,7 +397,7 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
             if (own) mbar_arrive_expect_tx(&tail[s], mine);
             else if (rank == 0) mbar_arrive_expect_tx(&full[s], 2u * mine);
             uint8_t* st = smem + s * kStageBytes;
-            const int row = s_offp[c.e] + kb * kStageK;
+            const int row = c.row + kb * kStageK;
             tma_load_2d_pair(st, ma, fb, m_first, row, pol_keep);
             tma_load_2d_pair(st + kBoxBytes, ma, fb, m_first + 64, row, pol_keep);
             tma_load_2d_pair(st + kOperandBytes, mb, fb, n_first, row, pol_keep);
@@ -383,15 +405,15 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
           }
         } else {
           // weights that one window alone reads leave L2 first
-          const uint64_t pol_w = s_win[c.e + 1] - s_win[c.e] == 1 ? pol_once : pol_normal;
+          const uint64_t pol_w = c.mat != 0 ? pol_once : pol_normal;
           const int pick = n_half <= 16 ? 0 : n_half <= 32 ? 1 : n_half <= 64 ? 2 : 3;
           const uint32_t bytes = 2u * (kOperandBytes + train_token_box(pick) * kStageK * 2);
-          const int row = c.n0 + n_half * static_cast<int>(rank);
+          const int row = c.row + n_half * static_cast<int>(rank);
           const int m_row = c.e * (kMode == kDownBwd ? p.I : p.H) + m_first;
           const int half = kMode == kUpBwd ? p.I / kStageK : nk;  // stages of the first term
           for (int kb = 0; kb < nk; ++kb, ++it) {
-            const uint32_t s = it % C::STAGES;
-            if (!mbar_wait(&empty[s], ((it / C::STAGES) & 1u) ^ 1u, abort_flag, status)) {
+            const uint32_t s = it % kStages;
+            if (!mbar_wait(&empty[s], ((it / kStages) & 1u) ^ 1u, abort_flag, status)) {
               stop = true;
               break;
             }
@@ -403,32 +425,13 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
             tma_load_2d_pair(st + kOperandBytes, &maps.b[term][pick], full0 + 8u * s, k0, row, pol_keep);
           }
         }
-        if (stop) break;
-        if (rank == 0) {
-          tile = next;
-        } else {
-          tile = ring_peek(ring, n + 1, rank, abort_flag, status);
-          if (tile >= 0) ring_release(ring, n + 1, rank, rempty0);
-        }
-      }
-      if (rank == 0) {
-        drew_zero |= drawn == 0u;
-        __threadfence();
-        const uint32_t mine = stopped(1u, cluster + 1u, drew_zero);
-        const uint32_t seen = atomicAdd(sched + 1, mine) + mine;
-        if ((seen & 0x3FFu) == nclusters) {  // every cluster has drawn its last index
-          if (seen != stopped(nclusters, nclusters * (nclusters + 1u) / 2u, true))
-            record_status(status, kStatusBounds);
-          atomicExch(sched, 0u);
-          atomicExch(sched + 1, 0u);
-        }
       }
       // every stage used must be consumed before the CTA may exit
-      const uint32_t nst = it < C::STAGES ? it : C::STAGES;
+      const uint32_t nst = it < kStages ? it : kStages;
       for (uint32_t s = 0; s < nst; ++s) {
-        const uint32_t last = s + C::STAGES * ((it - 1 - s) / C::STAGES);
+        const uint32_t last = s + kStages * ((it - 1 - s) / kStages);
         int no_abort = 0;
-        mbar_wait(&empty[s], (last / C::STAGES) & 1u, &no_abort, status);
+        mbar_wait(&empty[s], (last / kStages) & 1u, &no_abort, status);
       }
     }
     __syncwarp();
@@ -441,21 +444,20 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
       uint32_t it = 0;
       uint32_t tcount = 0;
       bool stop = false;
-      for (uint32_t n = 0; !stop; ++n) {
-        const int tile = ring_peek(ring, n, rank, abort_flag, status);
-        if (tile < 0 || tile >= total) break;
+      Tile c;
+      for (uint32_t n = 0; !stop && ring_get(ring, n, rank, c, abort_flag, status); ++n) {
+        if (c.last) break;
         ring_release(ring, n, rank, rempty0);
-        const Tile c = decode<kMode>(tile, p, s_win, s_offp, s_cnt);
         if (!c.ok || c.k == 0) continue;
         const uint32_t idesc = idesc_base | ((static_cast<uint32_t>(c.n + 15) / 16 * 2) << 17);
         const uint32_t a = tcount & 1u;
-        if (!mbar_wait<true>(&tempty[a], ((tcount >> 1) & 1u) ^ 1u, abort_flag, status)) break;
+        if (!mbar_wait(&tempty[a], ((tcount >> 1) & 1u) ^ 1u, abort_flag, status)) break;
         tc_fence_after();
         const uint32_t d = tmem + a * kTileN;
         const int nk = stages_of(c.k);
         for (int kb = 0; kb < nk; ++kb, ++it) {
-          const uint32_t s = it % C::STAGES;
-          if (!mbar_wait<true>(&full[s], (it / C::STAGES) & 1u, abort_flag, status)) {
+          const uint32_t s = it % kStages;
+          if (!mbar_wait(&full[s], (it / kStages) & 1u, abort_flag, status)) {
             stop = true;
             break;
           }
@@ -486,116 +488,96 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
       mbar_wait(drain, 0, &no_abort, status);
     }
     __syncwarp();
-  } else if (warp < 2 + kEpiWarps) {
+  } else if (warp < kSchedWarp) {
     // ---------------------------------------------------------- epilogue (both CTAs)
     const int q = warp & 3;
     const int turn = (warp - 2) / 4;
-    uint8_t* out = smem + C::OUT_OFF + turn * C::PIECES * kPieceBytes;
-    const uint32_t out_addr = smem_u32(out);
+    uint8_t* slots = smem + kOutOff + turn * kSlots * kPieceBytes;
     const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16);
-    const bool leader = q == 0 && lane == 0;  // of the turn's four warps: TMA
-    const int N_out = kMode == kDownBwd ? p.I : p.H;  // (weight backward: the output is never partial)
     uint32_t tcount = 0;
-    uint32_t loads = 0;  // pieces of g and u asked for
+    uint32_t asked = 0;  // pieces of g and u
     for (uint32_t n = 0;; ++n) {
-      const int tile = ring_peek(ring, n, rank, abort_flag, status);
+      Tile c{};
+      bool ok = ring_get(ring, n, rank, c, abort_flag, status);
       __syncwarp();
       if (lane == 0) ring_release(ring, n, rank, rempty0);
-      bool ok = tile >= 0;
-      const bool real = ok && tile < total;
-      const Tile c = decode<kMode>(real ? tile : 0, p, s_win, s_offp, s_cnt);
+      const bool real = ok && !c.last && c.ok;
       const uint32_t a = tcount & 1u;
+      const int cols = kMode == kDownBwd ? p.I : kMode == kUpBwd ? p.H : c.mat == 2 ? p.H : p.I;
       const int col0 = c.m0 + 128 * static_cast<int>(rank);
-      const int cols = kMode == kWeightBwd ? (c.mat == 2 ? p.H : p.I) : N_out;
-      const bool mine = real && c.ok && col0 < cols;  // this CTA has columns to write
-      const int pieces = (c.n + 31) / 32;
+      const int64_t row0 = kMode == kWeightBwd ? static_cast<int64_t>(c.e) * (c.mat == 2 ? p.I : p.H) + c.n0 : c.row;
+      const int pieces = real && col0 < cols ? (c.n + 31) / 32 : 0;  // (columns are multiples of 128)
       // g and u of piece pc, loaded to where dg and du will be staged
       auto ask = [&](int pc) {
-        if (leader) {
-          tma_store_wait_read<0>();
+        if (q == 0 && lane == 0) {
           mbar_arrive_expect_tx(&inbar[turn], 2 * kPieceBytes);
-          const int r = c.n0 + pc * 32;
+          const int r = static_cast<int>(row0) + pc * 32;
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            tma_load_2d(out + i * kPieceBytes, &maps.in[i], &inbar[turn], col0, r, policy_evict_first());
-            tma_load_2d(out + i * kPieceBytes + kPieceBytes / 2, &maps.in[i], &inbar[turn], col0 + 64, r,
+            tma_load_2d(slots + i * kPieceBytes, &maps.in[i], &inbar[turn], col0, r, policy_evict_first());
+            tma_load_2d(slots + i * kPieceBytes + kPieceBytes / 2, &maps.in[i], &inbar[turn], col0 + 64, r,
                         policy_evict_first());
           }
         }
-        ++loads;
+        ++asked;
       };
-      const bool early = kMode == kDownBwd && mine && turn < pieces;
-      if (early) ask(turn);
-      if (real && c.ok && c.k > 0) ok = mbar_wait<true>(&tfull[a], (tcount >> 1) & 1u, abort_flag, status);
+      const bool early = kMode == kDownBwd && turn < pieces;
+      if (early) {  // before the accumulator is waited for
+        if (lane == 0) tma_store_wait_read<0>();
+        __syncwarp();
+        named_barrier_sync(3 + turn, 128);  // the previous tile's last piece has left
+        ask(turn);
+      }
+      if (real && c.k > 0) ok = mbar_wait(&tfull[a], (tcount >> 1) & 1u, abort_flag, status);
       if (vote_any(!ok)) {  // every warp gives up together (they share barriers)
-        if (early && leader) {
+        if (early) {
           int no_abort = 0;
-          mbar_wait(&inbar[turn], (loads - 1) & 1u, &no_abort, status);
+          mbar_wait(&inbar[turn], (asked - 1) & 1u, &no_abort, status);
         }
         break;
       }
-      if (tile >= total) break;
+      if (c.last) break;
       if (!c.ok) continue;
       tc_fence_after();
       if (c.k > 0) ++tcount;
+      // the accumulator has been read (by this warp)
       auto release = [&]() {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(tempty0 + 8u * a);
+        if (lane == 0) mbar_arrive_cluster_relaxed(tempty0 + 8u * a);
       };
-      // the output pieces in the staging leave: 32 full rows by TMA, fewer by
-      // the warps, eight rows each, sixteen lanes a row
-      auto store = [&](int pc) {
-        fence_proxy_async_smem();
-        named_barrier_sync(3 + turn, 128);
+      // The piece in a slot leaves: 32 rows by TMA, a half by either of the slot's
+      // two warps, fewer rows by all four, eight rows each, sixteen lanes a row.
+      auto leave = [&](int slot, uint16_t* D, const CUtensorMap* map, int pc) {
         const int left = c.n - pc * 32;
-        const int r0 = (kMode == kWeightBwd ? c.e * (c.mat == 2 ? p.I : p.H) : 0) + c.n0 + pc * 32;
+        uint8_t* buf = slots + slot * kPieceBytes;
         if (left >= 32) {
-          if (leader) {
-#pragma unroll
-            for (int i = 0; i < C::PIECES; ++i) {
-              const CUtensorMap* m = kMode == kWeightBwd ? &maps.out[c.mat] : &maps.out[i];
-              tma_store_2d(m, out + i * kPieceBytes, col0, r0);
-              tma_store_2d(m, out + i * kPieceBytes + kPieceBytes / 2, col0 + 64, r0);
-            }
-            tma_store_commit();
-          }
-          __syncwarp();
+          if (lane == 0 && (q >> 1) == slot)
+            tma_store_2d(map, buf + (q & 1) * (kPieceBytes / 2), col0 + 64 * (q & 1),
+                         static_cast<int32_t>(row0) + pc * 32);
           return;
         }
 #pragma unroll
-        for (int i = 0; i < C::PIECES; ++i) {
-          uint16_t* D = i == 0 ? D0 : D1;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int t = 8 * q + 2 * j + (lane >> 4);
-            if (t < left)
-              *reinterpret_cast<uint4*>(D + static_cast<int64_t>(r0 + t) * N_out + col0 + (lane & 15) * 8) =
-                  *reinterpret_cast<const uint4*>(out + i * kPieceBytes + staged_at(t, lane & 15));
-          }
+        for (int j = 0; j < 4; ++j) {
+          const int t = 8 * q + 2 * j + (lane >> 4);
+          if (t < left)
+            *reinterpret_cast<uint4*>(D + (row0 + pc * 32 + t) * cols + col0 + (lane & 15) * 8) =
+                *reinterpret_cast<const uint4*>(buf + staged_at(t, lane & 15));
         }
-        named_barrier_sync(3 + turn, 128);  // read before the next piece arrives
       };
-      const int count = pieces > turn ? (pieces - turn + kTurns - 1) / kTurns : 0;  // this turn's pieces
-      if (!mine || count == 0) {
+      if (turn >= pieces) {
         if (c.k > 0) release();
         continue;
       }
-      for (int i = 0; i < count; ++i) {
-        const int pc = turn + kTurns * i;
-        uint32_t v[32];
-        if (kMode != kWeightBwd || c.k > 0) {
+      if constexpr (kMode == kDownBwd) {
+        for (int pc = turn; pc < pieces; pc += kTurns) {
+          uint32_t v[32];
           load_piece(tb + a * kTileN + pc * 32, v);
           tmem_ld_wait();
-          if (i == count - 1) release();
-        } else {  // an expert without rows: its gradient is zero
-#pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = 0u;
-        }
-        if constexpr (kMode == kDownBwd) {
-          bool in = mbar_wait(&inbar[turn], (loads - 1) & 1u, abort_flag, status);
-          (void)in;  // (a wait that gave up has raised the abort flag: the values are not used)
-          const uint32_t at = out_addr + staged_at(lane & 7, 4 * q + (lane >> 3));
+          if (pc + kTurns >= pieces) release();
+          // (a wait that gives up raises the abort flag: the values are not used)
+          mbar_wait(&inbar[turn], (asked - 1) & 1u, abort_flag, status);
+          const uint32_t at = smem_u32(slots) + staged_at(lane & 7, 4 * q + (lane >> 3));
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             uint32_t g[4], u[4];
@@ -614,35 +596,68 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
             stmatrix_x4_trans(at + 8 * j * 128, g[0], g[1], g[2], g[3]);
             stmatrix_x4_trans(at + kPieceBytes + 8 * j * 128, u[0], u[1], u[2], u[3]);
           }
-        } else {
-          uint32_t packed[16];
-          round_piece(v, packed);
-          if (leader) tma_store_wait_read<0>();
-          __syncwarp();
-          named_barrier_sync(3 + turn, 128);  // the previous piece has been read
-          stage_piece(out_addr, q, packed, lane);
+          fence_proxy_async_smem();
+          named_barrier_sync(3 + turn, 128);
+          leave(0, D0, &maps.out[0], pc);
+          leave(1, D1, &maps.out[1], pc);
+          if (lane == 0) tma_store_commit();
+          if (pc + kTurns < pieces) {
+            if (lane == 0) tma_store_wait_read<0>();
+            __syncwarp();
+            named_barrier_sync(3 + turn, 128);  // this piece has left
+            ask(pc + kTurns);
+          }
         }
-        store(pc);
-        if (kMode == kDownBwd && i + 1 < count) ask(pc + kTurns);
+      } else {
+        const CUtensorMap* map = &maps.out[kMode == kWeightBwd ? c.mat : 0];
+        for (int pc = turn; pc < pieces; pc += kSlots * kTurns) {  // two pieces at a time
+          const bool two = pc + kTurns < pieces;
+          uint32_t v[kSlots][32];
+          if (kMode != kWeightBwd || c.k > 0) {
+            load_piece(tb + a * kTileN + pc * 32, v[0]);
+            if (two) load_piece(tb + a * kTileN + (pc + kTurns) * 32, v[1]);
+            tmem_ld_wait();
+            if (pc + kSlots * kTurns >= pieces) release();
+          } else {  // an expert without rows: its gradient is zero
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[0][j] = v[1][j] = 0u;
+          }
+          if (lane == 0) tma_store_wait_read<0>();
+          __syncwarp();
+          named_barrier_sync(3 + turn, 128);  // the previous pieces have left
+#pragma unroll
+          for (int i = 0; i < kSlots; ++i) {
+            uint32_t packed[16];
+            round_piece(v[i], packed);
+            if (i == 0 || two) stage_piece(smem_u32(slots + i * kPieceBytes), q, packed, lane);
+          }
+          fence_proxy_async_smem();
+          named_barrier_sync(3 + turn, 128);
+          leave(0, D0, map, pc);
+          if (two) leave(1, D0, map, pc + kTurns);
+          if (lane == 0) tma_store_commit();
+        }
       }
     }
-    if (leader) tma_store_wait_all<0>();  // this thread's stores are written
+    if (lane == 0) tma_store_wait_all<0>();  // this thread's stores are written
+    __syncwarp();
+  } else if (warp == kSchedWarp) {
+    if (rank == 0)
+      schedule<kMode>(ring, p, off_pad, counts, blockIdx.x >> 1, gridDim.x >> 1, lane, abort_flag, status, sched);
     __syncwarp();
   } else if constexpr (kMode == kWeightBwd) {
     // ---------------------------------------------------------- clearing (both CTAs)
     uint32_t it = 0;
     uint32_t phases = 0;  // bit s: parity of the next use of stage s's barriers
     for (uint32_t n = 0;; ++n) {
-      const int tile = ring_peek(ring, n, rank, abort_flag, status);
-      __syncwarp();
-      if (tile < 0) break;
+      Tile c{};
+      const bool got = ring_get(ring, n, rank, c, abort_flag, status);
+      if (__any_sync(0xffffffffu, !got) || c.last) break;
       if (lane == 0) ring_release(ring, n, rank, rempty0);
-      if (tile >= total) break;
-      const Tile c = decode<kMode>(tile, p, s_win, s_offp, s_cnt);
       if (!c.ok) continue;
       it += stages_of(c.k);
       if (!has_tail(c)) continue;
-      const uint32_t s = (it - 1) % C::STAGES;
+      const uint32_t s = (it - 1) % kStages;
       const uint32_t ph = (phases >> s) & 1u;
       phases ^= 1u << s;
       if (__any_sync(0xffffffffu, !mbar_wait(&tail[s], ph, abort_flag, status))) break;
@@ -689,7 +704,7 @@ cudaError_t launch(const moe_shape& s, const TrainMaps& m, uint16_t* D0, uint16_
   {
     std::lock_guard<std::mutex> lock(mu);
     if (dev >= 64 || !done[dev]) {
-      err = cudaFuncSetAttribute(train_gemm_kernel<kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::ALLOC);
+      err = cudaFuncSetAttribute(train_gemm_kernel<kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
       if (err != cudaSuccess) return err;
       if (dev < 64) done[dev] = true;
     }
@@ -704,7 +719,7 @@ cudaError_t launch(const moe_shape& s, const TrainMaps& m, uint16_t* D0, uint16_
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * clusters));
   cfg.blockDim = dim3(C::THREADS);
-  cfg.dynamicSmemBytes = C::ALLOC;
+  cfg.dynamicSmemBytes = kSmem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
