@@ -299,8 +299,8 @@ moe_status run_down_backward(const moe_shape& s, const uint16_t* dY, const int32
   const uint64_t mr = static_cast<uint64_t>(max_rows_of(s));
   TrainMaps m = {};
   bool ok = encode_bf16_2d(&m.a[0], Wd, static_cast<uint64_t>(s.E) * s.I, s.H, 128, 64) &&
-            encode_bf16_2d(&m.in[0], g, mr, s.I, 32, 64) && encode_bf16_2d(&m.in[1], u, mr, s.I, 32, 64) &&
-            encode_bf16_2d(&m.out[0], dg, mr, s.I, 32, 64) && encode_bf16_2d(&m.out[1], du, mr, s.I, 32, 64);
+            encode_bf16_groups(&m.in[0], g, mr, s.I, 32) && encode_bf16_groups(&m.in[1], u, mr, s.I, 32) &&
+            encode_bf16_groups(&m.out[0], dg, mr, s.I, 32) && encode_bf16_groups(&m.out[1], du, mr, s.I, 32);
   for (int i = 0; i < 4; ++i) ok = ok && encode_bf16_2d(&m.b[0][i], dY, mr, s.H, train_token_box(i), 64);
   if (!ok) return MOE_ERR_CUDA;
   return cuda_status(launch_down_backward(s, m, dg, du, off_pad, counts, status, ws_sched_up(status), num_sms, st));
@@ -312,7 +312,7 @@ moe_status run_up_backward(const moe_shape& s, const uint16_t* dg, const uint16_
   const uint64_t mr = static_cast<uint64_t>(max_rows_of(s)), EH = static_cast<uint64_t>(s.E) * s.H;
   TrainMaps m = {};
   bool ok = encode_bf16_2d(&m.a[0], Wg, EH, s.I, 128, 64) && encode_bf16_2d(&m.a[1], Wu, EH, s.I, 128, 64) &&
-            encode_bf16_2d(&m.out[0], dXp, mr, s.H, 32, 64);
+            encode_bf16_groups(&m.out[0], dXp, mr, s.H, 64);
   for (int i = 0; i < 4; ++i)
     ok = ok && encode_bf16_2d(&m.b[0][i], dg, mr, s.I, train_token_box(i), 64) &&
          encode_bf16_2d(&m.b[1][i], du, mr, s.I, train_token_box(i), 64);
@@ -329,8 +329,8 @@ moe_status run_weight_backward(const moe_shape& s, const uint16_t* Xp, const uin
   TrainMaps m = {};
   if (!encode_bf16_2d(&m.a[0], dg, mr, s.I, 64, 64) || !encode_bf16_2d(&m.a[1], du, mr, s.I, 64, 64) ||
       !encode_bf16_2d(&m.a[2], dY, mr, s.H, 64, 64) || !encode_bf16_2d(&m.b[0][0], Xp, mr, s.H, 64, 64) ||
-      !encode_bf16_2d(&m.b[1][0], h, mr, s.I, 64, 64) || !encode_bf16_2d(&m.out[0], dWg, EH, s.I, 32, 64) ||
-      !encode_bf16_2d(&m.out[1], dWu, EH, s.I, 32, 64) || !encode_bf16_2d(&m.out[2], dWd, EI, s.H, 32, 64))
+      !encode_bf16_2d(&m.b[1][0], h, mr, s.I, 64, 64) || !encode_bf16_groups(&m.out[0], dWg, EH, s.I, 64) ||
+      !encode_bf16_groups(&m.out[1], dWu, EH, s.I, 64) || !encode_bf16_groups(&m.out[2], dWd, EI, s.H, 64))
     return MOE_ERR_CUDA;
   return cuda_status(launch_weight_backward(s, m, off_pad, counts, status, ws_sched_up(status), num_sms, st));
 }
@@ -410,6 +410,18 @@ bool encode_bf16_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t 
   const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
                               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
+bool encode_bf16_groups(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows) {
+  if (g_encode == nullptr) return false;
+  cuuint64_t dims[3] = {64, rows, cols / 64};
+  cuuint64_t strides[2] = {cols * 2, 128};
+  cuuint32_t box[3] = {64, box_rows, 2};
+  cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+                              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
 

@@ -204,8 +204,9 @@ __host__ __device__ constexpr int train_token_box(int i) { return 16 << i; }
 struct TrainMaps {
   CUtensorMap a[3];     // down: W_down; up: W_gate, W_up (box 128 x 64); weights: dg, du, dY (box 64 x 64)
   CUtensorMap b[2][4];
-  CUtensorMap in[2];    // down: g, u, box 32 x 64
-  CUtensorMap out[3];   // down: dg, du; up: dX; weights: dW_gate, dW_up, dW_down; box 32 x 64
+  // as 3-D maps (encode_bf16_groups)
+  CUtensorMap in[2];    // down: g, u, 32 rows
+  CUtensorMap out[3];   // down: dg, du, 32 rows; up: dX; weights: dW_gate, dW_up, dW_down; 64 rows
 };
 cudaError_t launch_down_backward(const moe_shape& s, const TrainMaps& m, uint16_t* dg, uint16_t* du,
                                  const int32_t* off_pad, const int32_t* counts, uint32_t* status, uint32_t* sched,
@@ -275,6 +276,9 @@ cudaError_t launch_wait_timeout(uint32_t* status, cudaStream_t st);
 // span equals the box's inner extent in bytes (64 or 128).
 bool encode_bf16_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows,
                     uint32_t box_cols);
+// rows x cols bf16 row-major as 64 columns x rows x column groups, box 64 x
+// box_rows x 2 (128 columns), 128-byte swizzle.
+bool encode_bf16_groups(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows);
 // rows x bytes_per_row bytes row-major, box 128 bytes x box_rows, 128-byte
 // swizzle.
 bool encode_bytes_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t bytes_per_row, uint32_t box_rows);

@@ -47,13 +47,13 @@ constexpr int kBoxBytes = kStageK * 128;  // 64 k x 64 columns (weight backward)
 constexpr int kStages = 6;
 constexpr int kEpiWarps = 8;              // two per TMEM lane quarter, taking 32-row pieces in turn
 constexpr int kTurns = kEpiWarps / 4;
-constexpr int kSlots = 2;                 // pieces in a turn's staging
+constexpr int kTurnBytes = 2 * kPieceBytes;  // a turn's staging: dg and du of 32 rows, or 64 output rows
 constexpr int kTileRing = 4;              // tiles on their way from the scheduler
 constexpr uint32_t kTmemCols = 512;
 // warps: loads, MMAs, epilogue, scheduler, clearing (weight backward)
 constexpr int kSchedWarp = 2 + kEpiWarps;
 constexpr int kOutOff = kStages * kStageBytes;
-constexpr int kRingOff = kOutOff + kTurns * kSlots * kPieceBytes;
+constexpr int kRingOff = kOutOff + kTurns * kTurnBytes;
 constexpr int kBarOff = kRingOff + kTileRing * 16;
 // full, empty, tail, cleared [kStages]; tfull, tempty [2]; inputs [kTurns]; drain;
 // ring full, empty [kTileRing]
@@ -278,16 +278,16 @@ __device__ __forceinline__ void schedule(const TileRing& ring, const Problem& p,
   }
 }
 
-// OR-vote over the epilogue's threads (named barrier 2).
-__device__ __forceinline__ bool vote_any(bool flag) {
+// OR-vote over the threads of a turn of the epilogue (its named barrier).
+__device__ __forceinline__ bool vote_any(bool flag, int turn) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred pi, po;\n\t"
       "setp.ne.u32 pi, %1, 0;\n\t"
-      "bar.red.or.pred po, 2, %2, pi;\n\t"
+      "bar.red.or.pred po, %3, %2, pi;\n\t"
       "selp.u32 %0, 1, 0, po;\n\t}"
       : "=r"(r)
-      : "r"(flag ? 1u : 0u), "n"(kEpiWarps * 32)
+      : "r"(flag ? 1u : 0u), "n"(kEpiWarps / kTurns * 32), "r"(3 + turn)
       : "memory");
   return r != 0;
 }
@@ -492,7 +492,8 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
     // ---------------------------------------------------------- epilogue (both CTAs)
     const int q = warp & 3;
     const int turn = (warp - 2) / 4;
-    uint8_t* slots = smem + kOutOff + turn * kSlots * kPieceBytes;
+    const bool leader = q == 0 && lane == 0;  // of the turn's four warps: TMA
+    uint8_t* staging = smem + kOutOff + turn * kTurnBytes;
     const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16);
     uint32_t tcount = 0;
     uint32_t asked = 0;  // pieces of g and u
@@ -506,30 +507,42 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
       const int cols = kMode == kDownBwd ? p.I : kMode == kUpBwd ? p.H : c.mat == 2 ? p.H : p.I;
       const int col0 = c.m0 + 128 * static_cast<int>(rank);
       const int64_t row0 = kMode == kWeightBwd ? static_cast<int64_t>(c.e) * (c.mat == 2 ? p.I : p.H) + c.n0 : c.row;
-      const int pieces = real && col0 < cols ? (c.n + 31) / 32 : 0;  // (columns are multiples of 128)
-      // g and u of piece pc, loaded to where dg and du will be staged
-      auto ask = [&](int pc) {
-        if (q == 0 && lane == 0) {
+      const int rows = real && col0 < cols ? c.n : 0;  // (columns are multiples of 128)
+      // The turn's four warps: what was staged before has left.
+      auto staging_free = [&]() {
+        if (leader) tma_store_wait_read<0>();
+        __syncwarp();
+        named_barrier_sync(3 + turn, 128);
+      };
+      // They have all staged rows r.. of the tile, `height` of them at most: all by
+      // TMA, or fewer by the warps, sixteen lanes a row.
+      auto leave = [&](const uint8_t* buf, uint16_t* D, const CUtensorMap* map, int r, int height) {
+        const int left = rows - r;
+        if (left >= height) {
+          if (leader) tma_store_3d(map, buf, 0, static_cast<int32_t>(row0) + r, col0 / 64);
+          return;
+        }
+        for (int t = 2 * q + (lane >> 4); t < left; t += 8)
+          *reinterpret_cast<uint4*>(D + (row0 + r + t) * cols + col0 + (lane & 15) * 8) =
+              *reinterpret_cast<const uint4*>(buf + staged_at(t, lane & 15, height));
+      };
+      // g and u of the 32 rows from r, loaded to where dg and du will be staged
+      auto ask = [&](int r) {
+        if (leader) {
           mbar_arrive_expect_tx(&inbar[turn], 2 * kPieceBytes);
-          const int r = static_cast<int>(row0) + pc * 32;
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            tma_load_2d(slots + i * kPieceBytes, &maps.in[i], &inbar[turn], col0, r, policy_evict_first());
-            tma_load_2d(slots + i * kPieceBytes + kPieceBytes / 2, &maps.in[i], &inbar[turn], col0 + 64, r,
-                        policy_evict_first());
-          }
+          for (int i = 0; i < 2; ++i)
+            tma_load_3d(staging + i * kPieceBytes, &maps.in[i], &inbar[turn], 0, static_cast<int32_t>(row0) + r,
+                        col0 / 64, policy_evict_first());
         }
         ++asked;
       };
-      const bool early = kMode == kDownBwd && turn < pieces;
+      const bool early = kMode == kDownBwd && turn * 32 < rows;
       if (early) {  // before the accumulator is waited for
-        if (lane == 0) tma_store_wait_read<0>();
-        __syncwarp();
-        named_barrier_sync(3 + turn, 128);  // the previous tile's last piece has left
-        ask(turn);
+        staging_free();
+        ask(turn * 32);
       }
       if (real && c.k > 0) ok = mbar_wait(&tfull[a], (tcount >> 1) & 1u, abort_flag, status);
-      if (vote_any(!ok)) {  // every warp gives up together (they share barriers)
+      if (vote_any(!ok, turn)) {  // the turn's warps give up together (they share barriers)
         if (early) {
           int no_abort = 0;
           mbar_wait(&inbar[turn], (asked - 1) & 1u, &no_abort, status);
@@ -546,38 +559,17 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster_relaxed(tempty0 + 8u * a);
       };
-      // The piece in a slot leaves: 32 rows by TMA, a half by either of the slot's
-      // two warps, fewer rows by all four, eight rows each, sixteen lanes a row.
-      auto leave = [&](int slot, uint16_t* D, const CUtensorMap* map, int pc) {
-        const int left = c.n - pc * 32;
-        uint8_t* buf = slots + slot * kPieceBytes;
-        if (left >= 32) {
-          if (lane == 0 && (q >> 1) == slot)
-            tma_store_2d(map, buf + (q & 1) * (kPieceBytes / 2), col0 + 64 * (q & 1),
-                         static_cast<int32_t>(row0) + pc * 32);
-          return;
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int t = 8 * q + 2 * j + (lane >> 4);
-          if (t < left)
-            *reinterpret_cast<uint4*>(D + (row0 + pc * 32 + t) * cols + col0 + (lane & 15) * 8) =
-                *reinterpret_cast<const uint4*>(buf + staged_at(t, lane & 15));
-        }
-      };
-      if (turn >= pieces) {
-        if (c.k > 0) release();
-        continue;
-      }
       if constexpr (kMode == kDownBwd) {
-        for (int pc = turn; pc < pieces; pc += kTurns) {
+        // pieces of 32 rows, the turns' in turn
+        if (!early) release();
+        for (int r = turn * 32; r < rows; r += kTurns * 32) {
           uint32_t v[32];
-          load_piece(tb + a * kTileN + pc * 32, v);
+          load_piece(tb + a * kTileN + r, v);
           tmem_ld_wait();
-          if (pc + kTurns >= pieces) release();
+          if (r + kTurns * 32 >= rows) release();
           // (a wait that gives up raises the abort flag: the values are not used)
           mbar_wait(&inbar[turn], (asked - 1) & 1u, abort_flag, status);
-          const uint32_t at = smem_u32(slots) + staged_at(lane & 7, 4 * q + (lane >> 3));
+          const uint32_t at = smem_u32(staging) + staged_at(lane & 7, 4 * q + (lane >> 3), 32);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             uint32_t g[4], u[4];
@@ -598,48 +590,50 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
           }
           fence_proxy_async_smem();
           named_barrier_sync(3 + turn, 128);
-          leave(0, D0, &maps.out[0], pc);
-          leave(1, D1, &maps.out[1], pc);
-          if (lane == 0) tma_store_commit();
-          if (pc + kTurns < pieces) {
-            if (lane == 0) tma_store_wait_read<0>();
-            __syncwarp();
-            named_barrier_sync(3 + turn, 128);  // this piece has left
-            ask(pc + kTurns);
+          leave(staging, D0, &maps.out[0], r, 32);
+          leave(staging + kPieceBytes, D1, &maps.out[1], r, 32);
+          if (leader) tma_store_commit();
+          if (r + kTurns * 32 < rows) {
+            staging_free();
+            ask(r + kTurns * 32);
           }
         }
       } else {
-        const CUtensorMap* map = &maps.out[kMode == kWeightBwd ? c.mat : 0];
-        for (int pc = turn; pc < pieces; pc += kSlots * kTurns) {  // two pieces at a time
-          const bool two = pc + kTurns < pieces;
-          uint32_t v[kSlots][32];
-          if (kMode != kWeightBwd || c.k > 0) {
-            load_piece(tb + a * kTileN + pc * 32, v[0]);
-            if (two) load_piece(tb + a * kTileN + (pc + kTurns) * 32, v[1]);
+        // a turn's 128 rows: all rounded to registers, the accumulator released,
+        // then staged and stored 64 rows at a time
+        const int first = turn * (kTileN / kTurns);
+        uint32_t packed[4][16];
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+          if ((kMode != kWeightBwd || c.k > 0) && first + 32 * i < rows) {
+            uint32_t v[2][32];
+            load_piece(tb + a * kTileN + first + 32 * i, v[0]);
+            load_piece(tb + a * kTileN + first + 32 * i + 32, v[1]);  // (in TMEM whatever the rows)
             tmem_ld_wait();
-            if (pc + kSlots * kTurns >= pieces) release();
+            round_piece(v[0], packed[i]);
+            round_piece(v[1], packed[i + 1]);
           } else {  // an expert without rows: its gradient is zero
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[0][j] = v[1][j] = 0u;
+            for (int j = 0; j < 16; ++j) packed[i][j] = packed[i + 1][j] = 0u;
           }
-          if (lane == 0) tma_store_wait_read<0>();
-          __syncwarp();
-          named_barrier_sync(3 + turn, 128);  // the previous pieces have left
+        }
+        if (c.k > 0) release();
 #pragma unroll
-          for (int i = 0; i < kSlots; ++i) {
-            uint32_t packed[16];
-            round_piece(v[i], packed);
-            if (i == 0 || two) stage_piece(smem_u32(slots + i * kPieceBytes), q, packed, lane);
+        for (int i = 0; i < 2; ++i) {
+          const int r = first + 64 * i;
+          if (r < rows) {
+            staging_free();
+            stage_piece(smem_u32(staging), q, packed[2 * i], lane, 64);
+            if (r + 32 < rows) stage_piece(smem_u32(staging) + 32 * 128, q, packed[2 * i + 1], lane, 64);
+            fence_proxy_async_smem();
+            named_barrier_sync(3 + turn, 128);
+            leave(staging, D0, &maps.out[kMode == kWeightBwd ? c.mat : 0], r, 64);
+            if (leader) tma_store_commit();
           }
-          fence_proxy_async_smem();
-          named_barrier_sync(3 + turn, 128);
-          leave(0, D0, map, pc);
-          if (two) leave(1, D0, map, pc + kTurns);
-          if (lane == 0) tma_store_commit();
         }
       }
     }
-    if (lane == 0) tma_store_wait_all<0>();  // this thread's stores are written
+    if (leader) tma_store_wait_all<0>();  // this thread's stores are written
     __syncwarp();
   } else if (warp == kSchedWarp) {
     if (rank == 0)

@@ -13,9 +13,9 @@ namespace moe {
 // two halves of 64 columns, rows of 128 bytes, in the 128-byte swizzle of the
 // stores' tensor map (which also puts eight rows on different banks).
 constexpr int kPieceBytes = 32 * 128 * 2;
-// byte offset of row t, 16-byte chunk c (of 16) in the staging
-__device__ __forceinline__ int staged_at(int t, int c) {
-  return (c >> 3) * (kPieceBytes / 2) + t * 128 + (((c & 7) ^ (t & 7)) << 4);
+// byte offset of row t, 16-byte chunk c (of 16) in the staging (of `rows` rows)
+__device__ __forceinline__ int staged_at(int t, int c, int rows = 32) {
+  return (c >> 3) * (rows * 128) + t * 128 + (((c & 7) ^ (t & 7)) << 4);
 }
 
 // 16 TMEM lanes x 32 columns: thread i gets, for each group j of eight columns,
@@ -61,8 +61,9 @@ __device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uin
 // Writes a piece as bf16 to the staging at `out`, columns 32 q..: packed[4 j + x]
 // holds the rows 8 j + 2 (i % 4) and the next of column x * 8 + i / 4, so matrix
 // (j, x) lands at rows 8 j.., columns 32 q + 8 x...
-__device__ __forceinline__ void stage_piece(uint32_t out, int q, const uint32_t (&packed)[16], int lane) {
-  const uint32_t at = out + staged_at(lane & 7, 4 * q + (lane >> 3));  // thread 8 x + r: row r, columns 8 x
+__device__ __forceinline__ void stage_piece(uint32_t out, int q, const uint32_t (&packed)[16], int lane,
+                                            int rows = 32) {
+  const uint32_t at = out + staged_at(lane & 7, 4 * q + (lane >> 3), rows);  // thread 8 x + r: row r, columns 8 x
 #pragma unroll
   for (int j = 0; j < 4; ++j)
     stmatrix_x4_trans(at + 8 * j * 128, packed[4 * j], packed[4 * j + 1], packed[4 * j + 2], packed[4 * j + 3]);
