@@ -303,7 +303,7 @@ moe_status run_down_backward(const moe_shape& s, const uint16_t* dY, const int32
             encode_bf16_groups(&m.out[0], dg, mr, s.I, 32) && encode_bf16_groups(&m.out[1], du, mr, s.I, 32);
   for (int i = 0; i < 4; ++i) ok = ok && encode_bf16_2d(&m.b[0][i], dY, mr, s.H, train_token_box(i), 64);
   if (!ok) return MOE_ERR_CUDA;
-  return cuda_status(launch_down_backward(s, m, dg, du, off_pad, counts, status, ws_sched_up(status), num_sms, st));
+  return cuda_status(launch_down_backward(s, m, TrainOut{{dg, du, nullptr}}, off_pad, counts, status, ws_sched_up(status), num_sms, st));
 }
 
 moe_status run_up_backward(const moe_shape& s, const uint16_t* dg, const uint16_t* du, const int32_t* counts,
@@ -317,7 +317,7 @@ moe_status run_up_backward(const moe_shape& s, const uint16_t* dg, const uint16_
     ok = ok && encode_bf16_2d(&m.b[0][i], dg, mr, s.I, train_token_box(i), 64) &&
          encode_bf16_2d(&m.b[1][i], du, mr, s.I, train_token_box(i), 64);
   if (!ok) return MOE_ERR_CUDA;
-  return cuda_status(launch_up_backward(s, m, dXp, off_pad, counts, status, ws_sched_down(status), num_sms, st));
+  return cuda_status(launch_up_backward(s, m, TrainOut{{dXp, nullptr, nullptr}}, off_pad, counts, status, ws_sched_down(status), num_sms, st));
 }
 
 moe_status run_weight_backward(const moe_shape& s, const uint16_t* Xp, const uint16_t* h, const uint16_t* dg,
@@ -329,10 +329,10 @@ moe_status run_weight_backward(const moe_shape& s, const uint16_t* Xp, const uin
   TrainMaps m = {};
   if (!encode_bf16_2d(&m.a[0], dg, mr, s.I, 64, 64) || !encode_bf16_2d(&m.a[1], du, mr, s.I, 64, 64) ||
       !encode_bf16_2d(&m.a[2], dY, mr, s.H, 64, 64) || !encode_bf16_2d(&m.b[0][0], Xp, mr, s.H, 64, 64) ||
-      !encode_bf16_2d(&m.b[1][0], h, mr, s.I, 64, 64) || !encode_bf16_groups(&m.out[0], dWg, EH, s.I, 64) ||
-      !encode_bf16_groups(&m.out[1], dWu, EH, s.I, 64) || !encode_bf16_groups(&m.out[2], dWd, EI, s.H, 64))
+      !encode_bf16_2d(&m.b[1][0], h, mr, s.I, 64, 64) || !encode_bf16_groups(&m.out[0], dWg, EH, s.I, 128) ||
+      !encode_bf16_groups(&m.out[1], dWu, EH, s.I, 128) || !encode_bf16_groups(&m.out[2], dWd, EI, s.H, 128))
     return MOE_ERR_CUDA;
-  return cuda_status(launch_weight_backward(s, m, off_pad, counts, status, ws_sched_up(status), num_sms, st));
+  return cuda_status(launch_weight_backward(s, m, TrainOut{{dWg, dWu, dWd}}, off_pad, counts, status, ws_sched_up(status), num_sms, st));
 }
 
 // moe_forward, or with g and u (both or neither) the training forward.

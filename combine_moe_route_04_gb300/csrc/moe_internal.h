@@ -204,17 +204,20 @@ __host__ __device__ constexpr int train_token_box(int i) { return 16 << i; }
 struct TrainMaps {
   CUtensorMap a[3];     // down: W_down; up: W_gate, W_up (box 128 x 64); weights: dg, du, dY (box 64 x 64)
   CUtensorMap b[2][4];
-  // as 3-D maps (encode_bf16_groups)
+  // as 3-D maps (encode_bf16_groups), for the outputs in boxes of the rows stored at once
   CUtensorMap in[2];    // down: g, u, 32 rows
-  CUtensorMap out[3];   // down: dg, du, 32 rows; up: dX; weights: dW_gate, dW_up, dW_down; 64 rows
+  CUtensorMap out[3];   // down: dg, du, 32 rows; up: dX, 64; weights: dW_gate, dW_up, dW_down, 128
 };
-cudaError_t launch_down_backward(const moe_shape& s, const TrainMaps& m, uint16_t* dg, uint16_t* du,
-                                 const int32_t* off_pad, const int32_t* counts, uint32_t* status, uint32_t* sched,
-                                 int num_sms, cudaStream_t st);
-cudaError_t launch_up_backward(const moe_shape& s, const TrainMaps& m, uint16_t* dx, const int32_t* off_pad,
+struct TrainOut {
+  uint16_t* d[3];  // the outputs
+};
+cudaError_t launch_down_backward(const moe_shape& s, const TrainMaps& m, const TrainOut& out, const int32_t* off_pad,
+                                 const int32_t* counts, uint32_t* status, uint32_t* sched, int num_sms,
+                                 cudaStream_t st);
+cudaError_t launch_up_backward(const moe_shape& s, const TrainMaps& m, const TrainOut& out, const int32_t* off_pad,
                                const int32_t* counts, uint32_t* status, uint32_t* sched, int num_sms,
                                cudaStream_t st);
-cudaError_t launch_weight_backward(const moe_shape& s, const TrainMaps& m, const int32_t* off_pad,
+cudaError_t launch_weight_backward(const moe_shape& s, const TrainMaps& m, const TrainOut& out, const int32_t* off_pad,
                                    const int32_t* counts, uint32_t* status, uint32_t* sched, int num_sms,
                                    cudaStream_t st);
 // The combine's gradients: dY[row] = w dout, and the router's dlogits.

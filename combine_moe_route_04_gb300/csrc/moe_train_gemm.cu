@@ -44,23 +44,12 @@ constexpr int kTileN = 256;               // most output rows per tile
 constexpr int kOperandBytes = 128 * kStageK * 2;  // 128 m (or n) x 64 k
 constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kBoxBytes = kStageK * 128;  // 64 k x 64 columns (weight backward)
-constexpr int kStages = 6;
 constexpr int kEpiWarps = 8;              // two per TMEM lane quarter, taking 32-row pieces in turn
 constexpr int kTurns = kEpiWarps / 4;
-constexpr int kTurnBytes = 2 * kPieceBytes;  // a turn's staging: dg and du of 32 rows, or 64 output rows
 constexpr int kTileRing = 4;              // tiles on their way from the scheduler
 constexpr uint32_t kTmemCols = 512;
 // warps: loads, MMAs, epilogue, scheduler, clearing (weight backward)
 constexpr int kSchedWarp = 2 + kEpiWarps;
-constexpr int kOutOff = kStages * kStageBytes;
-constexpr int kRingOff = kOutOff + kTurns * kTurnBytes;
-constexpr int kBarOff = kRingOff + kTileRing * 16;
-// full, empty, tail, cleared [kStages]; tfull, tempty [2]; inputs [kTurns]; drain;
-// ring full, empty [kTileRing]
-constexpr int kNumBars = 4 * kStages + 4 + kTurns + 1 + 2 * kTileRing;
-constexpr int kSlotOff = kBarOff + kNumBars * 8;
-constexpr int kSmem = kSlotOff + 16 + 1024;
-static_assert(kSmem <= 232448, "shared memory budget");
 
 template <int kMode>
 struct Cfg {
@@ -69,6 +58,22 @@ struct Cfg {
   // readers of a tile: CTA 0's MMA lane, both CTAs' loading lanes, epilogue and
   // clearing warps
   static constexpr int READERS = 3 + 2 * (kEpiWarps + FIX_WARPS);
+  // A turn's staging: dg and du of 32 rows; 64 output rows; or, where reductions
+  // are short and the stores bound the kernel, all of the turn's 128, so that they
+  // leave under the next tile's work (64 rows and a sixth stage: 806 us where this
+  // takes MEASURED).
+  static constexpr int HEIGHT = kMode == kWeightBwd ? kTileN / kTurns : 64;
+  static constexpr int STAGES = kMode == kWeightBwd ? 5 : 6;
+  static constexpr int TURN_BYTES = HEIGHT * 256;
+  static constexpr int OUT_OFF = STAGES * kStageBytes;
+  static constexpr int RING_OFF = OUT_OFF + kTurns * TURN_BYTES;
+  static constexpr int BAR_OFF = RING_OFF + kTileRing * 16;
+  // full, empty, tail, cleared [STAGES]; tfull, tempty [2]; inputs [kTurns]; drain;
+  // ring full, empty [kTileRing]
+  static constexpr int NUM_BARS = 4 * STAGES + 4 + kTurns + 1 + 2 * kTileRing;
+  static constexpr int SLOT_OFF = BAR_OFF + NUM_BARS * 8;
+  static constexpr int SMEM = SLOT_OFF + 16 + 1024;
+  static_assert(SMEM <= 232448, "shared memory budget");
 };
 
 struct Problem {
@@ -304,22 +309,22 @@ __device__ __forceinline__ void swiglu_backward(float dh, float g, float u, floa
 
 template <int kMode>
 __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
-    train_gemm_kernel(const __grid_constant__ TrainMaps maps, uint16_t* __restrict__ D0, uint16_t* __restrict__ D1,
-                      const int32_t* __restrict__ off_pad, const int32_t* __restrict__ counts, Problem p,
-                      uint32_t* __restrict__ status, uint32_t* __restrict__ sched) {
+    train_gemm_kernel(const __grid_constant__ TrainMaps maps, const TrainOut out, const int32_t* __restrict__ off_pad,
+                      const int32_t* __restrict__ counts, Problem p, uint32_t* __restrict__ status,
+                      uint32_t* __restrict__ sched) {
   using C = Cfg<kMode>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kBarOff);
-  uint64_t* empty = full + kStages;
-  uint64_t* tail = empty + kStages;      // this CTA's loads of a stage that is to be cleared
-  uint64_t* cleared = tail + kStages;    // used in CTA 0: CTA 1 has cleared its part
-  uint64_t* tfull = cleared + kStages;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);
+  uint64_t* empty = full + C::STAGES;
+  uint64_t* tail = empty + C::STAGES;      // this CTA's loads of a stage that is to be cleared
+  uint64_t* cleared = tail + C::STAGES;    // used in CTA 0: CTA 1 has cleared its part
+  uint64_t* tfull = cleared + C::STAGES;
   uint64_t* tempty = tfull + 2;
   uint64_t* inbar = tempty + 2;          // [kTurns] g and u of a piece
   uint64_t* drain = inbar + kTurns;
-  const TileRing ring{drain + 1, drain + 1 + kTileRing, reinterpret_cast<int4*>(smem + kRingOff)};
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kSlotOff);
+  const TileRing ring{drain + 1, drain + 1 + kTileRing, reinterpret_cast<int4*>(smem + C::RING_OFF)};
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::SLOT_OFF);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -327,7 +332,7 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
 
   pdl_launch_dependents();
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
       mbar_init(&tail[s], 1);
@@ -387,8 +392,8 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
           const int n_first = c.n0 + n_half * static_cast<int>(rank);  // 64 or 128 columns
           const uint32_t mine = static_cast<uint32_t>(2 + n_half / 64) * kBoxBytes;
           for (int kb = 0; kb < nk; ++kb, ++it) {
-            const uint32_t s = it % kStages;
-            if (!mbar_wait(&empty[s], ((it / kStages) & 1u) ^ 1u, abort_flag, status)) {
+            const uint32_t s = it % C::STAGES;
+            if (!mbar_wait(&empty[s], ((it / C::STAGES) & 1u) ^ 1u, abort_flag, status)) {
               stop = true;
               break;
             }
@@ -412,8 +417,8 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
           const int m_row = c.e * (kMode == kDownBwd ? p.I : p.H) + m_first;
           const int half = kMode == kUpBwd ? p.I / kStageK : nk;  // stages of the first term
           for (int kb = 0; kb < nk; ++kb, ++it) {
-            const uint32_t s = it % kStages;
-            if (!mbar_wait(&empty[s], ((it / kStages) & 1u) ^ 1u, abort_flag, status)) {
+            const uint32_t s = it % C::STAGES;
+            if (!mbar_wait(&empty[s], ((it / C::STAGES) & 1u) ^ 1u, abort_flag, status)) {
               stop = true;
               break;
             }
@@ -427,11 +432,11 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
         }
       }
       // every stage used must be consumed before the CTA may exit
-      const uint32_t nst = it < kStages ? it : kStages;
+      const uint32_t nst = it < C::STAGES ? it : C::STAGES;
       for (uint32_t s = 0; s < nst; ++s) {
-        const uint32_t last = s + kStages * ((it - 1 - s) / kStages);
+        const uint32_t last = s + C::STAGES * ((it - 1 - s) / C::STAGES);
         int no_abort = 0;
-        mbar_wait(&empty[s], (last / kStages) & 1u, &no_abort, status);
+        mbar_wait(&empty[s], (last / C::STAGES) & 1u, &no_abort, status);
       }
     }
     __syncwarp();
@@ -456,8 +461,8 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
         const uint32_t d = tmem + a * kTileN;
         const int nk = stages_of(c.k);
         for (int kb = 0; kb < nk; ++kb, ++it) {
-          const uint32_t s = it % kStages;
-          if (!mbar_wait(&full[s], (it / kStages) & 1u, abort_flag, status)) {
+          const uint32_t s = it % C::STAGES;
+          if (!mbar_wait(&full[s], (it / C::STAGES) & 1u, abort_flag, status)) {
             stop = true;
             break;
           }
@@ -493,7 +498,7 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
     const int q = warp & 3;
     const int turn = (warp - 2) / 4;
     const bool leader = q == 0 && lane == 0;  // of the turn's four warps: TMA
-    uint8_t* staging = smem + kOutOff + turn * kTurnBytes;
+    uint8_t* staging = smem + C::OUT_OFF + turn * C::TURN_BYTES;
     const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16);
     uint32_t tcount = 0;
     uint32_t asked = 0;  // pieces of g and u
@@ -590,8 +595,8 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
           }
           fence_proxy_async_smem();
           named_barrier_sync(3 + turn, 128);
-          leave(staging, D0, &maps.out[0], r, 32);
-          leave(staging + kPieceBytes, D1, &maps.out[1], r, 32);
+          leave(staging, out.d[0], &maps.out[0], r, 32);
+          leave(staging + kPieceBytes, out.d[1], &maps.out[1], r, 32);
           if (leader) tma_store_commit();
           if (r + kTurns * 32 < rows) {
             staging_free();
@@ -600,7 +605,7 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
         }
       } else {
         // a turn's 128 rows: all rounded to registers, the accumulator released,
-        // then staged and stored 64 rows at a time
+        // then staged and stored HEIGHT rows at a time
         const int first = turn * (kTileN / kTurns);
         uint32_t packed[4][16];
 #pragma unroll
@@ -619,15 +624,17 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
         }
         if (c.k > 0) release();
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int r = first + 64 * i;
+        for (int i = 0; i < 4; i += C::HEIGHT / 32) {
+          const int r = first + 32 * i;
           if (r < rows) {
             staging_free();
-            stage_piece(smem_u32(staging), q, packed[2 * i], lane, 64);
-            if (r + 32 < rows) stage_piece(smem_u32(staging) + 32 * 128, q, packed[2 * i + 1], lane, 64);
+#pragma unroll
+            for (int j = 0; j < C::HEIGHT / 32; ++j)
+              if (r + 32 * j < rows)
+                stage_piece(smem_u32(staging) + j * 32 * 128, q, packed[i + j], lane, C::HEIGHT);
             fence_proxy_async_smem();
             named_barrier_sync(3 + turn, 128);
-            leave(staging, D0, &maps.out[kMode == kWeightBwd ? c.mat : 0], r, 64);
+            leave(staging, out.d[kMode == kWeightBwd ? c.mat : 0], &maps.out[kMode == kWeightBwd ? c.mat : 0], r, C::HEIGHT);
             if (leader) tma_store_commit();
           }
         }
@@ -651,7 +658,7 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
       if (!c.ok) continue;
       it += stages_of(c.k);
       if (!has_tail(c)) continue;
-      const uint32_t s = (it - 1) % kStages;
+      const uint32_t s = (it - 1) % C::STAGES;
       const uint32_t ph = (phases >> s) & 1u;
       phases ^= 1u << s;
       if (__any_sync(0xffffffffu, !mbar_wait(&tail[s], ph, abort_flag, status))) break;
@@ -686,8 +693,8 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
 }
 
 template <int kMode>
-cudaError_t launch(const moe_shape& s, const TrainMaps& m, uint16_t* D0, uint16_t* D1, const int32_t* off_pad,
-                   const int32_t* counts, uint32_t* status, uint32_t* sched, int num_sms, cudaStream_t st) {
+cudaError_t launch(const moe_shape& s, const TrainMaps& m, const TrainOut& out, const int32_t* off_pad, const int32_t* counts,
+                   uint32_t* status, uint32_t* sched, int num_sms, cudaStream_t st) {
   using C = Cfg<kMode>;
   // the shared-memory opt-in, once per device (host threads may race here)
   static bool done[64] = {};
@@ -698,7 +705,7 @@ cudaError_t launch(const moe_shape& s, const TrainMaps& m, uint16_t* D0, uint16_
   {
     std::lock_guard<std::mutex> lock(mu);
     if (dev >= 64 || !done[dev]) {
-      err = cudaFuncSetAttribute(train_gemm_kernel<kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+      err = cudaFuncSetAttribute(train_gemm_kernel<kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
       if (err != cudaSuccess) return err;
       if (dev < 64) done[dev] = true;
     }
@@ -713,7 +720,7 @@ cudaError_t launch(const moe_shape& s, const TrainMaps& m, uint16_t* D0, uint16_
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * clusters));
   cfg.blockDim = dim3(C::THREADS);
-  cfg.dynamicSmemBytes = kSmem;
+  cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -724,28 +731,28 @@ cudaError_t launch(const moe_shape& s, const TrainMaps& m, uint16_t* D0, uint16_
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, train_gemm_kernel<kMode>, m, D0, D1, off_pad, counts,
+  return cudaLaunchKernelEx(&cfg, train_gemm_kernel<kMode>, m, out, off_pad, counts,
                             Problem{s.E, s.H, s.I, max_rows_of(s)}, status, sched);
 }
 
 }  // namespace
 
-cudaError_t launch_down_backward(const moe_shape& s, const TrainMaps& m, uint16_t* dg, uint16_t* du,
-                                 const int32_t* off_pad, const int32_t* counts, uint32_t* status, uint32_t* sched,
-                                 int num_sms, cudaStream_t st) {
-  return launch<kDownBwd>(s, m, dg, du, off_pad, counts, status, sched, num_sms, st);
+cudaError_t launch_down_backward(const moe_shape& s, const TrainMaps& m, const TrainOut& out, const int32_t* off_pad,
+                                 const int32_t* counts, uint32_t* status, uint32_t* sched, int num_sms,
+                                 cudaStream_t st) {
+  return launch<kDownBwd>(s, m, out, off_pad, counts, status, sched, num_sms, st);
 }
 
-cudaError_t launch_up_backward(const moe_shape& s, const TrainMaps& m, uint16_t* dx, const int32_t* off_pad,
+cudaError_t launch_up_backward(const moe_shape& s, const TrainMaps& m, const TrainOut& out, const int32_t* off_pad,
                                const int32_t* counts, uint32_t* status, uint32_t* sched, int num_sms,
                                cudaStream_t st) {
-  return launch<kUpBwd>(s, m, dx, nullptr, off_pad, counts, status, sched, num_sms, st);
+  return launch<kUpBwd>(s, m, out, off_pad, counts, status, sched, num_sms, st);
 }
 
-cudaError_t launch_weight_backward(const moe_shape& s, const TrainMaps& m, const int32_t* off_pad,
+cudaError_t launch_weight_backward(const moe_shape& s, const TrainMaps& m, const TrainOut& out, const int32_t* off_pad,
                                    const int32_t* counts, uint32_t* status, uint32_t* sched, int num_sms,
                                    cudaStream_t st) {
-  return launch<kWeightBwd>(s, m, nullptr, nullptr, off_pad, counts, status, sched, num_sms, st);
+  return launch<kWeightBwd>(s, m, out, off_pad, counts, status, sched, num_sms, st);
 }
 
 }  // namespace moe
