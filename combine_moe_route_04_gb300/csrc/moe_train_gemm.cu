@@ -46,7 +46,7 @@ constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kBoxBytes = kStageK * 128;  // 64 k x 64 columns (weight backward)
 constexpr int kEpiWarps = 8;              // two per TMEM lane quarter, taking 32-row pieces in turn
 constexpr int kTurns = kEpiWarps / 4;
-constexpr int kTileRing = 8;              // tiles on their way from the scheduler
+constexpr int kTileRing = 8;              // most tiles on their way from the scheduler
 constexpr uint32_t kTmemCols = 512;
 // warps: loads, MMAs, epilogue, scheduler, clearing (weight backward)
 constexpr int kSchedWarp = 2 + kEpiWarps;
@@ -129,10 +129,13 @@ struct TileRing {
   uint64_t* empty;  // [kTileRing], used in CTA 0: READERS arrivals
   int4* tile;       // [kTileRing], this CTA
 };
-__device__ __forceinline__ bool ring_put(const TileRing& r, uint32_t n, const Tile& c, volatile int* abort,
-                                         uint32_t* status) {
-  const uint32_t slot = n % kTileRing;
-  if (!mbar_wait<true>(&r.empty[slot], ((n / kTileRing) & 1u) ^ 1u, abort, status)) return false;
+// Hands out the n-th tile once every role has taken the one `ahead` (at most
+// kTileRing) before it.
+__device__ __forceinline__ bool ring_put(const TileRing& r, uint32_t n, uint32_t ahead, const Tile& c,
+                                         volatile int* abort, uint32_t* status) {
+  const uint32_t slot = n % kTileRing, before = n - ahead;
+  if (n >= ahead && !mbar_wait<true>(&r.empty[before % kTileRing], (before / kTileRing) & 1u, abort, status))
+    return false;
   const int4 v = pack_tile(c);
   *const_cast<volatile int*>(&r.tile[slot].x) = v.x;
   *const_cast<volatile int*>(&r.tile[slot].y) = v.y;
@@ -174,8 +177,8 @@ __device__ __forceinline__ void ring_release(const TileRing& r, uint32_t n, uint
 //   weight backward: expert, then gate / up / down, then row tile, column tile.
 template <int kMode>
 __device__ __forceinline__ void schedule(const TileRing& ring, const Problem& p, const int32_t* off_pad,
-                                         const int32_t* counts, uint32_t cluster, uint32_t nclusters, int lane,
-                                         volatile int* abort, uint32_t* status, uint32_t* sched) {
+                                         const int32_t* counts, uint32_t cluster, uint32_t nclusters, uint32_t ahead,
+                                         int lane, volatile int* abort, uint32_t* status, uint32_t* sched) {
   constexpr int per = kMaxExperts / 32;
   const uint32_t all = 0xffffffffu;
   const int ti = (p.I + kTileM - 1) / kTileM, th = (p.H + kTileM - 1) / kTileM;
@@ -212,8 +215,13 @@ __device__ __forceinline__ void schedule(const TileRing& ring, const Problem& p,
   if (!fits && lane == 0) record_status(status, kStatusBounds);
   const int total = kMode == kWeightBwd ? p.E * 3 * ti * th : fits ? col_tiles * windows : 0;
 
-  uint32_t drawn = 0;
-  if (lane == 0) drawn = atomicAdd(sched, 1u);
+  // two draws on their way (with one, a short tile's time was the atomic's under
+  // the output's traffic)
+  uint32_t drawn = 0, later = 0;
+  if (lane == 0) {
+    drawn = atomicAdd(sched, 1u);
+    later = atomicAdd(sched, 1u);
+  }
   bool drew_zero = false;
   int tile = static_cast<int>(cluster);
   for (uint32_t n = 0;; ++n) {
@@ -264,18 +272,19 @@ __device__ __forceinline__ void schedule(const TileRing& ring, const Problem& p,
       }
     }
     bool put = true;
-    if (lane == owner) put = ring_put(ring, n, c, abort, status);
+    if (lane == owner) put = ring_put(ring, n, ahead, c, abort, status);
     if (__any_sync(all, !put) || tile >= total) break;
     const uint32_t d = __shfl_sync(all, drawn, 0);
     drew_zero |= d == 0u;
-    // a cleared counter gives less than total + 2 clusters here
+    // a cleared counter gives less than total + 3 clusters here
     const uint64_t next = static_cast<uint64_t>(nclusters) + d;
-    if (next >= static_cast<uint64_t>(total) + 2u * nclusters && lane == 0) record_status(status, kStatusBounds);
+    if (next >= static_cast<uint64_t>(total) + 3u * nclusters && lane == 0) record_status(status, kStatusBounds);
     tile = next < static_cast<uint64_t>(total) ? static_cast<int>(next) : total;
-    if (lane == 0) drawn = atomicAdd(sched, 1u);
+    drawn = later;
+    if (lane == 0) later = atomicAdd(sched, 1u);
   }
   if (lane == 0) {
-    drew_zero |= drawn == 0u;
+    drew_zero |= drawn == 0u || later == 0u;
     __threadfence();
     const uint32_t mine = stopped(1u, cluster + 1u, drew_zero);
     const uint32_t seen = atomicAdd(sched + 1, mine) + mine;
@@ -314,7 +323,7 @@ __device__ __forceinline__ void swiglu_backward(float dh, float g, float u, floa
 template <int kMode>
 __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
     train_gemm_kernel(const __grid_constant__ TrainMaps maps, const TrainOut out, const int32_t* __restrict__ off_pad,
-                      const int32_t* __restrict__ counts, Problem p, uint32_t* __restrict__ status,
+                      const int32_t* __restrict__ counts, Problem p, uint32_t ahead, uint32_t* __restrict__ status,
                       uint32_t* __restrict__ sched) {
   using C = Cfg<kMode>;
   extern __shared__ uint8_t smem_raw[];
@@ -647,7 +656,8 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
     __syncwarp();
   } else if (warp == kSchedWarp) {
     if (rank == 0)
-      schedule<kMode>(ring, p, off_pad, counts, blockIdx.x >> 1, gridDim.x >> 1, lane, abort_flag, status, sched);
+      schedule<kMode>(ring, p, off_pad, counts, blockIdx.x >> 1, gridDim.x >> 1, ahead, lane,
+                      abort_flag, status, sched);
     __syncwarp();
   } else if constexpr (kMode == kWeightBwd) {
     // ---------------------------------------------------------- clearing (both CTAs)
@@ -677,7 +687,9 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
           ok = mbar_wait<true>(&cleared[s], ph, abort_flag, status);
           if (ok) mbar_arrive(&full[s]);
         } else {
-          mbar_arrive_cluster(map_to_cta(&cleared[s], 0));
+          // CTA 1's tensor core reads what was cleared, which the fence above has
+          // put in its shared memory: the arrival itself has nothing to publish
+          mbar_arrive_cluster_relaxed(map_to_cta(&cleared[s], 0));
         }
       }
       if (__any_sync(0xffffffffu, !ok)) break;
@@ -719,6 +731,12 @@ cudaError_t launch(const moe_shape& s, const TrainMaps& m, const TrainOut& out, 
   else tiles = max_windows_of(s) * (kMode == kDownBwd ? ti : th);
   int64_t clusters = num_sms / 2;
   if (clusters > kMaxClusters) clusters = kMaxClusters;
+  // tiles handed out ahead: enough that the loads of eight stages know theirs
+  // (what a cluster has been handed no other can take)
+  const int64_t k = kMode == kDownBwd ? s.H : kMode == kUpBwd ? 2 * s.I : static_cast<int64_t>(s.T) * s.k / s.E;
+  const int64_t stages = k / kStageK + 1;
+  int64_t ahead = 2 + 8 / stages;
+  if (ahead > kTileRing) ahead = kTileRing;
   if (tiles < clusters) clusters = tiles;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * clusters));
@@ -735,7 +753,7 @@ cudaError_t launch(const moe_shape& s, const TrainMaps& m, const TrainOut& out, 
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, train_gemm_kernel<kMode>, m, out, off_pad, counts,
-                            Problem{s.E, s.H, s.I, max_rows_of(s)}, status, sched);
+                            Problem{s.E, s.H, s.I, max_rows_of(s)}, static_cast<uint32_t>(ahead), status, sched);
 }
 
 }  // namespace
