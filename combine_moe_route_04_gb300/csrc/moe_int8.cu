@@ -28,37 +28,45 @@ __device__ __forceinline__ uint32_t max_magnitude(uint32_t m, const uint4& v) {
   return max_magnitude(max_magnitude(max_magnitude(max_magnitude(m, v.x), v.y), v.z), v.w);
 }
 
-// What a row's largest magnitude (bf16 bits) makes of its elements: the code of
-// x is rint(pre * x * mul), the scale `scale`.
-struct RowScale {
-  float pre, mul, scale;
-};
-__device__ __forceinline__ RowScale row_scale(uint32_t amax_bits) {
-  const float amax = __uint_as_float(amax_bits << 16);
-  RowScale r;
-  // far below one, 127 / amax would overflow: both are raised by 2^64 (exact)
-  r.pre = amax < 0x1p-64f ? 0x1p64f : 1.0f;
-  r.mul = __fdiv_rn(127.0f, amax * r.pre);
-  r.scale = __fdiv_rn(amax, 127.0f);
-  if (amax_bits == 0u) r.mul = 0.0f;
-  if (amax_bits >= kInfBits) {  // a NaN or an infinity: the row reads as NaN
-    r.mul = 0.0f;
-    r.scale = __uint_as_float(0x7FC00000u);
-  }
-  return r;
+// Below 2^-64 and from 2^100, where 1 / amax may leave the normal numbers, x and
+// amax are raised by this power of two first (exactly, but for elements that
+// become subnormal, whose codes are 0 either way).
+__device__ __forceinline__ float raise_of(uint32_t amax_bits) {
+  return amax_bits < 0x1F80u ? 0x1p64f : amax_bits >= 0x7180u ? 0x1p-64f : 1.0f;
 }
-// (x may be a NaN or infinite only where mul = 0; the conversion gives 0 for the
-// NaN that comes out)
-__device__ __forceinline__ uint32_t code_of(float x, const RowScale& r) {
-  const float y = x * r.pre * r.mul;
+// 127 / (amax * raise), off by less than 2^-22; 0 for a row of zeros.
+__device__ __forceinline__ float inverse_of(uint32_t amax_bits, float raise) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(__uint_as_float(amax_bits << 16) * raise));
+  return amax_bits == 0u ? 0.0f : 127.0f * r;
+}
+// The scale amax / 127, NaN for a row that holds a NaN or an infinity.
+__device__ __forceinline__ float scale_of(uint32_t amax_bits) {
+  return amax_bits >= kInfBits ? __uint_as_float(0x7FC00000u) : __fdiv_rn(__uint_as_float(amax_bits << 16), 127.0f);
+}
+// The code in the low byte: y rounded to 19 bits behind the leading one, then to an
+// integer by adding 1.5 * 2^23 (the conversion instruction has an eighth of the
+// adder's rate).
+__device__ __forceinline__ uint32_t code_of(float y) {
   const float z = __uint_as_float((__float_as_uint(y) + 8u) & ~15u);
-  return static_cast<uint32_t>(__float2int_rn(z));
+  return __float_as_uint(z + 12582912.0f);
 }
-// four codes of the bf16 pairs a, b
-__device__ __forceinline__ uint32_t codes4(uint32_t a, uint32_t b, const RowScale& r) {
-  const uint32_t lo = __byte_perm(code_of(bf16lo_to_f32(a), r), code_of(bf16hi_to_f32(a), r), 0x0040);
-  const uint32_t hi = __byte_perm(code_of(bf16lo_to_f32(b), r), code_of(bf16hi_to_f32(b), r), 0x0040);
-  return __byte_perm(lo, hi, 0x5410);
+__device__ __forceinline__ uint32_t pack4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+}
+// Eight codes of v * raise * inv.
+template <bool kRaise>
+__device__ __forceinline__ uint2 codes8(const uint4& v, float raise, float inv) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t q[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float a = kRaise ? bf16lo_to_f32(w[i]) * raise : bf16lo_to_f32(w[i]);
+    const float b = kRaise ? bf16hi_to_f32(w[i]) * raise : bf16hi_to_f32(w[i]);
+    q[2 * i] = code_of(a * inv);
+    q[2 * i + 1] = code_of(b * inv);
+  }
+  return make_uint2(pack4(q[0], q[1], q[2], q[3]), pack4(q[4], q[5], q[6], q[7]));
 }
 
 constexpr int kRowVecs = 4;  // 16-byte vectors of a row that a lane keeps
@@ -68,12 +76,13 @@ constexpr int kRowVecs = 4;  // 16-byte vectors of a row that a lane keeps
 // expert order).  A row is taken by a group of 1, 2, 4 or 8 warps, enough to keep
 // 8192 columns in registers between the maximum and the codes; further columns
 // are read twice.
-__global__ void __launch_bounds__(256) quantize_rows_kernel(const uint16_t* __restrict__ x, int64_t rows, int cols,
-                                                            const int32_t* __restrict__ scatter_idx, int k,
-                                                            int64_t max_rows, const int32_t* __restrict__ gather_idx,
-                                                            const int32_t* __restrict__ num_blocks, int group,
-                                                            int8_t* __restrict__ codes, float* __restrict__ scales,
-                                                            uint32_t* __restrict__ status) {
+__global__ void __launch_bounds__(256, 5) quantize_rows_kernel(const uint16_t* __restrict__ x, int64_t rows, int cols,
+                                                               const int32_t* __restrict__ scatter_idx, int k,
+                                                               int64_t max_rows,
+                                                               const int32_t* __restrict__ gather_idx,
+                                                               const int32_t* __restrict__ num_blocks, int group,
+                                                               int8_t* __restrict__ codes, float* __restrict__ scales,
+                                                               uint32_t* __restrict__ status) {
   __shared__ uint32_t s_max[8];
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
@@ -84,30 +93,31 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const uint16_t* __re
   bool there = t < rows;
   if (there && gather_idx != nullptr)
     there = t < static_cast<int64_t>(__ldcg(num_blocks)) * kRowBlock && __ldcg(gather_idx + t) >= 0;
-  int64_t my_row = -1;  // lane j: the j-th row to write
-  if (there) {
-    if (scatter_idx == nullptr) {
-      my_row = t;
-    } else if (lane < k) {
-      const int32_t r = __ldcg(scatter_idx + t * k + lane);
-      if (r >= 0 && r < max_rows) my_row = r;
-      else if (part == 0) record_status(status, kStatusBounds);
-    }
-  }
   const int vpr = cols / 8;
   const uint4* src = reinterpret_cast<const uint4*>(x) + t * vpr;
-  const int first = part * 32 + lane, step = group * 32;
+  const int step = group * 32;
+  int c0 = part * 32 + lane;  // this lane's first vector
   uint4 v[kRowVecs];
   uint32_t m = 0u;
 #pragma unroll
   for (int i = 0; i < kRowVecs; ++i) {
     v[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (there && first + i * step < vpr) v[i] = __ldcg(src + first + i * step);
+    if (there && c0 + i * step < vpr) v[i] = __ldcg(src + c0 + i * step);
+  }
+  int64_t my_row = -1;  // lane j: the j-th row to write
+  if (there && lane < k) {
+    if (scatter_idx == nullptr) {
+      my_row = t;
+    } else {
+      const int32_t r = __ldcg(scatter_idx + t * k + lane);
+      if (r >= 0 && r < max_rows) my_row = r;
+      else if (part == 0) record_status(status, kStatusBounds);
+    }
   }
 #pragma unroll
   for (int i = 0; i < kRowVecs; ++i) m = max_magnitude(m, v[i]);
   if (there)
-    for (int c = first + kRowVecs * step; c < vpr; c += step) m = max_magnitude(m, __ldcg(src + c));
+    for (int c = c0 + kRowVecs * step; c < vpr; c += step) m = max_magnitude(m, __ldcg(src + c));
   m = max(m & 0xFFFFu, m >> 16);
   m = __reduce_max_sync(0xffffffffu, m);
   if (group > 1) {
@@ -117,68 +127,92 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const uint16_t* __re
     for (int i = 0; i < group; ++i) m = max(m, s_max[warp - part + i]);
   }
   if (!there) return;
-  const RowScale r = row_scale(m);
+  const float raise = raise_of(m);
+  const float inv = inverse_of(m, raise);
+  if (part == 0 && my_row >= 0) scales[my_row] = scale_of(m);
   uint2* dst = reinterpret_cast<uint2*>(codes);
-  for (int c0 = part * 32; c0 < vpr; c0 += kRowVecs * step) {  // alike for the warp's lanes
+  for (;;) {
     uint2 q[kRowVecs];
+    if (m >= kInfBits) {
 #pragma unroll
-    for (int i = 0; i < kRowVecs; ++i) {
-      const int c = c0 + lane + i * step;
-      if (c0 != part * 32 && c < vpr) v[i] = __ldcg(src + c);
-      q[i] = make_uint2(codes4(v[i].x, v[i].y, r), codes4(v[i].z, v[i].w, r));
+      for (int i = 0; i < kRowVecs; ++i) q[i] = make_uint2(0u, 0u);
+    } else if (raise == 1.0f) {
+#pragma unroll
+      for (int i = 0; i < kRowVecs; ++i) q[i] = codes8<false>(v[i], 1.0f, inv);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kRowVecs; ++i) q[i] = codes8<true>(v[i], raise, inv);
     }
     for (int j = 0; j < k; ++j) {
       const int64_t row = __shfl_sync(0xffffffffu, my_row, j);
       if (row < 0) continue;
+      uint2* to = dst + row * vpr + c0;
 #pragma unroll
       for (int i = 0; i < kRowVecs; ++i)
-        if (c0 + lane + i * step < vpr) dst[row * vpr + c0 + lane + i * step] = q[i];
+        if (c0 + i * step < vpr) to[i * step] = q[i];
     }
+    c0 += kRowVecs * step;
+    if (c0 - lane >= vpr) break;  // alike for the warp's lanes
+#pragma unroll
+    for (int i = 0; i < kRowVecs; ++i)
+      if (c0 + i * step < vpr) v[i] = __ldcg(src + c0 + i * step);
   }
-  if (part == 0 && my_row >= 0 && lane < k) scales[my_row] = r.scale;
 }
 
-// Values bf16(q s): a thread takes 16 codes.
+// Values bf16(q s): a thread takes kDeqVecs times 8 codes, a block's apart, so
+// that a warp's stores are 512 contiguous bytes each.
+constexpr int kDeqVecs = 4;
 __global__ void __launch_bounds__(256) dequantize_rows_kernel(const int8_t* __restrict__ codes,
-                                                              const float* __restrict__ scales, int64_t n16,
+                                                              const float* __restrict__ scales, int64_t n8,
                                                               int vecs_per_row, uint16_t* __restrict__ x) {
   pdl_launch_dependents();
   pdl_wait();
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (i >= n16) return;
-  const uint4 q = __ldcg(reinterpret_cast<const uint4*>(codes) + i);
-  const float s = __ldcg(scales + i / vecs_per_row);
-  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-  uint32_t o[8];
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * (256 * kDeqVecs) + threadIdx.x;
+  uint2 q[kDeqVecs];
+  float s[kDeqVecs];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const uint32_t b = w[j >> 1] >> (16 * (j & 1));
-    o[j] = pack_bf16x2(static_cast<float>(static_cast<int8_t>(b)) * s,
-                       static_cast<float>(static_cast<int8_t>(b >> 8)) * s);
+  for (int i = 0; i < kDeqVecs; ++i) {
+    const int64_t v = first + 256 * i;
+    if (v < n8) {
+      q[i] = __ldcg(reinterpret_cast<const uint2*>(codes) + v);
+      s[i] = __ldca(scales + v / vecs_per_row);
+    }
   }
-  uint4* dst = reinterpret_cast<uint4*>(x) + 2 * i;
-  dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-  dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+#pragma unroll
+  for (int i = 0; i < kDeqVecs; ++i) {
+    const int64_t v = first + 256 * i;
+    if (v >= n8) return;
+    const uint32_t w[2] = {q[i].x, q[i].y};
+    uint32_t o[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t b = w[j >> 1] >> (16 * (j & 1));
+      o[j] = pack_bf16x2(static_cast<float>(static_cast<int8_t>(b)) * s[i],
+                         static_cast<float>(static_cast<int8_t>(b >> 8)) * s[i]);
+    }
+    reinterpret_cast<uint4*>(x)[v] = make_uint4(o[0], o[1], o[2], o[3]);
+  }
 }
 
 // Weights w [E][K][N] to codes [E][N][K], the reduction axis K contiguous, and a
-// scale per (e, n).  A CTA takes 64 columns of one expert: a first pass over
-// their K rows (128 bytes each) for the maxima, a second one in steps of kWk rows
-// for the codes, which cross shared memory once so that each column's 128 bytes
-// leave together.
-constexpr int kWn = 64;
-constexpr int kWeightThreads = 1024;
-constexpr int kWk = kWeightThreads / 8 * 4;  // four rows x eight columns per thread
+// scale per (e, n).  A CTA takes 32 columns of one expert: a first pass over
+// their K rows (64 bytes each) for the maxima, a second one, backwards, in steps of
+// kWk rows for the codes, which cross shared memory once so that each column's
+// bytes leave together.  Two CTAs an SM: their strips, 256 KB each for K = 4096,
+// stay in L2 between the passes, and one's loads run under the other's arithmetic.
+constexpr int kWn = 32;
+constexpr int kWeightThreads = 512;
+constexpr int kWk = kWeightThreads / 4 * 4;  // four rows x eight columns per thread
 
-__global__ void __launch_bounds__(kWeightThreads) quantize_weights_kernel(const uint16_t* __restrict__ w, int K, int N,
-                                                                          int8_t* __restrict__ codes,
-                                                                          float* __restrict__ scales) {
+__global__ void __launch_bounds__(kWeightThreads, 2) quantize_weights_kernel(const uint16_t* __restrict__ w, int K,
+                                                                             int N, int8_t* __restrict__ codes,
+                                                                             float* __restrict__ scales) {
   __shared__ __align__(16) uint32_t s_codes[kWn * kWk / 4];
-  __shared__ uint4 s_max[kWeightThreads / 32][8];
+  __shared__ uint4 s_max[kWeightThreads / 32][4];
   pdl_launch_dependents();
   pdl_wait();
-  const int cg = threadIdx.x & 7;   // columns 8 cg..
-  const int kr = threadIdx.x >> 3;  // row of the thread, or group of four rows
+  const int cg = threadIdx.x & 3;   // columns 8 cg..
+  const int kr = threadIdx.x >> 2;  // row of the thread, or group of four rows
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t e = blockIdx.y;
   const int64_t n0 = static_cast<int64_t>(blockIdx.x) * kWn;
@@ -186,7 +220,7 @@ __global__ void __launch_bounds__(kWeightThreads) quantize_weights_kernel(const 
   const int64_t pitch = N / 8;
   uint4 m = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll 8
-  for (int k = kr; k < K; k += kWeightThreads / 8) {
+  for (int k = kr; k < K; k += kWeightThreads / 4) {
     const uint4 v = __ldcg(src + k * pitch);
     m.x = max_magnitude(m.x, v.x);
     m.y = max_magnitude(m.y, v.y);
@@ -194,13 +228,13 @@ __global__ void __launch_bounds__(kWeightThreads) quantize_weights_kernel(const 
     m.w = max_magnitude(m.w, v.w);
   }
 #pragma unroll
-  for (int o = 8; o < 32; o <<= 1) {  // the warp's four rows
+  for (int o = 4; o < 32; o <<= 1) {  // the warp's eight rows
     m.x = __vmaxu2(m.x, __shfl_xor_sync(0xffffffffu, m.x, o));
     m.y = __vmaxu2(m.y, __shfl_xor_sync(0xffffffffu, m.y, o));
     m.z = __vmaxu2(m.z, __shfl_xor_sync(0xffffffffu, m.z, o));
     m.w = __vmaxu2(m.w, __shfl_xor_sync(0xffffffffu, m.w, o));
   }
-  if (lane < 8) s_max[warp][lane] = m;
+  if (lane < 4) s_max[warp][lane] = m;
   __syncthreads();
   m = s_max[0][cg];
   for (int i = 1; i < kWeightThreads / 32; ++i) {
@@ -210,14 +244,20 @@ __global__ void __launch_bounds__(kWeightThreads) quantize_weights_kernel(const 
     m.z = __vmaxu2(m.z, v.z);
     m.w = __vmaxu2(m.w, v.w);
   }
-  RowScale r[8];
+  float inv[8];
+  uint32_t bad = 0u, raised = 0u;  // bit i: column 8 cg + i reads as NaN, is raised
   const uint32_t mw[4] = {m.x, m.y, m.z, m.w};
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    r[i] = row_scale((mw[i >> 1] >> (16 * (i & 1))) & 0xFFFFu);
-    if (kr == 0) scales[e * N + n0 + 8 * cg + i] = r[i].scale;
+    const uint32_t b = (mw[i >> 1] >> (16 * (i & 1))) & 0xFFFFu;
+    const float raise = raise_of(b);
+    inv[i] = inverse_of(b, raise);
+    if (b >= kInfBits) bad |= 1u << i;
+    if (raise != 1.0f) raised |= 1u << i;
+    if (kr == 0) scales[e * N + n0 + 8 * cg + i] = scale_of(b);
   }
-  for (int k0 = 0; k0 < K; k0 += kWk) {
+  const bool any_raised = __any_sync(0xffffffffu, raised != 0u);
+  for (int k0 = (K - 1) / kWk * kWk; k0 >= 0; k0 -= kWk) {
     const int k = k0 + 4 * kr;
     if (k < K) {  // K is a multiple of 128
       uint4 v[4];
@@ -227,15 +267,20 @@ __global__ void __launch_bounds__(kWeightThreads) quantize_weights_kernel(const 
                                 {v[2].x, v[2].y, v[2].z, v[2].w}, {v[3].x, v[3].y, v[3].z, v[3].w}};
 #pragma unroll
       for (int i = 0; i < 8; ++i) {  // column 8 cg + i: its four k's are one word
-        uint32_t q[4];
+        float f[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          q[j] = code_of(i & 1 ? bf16hi_to_f32(a[j][i >> 1]) : bf16lo_to_f32(a[j][i >> 1]), r[i]);
+        for (int j = 0; j < 4; ++j) f[j] = i & 1 ? bf16hi_to_f32(a[j][i >> 1]) : bf16lo_to_f32(a[j][i >> 1]);
+        if (any_raised && ((raised >> i) & 1u)) {
+          const float raise = inv[i] > 1.0f ? 0x1p64f : 0x1p-64f;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) f[j] *= raise;
+        }
+        const uint32_t q =
+            pack4(code_of(f[0] * inv[i]), code_of(f[1] * inv[i]), code_of(f[2] * inv[i]), code_of(f[3] * inv[i]));
         // 16-byte chunks of a column are permuted by its group, which spreads
         // both accesses over all banks
-        const int chunk = (kr >> 2) ^ cg;
-        s_codes[(8 * cg + i) * (kWk / 4) + chunk * 4 + (kr & 3)] =
-            __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
+        const int chunk = (kr >> 2) ^ (2 * cg);
+        s_codes[(8 * cg + i) * (kWk / 4) + chunk * 4 + (kr & 3)] = (bad >> i) & 1u ? 0u : q;
       }
     }
     __syncthreads();
@@ -244,7 +289,7 @@ __global__ void __launch_bounds__(kWeightThreads) quantize_weights_kernel(const 
       const int n = i / (kWk / 16), c = i % (kWk / 16);
       if (c < left)
         *reinterpret_cast<uint4*>(codes + (e * N + n0 + n) * K + k0 + c * 16) =
-            *reinterpret_cast<const uint4*>(s_codes + n * (kWk / 4) + (c ^ (n >> 3)) * 4);
+            *reinterpret_cast<const uint4*>(s_codes + n * (kWk / 4) + (c ^ (2 * (n >> 3))) * 4);
     }
     __syncthreads();
   }
@@ -287,9 +332,10 @@ cudaError_t launch_quantize_permute_int8(const moe_shape& s, const uint16_t* X, 
 
 cudaError_t launch_dequantize_rows_int8(const int8_t* codes, const float* scales, int64_t rows, int64_t cols,
                                         uint16_t* x, cudaStream_t st) {
-  const int64_t n16 = rows * (cols / 16);
-  return launch_pdl(dequantize_rows_kernel, dim3(static_cast<unsigned>((n16 + 255) / 256)), dim3(256), 0, st, codes,
-                    scales, n16, static_cast<int>(cols / 16), x);
+  const int64_t n8 = rows * (cols / 8);
+  constexpr int kPer = 256 * kDeqVecs;
+  return launch_pdl(dequantize_rows_kernel, dim3(static_cast<unsigned>((n8 + kPer - 1) / kPer)), dim3(256), 0, st,
+                    codes, scales, n8, static_cast<int>(cols / 8), x);
 }
 
 cudaError_t launch_quantize_weights_int8(const uint16_t* w, int E, int64_t K, int64_t N, int8_t* codes, float* scales,

@@ -735,7 +735,7 @@ cudaError_t launch(const moe_shape& s, const TrainMaps& m, const TrainOut& out, 
   // (what a cluster has been handed no other can take)
   const int64_t k = kMode == kDownBwd ? s.H : kMode == kUpBwd ? 2 * s.I : static_cast<int64_t>(s.T) * s.k / s.E;
   const int64_t stages = k / kStageK + 1;
-  int64_t ahead = 2 + 8 / stages;
+  int64_t ahead = 3 + 8 / stages;
   if (ahead > kTileRing) ahead = kTileRing;
   if (tiles < clusters) clusters = tiles;
   cudaLaunchConfig_t cfg = {};
