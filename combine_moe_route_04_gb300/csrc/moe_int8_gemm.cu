@@ -10,11 +10,16 @@
 // A tile is one window of up to 128 of an expert's rows times two blocks of 128
 // output columns (up: the same columns of gate and of up; down: 256 neighbouring
 // columns).  The weights are the M = 128 operand, the rows the N operand.  TMA
-// brings the codes in stages of 128 k.  Eight warps widen them in steps of 64 k:
-// the weights into TMEM, from where the MMA reads its first operand (lane = weight
-// row, two k per column: a thread widens its own row), the rows into shared
-// memory in the swizzle of the second operand.  TMEM holds two 128 x 128
-// accumulators and kSteps such steps of both blocks.
+// brings the codes in stages of 128 k.  Two groups of eight warps widen them, each
+// one half of every stage, a step of 64 k: the weights into TMEM, from where the
+// MMA reads its first operand (lane = weight row, two k per column: a thread widens
+// its own row), the rows into shared memory in the swizzle of the second operand.
+// TMEM holds two 128 x 128 accumulators and kSteps such steps of both blocks.
+//
+// What bounds it with many rows is the widening: a step is 512 cycles of MMAs and
+// about 440 of instruction issue, and a group needs some 800 from its wait to its
+// arrival (one group alone: 1040 cycles a step, up product of 2048 tokens and 64
+// experts of 4096 x 1536 444 us, of 16384 tokens and 128 experts 2914 us).
 #include <cstdint>
 #include <mutex>
 
@@ -36,12 +41,19 @@ constexpr int kSteps = 3;
 constexpr int kWBytes = 128 * kStageK;    // codes of one block of 128 weight rows
 constexpr int kStageBytes = 2 * kWBytes + kTok * kStageK;
 constexpr int kStepBytes = kTok * kStepK * 2;  // widened rows
-constexpr int kFirstEpi = 2;              // warps: loads, MMAs, epilogue, widening
+// Warps: loads, MMAs (and two idle ones), epilogue, widening, each role whole
+// groups of four warps, which share out the registers: kLaunchRegs a thread at
+// launch, then what each role asks for.
+constexpr int kFirstEpi = 4;
 constexpr int kEpiWarps = 8;
 constexpr int kTurns = kEpiWarps / 4;
 constexpr int kFirstWide = kFirstEpi + kEpiWarps;
-constexpr int kWideWarps = 8;
+constexpr int kWideGroup = 8;
+constexpr int kWideWarps = 2 * kWideGroup;
 constexpr int kThreads = (kFirstWide + kWideWarps) * 32;
+constexpr int kLaunchRegs = 72, kControlRegs = 40, kEpiRegs = 112, kWideRegs = 56;
+static_assert(kThreads * kLaunchRegs <= 65536 && kFirstEpi * kControlRegs + kEpiWarps * kEpiRegs +
+                  kWideWarps * kWideRegs <= kThreads / 32 * kLaunchRegs, "registers");
 constexpr int kReaders = 1 + kEpiWarps + kWideWarps;  // of a tile index
 // TMEM columns: the accumulators, then the widened weights of each step
 constexpr uint32_t kAcc1 = kTok;
@@ -60,6 +72,15 @@ constexpr int kCntOff = kWinOff + (kMaxExperts + 1) * 4;
 constexpr int kOffpOff = kCntOff + kMaxExperts * 4;
 constexpr int kSmem = kOffpOff + (kMaxExperts + 1) * 4 + 1024;
 static_assert(kSmem <= 232448, "shared memory budget");
+
+template <int kRegs>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
 
 // D(tmem) (+)= A(tmem) B(smem), fp16 with float32 sums, 16 deep.
 __device__ __forceinline__ void mma_f16_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
@@ -131,7 +152,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&empty[s], kWideWarps);
     }
     for (int s = 0; s < kSteps; ++s) {
-      mbar_init(&wide[s], kWideWarps);
+      mbar_init(&wide[s], kWideGroup);
       mbar_init(&used[s], 1);
     }
     mbar_init(tfull, 1);
@@ -168,109 +189,113 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int total = fits ? NT * s_win[E] : 0;
   const int KS = K / kStageK;
 
-  if (warp == 0) {
-    // ---------------------------------------------------------- loads
-    if (elect_one_sync()) {
-      const uint64_t pol_keep = policy_evict_last();
-      uint32_t it = 0;
-      int tile = blockIdx.x;
-      bool drew_zero = false;
-      bool stop = !ring_put(ring, 0, tile, abort_flag, status);
-      for (uint32_t n = 0; !stop && tile < total; ++n) {
-        const uint32_t drawn = atomicAdd(sched, 1u);  // the next tile: needed after this one's loads
-        const Win c = decode<kTok>(tile, NT, E, s_win, s_offp, s_cnt, max_rows);
-        if (!c.ok) record_status(status, kStatusBounds);
-        // a one-window expert reads this weight tile once
-        const uint64_t pol_w = s_win[c.e + 1] - s_win[c.e] == 1 ? policy_evict_first() : pol_keep;
-        const int n0 = c.j * (kUp ? 128 : 256);
-        const bool two = kUp || n0 + 128 < N_out;  // the second weight block exists
-        const int w_row = c.e * N_out + n0;        // E * N_out < 2^31
-        const int pick = c.rows <= 32 ? 0 : c.rows <= 64 ? 1 : 2;  // the smallest box that holds the window
-        const uint32_t bytes = (two ? 2u : 1u) * kWBytes + int8_token_box(pick) * kStageK;
-        for (int ks = 0; c.ok && ks < KS; ++ks, ++it) {
-          const uint32_t s = it % kStages;
-          if (!mbar_wait(&empty[s], ((it / kStages) & 1u) ^ 1u, abort_flag, status)) {
-            stop = true;
-            break;
+  if (warp < kFirstEpi) {
+    fewer_registers<kControlRegs>();
+    if (warp == 0) {
+      // ---------------------------------------------------------- loads
+      if (elect_one_sync()) {
+        const uint64_t pol_keep = policy_evict_last();
+        uint32_t it = 0;
+        int tile = blockIdx.x;
+        bool drew_zero = false;
+        bool stop = !ring_put(ring, 0, tile, abort_flag, status);
+        for (uint32_t n = 0; !stop && tile < total; ++n) {
+          const uint32_t drawn = atomicAdd(sched, 1u);  // the next tile: needed after this one's loads
+          const Win c = decode<kTok>(tile, NT, E, s_win, s_offp, s_cnt, max_rows);
+          if (!c.ok) record_status(status, kStatusBounds);
+          // a one-window expert reads this weight tile once
+          const uint64_t pol_w = s_win[c.e + 1] - s_win[c.e] == 1 ? policy_evict_first() : pol_keep;
+          const int n0 = c.j * (kUp ? 128 : 256);
+          const bool two = kUp || n0 + 128 < N_out;  // the second weight block exists
+          const int w_row = c.e * N_out + n0;        // E * N_out < 2^31
+          const int pick = c.rows <= 32 ? 0 : c.rows <= 64 ? 1 : 2;  // the smallest box that holds the window
+          const uint32_t bytes = (two ? 2u : 1u) * kWBytes + int8_token_box(pick) * kStageK;
+          for (int ks = 0; c.ok && ks < KS; ++ks, ++it) {
+            const uint32_t s = it % kStages;
+            if (!mbar_wait(&empty[s], ((it / kStages) & 1u) ^ 1u, abort_flag, status)) {
+              stop = true;
+              break;
+            }
+            mbar_arrive_expect_tx(&full[s], bytes);
+            uint8_t* st = smem + s * kStageBytes;
+            const int kx = ks * kStageK;
+            tma_load_2d(st, &maps.w0, &full[s], kx, w_row, pol_w);
+            if (two) tma_load_2d(st + kWBytes, kUp ? &maps.w1 : &maps.w0, &full[s], kx, kUp ? w_row : w_row + 128, pol_w);
+            tma_load_2d(st + 2 * kWBytes, &maps.t[pick], &full[s], kx, c.row0, pol_keep);
           }
-          mbar_arrive_expect_tx(&full[s], bytes);
-          uint8_t* st = smem + s * kStageBytes;
-          const int kx = ks * kStageK;
-          tma_load_2d(st, &maps.w0, &full[s], kx, w_row, pol_w);
-          if (two) tma_load_2d(st + kWBytes, kUp ? &maps.w1 : &maps.w0, &full[s], kx, kUp ? w_row : w_row + 128, pol_w);
-          tma_load_2d(st + 2 * kWBytes, &maps.t[pick], &full[s], kx, c.row0, pol_keep);
+          drew_zero |= drawn == 0u;
+          if (stop) break;
+          // a cleared counter gives at most total + grid - 1 here
+          const uint64_t next = static_cast<uint64_t>(gridDim.x) + drawn;
+          tile = next < static_cast<uint64_t>(total) + gridDim.x ? static_cast<int>(next) : total;
+          if (static_cast<uint64_t>(tile) != next) record_status(status, kStatusBounds);
+          stop = !ring_put(ring, n + 1, tile, abort_flag, status);
         }
-        drew_zero |= drawn == 0u;
-        if (stop) break;
-        // a cleared counter gives at most total + grid - 1 here
-        const uint64_t next = static_cast<uint64_t>(gridDim.x) + drawn;
-        tile = next < static_cast<uint64_t>(total) + gridDim.x ? static_cast<int>(next) : total;
-        if (static_cast<uint64_t>(tile) != next) record_status(status, kStatusBounds);
-        stop = !ring_put(ring, n + 1, tile, abort_flag, status);
+        __threadfence();
+        const uint32_t mine = stopped(1u, blockIdx.x + 1u, drew_zero);
+        const uint32_t seen = atomicAdd(sched + 1, mine) + mine;
+        if ((seen & 0x3FFu) == gridDim.x) {  // every CTA has drawn its last index
+          const uint32_t clean = stopped(gridDim.x, gridDim.x * (gridDim.x + 1u) / 2u, total > 0);
+          if (seen != clean) record_status(status, kStatusBounds);
+          atomicExch(sched, 0u);
+          atomicExch(sched + 1, 0u);
+        }
+        // every stage used must have been read before the CTA may exit
+        const uint32_t nst = it < kStages ? it : kStages;
+        for (uint32_t s = 0; s < nst; ++s) {
+          const uint32_t last = s + kStages * ((it - 1 - s) / kStages);
+          int no_abort = 0;
+          mbar_wait(&empty[s], (last / kStages) & 1u, &no_abort, status);
+        }
       }
-      __threadfence();
-      const uint32_t mine = stopped(1u, blockIdx.x + 1u, drew_zero);
-      const uint32_t seen = atomicAdd(sched + 1, mine) + mine;
-      if ((seen & 0x3FFu) == gridDim.x) {  // every CTA has drawn its last index
-        const uint32_t clean = stopped(gridDim.x, gridDim.x * (gridDim.x + 1u) / 2u, total > 0);
-        if (seen != clean) record_status(status, kStatusBounds);
-        atomicExch(sched, 0u);
-        atomicExch(sched + 1, 0u);
-      }
-      // every stage used must have been read before the CTA may exit
-      const uint32_t nst = it < kStages ? it : kStages;
-      for (uint32_t s = 0; s < nst; ++s) {
-        const uint32_t last = s + kStages * ((it - 1 - s) / kStages);
-        int no_abort = 0;
-        mbar_wait(&empty[s], (last / kStages) & 1u, &no_abort, status);
-      }
-    }
-    __syncwarp();
-  } else if (warp == 1) {
-    // ---------------------------------------------------------- MMAs
-    if (elect_one_sync()) {
-      uint32_t it = 0;
-      uint32_t tcount = 0;
-      bool stop = false;
-      for (uint32_t n = 0; !stop; ++n) {
-        const int tile = ring_take(ring, n, abort_flag, status);
-        if (tile < 0 || tile >= total) break;
-        mbar_arrive(&ring.empty[n % kTileRing]);
-        const Win c = decode<kTok>(tile, NT, E, s_win, s_offp, s_cnt, max_rows);
-        if (!c.ok) continue;
-        const bool two = kUp || c.j * 256 + 128 < N_out;
-        // fp16 operands, float32 sums, both with k contiguous, M = 128, N
-        const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>((c.rows + 15) / 16 * 2) << 17) | ((128u >> 4) << 24);
-        if (!mbar_wait(tempty, (tcount & 1u) ^ 1u, abort_flag, status)) break;
-        tc_fence_after();
-        for (int ks = 0; ks < 2 * KS; ++ks, ++it) {
-          const uint32_t s = it % kSteps;
-          if (!mbar_wait(&wide[s], (it / kSteps) & 1u, abort_flag, status)) {
-            stop = true;
-            break;
-          }
+      __syncwarp();
+    } else if (warp == 1) {
+      // ---------------------------------------------------------- MMAs
+      if (elect_one_sync()) {
+        uint32_t it = 0;
+        uint32_t tcount = 0;
+        bool stop = false;
+        for (uint32_t n = 0; !stop; ++n) {
+          const int tile = ring_take(ring, n, abort_flag, status);
+          if (tile < 0 || tile >= total) break;
+          mbar_arrive(&ring.empty[n % kTileRing]);
+          const Win c = decode<kTok>(tile, NT, E, s_win, s_offp, s_cnt, max_rows);
+          if (!c.ok) continue;
+          const bool two = kUp || c.j * 256 + 128 < N_out;
+          // fp16 operands, float32 sums, both with k contiguous, M = 128, N
+          const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>((c.rows + 15) / 16 * 2) << 17) | ((128u >> 4) << 24);
+          if (!mbar_wait(tempty, (tcount & 1u) ^ 1u, abort_flag, status)) break;
           tc_fence_after();
-          const uint32_t sb = smem_u32(smem + kStepOff + s * kStepBytes);
-          const uint32_t ta = tmem + kWideCol + s * 2 * kWideBlockCols;
-#pragma unroll
-          for (int kk = 0; kk < kStepK / 16; ++kk) {
-            const uint64_t bd = smem_desc(sb + kk * 32, 16, 1024, kSwizzle128B);
-            const uint32_t acc = (ks | kk) != 0 ? 1u : 0u;
-            mma_f16_tmem(tmem, ta + 8 * kk, bd, idesc, acc);
-            if (two) mma_f16_tmem(tmem + kAcc1, ta + kWideBlockCols + 8 * kk, bd, idesc, acc);
+          for (int ks = 0; ks < 2 * KS; ++ks, ++it) {
+            const uint32_t s = it % kSteps;
+            if (!mbar_wait(&wide[s], (it / kSteps) & 1u, abort_flag, status)) {
+              stop = true;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t sb = smem_u32(smem + kStepOff + s * kStepBytes);
+            const uint32_t ta = tmem + kWideCol + s * 2 * kWideBlockCols;
+  #pragma unroll
+            for (int kk = 0; kk < kStepK / 16; ++kk) {
+              const uint64_t bd = smem_desc(sb + kk * 32, 16, 1024, kSwizzle128B);
+              const uint32_t acc = (ks | kk) != 0 ? 1u : 0u;
+              mma_f16_tmem(tmem, ta + 8 * kk, bd, idesc, acc);
+              if (two) mma_f16_tmem(tmem + kAcc1, ta + kWideBlockCols + 8 * kk, bd, idesc, acc);
+            }
+            tc_commit(&used[s]);
           }
-          tc_commit(&used[s]);
+          if (stop) break;
+          tc_commit(tfull);
+          ++tcount;
         }
-        if (stop) break;
-        tc_commit(tfull);
-        ++tcount;
+        tc_commit(drain);
+        int no_abort = 0;
+        mbar_wait(drain, 0, &no_abort, status);
       }
-      tc_commit(drain);
-      int no_abort = 0;
-      mbar_wait(drain, 0, &no_abort, status);
+      __syncwarp();
     }
-    __syncwarp();
   } else if (warp < kFirstWide) {
+    more_registers<kEpiRegs>();
     // ---------------------------------------------------------- epilogue
     // TMEM lane = output column, TMEM column = row of the window; the warps of
     // a lane quarter take the window's 32-row pieces in turn
@@ -390,13 +415,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (leader) tma_store_wait_all<0>();  // this thread's stores are written
     __syncwarp();
   } else {
+    fewer_registers<kWideRegs>();
     // ---------------------------------------------------------- widening
     const int w = warp - kFirstWide;
-    const int block = w >> 2;   // weight block; of the rows, which half of a step's 16-byte chunks
-    const int q = warp & 3;     // TMEM lane quarter; of the rows, which 32
+    const int half = w / kWideGroup;  // of each stage
+    const int block = (w >> 2) & 1;   // weight block; of the rows, which half of a step's 16-byte chunks
+    const int q = warp & 3;           // TMEM lane quarter; of the rows, which 32
     const int wrow = 32 * q + lane, trow = 32 * (w & 3) + lane;
     const uint32_t ta = tmem + (static_cast<uint32_t>(32 * q) << 16) + kWideCol + block * kWideBlockCols;
-    uint32_t it = 0, step = 0;
+    uint32_t it = 0;
     bool stop = false;
     for (uint32_t n = 0; !stop; ++n) {
       const int tile = ring_take(ring, n, abort_flag, status);
@@ -415,47 +442,45 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         const uint8_t* st = smem + s * kStageBytes;
-        for (int half = 0; half < 2; ++half, ++step) {
-          const uint32_t d = step % kSteps;
-          if (__any_sync(0xffffffffu, !mbar_wait(&used[d], ((step / kSteps) & 1u) ^ 1u, abort_flag, status))) {
-            stop = true;
-            break;
-          }
-          tc_fence_after();
-          if (block == 0 || two) {
-            uint32_t r[32];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint4 v = *reinterpret_cast<const uint4*>(st + block * kWBytes + swizzled(wrow, 4 * half + i));
-              widen4(v.x, r[8 * i], r[8 * i + 1]);
-              widen4(v.y, r[8 * i + 2], r[8 * i + 3]);
-              widen4(v.z, r[8 * i + 4], r[8 * i + 5]);
-              widen4(v.w, r[8 * i + 6], r[8 * i + 7]);
-            }
-            tmem_st_32x32b_x32(ta + d * 2 * kWideBlockCols, r);
-          }
-          if (rows_here) {
-            uint8_t* to = smem + kStepOff + d * kStepBytes;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const int ch = 2 * block + i;  // 16 k of the step
-              const uint4 v = *reinterpret_cast<const uint4*>(st + 2 * kWBytes + swizzled(trow, 4 * half + ch));
-              uint4 a, b;
-              widen4(v.x, a.x, a.y);
-              widen4(v.y, a.z, a.w);
-              widen4(v.z, b.x, b.y);
-              widen4(v.w, b.z, b.w);
-              *reinterpret_cast<uint4*>(to + swizzled(trow, 2 * ch)) = a;
-              *reinterpret_cast<uint4*>(to + swizzled(trow, 2 * ch + 1)) = b;
-            }
-            fence_proxy_async_smem();
-          }
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&wide[d]);
+        const uint32_t step = 2 * it + half, d = step % kSteps;
+        if (__any_sync(0xffffffffu, !mbar_wait(&used[d], ((step / kSteps) & 1u) ^ 1u, abort_flag, status))) {
+          stop = true;
+          break;
         }
-        if (!stop && lane == 0) mbar_arrive(&empty[s]);
+        tc_fence_after();
+        if (block == 0 || two) {
+          uint32_t r[32];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint4 v = *reinterpret_cast<const uint4*>(st + block * kWBytes + swizzled(wrow, 4 * half + i));
+            widen4(v.x, r[8 * i], r[8 * i + 1]);
+            widen4(v.y, r[8 * i + 2], r[8 * i + 3]);
+            widen4(v.z, r[8 * i + 4], r[8 * i + 5]);
+            widen4(v.w, r[8 * i + 6], r[8 * i + 7]);
+          }
+          tmem_st_32x32b_x32(ta + d * 2 * kWideBlockCols, r);
+        }
+        if (rows_here) {
+          uint8_t* to = smem + kStepOff + d * kStepBytes;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int ch = 2 * block + i;  // 16 k of the step
+            const uint4 v = *reinterpret_cast<const uint4*>(st + 2 * kWBytes + swizzled(trow, 4 * half + ch));
+            uint4 a, b;
+            widen4(v.x, a.x, a.y);
+            widen4(v.y, a.z, a.w);
+            widen4(v.z, b.x, b.y);
+            widen4(v.w, b.z, b.w);
+            *reinterpret_cast<uint4*>(to + swizzled(trow, 2 * ch)) = a;
+            *reinterpret_cast<uint4*>(to + swizzled(trow, 2 * ch + 1)) = b;
+          }
+          fence_proxy_async_smem();
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&wide[d]);
+        if (lane == 0) mbar_arrive(&empty[s]);
       }
     }
     __syncwarp();
