@@ -27,23 +27,23 @@
 
 #include "moe_device.cuh"
 #include "moe_internal.h"
-#include "moe_tiles.cuh"
 #include "moe_transpose.cuh"
 
 namespace moe {
 namespace {
 
+constexpr int kMaxExperts = 256;
 constexpr int kTok = 128;                 // most rows of a window
 constexpr int kStageK = 128;              // reduction elements (bytes) per stage of codes
 constexpr int kStepK = 64;                // and per widened step
 constexpr int kStages = 3;
-constexpr int kSteps = 3;
+constexpr int kSteps = 4;
 constexpr int kWBytes = 128 * kStageK;    // codes of one block of 128 weight rows
 constexpr int kStageBytes = 2 * kWBytes + kTok * kStageK;
 constexpr int kStepBytes = kTok * kStepK * 2;  // widened rows
-// Warps: loads, MMAs (and two idle ones), epilogue, widening, each role whole
-// groups of four warps, which share out the registers: kLaunchRegs a thread at
-// launch, then what each role asks for.
+// Warps: loads, MMAs, scheduler (and an idle one); epilogue; widening: whole groups
+// of four warps, which share out the registers: kLaunchRegs a thread at launch,
+// then what each group asks for.
 constexpr int kFirstEpi = 4;
 constexpr int kEpiWarps = 8;
 constexpr int kTurns = kEpiWarps / 4;
@@ -51,10 +51,11 @@ constexpr int kFirstWide = kFirstEpi + kEpiWarps;
 constexpr int kWideGroup = 8;
 constexpr int kWideWarps = 2 * kWideGroup;
 constexpr int kThreads = (kFirstWide + kWideWarps) * 32;
-constexpr int kLaunchRegs = 72, kControlRegs = 40, kEpiRegs = 112, kWideRegs = 56;
+constexpr int kLaunchRegs = 72, kControlRegs = 56, kEpiRegs = 112, kWideRegs = 56;
 static_assert(kThreads * kLaunchRegs <= 65536 && kFirstEpi * kControlRegs + kEpiWarps * kEpiRegs +
                   kWideWarps * kWideRegs <= kThreads / 32 * kLaunchRegs, "registers");
-constexpr int kReaders = 1 + kEpiWarps + kWideWarps;  // of a tile index
+constexpr int kTileRing = 4;                          // tiles on their way from the scheduler
+constexpr int kReaders = 2 + kEpiWarps + kWideWarps;  // of a tile
 // TMEM columns: the accumulators, then the widened weights of each step
 constexpr uint32_t kAcc1 = kTok;
 constexpr uint32_t kWideCol = 2 * kTok;
@@ -62,15 +63,12 @@ constexpr uint32_t kWideBlockCols = kStepK / 2;
 static_assert(kWideCol + kSteps * 2 * kWideBlockCols <= 512, "TMEM columns");
 constexpr int kStepOff = kStages * kStageBytes;
 constexpr int kOutOff = kStepOff + kSteps * kStepBytes;
-constexpr int kBarOff = kOutOff + kTurns * kPieceBytes;
+constexpr int kRingOff = kOutOff + kTurns * kPieceBytes;
+constexpr int kBarOff = kRingOff + kTileRing * 16;
 // full, empty [kStages]; wide, used [kSteps]; tfull, tempty, drain; the ring's
 constexpr int kNumBars = 2 * kStages + 2 * kSteps + 3 + 2 * kTileRing;
 constexpr int kSlotOff = kBarOff + kNumBars * 8;
-constexpr int kTileOff = kSlotOff + 16;
-constexpr int kWinOff = kTileOff + kTileRing * 4;
-constexpr int kCntOff = kWinOff + (kMaxExperts + 1) * 4;
-constexpr int kOffpOff = kCntOff + kMaxExperts * 4;
-constexpr int kSmem = kOffpOff + (kMaxExperts + 1) * 4 + 1024;
+constexpr int kSmem = kSlotOff + 16 + 1024;
 static_assert(kSmem <= 232448, "shared memory budget");
 
 template <int kRegs>
@@ -121,6 +119,176 @@ __device__ __forceinline__ void widen4(uint32_t v, uint32_t& lo, uint32_t& hi) {
 // byte offset of row t, 16-byte chunk c (of 8) in rows of 128 bytes, 128-byte swizzle
 __device__ __forceinline__ int swizzled(int t, int c) { return t * 128 + ((c ^ (t & 7)) << 4); }
 
+// A tile as the scheduler hands it out.
+struct Tile {
+  int e, j, row0, rows;  // expert, column tile, first row and rows of the window
+  bool alone;            // the expert has one window
+  bool last;             // no tile: the roles end
+};
+struct TileRing {
+  uint64_t* full;   // [kTileRing] one arrival (the scheduler)
+  uint64_t* empty;  // [kTileRing] kReaders arrivals
+  int4* tile;       // [kTileRing]
+};
+__device__ __forceinline__ bool ring_put(const TileRing& r, uint32_t n, const Tile& c, volatile int* abort,
+                                         uint32_t* status) {
+  const uint32_t slot = n % kTileRing;
+  if (!mbar_wait(&r.empty[slot], ((n / kTileRing) & 1u) ^ 1u, abort, status)) return false;
+  volatile int* w = reinterpret_cast<volatile int*>(&r.tile[slot]);
+  w[0] = c.rows | (c.alone ? 1 << 8 : 0) | (c.last ? 1 << 9 : 0);
+  w[1] = c.e;
+  w[2] = c.j;
+  w[3] = c.row0;
+  mbar_arrive(&r.full[slot]);
+  return true;
+}
+// The n-th tile of this CTA, false when the wait gave up; the caller arrives on
+// empty[n % kTileRing] afterwards.
+__device__ __forceinline__ bool ring_get(const TileRing& r, uint32_t n, Tile& c, volatile int* abort,
+                                         uint32_t* status) {
+  const uint32_t slot = n % kTileRing;
+  if (!mbar_wait(&r.full[slot], (n / kTileRing) & 1u, abort, status)) return false;
+  const volatile int* w = reinterpret_cast<const volatile int*>(&r.tile[slot]);
+  const int x = w[0];
+  c.rows = x & 255;
+  c.alone = (x >> 8) & 1;
+  c.last = (x >> 9) & 1;
+  c.e = w[1];
+  c.j = w[2];
+  c.row0 = w[3];
+  return true;
+}
+
+// Tiles are drawn from a counter in the workspace, in order: CTA b starts on tile
+// b, and its scheduler warp (a lane knowing eight experts) draws every later
+// index, finds the tile and hands it to the other roles.  Tile t: expert, column
+// tile, window, so that the windows sharing a weight tile are neighbours; all of an
+// expert's windows but the last have kTok rows.  The CTA that stops drawing last
+// clears the counter, and knows whether the launch started from a cleared one:
+// the word behind it counts the CTAs that have stopped (bits 0-9), sums their
+// indexes plus one (bits 10-29), and gets bit 30 from the one that drew 0.  With
+// anything else in either word the sum comes out wrong (tiles may have been left
+// out): an error.
+constexpr int kMaxGrid = 1023;
+__device__ __forceinline__ uint32_t stopped(uint32_t ctas, uint32_t index_sum, bool drew_zero) {
+  return ctas | (index_sum << 10) | (drew_zero ? 1u << 30 : 0u);
+}
+__device__ __forceinline__ void schedule(const TileRing& ring, int E, int NT, int64_t max_rows,
+                                         const int32_t* off_pad, const int32_t* counts, int lane,
+                                         volatile int* abort, uint32_t* status, uint32_t* sched) {
+  constexpr int per = kMaxExperts / 32;
+  const uint32_t all = 0xffffffffu;
+  int cnt[per], off[per];
+  int sum = 0;
+#pragma unroll
+  for (int i = 0; i < per; ++i) {
+    const int e = lane * per + i;
+    cnt[i] = off[i] = 0;
+    if (e < E) {
+      const int c = __ldcg(counts + e);
+      const int64_t first = __ldcg(off_pad + e), end = __ldcg(off_pad + e + 1);
+      // an expert whose rows do not lie inside its 128-row blocks and the buffers
+      // gets no tiles
+      if (c >= 0 && first >= 0 && (first & 127) == 0 && (end & 127) == 0 && first + c <= end && end <= max_rows) {
+        cnt[i] = c;
+        off[i] = static_cast<int>(first);
+      } else {
+        record_status(status, kStatusBounds);
+      }
+    }
+    sum += (cnt[i] + kTok - 1) / kTok;
+  }
+  int incl = sum;  // windows up to this lane's last expert
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(all, incl, o);
+    if (lane >= o) incl += y;
+  }
+  const int windows = __shfl_sync(all, incl, 31);
+  // windows of counts that fit the buffers (an expert has at most one that is not full)
+  const bool fits = static_cast<int64_t>(windows - E) * kTok <= max_rows;
+  if (!fits && lane == 0) record_status(status, kStatusBounds);
+  const int total = fits ? NT * windows : 0;
+
+  uint32_t drawn = 0, later = 0;  // two draws on their way
+  if (lane == 0) {
+    drawn = atomicAdd(sched, 1u);
+    later = atomicAdd(sched, 1u);
+  }
+  bool drew_zero = false;
+  int tile = blockIdx.x;
+  for (uint32_t n = 0;; ++n) {
+    Tile c{0, 0, 0, 0, false, tile >= total};
+    int owner = 0;  // the lane that knows the tile's expert
+    if (tile < total) {
+      const int q = tile / NT;  // (all column tiles of a window's expert lie together)
+      owner = __ffs(__ballot_sync(all, incl > q)) - 1;
+      int base = incl - sum;  // windows before this lane's first expert
+#pragma unroll
+      for (int i = 0; i < per; ++i) {
+        const int nw = (cnt[i] + kTok - 1) / kTok;
+        if (q >= base && q < base + nw) {
+          const int local = tile - NT * base;
+          c.e = lane * per + i;
+          c.j = local / nw;
+          const int w = local - c.j * nw;
+          c.row0 = off[i] + kTok * w;
+          c.rows = min(kTok, cnt[i] - kTok * w);
+          c.alone = nw == 1;
+        }
+        base += nw;
+      }
+    }
+    bool put = true;
+    if (lane == owner) put = ring_put(ring, n, c, abort, status);
+    if (__any_sync(all, !put) || tile >= total) break;
+    const uint32_t d = __shfl_sync(all, drawn, 0);
+    drew_zero |= d == 0u;
+    // a cleared counter gives less than total + 3 grids here
+    const uint64_t next = static_cast<uint64_t>(gridDim.x) + d;
+    if (next >= static_cast<uint64_t>(total) + 3u * gridDim.x && lane == 0) record_status(status, kStatusBounds);
+    tile = next < static_cast<uint64_t>(total) ? static_cast<int>(next) : total;
+    drawn = later;
+    if (lane == 0) later = atomicAdd(sched, 1u);
+  }
+  if (lane == 0) {
+    drew_zero |= drawn == 0u || later == 0u;
+    __threadfence();
+    const uint32_t mine = stopped(1u, blockIdx.x + 1u, drew_zero);
+    const uint32_t seen = atomicAdd(sched + 1, mine) + mine;
+    if ((seen & 0x3FFu) == gridDim.x) {  // every CTA has drawn its last index
+      if (seen != stopped(gridDim.x, gridDim.x * (gridDim.x + 1u) / 2u, true)) record_status(status, kStatusBounds);
+      atomicExch(sched, 0u);
+      atomicExch(sched + 1, 0u);
+    }
+  }
+}
+
+// OR-vote over the epilogue's threads (named barrier 2).
+__device__ __forceinline__ bool vote_any(bool flag) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred pi, po;\n\t"
+      "setp.ne.u32 pi, %1, 0;\n\t"
+      "bar.red.or.pred po, 2, %2, pi;\n\t"
+      "selp.u32 %0, 1, 0, po;\n\t}"
+      : "=r"(r)
+      : "r"(flag ? 1u : 0u), "n"(kEpiWarps * 32)
+      : "memory");
+  return r != 0;
+}
+
+// silu(g) * u with the sigmoid on the SFU.  The exponent g log2 e is rounded
+// before ex2, so below zero the relative error grows with |g|, to about
+// |g| 2^-24 and a few ulps (2^-17 at g = -88, below which the result is the
+// limit 0): far under h's rounding to bf16, 2^-9.
+__device__ __forceinline__ float silu_mul(float g, float u) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  return g * r * u;
+}
+
 template <bool kUp>
 __global__ void __launch_bounds__(kThreads, 1)
     int8_gemm_kernel(const __grid_constant__ Int8Maps maps, const float* __restrict__ sT,
@@ -136,12 +304,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* tfull = used + kSteps;
   uint64_t* tempty = tfull + 1;
   uint64_t* drain = tfull + 2;
-  const TileRing ring{tfull + 3, tfull + 3 + kTileRing, reinterpret_cast<volatile int32_t*>(smem + kTileOff)};
+  const TileRing ring{tfull + 3, tfull + 3 + kTileRing, reinterpret_cast<int4*>(smem + kRingOff)};
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kSlotOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int32_t* s_win = reinterpret_cast<int32_t*>(smem + kWinOff);
-  int32_t* s_cnt = reinterpret_cast<int32_t*>(smem + kCntOff);
-  int32_t* s_offp = reinterpret_cast<int32_t*>(smem + kOffpOff);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
 
@@ -173,20 +338,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
-  pdl_wait();
-  if (warp == 2) {
-    scan_windows<kTok>(counts, E, max_rows, s_win, s_cnt, lane, status);
-  } else if (warp == 3) {
-    for (int e = lane; e <= E; e += 32) s_offp[e] = __ldcg(off_pad + e);
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  // windows of counts that fit the buffers (an expert has at most one that is not full)
-  const bool fits = static_cast<int64_t>(s_win[E] - E) * kTok <= max_rows;
-  if (!fits && threadIdx.x == 0) record_status(status, kStatusBounds);
-  const int total = fits ? NT * s_win[E] : 0;
+  pdl_wait();
   const int KS = K / kStageK;
 
   if (warp < kFirstEpi) {
@@ -196,21 +352,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (elect_one_sync()) {
         const uint64_t pol_keep = policy_evict_last();
         uint32_t it = 0;
-        int tile = blockIdx.x;
-        bool drew_zero = false;
-        bool stop = !ring_put(ring, 0, tile, abort_flag, status);
-        for (uint32_t n = 0; !stop && tile < total; ++n) {
-          const uint32_t drawn = atomicAdd(sched, 1u);  // the next tile: needed after this one's loads
-          const Win c = decode<kTok>(tile, NT, E, s_win, s_offp, s_cnt, max_rows);
-          if (!c.ok) record_status(status, kStatusBounds);
+        bool stop = false;
+        Tile c;
+        for (uint32_t n = 0; !stop && ring_get(ring, n, c, abort_flag, status) && !c.last; ++n) {
+          mbar_arrive(&ring.empty[n % kTileRing]);
           // a one-window expert reads this weight tile once
-          const uint64_t pol_w = s_win[c.e + 1] - s_win[c.e] == 1 ? policy_evict_first() : pol_keep;
+          const uint64_t pol_w = c.alone ? policy_evict_first() : pol_keep;
           const int n0 = c.j * (kUp ? 128 : 256);
           const bool two = kUp || n0 + 128 < N_out;  // the second weight block exists
           const int w_row = c.e * N_out + n0;        // E * N_out < 2^31
           const int pick = c.rows <= 32 ? 0 : c.rows <= 64 ? 1 : 2;  // the smallest box that holds the window
           const uint32_t bytes = (two ? 2u : 1u) * kWBytes + int8_token_box(pick) * kStageK;
-          for (int ks = 0; c.ok && ks < KS; ++ks, ++it) {
+          for (int ks = 0; ks < KS; ++ks, ++it) {
             const uint32_t s = it % kStages;
             if (!mbar_wait(&empty[s], ((it / kStages) & 1u) ^ 1u, abort_flag, status)) {
               stop = true;
@@ -220,25 +373,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint8_t* st = smem + s * kStageBytes;
             const int kx = ks * kStageK;
             tma_load_2d(st, &maps.w0, &full[s], kx, w_row, pol_w);
-            if (two) tma_load_2d(st + kWBytes, kUp ? &maps.w1 : &maps.w0, &full[s], kx, kUp ? w_row : w_row + 128, pol_w);
+            if (two)
+              tma_load_2d(st + kWBytes, kUp ? &maps.w1 : &maps.w0, &full[s], kx, kUp ? w_row : w_row + 128, pol_w);
             tma_load_2d(st + 2 * kWBytes, &maps.t[pick], &full[s], kx, c.row0, pol_keep);
           }
-          drew_zero |= drawn == 0u;
-          if (stop) break;
-          // a cleared counter gives at most total + grid - 1 here
-          const uint64_t next = static_cast<uint64_t>(gridDim.x) + drawn;
-          tile = next < static_cast<uint64_t>(total) + gridDim.x ? static_cast<int>(next) : total;
-          if (static_cast<uint64_t>(tile) != next) record_status(status, kStatusBounds);
-          stop = !ring_put(ring, n + 1, tile, abort_flag, status);
-        }
-        __threadfence();
-        const uint32_t mine = stopped(1u, blockIdx.x + 1u, drew_zero);
-        const uint32_t seen = atomicAdd(sched + 1, mine) + mine;
-        if ((seen & 0x3FFu) == gridDim.x) {  // every CTA has drawn its last index
-          const uint32_t clean = stopped(gridDim.x, gridDim.x * (gridDim.x + 1u) / 2u, total > 0);
-          if (seen != clean) record_status(status, kStatusBounds);
-          atomicExch(sched, 0u);
-          atomicExch(sched + 1, 0u);
         }
         // every stage used must have been read before the CTA may exit
         const uint32_t nst = it < kStages ? it : kStages;
@@ -255,12 +393,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t it = 0;
         uint32_t tcount = 0;
         bool stop = false;
-        for (uint32_t n = 0; !stop; ++n) {
-          const int tile = ring_take(ring, n, abort_flag, status);
-          if (tile < 0 || tile >= total) break;
+        Tile c;
+        for (uint32_t n = 0; !stop && ring_get(ring, n, c, abort_flag, status) && !c.last; ++n) {
           mbar_arrive(&ring.empty[n % kTileRing]);
-          const Win c = decode<kTok>(tile, NT, E, s_win, s_offp, s_cnt, max_rows);
-          if (!c.ok) continue;
           const bool two = kUp || c.j * 256 + 128 < N_out;
           // fp16 operands, float32 sums, both with k contiguous, M = 128, N
           const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>((c.rows + 15) / 16 * 2) << 17) | ((128u >> 4) << 24);
@@ -275,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             const uint32_t sb = smem_u32(smem + kStepOff + s * kStepBytes);
             const uint32_t ta = tmem + kWideCol + s * 2 * kWideBlockCols;
-  #pragma unroll
+#pragma unroll
             for (int kk = 0; kk < kStepK / 16; ++kk) {
               const uint64_t bd = smem_desc(sb + kk * 32, 16, 1024, kSwizzle128B);
               const uint32_t acc = (ks | kk) != 0 ? 1u : 0u;
@@ -293,6 +428,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait(drain, 0, &no_abort, status);
       }
       __syncwarp();
+    } else if (warp == 2) {
+      schedule(ring, E, NT, max_rows, off_pad, counts, lane, abort_flag, status, sched);
+      __syncwarp();
     }
   } else if (warp < kFirstWide) {
     more_registers<kEpiRegs>();
@@ -307,12 +445,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool leader = q == 0 && lane == 0;
     uint32_t tcount = 0;
     for (uint32_t n = 0;; ++n) {
-      const int tile = ring_take(ring, n, abort_flag, status);
+      Tile c{};
+      bool ok = ring_get(ring, n, c, abort_flag, status);
       __syncwarp();
       if (lane == 0) mbar_arrive(&ring.empty[n % kTileRing]);
-      bool ok = tile >= 0;
-      const Win c = decode<kTok>(ok && tile < total ? tile : 0, NT, E, s_win, s_offp, s_cnt, max_rows);
-      const bool real = ok && tile < total && c.ok;
+      const bool real = ok && !c.last;
       const int n0 = c.j * (kUp ? 128 : 256);
       const bool two = kUp || n0 + 128 < N_out;
       // the scales of this thread's columns 32 q + 8 x + lane / 4 of both blocks
@@ -326,9 +463,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ok = mbar_wait(tfull, tcount & 1u, abort_flag, status);
       }
-      if (vote_any<kEpiWarps * 32>(!ok)) break;  // every warp gives up together (they share barriers)
-      if (tile >= total) break;
-      if (!c.ok) continue;
+      if (vote_any(!ok)) break;  // every warp gives up together (they share barriers)
+      if (c.last) break;
       ++tcount;
       tc_fence_after();
       const int pieces = (c.rows + 31) / 32;
@@ -426,13 +562,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t it = 0;
     bool stop = false;
     for (uint32_t n = 0; !stop; ++n) {
-      const int tile = ring_take(ring, n, abort_flag, status);
-      __syncwarp();
-      if (__any_sync(0xffffffffu, tile < 0)) break;
+      Tile c{};
+      const bool got = ring_get(ring, n, c, abort_flag, status);
+      if (__any_sync(0xffffffffu, !got) || c.last) break;
       if (lane == 0) mbar_arrive(&ring.empty[n % kTileRing]);
-      if (tile >= total) break;
-      const Win c = decode<kTok>(tile, NT, E, s_win, s_offp, s_cnt, max_rows);
-      if (!c.ok) continue;
       const bool two = kUp || c.j * 256 + 128 < N_out;
       const bool rows_here = 32 * (w & 3) < (c.rows + 15) / 16 * 16;
       for (int ks = 0; ks < KS && !stop; ++ks, ++it) {
