@@ -270,10 +270,14 @@ __device__ __forceinline__ void cluster_sync_all() {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_cluster) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
 }
-// The same without release: for an arrival that hands over no memory writes
-// (a release waits for the thread's own stores in flight).
-__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar_cluster) {
-  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
+// An arrival on a barrier of either CTA of a pair that orders this thread's earlier
+// accesses at CTA scope: for handing over what stays in this CTA's own SM (shared
+// memory and TMEM that its tensor core reads for the pair, an accumulator or a
+// slot that has been read).  A release at cluster scope also waits for the
+// thread's stores on their way to memory, over a thousand cycles where a kernel
+// writes a lot.
+__device__ __forceinline__ void mbar_arrive_peer(uint32_t bar_cluster) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
 }
 
 // ------------------------------------------------------------------ tcgen05

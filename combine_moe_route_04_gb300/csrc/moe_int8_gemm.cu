@@ -7,19 +7,20 @@
 // holds them exactly (sm_103a has no integer MMA in tcgen05): their products are
 // exact, and float32 sums of them stay exact while they are below 2^24.
 //
-// A tile is one window of up to 128 of an expert's rows times two blocks of 128
-// output columns (up: the same columns of gate and of up; down: 256 neighbouring
-// columns).  The weights are the M = 128 operand, the rows the N operand.  TMA
-// brings the codes in stages of 128 k.  Two groups of eight warps widen them, each
-// one half of every stage, a step of 64 k: the weights into TMEM, from where the
-// MMA reads its first operand (lane = weight row, two k per column: a thread widens
-// its own row), the rows into shared memory in the swizzle of the second operand.
-// TMEM holds two 128 x 128 accumulators and kSteps such steps of both blocks.
+// A cluster of two CTAs takes a tile: one window of up to 128 of an expert's rows
+// times 256 output columns of gate and of up, or 512 of down.  The weights are the
+// M = 256 operand (cta_group::2), two blocks of 128 rows in each CTA; the rows are
+// the N operand, half of them supplied by either CTA.  TMA brings the codes in
+// stages of 128 k.  In each CTA two groups of eight warps widen them, each one half
+// of every stage, a step of 64 k: the weights into TMEM, from where the MMA reads
+// its first operand (lane = weight row, two k per column: a thread widens its own
+// row), the CTA's half of the rows into shared memory in the swizzle of the second
+// operand.  TMEM holds two accumulators of 128 columns and kSteps such steps of
+// both blocks.
 //
-// What bounds it with many rows is the widening: a step is 512 cycles of MMAs and
-// about 440 of instruction issue, and a group needs some 800 from its wait to its
-// arrival (one group alone: 1040 cycles a step, up product of 2048 tokens and 64
-// experts of 4096 x 1536 444 us, of 16384 tokens and 128 experts 2914 us).
+// What bounds it with many rows is shared memory: codes in, out and widened rows
+// in, and the second operand, 64 KB for a step's 512 cycles of MMAs (one CTA alone
+// moves 96 KB, and widens twice the rows).
 #include <cstdint>
 #include <mutex>
 
@@ -34,14 +35,16 @@ namespace {
 
 constexpr int kMaxExperts = 256;
 constexpr int kTok = 128;                 // most rows of a window
+constexpr int kHalfTok = kTok / 2;        // of which a CTA supplies half
 constexpr int kStageK = 128;              // reduction elements (bytes) per stage of codes
 constexpr int kStepK = 64;                // and per widened step
-constexpr int kStages = 3;
+constexpr int kStages = 4;
 constexpr int kSteps = 4;
 constexpr int kWBytes = 128 * kStageK;    // codes of one block of 128 weight rows
-constexpr int kStageBytes = 2 * kWBytes + kTok * kStageK;
-constexpr int kStepBytes = kTok * kStepK * 2;  // widened rows
-// Warps: loads, MMAs, scheduler (and an idle one); epilogue; widening: whole groups
+constexpr int kStageBytes = 2 * kWBytes + kHalfTok * kStageK;
+constexpr int kStepBytes = kHalfTok * kStepK * 2;  // widened rows
+// Warps: loads, MMAs and scheduler (both in CTA 0 alone) and an idle one; epilogue;
+// widening: whole groups
 // of four warps, which share out the registers: kLaunchRegs a thread at launch,
 // then what each group asks for.
 constexpr int kFirstEpi = 4;
@@ -55,7 +58,7 @@ constexpr int kLaunchRegs = 72, kControlRegs = 56, kEpiRegs = 112, kWideRegs = 5
 static_assert(kThreads * kLaunchRegs <= 65536 && kFirstEpi * kControlRegs + kEpiWarps * kEpiRegs +
                   kWideWarps * kWideRegs <= kThreads / 32 * kLaunchRegs, "registers");
 constexpr int kTileRing = 4;                          // tiles on their way from the scheduler
-constexpr int kReaders = 2 + kEpiWarps + kWideWarps;  // of a tile
+constexpr int kReaders = 3 + 2 * (kEpiWarps + kWideWarps);  // of a tile, in both CTAs
 // TMEM columns: the accumulators, then the widened weights of each step
 constexpr uint32_t kAcc1 = kTok;
 constexpr uint32_t kWideCol = 2 * kTok;
@@ -80,12 +83,12 @@ __device__ __forceinline__ void fewer_registers() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
-// D(tmem) (+)= A(tmem) B(smem), fp16 with float32 sums, 16 deep.
+// D(tmem) (+)= A(tmem) B(smem) over both CTAs, fp16 with float32 sums, 16 deep.
 __device__ __forceinline__ void mma_f16_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
       "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
 }
@@ -126,28 +129,35 @@ struct Tile {
   bool last;             // no tile: the roles end
 };
 struct TileRing {
-  uint64_t* full;   // [kTileRing] one arrival (the scheduler)
-  uint64_t* empty;  // [kTileRing] kReaders arrivals
-  int4* tile;       // [kTileRing]
+  uint64_t* full;   // [kTileRing], this CTA: one arrival (the scheduler)
+  uint64_t* empty;  // [kTileRing], used in CTA 0: kReaders arrivals
+  int4* tile;       // [kTileRing], this CTA
 };
 __device__ __forceinline__ bool ring_put(const TileRing& r, uint32_t n, const Tile& c, volatile int* abort,
                                          uint32_t* status) {
   const uint32_t slot = n % kTileRing;
-  if (!mbar_wait(&r.empty[slot], ((n / kTileRing) & 1u) ^ 1u, abort, status)) return false;
+  if (!mbar_wait<true>(&r.empty[slot], ((n / kTileRing) & 1u) ^ 1u, abort, status)) return false;
   volatile int* w = reinterpret_cast<volatile int*>(&r.tile[slot]);
-  w[0] = c.rows | (c.alone ? 1 << 8 : 0) | (c.last ? 1 << 9 : 0);
+  const int x = c.rows | (c.alone ? 1 << 8 : 0) | (c.last ? 1 << 9 : 0);
+  w[0] = x;
   w[1] = c.e;
   w[2] = c.j;
   w[3] = c.row0;
   mbar_arrive(&r.full[slot]);
+  asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(map_to_cta(&r.tile[slot], 1)), "r"(x),
+               "r"(c.e), "r"(c.j), "r"(c.row0)
+               : "memory");
+  mbar_arrive_cluster(map_to_cta(&r.full[slot], 1));
   return true;
 }
-// The n-th tile of this CTA, false when the wait gave up; the caller arrives on
-// empty[n % kTileRing] afterwards.
-__device__ __forceinline__ bool ring_get(const TileRing& r, uint32_t n, Tile& c, volatile int* abort,
+// The n-th tile of this cluster, false when the wait gave up.
+__device__ __forceinline__ bool ring_get(const TileRing& r, uint32_t n, uint32_t rank, Tile& c, volatile int* abort,
                                          uint32_t* status) {
   const uint32_t slot = n % kTileRing;
-  if (!mbar_wait(&r.full[slot], (n / kTileRing) & 1u, abort, status)) return false;
+  const uint32_t ph = (n / kTileRing) & 1u;
+  if (!(rank == 0 ? mbar_wait<false>(&r.full[slot], ph, abort, status)
+                  : mbar_wait<true>(&r.full[slot], ph, abort, status)))
+    return false;
   const volatile int* w = reinterpret_cast<const volatile int*>(&r.tile[slot]);
   const int x = w[0];
   c.rows = x & 255;
@@ -159,23 +169,30 @@ __device__ __forceinline__ bool ring_get(const TileRing& r, uint32_t n, Tile& c,
   return true;
 }
 
-// Tiles are drawn from a counter in the workspace, in order: CTA b starts on tile
-// b, and its scheduler warp (a lane knowing eight experts) draws every later
-// index, finds the tile and hands it to the other roles.  Tile t: expert, column
-// tile, window, so that the windows sharing a weight tile are neighbours; all of an
-// expert's windows but the last have kTok rows.  The CTA that stops drawing last
-// clears the counter, and knows whether the launch started from a cleared one:
-// the word behind it counts the CTAs that have stopped (bits 0-9), sums their
-// indexes plus one (bits 10-29), and gets bit 30 from the one that drew 0.  With
-// anything else in either word the sum comes out wrong (tiles may have been left
-// out): an error.
-constexpr int kMaxGrid = 1023;
-__device__ __forceinline__ uint32_t stopped(uint32_t ctas, uint32_t index_sum, bool drew_zero) {
-  return ctas | (index_sum << 10) | (drew_zero ? 1u << 30 : 0u);
+__device__ __forceinline__ void ring_release(const TileRing& r, uint32_t n, uint32_t rank, uint32_t empty0) {
+  const uint32_t slot = n % kTileRing;
+  if (rank == 0) mbar_arrive(&r.empty[slot]);
+  else mbar_arrive_peer(empty0 + 8u * slot);
+}
+
+// Tiles are drawn from a counter in the workspace, in order: cluster b starts on
+// tile b, and a warp of its CTA 0 (a lane knowing eight experts) draws every later
+// index, finds the tile and hands it to all roles of both CTAs.  Tile t: expert,
+// column tile, window, so that the windows sharing a weight tile are neighbours;
+// all of an expert's windows but the last have kTok rows.  The cluster that stops
+// drawing last clears the counter, and knows whether the launch started from a
+// cleared one: the word behind it counts the clusters that have stopped (bits
+// 0-9), sums their indexes plus one (bits 10-29), and gets bit 30 from the one
+// that drew 0.  With anything else in either word the sum comes out wrong (tiles
+// may have been left out): an error.
+constexpr int kMaxClusters = 1023;
+__device__ __forceinline__ uint32_t stopped(uint32_t clusters, uint32_t index_sum, bool drew_zero) {
+  return clusters | (index_sum << 10) | (drew_zero ? 1u << 30 : 0u);
 }
 __device__ __forceinline__ void schedule(const TileRing& ring, int E, int NT, int64_t max_rows,
-                                         const int32_t* off_pad, const int32_t* counts, int lane,
-                                         volatile int* abort, uint32_t* status, uint32_t* sched) {
+                                         const int32_t* off_pad, const int32_t* counts, uint32_t cluster,
+                                         uint32_t nclusters, int lane, volatile int* abort, uint32_t* status,
+                                         uint32_t* sched) {
   constexpr int per = kMaxExperts / 32;
   const uint32_t all = 0xffffffffu;
   int cnt[per], off[per];
@@ -216,7 +233,7 @@ __device__ __forceinline__ void schedule(const TileRing& ring, int E, int NT, in
     later = atomicAdd(sched, 1u);
   }
   bool drew_zero = false;
-  int tile = blockIdx.x;
+  int tile = static_cast<int>(cluster);
   for (uint32_t n = 0;; ++n) {
     Tile c{0, 0, 0, 0, false, tile >= total};
     int owner = 0;  // the lane that knows the tile's expert
@@ -244,9 +261,9 @@ __device__ __forceinline__ void schedule(const TileRing& ring, int E, int NT, in
     if (__any_sync(all, !put) || tile >= total) break;
     const uint32_t d = __shfl_sync(all, drawn, 0);
     drew_zero |= d == 0u;
-    // a cleared counter gives less than total + 3 grids here
-    const uint64_t next = static_cast<uint64_t>(gridDim.x) + d;
-    if (next >= static_cast<uint64_t>(total) + 3u * gridDim.x && lane == 0) record_status(status, kStatusBounds);
+    // a cleared counter gives less than total + 3 clusters here
+    const uint64_t next = static_cast<uint64_t>(nclusters) + d;
+    if (next >= static_cast<uint64_t>(total) + 3u * nclusters && lane == 0) record_status(status, kStatusBounds);
     tile = next < static_cast<uint64_t>(total) ? static_cast<int>(next) : total;
     drawn = later;
     if (lane == 0) later = atomicAdd(sched, 1u);
@@ -254,10 +271,10 @@ __device__ __forceinline__ void schedule(const TileRing& ring, int E, int NT, in
   if (lane == 0) {
     drew_zero |= drawn == 0u || later == 0u;
     __threadfence();
-    const uint32_t mine = stopped(1u, blockIdx.x + 1u, drew_zero);
+    const uint32_t mine = stopped(1u, cluster + 1u, drew_zero);
     const uint32_t seen = atomicAdd(sched + 1, mine) + mine;
-    if ((seen & 0x3FFu) == gridDim.x) {  // every CTA has drawn its last index
-      if (seen != stopped(gridDim.x, gridDim.x * (gridDim.x + 1u) / 2u, true)) record_status(status, kStatusBounds);
+    if ((seen & 0x3FFu) == nclusters) {  // every cluster has drawn its last index
+      if (seen != stopped(nclusters, nclusters * (nclusters + 1u) / 2u, true)) record_status(status, kStatusBounds);
       atomicExch(sched, 0u);
       atomicExch(sched + 1, 0u);
     }
@@ -295,11 +312,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                      const float* __restrict__ sW0, const float* __restrict__ sW1, uint16_t* __restrict__ D,
                      const int32_t* __restrict__ off_pad, const int32_t* __restrict__ counts, int E, int K, int N_out,
                      int NT, int64_t max_rows, uint32_t* __restrict__ status, uint32_t* __restrict__ sched) {
+  constexpr int kTileCols = kUp ? 256 : 512;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + kBarOff);
   uint64_t* empty = full + kStages;
-  uint64_t* wide = empty + kStages;   // a step is widened
+  uint64_t* wide = empty + kStages;   // used in CTA 0: both CTAs have widened a step
   uint64_t* used = wide + kSteps;     // its MMAs are done
   uint64_t* tfull = used + kSteps;
   uint64_t* tempty = tfull + 1;
@@ -309,6 +327,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();  // 0: schedules and issues the MMAs
+  // the first columns of the CTA's two blocks in a tile that starts at n0
+  auto col_of = [&](int n0, int block) {
+    return n0 + 128 * static_cast<int>(rank) + (kUp ? 0 : 256 * block);
+  };
 
   pdl_launch_dependents();
   if (threadIdx.x == 0) {
@@ -317,11 +340,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&empty[s], kWideWarps);
     }
     for (int s = 0; s < kSteps; ++s) {
-      mbar_init(&wide[s], kWideGroup);
+      mbar_init(&wide[s], 2 * kWideGroup);
       mbar_init(&used[s], 1);
     }
     mbar_init(tfull, 1);
-    mbar_init(tempty, kEpiWarps);
+    mbar_init(tempty, 2 * kEpiWarps);
     mbar_init(drain, 1);
     for (int i = 0; i < kTileRing; ++i) {
       mbar_init(&ring.full[i], 1);
@@ -334,9 +357,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tmap(&maps.w1);
     prefetch_tmap(&maps.out);
   }
+  cluster_sync_all();  // both CTAs' barriers exist before any cross-CTA arrival
   if (warp == 1) {
-    tmem_alloc(tmem_slot, 512);
-    tmem_relinquish();
+    tmem_alloc_pair(tmem_slot, 512);
+    tmem_relinquish_pair();
   }
   tc_fence_before();
   __syncthreads();
@@ -344,6 +368,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   pdl_wait();
   const int KS = K / kStageK;
+  const uint32_t wide0 = map_to_cta(wide, 0);
+  const uint32_t tempty0 = map_to_cta(tempty, 0);
+  const uint32_t rempty0 = map_to_cta(ring.empty, 0);
 
   if (warp < kFirstEpi) {
     fewer_registers<kControlRegs>();
@@ -354,15 +381,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t it = 0;
         bool stop = false;
         Tile c;
-        for (uint32_t n = 0; !stop && ring_get(ring, n, c, abort_flag, status) && !c.last; ++n) {
-          mbar_arrive(&ring.empty[n % kTileRing]);
+        for (uint32_t n = 0; !stop && ring_get(ring, n, rank, c, abort_flag, status) && !c.last; ++n) {
+          ring_release(ring, n, rank, rempty0);
           // a one-window expert reads this weight tile once
           const uint64_t pol_w = c.alone ? policy_evict_first() : pol_keep;
-          const int n0 = c.j * (kUp ? 128 : 256);
-          const bool two = kUp || n0 + 128 < N_out;  // the second weight block exists
-          const int w_row = c.e * N_out + n0;        // E * N_out < 2^31
-          const int pick = c.rows <= 32 ? 0 : c.rows <= 64 ? 1 : 2;  // the smallest box that holds the window
-          const uint32_t bytes = (two ? 2u : 1u) * kWBytes + int8_token_box(pick) * kStageK;
+          const int c0 = col_of(c.j * kTileCols, 0), c1 = col_of(c.j * kTileCols, 1);
+          const bool has0 = c0 < N_out, has1 = c1 < N_out;  // the blocks exist (columns are multiples of 128)
+          const int w_row = c.e * N_out;                    // E * N_out < 2^31
+          const int mine = (c.rows + 15) / 16 * 8;          // rows that this CTA supplies
+          const int row = c.row0 + mine * static_cast<int>(rank);
+          const int pick = mine <= 16 ? 0 : mine <= 32 ? 1 : 2;  // the smallest box that holds them
+          const uint32_t bytes = (has0 ? kWBytes : 0) + (has1 ? kWBytes : 0) + int8_token_box(pick) * kStageK;
           for (int ks = 0; ks < KS; ++ks, ++it) {
             const uint32_t s = it % kStages;
             if (!mbar_wait(&empty[s], ((it / kStages) & 1u) ^ 1u, abort_flag, status)) {
@@ -372,10 +401,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive_expect_tx(&full[s], bytes);
             uint8_t* st = smem + s * kStageBytes;
             const int kx = ks * kStageK;
-            tma_load_2d(st, &maps.w0, &full[s], kx, w_row, pol_w);
-            if (two)
-              tma_load_2d(st + kWBytes, kUp ? &maps.w1 : &maps.w0, &full[s], kx, kUp ? w_row : w_row + 128, pol_w);
-            tma_load_2d(st + 2 * kWBytes, &maps.t[pick], &full[s], kx, c.row0, pol_keep);
+            if (has0) tma_load_2d(st, &maps.w0, &full[s], kx, w_row + c0, pol_w);
+            if (has1) tma_load_2d(st + kWBytes, kUp ? &maps.w1 : &maps.w0, &full[s], kx, w_row + c1, pol_w);
+            tma_load_2d(st + 2 * kWBytes, &maps.t[pick], &full[s], kx, row, pol_keep);
           }
         }
         // every stage used must have been read before the CTA may exit
@@ -388,22 +416,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     } else if (warp == 1) {
-      // ---------------------------------------------------------- MMAs
-      if (elect_one_sync()) {
+      // ---------------------------------------------------------- MMAs (CTA 0)
+      if (rank == 0 && elect_one_sync()) {
         uint32_t it = 0;
         uint32_t tcount = 0;
         bool stop = false;
         Tile c;
-        for (uint32_t n = 0; !stop && ring_get(ring, n, c, abort_flag, status) && !c.last; ++n) {
-          mbar_arrive(&ring.empty[n % kTileRing]);
-          const bool two = kUp || c.j * 256 + 128 < N_out;
-          // fp16 operands, float32 sums, both with k contiguous, M = 128, N
-          const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>((c.rows + 15) / 16 * 2) << 17) | ((128u >> 4) << 24);
+        for (uint32_t n = 0; !stop && ring_get(ring, n, rank, c, abort_flag, status) && !c.last; ++n) {
+          ring_release(ring, n, rank, rempty0);
+          const bool two = col_of(c.j * kTileCols, 1) < N_out;  // a second block in either CTA
+          // fp16 operands, float32 sums, both with k contiguous, M = 256, N
+          const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>((c.rows + 15) / 16 * 2) << 17) | ((256u >> 4) << 24);
           if (!mbar_wait(tempty, (tcount & 1u) ^ 1u, abort_flag, status)) break;
           tc_fence_after();
           for (int ks = 0; ks < 2 * KS; ++ks, ++it) {
             const uint32_t s = it % kSteps;
-            if (!mbar_wait(&wide[s], (it / kSteps) & 1u, abort_flag, status)) {
+            if (!mbar_wait<true>(&wide[s], (it / kSteps) & 1u, abort_flag, status)) {
               stop = true;
               break;
             }
@@ -417,19 +445,19 @@ __global__ void __launch_bounds__(kThreads, 1)
               mma_f16_tmem(tmem, ta + 8 * kk, bd, idesc, acc);
               if (two) mma_f16_tmem(tmem + kAcc1, ta + kWideBlockCols + 8 * kk, bd, idesc, acc);
             }
-            tc_commit(&used[s]);
+            tc_commit_pair(&used[s], 0x3);
           }
           if (stop) break;
-          tc_commit(tfull);
+          tc_commit_pair(tfull, 0x3);
           ++tcount;
         }
-        tc_commit(drain);
+        tc_commit_pair(drain, 0x1);
         int no_abort = 0;
         mbar_wait(drain, 0, &no_abort, status);
       }
       __syncwarp();
-    } else if (warp == 2) {
-      schedule(ring, E, NT, max_rows, off_pad, counts, lane, abort_flag, status, sched);
+    } else if (warp == 2 && rank == 0) {
+      schedule(ring, E, NT, max_rows, off_pad, counts, blockIdx.x >> 1, gridDim.x >> 1, lane, abort_flag, status, sched);
       __syncwarp();
     }
   } else if (warp < kFirstWide) {
@@ -446,33 +474,32 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t tcount = 0;
     for (uint32_t n = 0;; ++n) {
       Tile c{};
-      bool ok = ring_get(ring, n, c, abort_flag, status);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ring.empty[n % kTileRing]);
+      bool ok = ring_get(ring, n, rank, c, abort_flag, status);
       const bool real = ok && !c.last;
-      const int n0 = c.j * (kUp ? 128 : 256);
-      const bool two = kUp || n0 + 128 < N_out;
+      const int c0 = col_of(c.j * kTileCols, 0), c1 = col_of(c.j * kTileCols, 1);
+      const bool has0 = c0 < N_out, two = c1 < N_out;
       // the scales of this thread's columns 32 q + 8 x + lane / 4 of both blocks
       float w0[4], w1[4];
       if (real) {
-        const int64_t at = static_cast<int64_t>(c.e) * N_out + n0 + 32 * q + (lane >> 2);
+        const int64_t at = static_cast<int64_t>(c.e) * N_out + 32 * q + (lane >> 2);
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          w0[x] = __ldcg(sW0 + at + 8 * x);
-          w1[x] = two ? __ldcg((kUp ? sW1 : sW0 + 128) + at + 8 * x) : 0.0f;
+          w0[x] = has0 ? __ldcg(sW0 + at + c0 + 8 * x) : 0.0f;
+          w1[x] = two ? __ldcg((kUp ? sW1 : sW0) + at + c1 + 8 * x) : 0.0f;
         }
         ok = mbar_wait(tfull, tcount & 1u, abort_flag, status);
       }
       if (vote_any(!ok)) break;  // every warp gives up together (they share barriers)
       if (c.last) break;
+      if (lane == 0) ring_release(ring, n, rank, rempty0);
       ++tcount;
       tc_fence_after();
-      const int pieces = (c.rows + 31) / 32;
+      const int pieces = has0 ? (c.rows + 31) / 32 : 0;
       const int mine = pieces > turn ? (pieces - turn + kTurns - 1) / kTurns : 0;
       auto release = [&]() {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(tempty);
+        if (lane == 0) mbar_arrive_peer(tempty0);
       };
       auto store = [&](int p, int col0, const uint32_t (&a)[16]) {
         const int64_t r0 = c.row0 + (turn + kTurns * p) * 32;
@@ -541,9 +568,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
         if (p < mine) {
-          store(p, n0, pa[p]);
+          store(p, c0, pa[p]);
           if constexpr (!kUp) {
-            if (two) store(p, n0 + 128, pb[p]);
+            if (two) store(p, c1, pb[p]);
           }
         }
       }
@@ -555,19 +582,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------------------------------------------------- widening
     const int w = warp - kFirstWide;
     const int half = w / kWideGroup;  // of each stage
-    const int block = (w >> 2) & 1;   // weight block; of the rows, which half of a step's 16-byte chunks
-    const int q = warp & 3;           // TMEM lane quarter; of the rows, which 32
-    const int wrow = 32 * q + lane, trow = 32 * (w & 3) + lane;
+    const int block = (w >> 2) & 1;   // weight block
+    const int q = warp & 3;           // TMEM lane quarter
+    const int wrow = 32 * q + lane;
+    const int trow = 32 * (w & 1) + lane;  // of the rows: 32 of 64, and 16 k of the step
+    const int ch = (w >> 1) & 3;
     const uint32_t ta = tmem + (static_cast<uint32_t>(32 * q) << 16) + kWideCol + block * kWideBlockCols;
     uint32_t it = 0;
     bool stop = false;
     for (uint32_t n = 0; !stop; ++n) {
       Tile c{};
-      const bool got = ring_get(ring, n, c, abort_flag, status);
+      const bool got = ring_get(ring, n, rank, c, abort_flag, status);
       if (__any_sync(0xffffffffu, !got) || c.last) break;
-      if (lane == 0) mbar_arrive(&ring.empty[n % kTileRing]);
-      const bool two = kUp || c.j * 256 + 128 < N_out;
-      const bool rows_here = 32 * (w & 3) < (c.rows + 15) / 16 * 16;
+      if (lane == 0) ring_release(ring, n, rank, rempty0);
+      const bool block_here = col_of(c.j * kTileCols, block) < N_out;
+      const bool rows_here = 32 * (w & 1) < (c.rows + 15) / 16 * 8;
       for (int ks = 0; ks < KS && !stop; ++ks, ++it) {
         const uint32_t s = it % kStages;
         if (__any_sync(0xffffffffu, !mbar_wait(&full[s], (it / kStages) & 1u, abort_flag, status))) {
@@ -581,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         tc_fence_after();
-        if (block == 0 || two) {
+        if (block_here) {
           uint32_t r[32];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -595,25 +624,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (rows_here) {
           uint8_t* to = smem + kStepOff + d * kStepBytes;
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int ch = 2 * block + i;  // 16 k of the step
-            const uint4 v = *reinterpret_cast<const uint4*>(st + 2 * kWBytes + swizzled(trow, 4 * half + ch));
-            uint4 a, b;
-            widen4(v.x, a.x, a.y);
-            widen4(v.y, a.z, a.w);
-            widen4(v.z, b.x, b.y);
-            widen4(v.w, b.z, b.w);
-            *reinterpret_cast<uint4*>(to + swizzled(trow, 2 * ch)) = a;
-            *reinterpret_cast<uint4*>(to + swizzled(trow, 2 * ch + 1)) = b;
-          }
+          const uint4 v = *reinterpret_cast<const uint4*>(st + 2 * kWBytes + swizzled(trow, 4 * half + ch));
+          uint4 a, b;
+          widen4(v.x, a.x, a.y);
+          widen4(v.y, a.z, a.w);
+          widen4(v.z, b.x, b.y);
+          widen4(v.w, b.z, b.w);
+          *reinterpret_cast<uint4*>(to + swizzled(trow, 2 * ch)) = a;
+          *reinterpret_cast<uint4*>(to + swizzled(trow, 2 * ch + 1)) = b;
           fence_proxy_async_smem();
         }
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&wide[d]);
-        if (lane == 0) mbar_arrive(&empty[s]);
+        if (lane == 0) {
+          mbar_arrive_peer(wide0 + 8u * d);
+          mbar_arrive(&empty[s]);
+        }
       }
     }
     __syncwarp();
@@ -621,10 +648,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
+  cluster_sync_all();
   tc_fence_after();
   if (warp == 1) {
     __syncwarp();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc_pair(tmem, 512);
   }
 }
 
@@ -648,13 +676,29 @@ cudaError_t launch(const moe_shape& s, const Int8Maps& m, const float* sT, const
   }
   const int K = kUp ? s.H : s.I;
   const int N_out = kUp ? s.I : s.H;
-  const int NT = kUp ? N_out / 128 : (N_out + 255) / 256;
+  constexpr int kCols = kUp ? 256 : 512;
+  const int NT = (N_out + kCols - 1) / kCols;
   const int64_t R = static_cast<int64_t>(s.T) * s.k;
   const int64_t max_tiles = (R / kTok + (s.E < R ? s.E : R)) * NT;
-  if (num_sms > kMaxGrid) num_sms = kMaxGrid;
-  const int grid = static_cast<int>(max_tiles < num_sms ? max_tiles : num_sms);
-  return launch_pdl(int8_gemm_kernel<kUp>, dim3(grid), dim3(kThreads), kSmem, st, m, sT, sW0, sW1, D, off_pad, counts,
-                    s.E, K, N_out, NT, max_rows_of(s), status, sched);
+  int64_t clusters = num_sms / 2;
+  if (clusters > kMaxClusters) clusters = kMaxClusters;
+  if (max_tiles < clusters) clusters = max_tiles;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * clusters));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, int8_gemm_kernel<kUp>, m, sT, sW0, sW1, D, off_pad, counts, s.E, K, N_out, NT,
+                            max_rows_of(s), status, sched);
 }
 
 }  // namespace

@@ -248,7 +248,7 @@ struct Int8Maps {
   CUtensorMap w1;    // the up weights (down: a copy of w0)
   CUtensorMap out;   // bf16 output [max_rows][N], box 32 rows x 64 columns
 };
-__host__ __device__ constexpr int int8_token_box(int i) { return 32 << i; }
+__host__ __device__ constexpr int int8_token_box(int i) { return 16 << i; }
 cudaError_t launch_int8_up(const moe_shape& s, const Int8Maps& m, const float* x_scales, const float* wg_scales,
                            const float* wu_scales, uint16_t* h, const int32_t* off_pad, const int32_t* counts,
                            uint32_t* status, uint32_t* sched, int num_sms, cudaStream_t st);

@@ -160,14 +160,10 @@ __device__ __forceinline__ bool ring_get(const TileRing& r, uint32_t n, uint32_t
   c = unpack_tile(make_int4(w[0], w[1], w[2], w[3]));
   return true;
 }
-// Called once the tile's fields have decided a branch (so they have been read).
-// Nothing else is handed back, hence the relaxed arrival: with a release, which
-// waits for the thread's stores in flight, CTA 1's epilogue spent 3600 of the 5000
-// cycles that a weight tile of 8 rows took.
 __device__ __forceinline__ void ring_release(const TileRing& r, uint32_t n, uint32_t rank, uint32_t empty0) {
   const uint32_t slot = n % kTileRing;
   if (rank == 0) mbar_arrive(&r.empty[slot]);
-  else mbar_arrive_cluster_relaxed(empty0 + 8u * slot);
+  else mbar_arrive_peer(empty0 + 8u * slot);
 }
 
 // The scheduler: one warp, a lane knowing eight experts.
@@ -574,7 +570,7 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
       auto release = [&]() {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster_relaxed(tempty0 + 8u * a);
+        if (lane == 0) mbar_arrive_peer(tempty0 + 8u * a);
       };
       if constexpr (kMode == kDownBwd) {
         // pieces of 32 rows, the turns' in turn
@@ -687,9 +683,7 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
           ok = mbar_wait<true>(&cleared[s], ph, abort_flag, status);
           if (ok) mbar_arrive(&full[s]);
         } else {
-          // CTA 1's tensor core reads what was cleared, which the fence above has
-          // put in its shared memory: the arrival itself has nothing to publish
-          mbar_arrive_cluster_relaxed(map_to_cta(&cleared[s], 0));
+          mbar_arrive_peer(map_to_cta(&cleared[s], 0));
         }
       }
       if (__any_sync(0xffffffffu, !ok)) break;
