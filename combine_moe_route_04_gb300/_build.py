@@ -19,8 +19,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe_gb300.so")
 SOURCES = ["moe_api.cu", "moe_route.cu", "moe_gemm.cu", "moe_combine.cu", "moe_check.cu",
            "moe_mxfp4.cu", "moe_mxfp4_gemm.cu", "moe_balance.cu", "moe_train_gemm.cu", "moe_combine_backward.cu",
-           "moe_int8.cu", "moe_int8_gemm.cu"]
-HEADERS = ["moe_device.cuh", "moe_internal.h", "moe_mxfp4.cuh", "moe_transpose.cuh", "moe_tiles.cuh"]
+           "moe_int8.cu", "moe_int8_gemm.cu", "moe_int8_rows.cu"]
+HEADERS = ["moe_device.cuh", "moe_internal.h", "moe_mxfp4.cuh", "moe_epilogue.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

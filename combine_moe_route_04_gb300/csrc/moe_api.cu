@@ -293,6 +293,29 @@ bool int8_maps(const moe_shape& s, int64_t K, int64_t N, const int8_t* rows, con
          encode_bytes_2d(&m->w0, w0, wr, kb, 128) && encode_bytes_2d(&m->w1, w1, wr, kb, 128);
 }
 
+moe_status run_int8_up(const moe_shape& s, const int8_t* x, const float* x_scales, const int32_t* counts,
+                       const int32_t* off_pad, const int8_t* wg, const float* wg_scales, const int8_t* wu,
+                       const float* wu_scales, uint16_t* h, uint32_t* status, int num_sms, cudaStream_t st) {
+  if (int8_few_rows(s))
+    return cuda_status(
+        launch_int8_up_rows(s, x, x_scales, wg, wg_scales, wu, wu_scales, h, off_pad, counts, status, num_sms, st));
+  Int8Maps m;
+  if (!int8_maps(s, s.H, s.I, x, wg, wu, h, &m)) return MOE_ERR_CUDA;
+  return cuda_status(launch_int8_up(s, m, x_scales, wg_scales, wu_scales, h, off_pad, counts, status,
+                                    ws_sched_up(status), num_sms, st));
+}
+
+moe_status run_int8_down(const moe_shape& s, const int8_t* h, const float* h_scales, const int32_t* counts,
+                         const int32_t* off_pad, const int8_t* wd, const float* wd_scales, uint16_t* Y,
+                         uint32_t* status, int num_sms, cudaStream_t st) {
+  if (int8_few_rows(s))
+    return cuda_status(launch_int8_down_rows(s, h, h_scales, wd, wd_scales, Y, off_pad, counts, status, num_sms, st));
+  Int8Maps m;
+  if (!int8_maps(s, s.I, s.H, h, wd, wd, Y, &m)) return MOE_ERR_CUDA;
+  return cuda_status(
+      launch_int8_down(s, m, h_scales, wd_scales, Y, off_pad, counts, status, ws_sched_down(status), num_sms, st));
+}
+
 moe_status run_down_backward(const moe_shape& s, const uint16_t* dY, const int32_t* counts, const int32_t* off_pad,
                              const uint16_t* Wd, const uint16_t* g, const uint16_t* u, uint16_t* dg, uint16_t* du,
                              uint32_t* status, int num_sms, cudaStream_t st) {
@@ -1025,10 +1048,8 @@ moe_status moe_grouped_gemm_up_int8(const moe_shape* shape, const int8_t* x_code
   DeviceRestore restore;
   st = prepare_device(s, &sms, &restore);
   if (st != MOE_OK) return st;
-  Int8Maps m;
-  if (!int8_maps(*shape, shape->H, shape->I, x_codes, wg_codes, wu_codes, h, &m)) return MOE_ERR_CUDA;
-  return cuda_status(launch_int8_up(*shape, m, x_scales, wg_scales, wu_scales, h, off_pad, counts, ws_status(ws),
-                                    ws_sched_up(ws_status(ws)), sms, s));
+  return run_int8_up(*shape, x_codes, x_scales, counts, off_pad, wg_codes, wg_scales, wu_codes, wu_scales, h,
+                     ws_status(ws), sms, s);
 }
 
 moe_status moe_grouped_gemm_down_int8(const moe_shape* shape, const int8_t* h_codes, const float* h_scales,
@@ -1043,10 +1064,7 @@ moe_status moe_grouped_gemm_down_int8(const moe_shape* shape, const int8_t* h_co
   DeviceRestore restore;
   st = prepare_device(s, &sms, &restore);
   if (st != MOE_OK) return st;
-  Int8Maps m;
-  if (!int8_maps(*shape, shape->I, shape->H, h_codes, wd_codes, wd_codes, Y, &m)) return MOE_ERR_CUDA;
-  return cuda_status(launch_int8_down(*shape, m, h_scales, wd_scales, Y, off_pad, counts, ws_status(ws),
-                                      ws_sched_down(ws_status(ws)), sms, s));
+  return run_int8_down(*shape, h_codes, h_scales, counts, off_pad, wd_codes, wd_scales, Y, ws_status(ws), sms, s);
 }
 
 moe_status moe_int8_workspace_size(const moe_shape* shape, size_t* bytes) {
@@ -1079,10 +1097,6 @@ moe_status moe_forward_int8(const moe_shape* shape, const float* logits, const m
   uint16_t* h = reinterpret_cast<uint16_t*>(b + L.h);
   uint16_t* Y = reinterpret_cast<uint16_t*>(b + L.y);
   uint32_t* status = ws_status(ws);
-  Int8Maps up, down;
-  if (!int8_maps(sh, sh.H, sh.I, i8(L.x_codes), wg_codes, wu_codes, h, &up) ||
-      !int8_maps(sh, sh.I, sh.H, i8(L.h_codes), wd_codes, wd_codes, Y, &down))
-    return MOE_ERR_CUDA;
   if (launch_route(sh, logits, i32(L.topk_ids), f32(L.topk_w), i32(L.counts), i32(L.off_pad), i32(L.block_expert),
                    i32(L.num_blocks), i32(L.gather_idx), i32(L.scatter_idx), i32(L.chunk_counts),
                    ws_route_counter(ws), status, s) != cudaSuccess)
@@ -1090,15 +1104,15 @@ moe_status moe_forward_int8(const moe_shape* shape, const float* logits, const m
   if (launch_quantize_permute_int8(sh, X, i32(L.scatter_idx), i8(L.x_codes), f32(L.x_scales), status, s) !=
       cudaSuccess)
     return MOE_ERR_CUDA;
-  if (launch_int8_up(sh, up, f32(L.x_scales), wg_scales, wu_scales, h, i32(L.off_pad), i32(L.counts), status,
-                     ws_sched_up(status), sms, s) != cudaSuccess)
-    return MOE_ERR_CUDA;
+  st = run_int8_up(sh, i8(L.x_codes), f32(L.x_scales), i32(L.counts), i32(L.off_pad), wg_codes, wg_scales, wu_codes,
+                   wu_scales, h, status, sms, s);
+  if (st != MOE_OK) return st;
   if (launch_quantize_expert_rows_int8(sh, h, sh.I, i32(L.gather_idx), i32(L.num_blocks), i8(L.h_codes),
                                        f32(L.h_scales), s) != cudaSuccess)
     return MOE_ERR_CUDA;
-  if (launch_int8_down(sh, down, f32(L.h_scales), wd_scales, Y, i32(L.off_pad), i32(L.counts), status,
-                       ws_sched_down(status), sms, s) != cudaSuccess)
-    return MOE_ERR_CUDA;
+  st = run_int8_down(sh, i8(L.h_codes), f32(L.h_scales), i32(L.counts), i32(L.off_pad), wd_codes, wd_scales, Y, status,
+                     sms, s);
+  if (st != MOE_OK) return st;
   return cuda_status(launch_combine(sh, Y, i32(L.scatter_idx), f32(L.topk_w), out, status, sms, s));
 }
 

@@ -1,6 +1,7 @@
-// moe_transpose.cuh -- pieces of 32 rows x 128 columns between TMEM, registers and
-// shared memory, for products whose accumulators hold the output transposed
-// (TMEM lane = output column, TMEM column = output row).
+// moe_epilogue.cuh -- what the products' epilogues share: pieces of 32 rows x 128
+// columns between TMEM, registers and shared memory where accumulators hold the
+// output transposed (TMEM lane = output column, TMEM column = output row), and the
+// activation.
 #pragma once
 
 #include <cstdint>
@@ -77,6 +78,17 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&v)[4
                : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
                : "r"(addr)
                : "memory");
+}
+
+// silu(g) * u with the sigmoid on the SFU.  The exponent g log2 e is rounded
+// before ex2, so below zero the relative error grows with |g|, to about
+// |g| 2^-24 and a few ulps (2^-17 at g = -88, below which the result is the
+// limit 0, as in the bf16 GEMM): far under h's rounding to bf16, 2^-9.
+__device__ __forceinline__ float silu_mul(float g, float u) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  return g * r * u;
 }
 
 }  // namespace moe

@@ -27,8 +27,8 @@
 #include <cuda_fp16.h>
 
 #include "moe_device.cuh"
+#include "moe_epilogue.cuh"
 #include "moe_internal.h"
-#include "moe_transpose.cuh"
 
 namespace moe {
 namespace {
@@ -293,17 +293,6 @@ __device__ __forceinline__ bool vote_any(bool flag) {
       : "r"(flag ? 1u : 0u), "n"(kEpiWarps * 32)
       : "memory");
   return r != 0;
-}
-
-// silu(g) * u with the sigmoid on the SFU.  The exponent g log2 e is rounded
-// before ex2, so below zero the relative error grows with |g|, to about
-// |g| 2^-24 and a few ulps (2^-17 at g = -88, below which the result is the
-// limit 0): far under h's rounding to bf16, 2^-9.
-__device__ __forceinline__ float silu_mul(float g, float u) {
-  float e, r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
-  return g * r * u;
 }
 
 template <bool kUp>

@@ -255,6 +255,15 @@ cudaError_t launch_int8_up(const moe_shape& s, const Int8Maps& m, const float* x
 cudaError_t launch_int8_down(const moe_shape& s, const Int8Maps& m, const float* h_scales, const float* wd_scales,
                              uint16_t* Y, const int32_t* off_pad, const int32_t* counts, uint32_t* status,
                              uint32_t* sched, int num_sms, cudaStream_t st);
+// The same for a few rows per expert (the shapes that int8_few_rows names).
+bool int8_few_rows(const moe_shape& s);
+cudaError_t launch_int8_up_rows(const moe_shape& s, const int8_t* x, const float* x_scales, const int8_t* wg,
+                                const float* wg_scales, const int8_t* wu, const float* wu_scales, uint16_t* h,
+                                const int32_t* off_pad, const int32_t* counts, uint32_t* status, int num_sms,
+                                cudaStream_t st);
+cudaError_t launch_int8_down_rows(const moe_shape& s, const int8_t* h, const float* h_scales, const int8_t* wd,
+                                  const float* wd_scales, uint16_t* Y, const int32_t* off_pad, const int32_t* counts,
+                                  uint32_t* status, int num_sms, cudaStream_t st);
 
 // Balance loss.  partials: the workspace region past its first 256 bytes
 // (balance_partial_bytes); counter: a uint32 that is zero between calls.

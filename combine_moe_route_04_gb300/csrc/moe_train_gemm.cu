@@ -29,8 +29,8 @@
 #include <mutex>
 
 #include "moe_device.cuh"
+#include "moe_epilogue.cuh"
 #include "moe_internal.h"
-#include "moe_transpose.cuh"
 
 namespace moe {
 namespace {
