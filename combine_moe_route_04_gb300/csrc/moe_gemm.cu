@@ -220,7 +220,7 @@ struct TileRing {
 __device__ __forceinline__ void ring_release(const TileRing& r, uint32_t n, uint32_t rank, uint32_t empty0_cluster) {
   const uint32_t slot = n % S_TILE_RING;
   if (rank == 0) mbar_arrive(&r.empty[slot]);
-  else mbar_arrive_cluster(empty0_cluster + 8u * slot);
+  else mbar_arrive_peer(empty0_cluster + 8u * slot);
 }
 __device__ __forceinline__ int ring_take(const TileRing& r, uint32_t n, uint32_t rank, uint32_t empty0_cluster,
                                          bool release, volatile int* abort, uint32_t* status) {
@@ -634,7 +634,7 @@ __global__ void __launch_bounds__(S_THREADS, 1)
       auto release = [&]() {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(tempty0 + 8u * a);
+        if (lane == 0) mbar_arrive_peer(tempty0 + 8u * a);
       };
       if (mine == 0) release();
       uint32_t packed[CH_PER * 16];                 // bf16 pairs (token 2i, 2i+1 of chunk cl) of this column

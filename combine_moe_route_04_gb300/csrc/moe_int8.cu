@@ -198,13 +198,17 @@ __global__ void __launch_bounds__(256) dequantize_rows_kernel(const int8_t* __re
 // scale per (e, n).  A CTA takes 32 columns of one expert: a first pass over
 // their K rows (64 bytes each) for the maxima, a second one, backwards, in steps of
 // kWk rows for the codes, which cross shared memory once so that each column's
-// bytes leave together.  Two CTAs an SM: their strips, 256 KB each for K = 4096,
-// stay in L2 between the passes, and one's loads run under the other's arithmetic.
+// bytes leave together.  Four CTAs an SM: much of their strips, 256 KB each for K =
+// 4096, is in L2 for the second pass, and one's loads run under the others'
+// arithmetic.  (64 weights of 4096 x 1536 301 us, of 1536 x 4096 255 us, where reading
+// and writing once would take 178; two CTAs of 512 threads 302 and 329.  A cluster of
+// eight CTAs that holds 64 columns in registers and reads them once took 305 and 436:
+// a CTA's fixed steps, one after the other, bound it.)
 constexpr int kWn = 32;
-constexpr int kWeightThreads = 512;
+constexpr int kWeightThreads = 256;
 constexpr int kWk = kWeightThreads / 4 * 4;  // four rows x eight columns per thread
 
-__global__ void __launch_bounds__(kWeightThreads, 2) quantize_weights_kernel(const uint16_t* __restrict__ w, int K,
+__global__ void __launch_bounds__(kWeightThreads, 4) quantize_weights_kernel(const uint16_t* __restrict__ w, int K,
                                                                              int N, int8_t* __restrict__ codes,
                                                                              float* __restrict__ scales) {
   __shared__ __align__(16) uint32_t s_codes[kWn * kWk / 4];

@@ -75,7 +75,8 @@ def test_every_quotient_of_a_row(moe):
     assert torch.equal(codes, q) and torch.equal(scales, s)
 
 
-@pytest.mark.parametrize("shape", [(1, 128, 128), (3, 384, 256), (2, 640, 128), (1, 4096, 192 * 2), (2, 8320, 128)], ids=str)
+@pytest.mark.parametrize("shape", [(1, 128, 128), (3, 384, 256), (2, 640, 128), (1, 4096, 192 * 2), (2, 2304, 128), (1, 4224, 128),
+                                   (2, 8320, 128)], ids=str)
 def test_quantize_weights(moe, shape):
     E, K, N = shape
     w = special_rows(E * N, K, generator(1)).reshape(E, N, K).transpose(1, 2).contiguous()
