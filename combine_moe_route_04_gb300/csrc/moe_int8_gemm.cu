@@ -18,9 +18,17 @@
 // operand.  TMEM holds two accumulators of 128 columns and kSteps such steps of
 // both blocks.
 //
-// What bounds it with many rows is shared memory: codes in, out and widened rows
-// in, and the second operand, 64 KB for a step's 512 cycles of MMAs (one CTA alone
-// moves 96 KB, and widens twice the rows).
+// What bounds it with many rows is the widening: a step has 512 cycles of MMAs, and
+// takes 850; a group needs 1100 to 1300 from its wait to its arrival, and shared
+// memory moves 64 KB (codes in and out, widened rows, the second operand).  On single
+// CTAs, which widen twice the rows and move 96 KB, 2048 tokens and 64 experts of 4096
+// x 1536 took 409 us where this takes 336 (gate/up; down 212 and 192), 16384 tokens
+// and 128 experts 2637 and 2163 (1.52 PFLOP/s).  With 8 rows per expert 150 us, 5.4
+// TB/s of weights.
+//
+// Tried and slower: three groups in turn and four epilogue warps (367 us); four warps
+// for the rows alone (391); widening ahead of the wait for the step's buffers (458);
+// one group (444, on single CTAs).
 #include <cstdint>
 #include <mutex>
 

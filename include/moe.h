@@ -485,8 +485,8 @@ moe_status moe_balance_loss_backward(const moe_shape *shape, const float *logits
  *   dh = dY Wd^T, dg = dh u s (1 + g (1 - s)), du = dh g s
  *   dx = dg Wg^T + du Wu^T, dWg = x^T dg, dWu = x^T du, dWd = h^T dY
  * with float32 sums, and g, u, h, dg, du and every result rounded once to bf16.
- * One expert that takes every token (E = k = 1, counts[0] = T) is a dense gated
- * feed-forward.
+ * One expert that takes every token (E = k = 1, counts[0] = T, off_pad = {0, T rounded
+ * up to 128}) is a dense gated feed-forward.
  *
  * Buffers in expert order have max_rows rows, as above; padding rows are not
  * written, and what they hold does not reach a result.  ws: any workspace, or
