@@ -101,16 +101,13 @@ __device__ __forceinline__ void mma_f16_tmem(uint32_t d, uint32_t a, uint64_t b,
       : "memory");
 }
 
-// 32 lanes x 32 columns: thread i's registers to lane i.
-__device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t (&r)[32]) {
+// 32 lanes x 16 columns: thread i's registers to lane i.
+__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -600,7 +597,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           stop = true;
           break;
         }
+        // the codes are read before the step's buffers are waited for
         const uint8_t* st = smem + s * kStageBytes;
+        uint4 v[4], tv = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          v[i] = *reinterpret_cast<const uint4*>(st + block * kWBytes + swizzled(wrow, 4 * half + i));
+        if (rows_here) tv = *reinterpret_cast<const uint4*>(st + 2 * kWBytes + swizzled(trow, 4 * half + ch));
         const uint32_t step = 2 * it + half, d = step % kSteps;
         if (__any_sync(0xffffffffu, !mbar_wait(&used[d], ((step / kSteps) & 1u) ^ 1u, abort_flag, status))) {
           stop = true;
@@ -608,25 +611,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
         if (block_here) {
-          uint32_t r[32];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint4 v = *reinterpret_cast<const uint4*>(st + block * kWBytes + swizzled(wrow, 4 * half + i));
-            widen4(v.x, r[8 * i], r[8 * i + 1]);
-            widen4(v.y, r[8 * i + 2], r[8 * i + 3]);
-            widen4(v.z, r[8 * i + 4], r[8 * i + 5]);
-            widen4(v.w, r[8 * i + 6], r[8 * i + 7]);
+          for (int i = 0; i < 2; ++i) {
+            uint32_t r[16];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              widen4(v[2 * i + k].x, r[8 * k], r[8 * k + 1]);
+              widen4(v[2 * i + k].y, r[8 * k + 2], r[8 * k + 3]);
+              widen4(v[2 * i + k].z, r[8 * k + 4], r[8 * k + 5]);
+              widen4(v[2 * i + k].w, r[8 * k + 6], r[8 * k + 7]);
+            }
+            tmem_st_32x32b_x16(ta + d * 2 * kWideBlockCols + 16 * i, r);
           }
-          tmem_st_32x32b_x32(ta + d * 2 * kWideBlockCols, r);
         }
         if (rows_here) {
           uint8_t* to = smem + kStepOff + d * kStepBytes;
-          const uint4 v = *reinterpret_cast<const uint4*>(st + 2 * kWBytes + swizzled(trow, 4 * half + ch));
           uint4 a, b;
-          widen4(v.x, a.x, a.y);
-          widen4(v.y, a.z, a.w);
-          widen4(v.z, b.x, b.y);
-          widen4(v.w, b.z, b.w);
+          widen4(tv.x, a.x, a.y);
+          widen4(tv.y, a.z, a.w);
+          widen4(tv.z, b.x, b.y);
+          widen4(tv.w, b.z, b.w);
           *reinterpret_cast<uint4*>(to + swizzled(trow, 2 * ch)) = a;
           *reinterpret_cast<uint4*>(to + swizzled(trow, 2 * ch + 1)) = b;
           fence_proxy_async_smem();
