@@ -1003,10 +1003,11 @@ moe_status moe_quantize_weights_int8(const moe_bf16* w, int32_t E, int64_t K, in
   moe_status st = check_ptrs({w, codes, scales});
   if (st != MOE_OK) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int num_sms = 0;
   DeviceRestore restore;
-  st = prepare_device(s, nullptr, &restore);
+  st = prepare_device(s, &num_sms, &restore);
   if (st != MOE_OK) return st;
-  return cuda_status(launch_quantize_weights_int8(w, E, K, N, codes, scales, s));
+  return cuda_status(launch_quantize_weights_int8(w, E, K, N, codes, scales, num_sms, s));
 }
 
 moe_status moe_dequantize_int8(const int8_t* codes, const float* scales, int64_t rows, int64_t cols, moe_bf16* x,

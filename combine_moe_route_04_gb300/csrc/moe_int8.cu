@@ -197,36 +197,45 @@ __global__ void __launch_bounds__(256) dequantize_rows_kernel(const int8_t* __re
 }
 
 // Weights w [E][K][N] to codes [E][N][K], the reduction axis K contiguous, and a
-// scale per (e, n).  A CTA takes 32 columns of one expert: a first pass over
-// their K rows (64 bytes each) for the maxima, a second one, backwards, in steps of
-// kWk rows for the codes, which cross shared memory once so that each column's
-// bytes leave together.  Four CTAs an SM: much of their strips, 256 KB each for K =
-// 4096, is in L2 for the second pass, and one's loads run under the others'
-// arithmetic.  (64 weights of 4096 x 1536 301 us, of 1536 x 4096 255 us, where reading
-// and writing once would take 178; two CTAs of 512 threads 302 and 329.  A cluster of
-// eight CTAs that holds 64 columns in registers and reads them once took 305 and 436:
-// a CTA's fixed steps, one after the other, bound it.)
+// scale per (e, n).  A cluster of kWCtas CTAs takes 32 columns of one expert, each CTA
+// its share of their rows: a first pass over them (64 bytes each) for the maxima,
+// which meet in distributed shared memory, a second one, backwards, in steps of kWk
+// rows for the codes, which cross shared memory once so that each column's bytes
+// leave together.  Four CTAs an SM: much of what they hold is in L2 for the second
+// pass, and one's loads run under the others' arithmetic.  With one, two and four CTAs
+// a cluster: 64 weights of 4096 x 1536 304, 275, 259 us; of 7168 x 2048 698, 665, 694;
+// of 1536 x 4096 255, 304, 483 (reading and writing once would take 178); 7 of 1408 x
+// 640, which fill no device, 11.8, 9.5, 7.9.  ctas_of takes two from K = 2048 on, and
+// four where these would leave room.  (Two CTAs of 512 threads an SM 302 and 329.  A
+// cluster of eight CTAs that holds 64 columns in registers and reads them once took 305
+// and 436: a CTA's fixed steps, one after the other, bound it.)
 constexpr int kWn = 32;
 constexpr int kWeightThreads = 256;
 constexpr int kWk = kWeightThreads / 4 * 4;  // four rows x eight columns per thread
 
+template <int kWCtas>
 __global__ void __launch_bounds__(kWeightThreads, 4) quantize_weights_kernel(const uint16_t* __restrict__ w, int K,
                                                                              int N, int8_t* __restrict__ codes,
                                                                              float* __restrict__ scales) {
   __shared__ __align__(16) uint32_t s_codes[kWn * kWk / 4];
   __shared__ uint4 s_max[kWeightThreads / 32][4];
+  __shared__ uint4 s_all[kWCtas][4];  // the CTAs' maxima
+  if (kWCtas > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   pdl_launch_dependents();
   pdl_wait();
+  const uint32_t rank = kWCtas > 1 ? cluster_ctarank() : 0u;
+  const int rows = K / kWCtas;  // a multiple of 64
+  const int64_t first = static_cast<int64_t>(rank) * rows;
   const int cg = threadIdx.x & 3;   // columns 8 cg..
   const int kr = threadIdx.x >> 2;  // row of the thread, or group of four rows
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t e = blockIdx.y;
+  const int64_t e = blockIdx.z;
   const int64_t n0 = static_cast<int64_t>(blockIdx.x) * kWn;
-  const uint4* src = reinterpret_cast<const uint4*>(w + e * K * N + n0) + cg;
+  const uint4* src = reinterpret_cast<const uint4*>(w + (e * K + first) * N + n0) + cg;
   const int64_t pitch = N / 8;
   uint4 m = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll 8
-  for (int k = kr; k < K; k += kWeightThreads / 4) {
+  for (int k = kr; k < rows; k += kWeightThreads / 4) {
     const uint4 v = __ldcg(src + k * pitch);
     m.x = max_magnitude(m.x, v.x);
     m.y = max_magnitude(m.y, v.y);
@@ -242,13 +251,35 @@ __global__ void __launch_bounds__(kWeightThreads, 4) quantize_weights_kernel(con
   }
   if (lane < 4) s_max[warp][lane] = m;
   __syncthreads();
-  m = s_max[0][cg];
-  for (int i = 1; i < kWeightThreads / 32; ++i) {
-    const uint4 v = s_max[i][cg];
-    m.x = __vmaxu2(m.x, v.x);
-    m.y = __vmaxu2(m.y, v.y);
-    m.z = __vmaxu2(m.z, v.z);
-    m.w = __vmaxu2(m.w, v.w);
+  if constexpr (kWCtas == 1) {
+    m = s_max[0][cg];
+    for (int i = 1; i < kWeightThreads / 32; ++i) {
+      const uint4 v = s_max[i][cg];
+      m.x = __vmaxu2(m.x, v.x);
+      m.y = __vmaxu2(m.y, v.y);
+      m.z = __vmaxu2(m.z, v.z);
+      m.w = __vmaxu2(m.w, v.w);
+    }
+  } else {
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // every CTA has started
+    if (threadIdx.x < 16) {  // a word of the 32 columns' maxima
+      const uint32_t* word = reinterpret_cast<const uint32_t*>(s_max) + threadIdx.x;
+      uint32_t mine = 0u;
+      for (int i = 0; i < kWeightThreads / 32; ++i) mine = __vmaxu2(mine, word[16 * i]);
+      const uint32_t* to = reinterpret_cast<const uint32_t*>(s_all[rank]) + threadIdx.x;
+      for (uint32_t c = 0; c < kWCtas; ++c)
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_to_cta(to, c)), "r"(mine) : "memory");
+    }
+    cluster_sync_all();
+    m = s_all[0][cg];
+#pragma unroll
+    for (int i = 1; i < kWCtas; ++i) {
+      const uint4 v = s_all[i][cg];
+      m.x = __vmaxu2(m.x, v.x);
+      m.y = __vmaxu2(m.y, v.y);
+      m.z = __vmaxu2(m.z, v.z);
+      m.w = __vmaxu2(m.w, v.w);
+    }
   }
   float inv[8];
   uint32_t bad = 0u, raised = 0u;  // bit i: column 8 cg + i reads as NaN, is raised
@@ -260,12 +291,12 @@ __global__ void __launch_bounds__(kWeightThreads, 4) quantize_weights_kernel(con
     inv[i] = inverse_of(b, raise);
     if (b >= kInfBits) bad |= 1u << i;
     if (raise != 1.0f) raised |= 1u << i;
-    if (kr == 0) scales[e * N + n0 + 8 * cg + i] = scale_of(b);
+    if (kr == 0 && rank == 0) scales[e * N + n0 + 8 * cg + i] = scale_of(b);
   }
   const bool any_raised = __any_sync(0xffffffffu, raised != 0u);
-  for (int k0 = (K - 1) / kWk * kWk; k0 >= 0; k0 -= kWk) {
+  for (int k0 = (rows - 1) / kWk * kWk; k0 >= 0; k0 -= kWk) {
     const int k = k0 + 4 * kr;
-    if (k < K) {  // K is a multiple of 128
+    if (k < rows) {
       uint4 v[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] = __ldcg(src + (k + i) * pitch);
@@ -290,15 +321,22 @@ __global__ void __launch_bounds__(kWeightThreads, 4) quantize_weights_kernel(con
       }
     }
     __syncthreads();
-    const int left = min(kWk, K - k0) / 16;  // 16-byte chunks of a column
+    const int left = min(kWk, rows - k0) / 16;  // 16-byte chunks of a column
     for (int i = threadIdx.x; i < kWn * (kWk / 16); i += kWeightThreads) {
       const int n = i / (kWk / 16), c = i % (kWk / 16);
       if (c < left)
-        *reinterpret_cast<uint4*>(codes + (e * N + n0 + n) * K + k0 + c * 16) =
+        *reinterpret_cast<uint4*>(codes + (e * N + n0 + n) * K + first + k0 + c * 16) =
             *reinterpret_cast<const uint4*>(s_codes + n * (kWk / 4) + (c ^ (2 * (n >> 3))) * 4);
     }
     __syncthreads();
   }
+}
+
+// CTAs of a cluster of the weights' kernel; strips is the number of its clusters.
+int ctas_of(int64_t K, int64_t strips, int num_sms) {
+  int ctas = K >= 2048 ? 2 : 1;
+  while (ctas < 4 && 2 * strips * ctas <= 4 * num_sms) ctas *= 2;
+  return ctas;
 }
 
 int group_of(int64_t cols) {
@@ -345,10 +383,25 @@ cudaError_t launch_dequantize_rows_int8(const int8_t* codes, const float* scales
 }
 
 cudaError_t launch_quantize_weights_int8(const uint16_t* w, int E, int64_t K, int64_t N, int8_t* codes, float* scales,
-                                         cudaStream_t st) {
-  const dim3 grid(static_cast<unsigned>(N / kWn), static_cast<unsigned>(E));
-  return launch_pdl(quantize_weights_kernel, grid, dim3(kWeightThreads), 0, st, w, static_cast<int>(K),
-                    static_cast<int>(N), codes, scales);
+                                         int num_sms, cudaStream_t st) {
+  const int ctas = ctas_of(K, N / kWn * E, num_sms);
+  auto kernel = ctas == 1   ? quantize_weights_kernel<1>
+                : ctas == 2 ? quantize_weights_kernel<2>
+                            : quantize_weights_kernel<4>;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(N / kWn), static_cast<unsigned>(ctas), static_cast<unsigned>(E));
+  cfg.blockDim = dim3(kWeightThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 1;
+  attr[0].val.clusterDim.y = static_cast<unsigned>(ctas);
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, w, static_cast<int>(K), static_cast<int>(N), codes, scales);
 }
 
 }  // namespace moe

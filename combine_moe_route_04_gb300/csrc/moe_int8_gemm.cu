@@ -18,17 +18,22 @@
 // operand.  TMEM holds two accumulators of 128 columns and kSteps such steps of
 // both blocks.
 //
-// What bounds it with many rows is the widening: a step has 512 cycles of MMAs, and
-// takes 850; a group needs 1100 to 1300 from its wait to its arrival, and shared
-// memory moves 64 KB (codes in and out, widened rows, the second operand).  On single
-// CTAs, which widen twice the rows and move 96 KB, 2048 tokens and 64 experts of 4096
-// x 1536 took 409 us where this takes 336 (gate/up; down 212 and 192), 16384 tokens
-// and 128 experts 2637 and 2163 (1.52 PFLOP/s).  With 8 rows per expert 150 us, 5.4
-// TB/s of weights.
+// What bounds it with many rows is the MMAs and what of the widening they wait for:
+// 2048 tokens and 64 experts of 4096 x 1536 take 292 us (gate/up; down 168), 16384
+// tokens and 128 experts 1860 (1.77 PFLOP/s); with steps that are handed on unwidened
+// the same tiles take 256 and 1617.  A group reads its codes before it waits for the
+// step's buffers, so that shared memory's latency lies outside the chain from the MMA
+// that frees a buffer to the one that reads it anew: 336, 192 and 2163 us with the
+// reads behind the wait.  On single CTAs, which widen twice the rows and move 96 KB of
+// shared memory a step instead of 64, 409, 212 and 2637 (reads behind the wait).  With
+// 8 rows per expert 142 us, 5.7 TB/s of weights.
 //
-// Tried and slower: three groups in turn and four epilogue warps (367 us); four warps
-// for the rows alone (391); widening ahead of the wait for the step's buffers (458);
-// one group (444, on single CTAs).
+// Tried and slower, or no faster (reads behind the wait, 336 us, unless said): three
+// groups in turn and four epilogue warps (367); four warps for the rows alone (391);
+// the widened codes, not the codes, held across the wait (458: registers); a whole
+// stage per group (345); one wait for both steps of a stage (354); one group (444, on
+// single CTAs); with the reads ahead, the stage released right behind them (296, and
+// 292 without).
 #include <cstdint>
 #include <mutex>
 

@@ -237,7 +237,7 @@ cudaError_t launch_quantize_expert_rows_int8(const moe_shape& s, const uint16_t*
 cudaError_t launch_quantize_permute_int8(const moe_shape& s, const uint16_t* X, const int32_t* scatter_idx,
                                          int8_t* codes, float* scales, uint32_t* status, cudaStream_t st);
 cudaError_t launch_quantize_weights_int8(const uint16_t* w, int E, int64_t K, int64_t N, int8_t* codes, float* scales,
-                                         cudaStream_t st);
+                                         int num_sms, cudaStream_t st);
 cudaError_t launch_dequantize_rows_int8(const int8_t* codes, const float* scales, int64_t rows, int64_t cols,
                                         uint16_t* x, cudaStream_t st);
 

@@ -86,6 +86,12 @@ def test_quantize_weights(moe, shape):
     assert torch.equal(codes, q) and same_scales(scales, s)
 
 
+@pytest.mark.parametrize("shape", [(40, 384, 512), (24, 1152, 256), (20, 2176, 1024), (80, 128, 256), (9, 4224, 1280)], ids=str)
+def test_quantize_weights_of_many_columns(moe, shape):
+    """Columns enough to fill the device, where a cluster of fewer CTAs takes them."""
+    test_quantize_weights(moe, shape)
+
+
 @pytest.mark.parametrize("shape", [(1, 128, 1, 1), (50, 384, 7, 3), (300, 9216, 64, 16)], ids=str)
 def test_quantize_permute(moe, shape):
     T, H, E, k = shape
