@@ -352,8 +352,8 @@ moe_status run_weight_backward(const moe_shape& s, const uint16_t* Xp, const uin
   TrainMaps m = {};
   if (!encode_bf16_2d(&m.a[0], dg, mr, s.I, 64, 64) || !encode_bf16_2d(&m.a[1], du, mr, s.I, 64, 64) ||
       !encode_bf16_2d(&m.a[2], dY, mr, s.H, 64, 64) || !encode_bf16_2d(&m.b[0][0], Xp, mr, s.H, 64, 64) ||
-      !encode_bf16_2d(&m.b[1][0], h, mr, s.I, 64, 64) || !encode_bf16_groups(&m.out[0], dWg, EH, s.I, 128) ||
-      !encode_bf16_groups(&m.out[1], dWu, EH, s.I, 128) || !encode_bf16_groups(&m.out[2], dWd, EI, s.H, 128))
+      !encode_bf16_2d(&m.b[1][0], h, mr, s.I, 64, 64) || !encode_bf16_groups(&m.out[0], dWg, EH, s.I, 64) ||
+      !encode_bf16_groups(&m.out[1], dWu, EH, s.I, 64) || !encode_bf16_groups(&m.out[2], dWd, EI, s.H, 64))
     return MOE_ERR_CUDA;
   return cuda_status(launch_weight_backward(s, m, TrainOut{{dWg, dWu, dWd}}, off_pad, counts, status, ws_sched_up(status), num_sms, st));
 }

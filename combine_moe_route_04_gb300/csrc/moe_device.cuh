@@ -267,9 +267,6 @@ __device__ __forceinline__ uint32_t map_to_cta(const void* p, uint32_t rank) {
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_cluster) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
-}
 // An arrival on a barrier of either CTA of a pair that orders this thread's earlier
 // accesses at CTA scope: for handing over what stays in this CTA's own SM (shared
 // memory and TMEM that its tensor core reads for the pair, an accumulator or a
@@ -278,6 +275,30 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_cluster) {
 // writes a lot.
 __device__ __forceinline__ void mbar_arrive_peer(uint32_t bar_cluster) {
   asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
+}
+
+// Words for a reader in another CTA of the cluster: stored to its shared memory (dst)
+// together with the one arrival that its barrier expects.  The stores count on the
+// barrier by themselves, so nothing is released: a release at cluster scope also
+// waits for this thread's other accesses in flight, such as an atomic on its way.
+// The reader waits with cluster scope; the CTA at dst stays until it has, or, where
+// it gives up, for longer than a store takes (linger_after_abort).
+__device__ __forceinline__ void send_cluster(uint32_t dst, uint32_t bar, const int4& v) {
+  asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], 16;" ::"r"(bar) : "memory");
+  asm volatile(
+      "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.u32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(dst),
+      "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void send_cluster(uint32_t dst, uint32_t bar, int32_t v) {
+  asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], 4;" ::"r"(bar) : "memory");
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.u32 [%0], %1, [%2];" ::"r"(dst), "r"(v),
+               "r"(bar)
+               : "memory");
+}
+// Behind the last cluster barrier.
+__device__ __forceinline__ void linger_after_abort(volatile int* abort) {
+  if (*abort != 0) __nanosleep(100000);
 }
 
 // ------------------------------------------------------------------ tcgen05

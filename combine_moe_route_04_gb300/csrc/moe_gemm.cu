@@ -241,9 +241,7 @@ __device__ __forceinline__ bool ring_put(const TileRing& r, uint32_t n, int tile
   if (!mbar_wait(&r.empty[slot], ((n / S_TILE_RING) & 1u) ^ 1u, abort, status)) return false;
   r.idx[slot] = tile;
   mbar_arrive(&r.full[slot]);
-  const uint32_t remote_idx = map_to_cta(const_cast<int32_t*>(&r.idx[slot]), 1);
-  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(remote_idx), "r"(tile) : "memory");
-  mbar_arrive_cluster(map_to_cta(&r.full[slot], 1));
+  send_cluster(map_to_cta(const_cast<int32_t*>(&r.idx[slot]), 1), map_to_cta(&r.full[slot], 1), tile);
   return true;
 }
 
@@ -770,6 +768,7 @@ __global__ void __launch_bounds__(S_THREADS, 1)
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();
+  linger_after_abort(abort_flag);
   tc_fence_after();
   if (warp == 1) {
     __syncwarp();

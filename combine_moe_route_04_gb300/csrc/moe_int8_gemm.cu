@@ -154,10 +154,7 @@ __device__ __forceinline__ bool ring_put(const TileRing& r, uint32_t n, const Ti
   w[2] = c.j;
   w[3] = c.row0;
   mbar_arrive(&r.full[slot]);
-  asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(map_to_cta(&r.tile[slot], 1)), "r"(x),
-               "r"(c.e), "r"(c.j), "r"(c.row0)
-               : "memory");
-  mbar_arrive_cluster(map_to_cta(&r.full[slot], 1));
+  send_cluster(map_to_cta(&r.tile[slot], 1), map_to_cta(&r.full[slot], 1), make_int4(x, c.e, c.j, c.row0));
   return true;
 }
 // The n-th tile of this cluster, false when the wait gave up.
@@ -655,6 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();
+  linger_after_abort(abort_flag);
   tc_fence_after();
   if (warp == 1) {
     __syncwarp();

@@ -70,9 +70,10 @@ struct Cfg {
   // are short and the stores bound the kernel, all of the turn's 128, so that they
   // leave under the next tile's work (64 experts of 4096 x 1536, 256 rows each: 64
   // rows and a sixth stage 806 us, where this change made it 700).
-  static constexpr int HEIGHT = kMode == kWeightBwd ? kTileN / kTurns : 64;
+  static constexpr int HEIGHT = 64;
+  static constexpr int BUFS = kMode == kWeightBwd ? 2 : 1;
   static constexpr int STAGES = kMode == kWeightBwd ? 5 : 6;
-  static constexpr int TURN_BYTES = HEIGHT * 256;
+  static constexpr int TURN_BYTES = BUFS * HEIGHT * 256;
   static constexpr int OUT_OFF = STAGES * kStageBytes;
   static constexpr int RING_OFF = OUT_OFF + kTurns * TURN_BYTES;
   static constexpr int BAR_OFF = RING_OFF + kTileRing * 16;
@@ -152,10 +153,7 @@ __device__ __forceinline__ bool ring_put(const TileRing& r, uint32_t n, uint32_t
   *const_cast<volatile int*>(&r.tile[slot].z) = v.z;
   *const_cast<volatile int*>(&r.tile[slot].w) = v.w;
   mbar_arrive(&r.full[slot]);
-  asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(map_to_cta(&r.tile[slot], 1)), "r"(v.x),
-               "r"(v.y), "r"(v.z), "r"(v.w)
-               : "memory");
-  mbar_arrive_cluster(map_to_cta(&r.full[slot], 1));
+  send_cluster(map_to_cta(&r.tile[slot], 1), map_to_cta(&r.full[slot], 1), v);
   return true;
 }
 // The n-th tile of this cluster; false when the wait gave up.
@@ -644,17 +642,20 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
 #pragma unroll
         for (int i = 0; i < 4; i += C::HEIGHT / 32) {
           const int r = first + 32 * i;
+          uint8_t* buf = staging + (C::BUFS > 1 ? i / (C::HEIGHT / 32) * C::HEIGHT * 256 : 0);
           if (r < rows) {
-            staging_free();
+            if (leader) tma_store_wait_read<C::BUFS - 1>();
+            __syncwarp();
+            named_barrier_sync(3 + turn, 128);
 #pragma unroll
             for (int j = 0; j < C::HEIGHT / 32; ++j)
               if (r + 32 * j < rows)
-                stage_piece(smem_u32(staging) + j * 32 * 128, q, packed[i + j], lane, C::HEIGHT);
+                stage_piece(smem_u32(buf) + j * 32 * 128, q, packed[i + j], lane, C::HEIGHT);
             fence_proxy_async_smem();
             named_barrier_sync(3 + turn, 128);
-            leave(staging, out.d[kMode == kWeightBwd ? c.mat : 0], &maps.out[kMode == kWeightBwd ? c.mat : 0], r, C::HEIGHT);
-            if (leader) tma_store_commit();
+            leave(buf, out.d[kMode == kWeightBwd ? c.mat : 0], &maps.out[kMode == kWeightBwd ? c.mat : 0], r, C::HEIGHT);
           }
+          if (leader) tma_store_commit();  // (a group for each buffer, of nothing where r lies behind the rows)
         }
       }
     }
@@ -703,6 +704,7 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();
+  linger_after_abort(abort_flag);
   tc_fence_after();
   if (warp == 1) {
     __syncwarp();
