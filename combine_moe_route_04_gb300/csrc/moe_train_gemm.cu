@@ -20,13 +20,16 @@
 // staging first and read with ldmatrix, which gives each thread the elements
 // whose dh it holds; dg and du go back to the same places.
 //
+// In the weight backward a cluster takes a run of column tiles over the same rows of
+// a gradient matrix, and where the reduction's stages of the second operand all have
+// room (STAGES), they stay for the run's tiles: half the traffic from L2.
+//
 // What bounds it (64 experts of 4096 x 1536, 256 rows each): the down and up backward
-// HBM, 1.14 GB in 205 us and 1.85 GB in 325 us (5.6 and 5.7 TB/s; with 8 rows per
-// expert 5.9 and 6.9); the weight backward, 2.4 GB of gradients in 590 us, the latency
-// of a tile: 18432 of them with a reduction of four stages each, whose loads wait for
-// L2 and whose 128 KB leave under the next tile's work (with 8 rows per expert 510 us,
-// bound by that epilogue; with 1000 rows 1720 us, 1.44 PFLOP/s).  One dense block of
-// 5003 rows, 2176 x 5760: 100 + 165 + 230 us, 1.2, 1.5 and 1.6 PFLOP/s.
+// HBM, 1.14 GB in 210 us and 1.85 GB in 321 us (5.4 and 5.8 TB/s; with 8 rows per
+// expert 6.2 and 7.1); the weight backward, 2.4 GB of gradients and 0.6 PFLOP, 521 us,
+// the power cap (1.7 GHz and 1370 W when run on and on); with 8 rows per expert 385
+// us, HBM (6.3 TB/s); with 1000 rows 1650 us, 1.50 PFLOP/s.  One dense block of 5003
+// rows, 2176 x 5760: 107 + 167 + 237 us, 1.2, 1.5 and 1.6 PFLOP/s.
 //
 // The reduction of the weight backward ends inside a 16-row step of the MMA when
 // an expert's count is no multiple of 16, and the padding rows behind it may
@@ -50,7 +53,6 @@ constexpr int kStageK = 64;               // reduction elements per stage
 constexpr int kTileM = 256;               // output columns per tile (128 per CTA)
 constexpr int kTileN = 256;               // most output rows per tile
 constexpr int kOperandBytes = 128 * kStageK * 2;  // 128 m (or n) x 64 k
-constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kBoxBytes = kStageK * 128;  // 64 k x 64 columns (weight backward)
 constexpr int kEpiWarps = 8;              // two per TMEM lane quarter, taking 32-row pieces in turn
 constexpr int kTurns = kEpiWarps / 4;
@@ -66,20 +68,21 @@ struct Cfg {
   // readers of a tile: CTA 0's MMA lane, both CTAs' loading lanes, epilogue and
   // clearing warps
   static constexpr int READERS = 3 + 2 * (kEpiWarps + FIX_WARPS);
-  // A turn's staging: dg and du of 32 rows; 64 output rows; or, where reductions
-  // are short and the stores bound the kernel, all of the turn's 128, so that they
-  // leave under the next tile's work (64 experts of 4096 x 1536, 256 rows each: 64
-  // rows and a sixth stage 806 us, where this change made it 700).
+  // A turn's staging: dg and du of 32 rows; or 64 output rows, in the weight backward
+  // twice, so that one half's store is still being read while the other is written
+  // (64 experts of 4096 x 1536, 256 rows each: one buffer of 64 rows and a sixth stage
+  // 806 us, one of 128 rows 700; later, with cheaper hand-overs, 588 and with two of 64 560).
   static constexpr int HEIGHT = 64;
   static constexpr int BUFS = kMode == kWeightBwd ? 2 : 1;
   static constexpr int STAGES = kMode == kWeightBwd ? 5 : 6;
   static constexpr int TURN_BYTES = BUFS * HEIGHT * 256;
-  static constexpr int OUT_OFF = STAGES * kStageBytes;
+  static constexpr int B_OFF = STAGES * kOperandBytes;  // the second operand's slots
+  static constexpr int OUT_OFF = 2 * B_OFF;
   static constexpr int RING_OFF = OUT_OFF + kTurns * TURN_BYTES;
   static constexpr int BAR_OFF = RING_OFF + kTileRing * 16;
-  // full, empty, tail, cleared [STAGES]; tfull, tempty [2]; inputs [kTurns]; drain;
-  // ring full, empty [kTileRing]
-  static constexpr int NUM_BARS = 4 * STAGES + 4 + kTurns + 1 + 2 * kTileRing;
+  // full, empty, tail, cleared, bfree [STAGES]; tfull, tempty [2]; inputs [kTurns];
+  // drain; ring full, empty [kTileRing]
+  static constexpr int NUM_BARS = 5 * STAGES + 4 + kTurns + 1 + 2 * kTileRing;
   static constexpr int SLOT_OFF = BAR_OFF + NUM_BARS * 8;
   static constexpr int SMEM = SLOT_OFF + 16 + 1024;
   static_assert(SMEM <= 232448, "shared memory budget");
@@ -88,6 +91,7 @@ struct Cfg {
 struct Problem {
   int E, H, I;
   int window;      // most rows of a window (down and up backward)
+  int run;         // most tiles of a run (weight backward)
   uint32_t ahead;  // tiles handed out ahead
   int64_t max_rows;
 };
@@ -102,9 +106,11 @@ struct Tile {
   int row;  // first row of the window, or (weight backward) of the expert
   int k;    // length of the reduction
   bool ok, last;
+  bool load_b, free_b;  // weight backward: brings the second operand, is the last to use it
 };
 __device__ __forceinline__ int4 pack_tile(const Tile& c) {
-  return make_int4(c.n | (c.ok ? 1 << 9 : 0) | (c.last ? 1 << 10 : 0) | (c.mat << 11) | (c.e << 13),
+  return make_int4(c.n | (c.ok ? 1 << 9 : 0) | (c.last ? 1 << 10 : 0) | (c.mat << 11) | (c.e << 13) | (c.load_b ? 1 << 21 : 0) |
+                       (c.free_b ? 1 << 22 : 0),
                    (c.m0 / kTileM) | (c.n0 / kTileN << 16), c.row, c.k);
 }
 __device__ __forceinline__ Tile unpack_tile(const int4& v) {
@@ -113,7 +119,9 @@ __device__ __forceinline__ Tile unpack_tile(const int4& v) {
   c.ok = (v.x >> 9) & 1;
   c.last = (v.x >> 10) & 1;
   c.mat = (v.x >> 11) & 3;
-  c.e = v.x >> 13;
+  c.e = (v.x >> 13) & 255;
+  c.load_b = (v.x >> 21) & 1;
+  c.free_b = (v.x >> 22) & 1;
   c.m0 = (v.y & 0xFFFF) * kTileM;
   c.n0 = (v.y >> 16) * kTileN;
   c.row = v.z;
@@ -174,11 +182,21 @@ __device__ __forceinline__ void ring_release(const TileRing& r, uint32_t n, uint
   else mbar_arrive_peer(empty0 + 8u * slot);
 }
 
+// Runs of `tiles` column tiles, of at most `run`, as even as they come.
+__device__ __forceinline__ int even_run(int tiles, int run) {
+  const int runs = (tiles + run - 1) / run;
+  return (tiles + runs - 1) / runs;
+}
+
 // The scheduler: one warp, a lane knowing eight experts.
 //   down and up backward: an expert's c rows are cut into ceil(c / window) windows of
 //   equal size (rounded up to 16), so that those which share a weight tile run in
 //   step; tiles in the order expert, column tile, window.
-//   weight backward: expert, then gate / up / down, then row tile, column tile.
+//   weight backward: what is drawn is a run of column tiles (of dWg and dWu, whose
+//   second operand is X, or of dWd, whose second operand is h) over one row tile, so
+//   that the second operand is brought once for all of them; order: expert, row tile,
+//   run, first of dWg and dWu, then of dWd.  Runs have one tile where the operand's
+//   stages do not all stay.
 template <int kMode>
 __device__ __forceinline__ void schedule(const TileRing& ring, const Problem& p, const int32_t* off_pad,
                                          const int32_t* counts, uint32_t cluster, uint32_t nclusters, int lane,
@@ -186,7 +204,11 @@ __device__ __forceinline__ void schedule(const TileRing& ring, const Problem& p,
   constexpr int per = kMaxExperts / 32;
   const uint32_t all = 0xffffffffu;
   const int ti = (p.I + kTileM - 1) / kTileM, th = (p.H + kTileM - 1) / kTileM;
-  const int col_tiles = kMode == kDownBwd ? ti : th;
+  const int col_tiles = kMode == kWeightBwd ? 1 : kMode == kDownBwd ? ti : th;
+  // lengths and numbers of a row tile's runs
+  const int len_x = even_run(2 * ti, p.run), runs_x = (2 * ti + len_x - 1) / len_x;
+  const int len_h = even_run(th, p.run), runs_h = (th + len_h - 1) / len_h;
+  auto stays = [](int rows) { return rows <= Cfg<kMode>::STAGES * kStageK; };
   int cnt[per], off[per + 1], nw[per];
   int sum = 0;
 #pragma unroll
@@ -204,10 +226,13 @@ __device__ __forceinline__ void schedule(const TileRing& ring, const Problem& p,
       record_status(status, kStatusBounds);
       cnt[i] = kMode == kWeightBwd ? -1 : 0;
     }
-    nw[i] = cnt[i] > 0 ? (cnt[i] - 1) / p.window + 1 : 0;
+    if constexpr (kMode == kWeightBwd)
+      nw[i] = e >= p.E || cnt[i] < 0 ? 0 : stays(cnt[i]) ? th * runs_x + ti * runs_h : 3 * th * ti;
+    else
+      nw[i] = cnt[i] > 0 ? (cnt[i] - 1) / p.window + 1 : 0;
     sum += nw[i];
   }
-  int incl = sum;  // windows up to this lane's last expert
+  int incl = sum;  // windows (or runs) up to this lane's last expert
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int y = __shfl_up_sync(all, incl, o);
@@ -215,9 +240,9 @@ __device__ __forceinline__ void schedule(const TileRing& ring, const Problem& p,
   }
   const int windows = __shfl_sync(all, incl, 31);
   // windows of counts that fit the buffers: nw of them hold more than window * (nw - 1) rows
-  const bool fits = static_cast<int64_t>(windows - p.E) * p.window <= p.max_rows;
+  const bool fits = kMode == kWeightBwd || static_cast<int64_t>(windows - p.E) * p.window <= p.max_rows;
   if (!fits && lane == 0) record_status(status, kStatusBounds);
-  const int total = kMode == kWeightBwd ? p.E * 3 * ti * th : fits ? col_tiles * windows : 0;
+  const int total = fits ? col_tiles * windows : 0;
 
   // two draws on their way (with one, a short tile's time was the atomic's under
   // the output's traffic)
@@ -228,42 +253,38 @@ __device__ __forceinline__ void schedule(const TileRing& ring, const Problem& p,
   }
   bool drew_zero = false;
   int tile = static_cast<int>(cluster);
-  for (uint32_t n = 0;; ++n) {
-    Tile c{0, 0, 0, 0, 0, 0, 0, false, tile >= total};
+  for (uint32_t n = 0;;) {
+    Tile c{0, 0, 0, 0, 0, 0, 0, false, tile >= total, false, false};
     int owner = 0;  // the lane that knows the tile's expert
+    int first = 0, len = 1;  // weight backward: the run's first column tile, its tiles
     if (tile < total) {
-      if constexpr (kMode == kWeightBwd) {
-        const int e = tile / (3 * ti * th);
-        int at = tile - e * 3 * ti * th;
-        owner = e / per;
-        c.e = e;
-        c.mat = at / (ti * th);
-        at -= c.mat * ti * th;
-        const int tm = c.mat == 2 ? th : ti;  // column tiles
-        const int tn = at / tm;
-        c.m0 = (at - tn * tm) * kTileM;
-        c.n0 = tn * kTileN;
-        c.n = min(kTileN, (c.mat == 2 ? p.I : p.H) - c.n0);
+      const int q = tile / col_tiles;  // (all column tiles of a window's expert lie together)
+      owner = __ffs(__ballot_sync(all, incl > q)) - 1;
+      int base = incl - sum;  // windows before this lane's first expert
 #pragma unroll
-        for (int i = 0; i < per; ++i) {
-          if (i == e % per) {
+      for (int i = 0; i < per; ++i) {
+        if (q >= base && q < base + nw[i]) {
+          c.e = lane * per + i;
+          if constexpr (kMode == kWeightBwd) {
+            const int lx = stays(cnt[i]) ? len_x : 1, lh = stays(cnt[i]) ? len_h : 1;
+            const int rx = stays(cnt[i]) ? runs_x : 2 * ti, rh = stays(cnt[i]) ? runs_h : th;
+            const int at = q - base;
+            const bool of_x = at < th * rx;
+            const int a = of_x ? at : at - th * rx;
+            const int panel = a / (of_x ? rx : rh);
+            first = of_x ? (a - panel * rx) * lx : (a - panel * rh) * lh;
+            len = of_x ? min(lx, 2 * ti - first) : min(lh, th - first);
+            c.mat = of_x ? 0 : 2;
+            c.n0 = panel * kTileN;
+            c.n = min(kTileN, (of_x ? p.H : p.I) - c.n0);
             c.row = off[i];
             c.k = cnt[i];
-          }
-        }
-        c.ok = c.k >= 0;
-      } else {
-        const int q = tile / col_tiles;  // (all column tiles of a window's expert lie together)
-        owner = __ffs(__ballot_sync(all, incl > q)) - 1;
-        int base = incl - sum;  // windows before this lane's first expert
-#pragma unroll
-        for (int i = 0; i < per; ++i) {
-          if (q >= base && q < base + nw[i]) {
+            c.ok = true;
+          } else {
             const int local = tile - col_tiles * base;
             const int j = local / nw[i];
             const int w = local - j * nw[i];
             const int size = ((cnt[i] + nw[i] - 1) / nw[i] + 15) / 16 * 16;
-            c.e = lane * per + i;
             c.mat = nw[i] == 1 ? 1 : 0;
             c.m0 = j * kTileM;
             c.n = min(size, cnt[i] - size * w);
@@ -271,13 +292,28 @@ __device__ __forceinline__ void schedule(const TileRing& ring, const Problem& p,
             c.k = kMode == kDownBwd ? p.H : 2 * p.I;
             c.ok = c.n > 0;
           }
-          base += nw[i];
         }
+        base += nw[i];
       }
     }
     bool put = true;
-    if (lane == owner) put = ring_put(ring, n, p.ahead, c, abort, status);
+    if (lane == owner) {
+      if (kMode == kWeightBwd && !c.last) {
+        const bool of_x = c.mat != 2;
+        for (int j = 0; j < len && put; ++j) {
+          const int m = first + j;
+          if (of_x) c.mat = m >= ti ? 1 : 0;
+          c.m0 = (c.mat == 1 ? m - ti : m) * kTileM;
+          c.load_b = j == 0;
+          c.free_b = j == len - 1;
+          put = ring_put(ring, n + j, p.ahead, c, abort, status);
+        }
+      } else {
+        put = ring_put(ring, n, p.ahead, c, abort, status);
+      }
+    }
     if (__any_sync(all, !put) || tile >= total) break;
+    n += kMode == kWeightBwd ? static_cast<uint32_t>(__shfl_sync(all, len, owner)) : 1u;
     const uint32_t d = __shfl_sync(all, drawn, 0);
     drew_zero |= d == 0u;
     // a cleared counter gives less than total + 3 clusters here
@@ -336,7 +372,8 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
   uint64_t* empty = full + C::STAGES;
   uint64_t* tail = empty + C::STAGES;      // this CTA's loads of a stage that is to be cleared
   uint64_t* cleared = tail + C::STAGES;    // used in CTA 0: CTA 1 has cleared its part
-  uint64_t* tfull = cleared + C::STAGES;
+  uint64_t* bfree = cleared + C::STAGES;   // weight backward: a slot of the second operand
+  uint64_t* tfull = bfree + C::STAGES;
   uint64_t* tempty = tfull + 2;
   uint64_t* inbar = tempty + 2;          // [kTurns] g and u of a piece
   uint64_t* drain = inbar + kTurns;
@@ -354,6 +391,7 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
       mbar_init(&empty[s], 1);
       mbar_init(&tail[s], 1);
       mbar_init(&cleared[s], 1);
+      mbar_init(&bfree[s], 1);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tfull[a], 1);
@@ -394,7 +432,7 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
       const uint64_t pol_keep = policy_evict_last();
       const uint64_t pol_normal = policy_evict_normal();
       const uint64_t pol_once = policy_evict_first();
-      uint32_t it = 0;
+      uint32_t it = 0, bit = 0;  // stages so far, and (weight backward) of the second operand
       bool stop = false;
       Tile c;
       for (uint32_t n = 0; !stop && ring_get(ring, n, rank, c, abort_flag, status); ++n) {
@@ -407,10 +445,11 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
           const CUtensorMap* ma = &maps.a[c.mat];
           const CUtensorMap* mb = &maps.b[c.mat == 2 ? 1 : 0][0];
           const int n_first = c.n0 + n_half * static_cast<int>(rank);  // 64 or 128 columns
-          const uint32_t mine = static_cast<uint32_t>(2 + n_half / 64) * kBoxBytes;
+          const uint32_t mine = static_cast<uint32_t>(2 + (c.load_b ? n_half / 64 : 0)) * kBoxBytes;
           for (int kb = 0; kb < nk; ++kb, ++it) {
-            const uint32_t s = it % C::STAGES;
-            if (!mbar_wait(&empty[s], ((it / C::STAGES) & 1u) ^ 1u, abort_flag, status)) {
+            const uint32_t s = it % C::STAGES, b = bit % C::STAGES;
+            if (!mbar_wait(&empty[s], ((it / C::STAGES) & 1u) ^ 1u, abort_flag, status) ||
+                (c.load_b && !mbar_wait(&bfree[b], ((bit / C::STAGES) & 1u) ^ 1u, abort_flag, status))) {
               stop = true;
               break;
             }
@@ -418,12 +457,16 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
             const uint32_t fb = own ? map_to_cta(&tail[s], rank) : full0 + 8u * s;
             if (own) mbar_arrive_expect_tx(&tail[s], mine);
             else if (rank == 0) mbar_arrive_expect_tx(&full[s], 2u * mine);
-            uint8_t* st = smem + s * kStageBytes;
+            uint8_t* st = smem + s * kOperandBytes;
             const int row = c.row + kb * kStageK;
             tma_load_2d_pair(st, ma, fb, m_first, row, pol_keep);
             tma_load_2d_pair(st + kBoxBytes, ma, fb, m_first + 64, row, pol_keep);
-            tma_load_2d_pair(st + kOperandBytes, mb, fb, n_first, row, pol_keep);
-            if (n_half > 64) tma_load_2d_pair(st + kOperandBytes + kBoxBytes, mb, fb, n_first + 64, row, pol_keep);
+            if (c.load_b) {
+              uint8_t* sb = smem + C::B_OFF + b * kOperandBytes;
+              tma_load_2d_pair(sb, mb, fb, n_first, row, pol_keep);
+              if (n_half > 64) tma_load_2d_pair(sb + kBoxBytes, mb, fb, n_first + 64, row, pol_keep);
+              ++bit;
+            }
           }
         } else {
           // weights that one window alone reads leave L2 first
@@ -440,11 +483,11 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
               break;
             }
             if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
-            uint8_t* st = smem + s * kStageBytes;
+            uint8_t* st = smem + s * kOperandBytes;
             const int term = kb >= half ? 1 : 0;
             const int k0 = (kb - term * half) * kStageK;
             tma_load_2d_pair(st, &maps.a[term], full0 + 8u * s, k0, m_row, pol_w);
-            tma_load_2d_pair(st + kOperandBytes, &maps.b[term][pick], full0 + 8u * s, k0, row, pol_keep);
+            tma_load_2d_pair(st + C::B_OFF, &maps.b[term][pick], full0 + 8u * s, k0, row, pol_keep);
           }
         }
       }
@@ -455,6 +498,12 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
         int no_abort = 0;
         mbar_wait(&empty[s], (last / C::STAGES) & 1u, &no_abort, status);
       }
+      const uint32_t nb = bit < C::STAGES ? bit : C::STAGES;
+      for (uint32_t b = 0; b < nb; ++b) {
+        const uint32_t last = b + C::STAGES * ((bit - 1 - b) / C::STAGES);
+        int no_abort = 0;
+        mbar_wait(&bfree[b], (last / C::STAGES) & 1u, &no_abort, status);
+      }
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -463,7 +512,7 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
       constexpr bool kOuterK = kMode == kWeightBwd;  // k is the operands' outer axis
       constexpr uint32_t idesc_base = (1u << 4) | (1u << 7) | (1u << 10) | (kOuterK ? 3u << 15 : 0u) |
                                       ((256u >> 4) << 24);
-      uint32_t it = 0;
+      uint32_t it = 0, bit = 0;  // (bit: where the run's second operand starts)
       uint32_t tcount = 0;
       bool stop = false;
       Tile c;
@@ -484,8 +533,9 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
             break;
           }
           tc_fence_after();
-          const uint32_t sa = smem_u32(smem + s * kStageBytes);
-          const uint32_t sb = sa + kOperandBytes;
+          const uint32_t b = kOuterK ? (bit + kb) % C::STAGES : s;
+          const uint32_t sa = smem_u32(smem + s * kOperandBytes);
+          const uint32_t sb = smem_u32(smem + C::B_OFF + b * kOperandBytes);
           if constexpr (kOuterK) {
             // 64-column boxes 8 KB apart, 8-row groups 1 KB apart, a step of 16 rows 2 KB
             const int steps = min(kStageK, c.k - kb * kStageK + 15) / 16;
@@ -500,8 +550,10 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
                               smem_desc(sb + kk * 32, 16, 1024, kSwizzle128B), idesc, (kb | kk) != 0 ? 1u : 0u);
           }
           tc_commit_pair(&empty[s], 0x3);
+          if (kOuterK && c.free_b) tc_commit_pair(&bfree[b], 0x3);
         }
         if (stop) break;
+        if (c.free_b) bit += nk;
         tc_commit_pair(&tfull[a], 0x3);
         ++tcount;
       }
@@ -667,7 +719,7 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
     __syncwarp();
   } else if constexpr (kMode == kWeightBwd) {
     // ---------------------------------------------------------- clearing (both CTAs)
-    uint32_t it = 0;
+    uint32_t it = 0, bit = 0;
     uint32_t phases = 0;  // bit s: parity of the next use of stage s's barriers
     for (uint32_t n = 0;; ++n) {
       Tile c{};
@@ -676,6 +728,7 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
       if (lane == 0) ring_release(ring, n, rank, rempty0);
       if (!c.ok) continue;
       it += stages_of(c.k);
+      if (c.load_b) bit += stages_of(c.k);
       if (!has_tail(c)) continue;
       const uint32_t s = (it - 1) % C::STAGES;
       const uint32_t ph = (phases >> s) & 1u;
@@ -683,8 +736,10 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
       if (__any_sync(0xffffffffu, !mbar_wait(&tail[s], ph, abort_flag, status))) break;
       const int first = c.k & (kStageK - 1), last = (first + 15) & ~15;
       // lane: box (two of each operand, or one of the second) and 16-byte chunk
-      uint8_t* box = smem + s * kStageBytes + (lane >> 3) * kBoxBytes + (lane & 7) * 16;
-      for (int r = first; r < last; ++r) *reinterpret_cast<uint4*>(box + r * 128) = make_uint4(0u, 0u, 0u, 0u);
+      const int slot = lane < 16 ? static_cast<int>(s) : C::STAGES + static_cast<int>((bit - 1) % C::STAGES);
+      uint8_t* box = smem + slot * kOperandBytes + ((lane >> 3) & 1) * kBoxBytes + (lane & 7) * 16;
+      if (lane < 16 || c.load_b)
+        for (int r = first; r < last; ++r) *reinterpret_cast<uint4*>(box + r * 128) = make_uint4(0u, 0u, 0u, 0u);
       fence_proxy_async_smem();
       __syncwarp();
       bool ok = true;
@@ -748,6 +803,12 @@ cudaError_t launch(const moe_shape& s, const TrainMaps& m, const TrainOut& out, 
   const int64_t stages = k / kStageK + 1;
   int64_t ahead = 3 + 8 / stages;
   if (ahead > kTileRing) ahead = kTileRing;
+  // Runs of at most three tiles, and at least sixteen of them for every cluster (64
+  // experts of 4096 x 1536, 256 rows each on average: 555 us with runs of one tile, 521
+  // with three, 528 with six, 538 with eight; 320 rows 640, 585, 580, 592; 16 rows,
+  // which load little, 383, 385, 391, 393).
+  int64_t run = tiles / (16 * clusters);
+  run = run < 1 ? 1 : run > 3 ? 3 : run;
   if (tiles < clusters) clusters = tiles;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * clusters));
@@ -764,7 +825,7 @@ cudaError_t launch(const moe_shape& s, const TrainMaps& m, const TrainOut& out, 
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, train_gemm_kernel<kMode>, m, out, off_pad, counts,
-                            Problem{s.E, s.H, s.I, window, static_cast<uint32_t>(ahead), max_rows_of(s)}, status, sched);
+                            Problem{s.E, s.H, s.I, window, static_cast<int>(run), static_cast<uint32_t>(ahead), max_rows_of(s)}, status, sched);
 }
 
 }  // namespace
