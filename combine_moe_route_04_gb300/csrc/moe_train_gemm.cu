@@ -796,6 +796,21 @@ cudaError_t launch(const moe_shape& s, const TrainMaps& m, const TrainOut& out, 
   const int64_t cols = kMode == kDownBwd ? ti : th;
   int window = kTileN;
   while (window > 64 && (R / (window / 2) + touched) * cols <= clusters) window /= 2;
+  // One expert has all rows, and its windows are taken as they fill the last wave of
+  // tiles best, a tile costing its rows and half a tile's more (5003 rows, 2176 x 5760:
+  // up 164 us with 256 rows, 154 so; 3000 rows, 2048 x 2048: down 44 and 35, up 61 and
+  // 45; without the constant, 16384 rows of 4096 x 4096: down 474 where 256 rows take
+  // 376).
+  if (s.E == 1 && window == kTileN) {
+    int64_t best = 0;
+    for (int w = kTileN; w >= kTileN / 2; w -= 16) {
+      const int64_t cost = ((R + w - 1) / w * cols + clusters - 1) / clusters * (w + kTileN / 2);
+      if (best == 0 || cost < best) {
+        best = cost;
+        window = w;
+      }
+    }
+  }
   const int64_t tiles = kMode == kWeightBwd ? s.E * 3 * ti * th : (R / window + touched) * cols;
   // tiles handed out ahead: enough that the loads of eight stages know theirs
   // (what a cluster has been handed no other can take)

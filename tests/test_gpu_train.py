@@ -122,6 +122,28 @@ def test_weight_backward(moe, counts, size):
             ref.check(w[e], want[name], "%s of expert %d" % (name, e))
 
 
+# row counts around the ends of MMA steps (16), of stages (64) and of what stays in
+# shared memory for a run (320), long ones between
+RUN_COUNTS = [0, 1, 7, 16, 17, 63, 64, 65, 130, 0, 255, 256, 257, 300, 319, 320, 321, 15, 700, 335, 384, 2]
+
+
+@pytest.mark.parametrize("size", [(256, 1280), (640, 384), (128, 2176), (1152, 256)], ids=lambda s: "%dx%d" % s)
+def test_weight_backward_in_runs(moe, size):
+    """Gradient tiles enough that a cluster takes several of a row tile in turn, over
+    one copy of their second operand."""
+    counts = [RUN_COUNTS[(5 * e + e // 22) % len(RUN_COUNTS)] for e in range(256)]
+    test_weight_backward(moe, counts, size)
+
+
+@pytest.mark.parametrize("case", [([1500], 2048, 256), ([3001], 256, 1664), ([2003], 1408, 1408)], ids=str)
+def test_one_expert_of_many_rows(moe, case):
+    """A dense block: windows of other sizes than powers of two."""
+    counts, H, I = case
+    test_down_backward(moe, counts, (H, I))
+    test_up_backward(moe, counts, (H, I))
+    test_weight_backward(moe, counts, (H, I))
+
+
 @pytest.mark.parametrize("counts", COUNTS, ids=lambda c: "-".join(map(str, c)))
 @pytest.mark.parametrize("size", SIZES, ids=lambda s: "%dx%d" % s)
 def test_up_train(moe, counts, size):
