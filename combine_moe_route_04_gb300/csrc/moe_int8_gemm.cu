@@ -248,20 +248,24 @@ __device__ __forceinline__ void schedule(const TileRing& ring, int E, int NT, in
       const int q = tile / NT;  // (all column tiles of a window's expert lie together)
       owner = __ffs(__ballot_sync(all, incl > q)) - 1;
       int base = incl - sum;  // windows before this lane's first expert
+      int rows = 0, row = 0, nw = 1, local = 0;  // the expert's, and the window's place
 #pragma unroll
       for (int i = 0; i < per; ++i) {
-        const int nw = (cnt[i] + kTok - 1) / kTok;
-        if (q >= base && q < base + nw) {
-          const int local = tile - NT * base;
+        const int n_windows = (cnt[i] + kTok - 1) / kTok;
+        if (q >= base && q < base + n_windows) {
           c.e = lane * per + i;
-          c.j = local / nw;
-          const int w = local - c.j * nw;
-          c.row0 = off[i] + kTok * w;
-          c.rows = min(kTok, cnt[i] - kTok * w);
-          c.alone = nw == 1;
+          rows = cnt[i];
+          row = off[i];
+          nw = n_windows;
+          local = tile - NT * base;
         }
-        base += nw;
+        base += n_windows;
       }
+      c.j = local / nw;
+      const int w = local - c.j * nw;
+      c.row0 = row + kTok * w;
+      c.rows = min(kTok, rows - kTok * w);
+      c.alone = nw == 1;
     }
     bool put = true;
     if (lane == owner) put = ring_put(ring, n, c, abort, status);

@@ -91,7 +91,9 @@ struct Cfg {
 struct Problem {
   int E, H, I;
   int window;      // most rows of a window (down and up backward)
-  int run;         // most tiles of a run (weight backward)
+  // weight backward, over a row tile: lengths and numbers of the runs of dWg's and
+  // dWu's column tiles, and of dWd's
+  int len_x, runs_x, len_h, runs_h;
   uint32_t ahead;  // tiles handed out ahead
   int64_t max_rows;
 };
@@ -182,12 +184,6 @@ __device__ __forceinline__ void ring_release(const TileRing& r, uint32_t n, uint
   else mbar_arrive_peer(empty0 + 8u * slot);
 }
 
-// Runs of `tiles` column tiles, of at most `run`, as even as they come.
-__device__ __forceinline__ int even_run(int tiles, int run) {
-  const int runs = (tiles + run - 1) / run;
-  return (tiles + runs - 1) / runs;
-}
-
 // The scheduler: one warp, a lane knowing eight experts.
 //   down and up backward: an expert's c rows are cut into ceil(c / window) windows of
 //   equal size (rounded up to 16), so that those which share a weight tile run in
@@ -205,9 +201,6 @@ __device__ __forceinline__ void schedule(const TileRing& ring, const Problem& p,
   const uint32_t all = 0xffffffffu;
   const int ti = (p.I + kTileM - 1) / kTileM, th = (p.H + kTileM - 1) / kTileM;
   const int col_tiles = kMode == kWeightBwd ? 1 : kMode == kDownBwd ? ti : th;
-  // lengths and numbers of a row tile's runs
-  const int len_x = even_run(2 * ti, p.run), runs_x = (2 * ti + len_x - 1) / len_x;
-  const int len_h = even_run(th, p.run), runs_h = (th + len_h - 1) / len_h;
   auto stays = [](int rows) { return rows <= Cfg<kMode>::STAGES * kStageK; };
   int cnt[per], off[per + 1], nw[per];
   int sum = 0;
@@ -227,7 +220,7 @@ __device__ __forceinline__ void schedule(const TileRing& ring, const Problem& p,
       cnt[i] = kMode == kWeightBwd ? -1 : 0;
     }
     if constexpr (kMode == kWeightBwd)
-      nw[i] = e >= p.E || cnt[i] < 0 ? 0 : stays(cnt[i]) ? th * runs_x + ti * runs_h : 3 * th * ti;
+      nw[i] = e >= p.E || cnt[i] < 0 ? 0 : stays(cnt[i]) ? th * p.runs_x + ti * p.runs_h : 3 * th * ti;
     else
       nw[i] = cnt[i] > 0 ? (cnt[i] - 1) / p.window + 1 : 0;
     sum += nw[i];
@@ -261,39 +254,42 @@ __device__ __forceinline__ void schedule(const TileRing& ring, const Problem& p,
       const int q = tile / col_tiles;  // (all column tiles of a window's expert lie together)
       owner = __ffs(__ballot_sync(all, incl > q)) - 1;
       int base = incl - sum;  // windows before this lane's first expert
+      int rows = 0, row = 0, parts = 1, at = 0;  // the expert's, and the window's place
 #pragma unroll
       for (int i = 0; i < per; ++i) {
         if (q >= base && q < base + nw[i]) {
           c.e = lane * per + i;
-          if constexpr (kMode == kWeightBwd) {
-            const int lx = stays(cnt[i]) ? len_x : 1, lh = stays(cnt[i]) ? len_h : 1;
-            const int rx = stays(cnt[i]) ? runs_x : 2 * ti, rh = stays(cnt[i]) ? runs_h : th;
-            const int at = q - base;
-            const bool of_x = at < th * rx;
-            const int a = of_x ? at : at - th * rx;
-            const int panel = a / (of_x ? rx : rh);
-            first = of_x ? (a - panel * rx) * lx : (a - panel * rh) * lh;
-            len = of_x ? min(lx, 2 * ti - first) : min(lh, th - first);
-            c.mat = of_x ? 0 : 2;
-            c.n0 = panel * kTileN;
-            c.n = min(kTileN, (of_x ? p.H : p.I) - c.n0);
-            c.row = off[i];
-            c.k = cnt[i];
-            c.ok = true;
-          } else {
-            const int local = tile - col_tiles * base;
-            const int j = local / nw[i];
-            const int w = local - j * nw[i];
-            const int size = ((cnt[i] + nw[i] - 1) / nw[i] + 15) / 16 * 16;
-            c.mat = nw[i] == 1 ? 1 : 0;
-            c.m0 = j * kTileM;
-            c.n = min(size, cnt[i] - size * w);
-            c.row = off[i] + size * w;
-            c.k = kMode == kDownBwd ? p.H : 2 * p.I;
-            c.ok = c.n > 0;
-          }
+          rows = cnt[i];
+          row = off[i];
+          parts = nw[i];
+          at = tile - col_tiles * base;
         }
         base += nw[i];
+      }
+      c.ok = lane == owner;
+      if constexpr (kMode == kWeightBwd) {
+        const bool of_x = at < th * (stays(rows) ? p.runs_x : 2 * ti);
+        const int a = of_x ? at : at - th * (stays(rows) ? p.runs_x : 2 * ti);
+        const int runs = of_x ? (stays(rows) ? p.runs_x : 2 * ti) : stays(rows) ? p.runs_h : th;
+        const int most = !stays(rows) ? 1 : of_x ? p.len_x : p.len_h;
+        const int panel = a / runs;
+        first = (a - panel * runs) * most;
+        len = min(most, (of_x ? 2 * ti : th) - first);
+        c.mat = of_x ? 0 : 2;
+        c.n0 = panel * kTileN;
+        c.n = min(kTileN, (of_x ? p.H : p.I) - c.n0);
+        c.row = row;
+        c.k = rows;
+      } else {
+        const int j = at / parts;
+        const int w = at - j * parts;
+        const int size = ((rows + parts - 1) / parts + 15) / 16 * 16;
+        c.mat = parts == 1 ? 1 : 0;
+        c.m0 = j * kTileM;
+        c.n = min(size, rows - size * w);
+        c.row = row + size * w;
+        c.k = kMode == kDownBwd ? p.H : 2 * p.I;
+        c.ok = c.n > 0;
       }
     }
     bool put = true;
@@ -824,6 +820,15 @@ cudaError_t launch(const moe_shape& s, const TrainMaps& m, const TrainOut& out, 
   // which load little, 383, 385, 391, 393).
   int64_t run = tiles / (16 * clusters);
   run = run < 1 ? 1 : run > 3 ? 3 : run;
+  auto even = [run](int64_t n) {  // length of n tiles' runs, as even as they come
+    const int64_t runs = (n + run - 1) / run;
+    return (n + runs - 1) / runs;
+  };
+  Problem p = {s.E, s.H, s.I, window, 0, 0, 0, 0, static_cast<uint32_t>(ahead), max_rows_of(s)};
+  p.len_x = static_cast<int>(even(2 * ti));
+  p.len_h = static_cast<int>(even(th));
+  p.runs_x = static_cast<int>((2 * ti + p.len_x - 1) / p.len_x);
+  p.runs_h = static_cast<int>((th + p.len_h - 1) / p.len_h);
   if (tiles < clusters) clusters = tiles;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * clusters));
@@ -840,7 +845,7 @@ cudaError_t launch(const moe_shape& s, const TrainMaps& m, const TrainOut& out, 
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, train_gemm_kernel<kMode>, m, out, off_pad, counts,
-                            Problem{s.E, s.H, s.I, window, static_cast<int>(run), static_cast<uint32_t>(ahead), max_rows_of(s)}, status, sched);
+                            p, status, sched);
 }
 
 }  // namespace
