@@ -15,6 +15,7 @@
 // Inputs may be what an earlier kernel of a chain of dependent launches wrote, so
 // they are read past L1 (__ldcg), not through the non-coherent path.
 #include <cstdint>
+#include <mutex>
 
 #include "moe_device.cuh"
 #include "moe_internal.h"
@@ -199,21 +200,26 @@ __global__ void __launch_bounds__(256) dequantize_rows_kernel(const int8_t* __re
 // Weights w [E][K][N] to codes [E][N][K], the reduction axis K contiguous, and a
 // scale per (e, n).  A cluster of kWCtas CTAs takes 32 columns of one expert, each CTA
 // its share of their rows: a first pass over them (64 bytes each) for the maxima,
-// which meet in distributed shared memory, a second one, backwards, in steps of kWk
-// rows for the codes, which cross shared memory once so that each column's bytes
-// leave together.  Four CTAs an SM: much of what they hold is in L2 for the second
-// pass, and one's loads run under the others' arithmetic.  With one, two and four CTAs
-// a cluster: 64 weights of 4096 x 1536 304, 275, 259 us; of 7168 x 2048 698, 665, 694;
-// of 1536 x 4096 255, 304, 483 (reading and writing once would take 178); 7 of 1408 x
-// 640, which fill no device, 11.8, 9.5, 7.9.  ctas_of takes two from K = 2048 on, and
-// four where these would leave room.  (Two CTAs of 512 threads an SM 302 and 329.  A
-// cluster of eight CTAs that holds 64 columns in registers and reads them once took 305
-// and 436: a CTA's fixed steps, one after the other, bound it.)
+// which meet in distributed shared memory, a second one, in steps of kWk rows, for the
+// codes, which cross shared memory once so that each column's bytes leave together.
+// The first pass brings the rows to shared memory, each thread those that it takes in
+// the second (kHeld; up to kMostHeld rows, two or three CTAs an SM, so that one's loads
+// run under the others' arithmetic); longer columns are read twice, backwards the
+// second time, when much of them is still in L2.
+//
+// 64 weights of 4096 x 1536 239 us with four CTAs of 1024 rows, where reading and
+// writing once would take 178 (8 CTAs 276; two that read twice 275); of 1536 x 4096
+// 230 with one (two 255, four 311; reading twice 255); of 2816 x 2048 237 with two (286);
+// of 7168 x 2048 603 with eight (665); 7 of 1408 x 640, which fill no device, 8.2, 7.8
+// and 7.0 with one, two and four.  So: as few CTAs as hold the rows, and more, up to
+// four, where the grid leaves room.  (A cluster of eight that holds 64 columns in
+// registers took 305 us for 4096 x 1536 and 436 for 1536 x 4096.)
 constexpr int kWn = 32;
 constexpr int kWeightThreads = 256;
 constexpr int kWk = kWeightThreads / 4 * 4;  // four rows x eight columns per thread
+constexpr int kMostHeld = 6 * kWk;           // rows of a CTA: 96 KB
 
-template <int kWCtas>
+template <int kWCtas, bool kHeld>
 __global__ void __launch_bounds__(kWeightThreads, 4) quantize_weights_kernel(const uint16_t* __restrict__ w, int K,
                                                                              int N, int8_t* __restrict__ codes,
                                                                              float* __restrict__ scales) {
@@ -224,7 +230,7 @@ __global__ void __launch_bounds__(kWeightThreads, 4) quantize_weights_kernel(con
   pdl_launch_dependents();
   pdl_wait();
   const uint32_t rank = kWCtas > 1 ? cluster_ctarank() : 0u;
-  const int rows = K / kWCtas;  // a multiple of 64
+  const int rows = K / kWCtas;  // a multiple of 16
   const int64_t first = static_cast<int64_t>(rank) * rows;
   const int cg = threadIdx.x & 3;   // columns 8 cg..
   const int kr = threadIdx.x >> 2;  // row of the thread, or group of four rows
@@ -234,13 +240,29 @@ __global__ void __launch_bounds__(kWeightThreads, 4) quantize_weights_kernel(con
   const uint4* src = reinterpret_cast<const uint4*>(w + (e * K + first) * N + n0) + cg;
   const int64_t pitch = N / 8;
   uint4 m = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll 8
-  for (int k = kr; k < rows; k += kWeightThreads / 4) {
-    const uint4 v = __ldcg(src + k * pitch);
+  extern __shared__ uint4 s_held[];
+  auto more = [&](const uint4& v) {
     m.x = max_magnitude(m.x, v.x);
     m.y = max_magnitude(m.y, v.y);
     m.z = max_magnitude(m.z, v.z);
     m.w = max_magnitude(m.w, v.w);
+  };
+  if constexpr (kHeld) {  // each thread's own rows of the second pass
+    uint4* to = s_held + threadIdx.x;
+    for (int k = 4 * kr; k < rows; k += kWk, to += 4 * kWeightThreads)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to + i * kWeightThreads)),
+                     "l"(src + (k + i) * pitch)
+                     : "memory");
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    to = s_held + threadIdx.x;
+    for (int k = 4 * kr; k < rows; k += kWk, to += 4 * kWeightThreads)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) more(to[i * kWeightThreads]);
+  } else {
+#pragma unroll 8
+    for (int k = kr; k < rows; k += kWeightThreads / 4) more(__ldcg(src + k * pitch));
   }
 #pragma unroll
   for (int o = 4; o < 32; o <<= 1) {  // the warp's eight rows
@@ -299,7 +321,8 @@ __global__ void __launch_bounds__(kWeightThreads, 4) quantize_weights_kernel(con
     if (k < rows) {
       uint4 v[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = __ldcg(src + (k + i) * pitch);
+      for (int i = 0; i < 4; ++i)
+        v[i] = kHeld ? s_held[(k0 / kWk * 4 + i) * kWeightThreads + threadIdx.x] : __ldcg(src + (k + i) * pitch);
       const uint32_t a[4][4] = {{v[0].x, v[0].y, v[0].z, v[0].w}, {v[1].x, v[1].y, v[1].z, v[1].w},
                                 {v[2].x, v[2].y, v[2].z, v[2].w}, {v[3].x, v[3].y, v[3].z, v[3].w}};
 #pragma unroll
@@ -332,11 +355,14 @@ __global__ void __launch_bounds__(kWeightThreads, 4) quantize_weights_kernel(con
   }
 }
 
-// CTAs of a cluster of the weights' kernel; strips is the number of its clusters.
-int ctas_of(int64_t K, int64_t strips, int num_sms) {
-  int ctas = K >= 2048 ? 2 : 1;
-  while (ctas < 4 && 2 * strips * ctas <= 4 * num_sms) ctas *= 2;
-  return ctas;
+// The weights' kernel for a cluster of `ctas` CTAs.
+using WeightsKernel = void (*)(const uint16_t*, int, int, int8_t*, float*);
+WeightsKernel weights_kernel(int ctas, bool held) {
+  return !held       ? quantize_weights_kernel<2, false>
+         : ctas == 1 ? quantize_weights_kernel<1, true>
+         : ctas == 2 ? quantize_weights_kernel<2, true>
+         : ctas == 4 ? quantize_weights_kernel<4, true>
+                     : quantize_weights_kernel<8, true>;
 }
 
 int group_of(int64_t cols) {
@@ -384,13 +410,33 @@ cudaError_t launch_dequantize_rows_int8(const int8_t* codes, const float* scales
 
 cudaError_t launch_quantize_weights_int8(const uint16_t* w, int E, int64_t K, int64_t N, int8_t* codes, float* scales,
                                          int num_sms, cudaStream_t st) {
-  const int ctas = ctas_of(K, N / kWn * E, num_sms);
-  auto kernel = ctas == 1   ? quantize_weights_kernel<1>
-                : ctas == 2 ? quantize_weights_kernel<2>
-                            : quantize_weights_kernel<4>;
+  constexpr auto held_bytes = [](int64_t rows) { return (rows + kWk - 1) / kWk * 4 * kWeightThreads * 16; };
+  // the shared-memory opt-in, once per device (host threads may race here)
+  static bool done[64] = {};
+  static std::mutex mu;
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (dev >= 64 || !done[dev]) {
+      for (int ctas = 1; ctas <= 8 && err == cudaSuccess; ctas *= 2)
+        err = cudaFuncSetAttribute(weights_kernel(ctas, true), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                   static_cast<int>(held_bytes(kMostHeld)));
+      if (err != cudaSuccess) return err;
+      if (dev < 64) done[dev] = true;
+    }
+  }
+  int ctas = 1;
+  while (ctas < 8 && K > ctas * kMostHeld) ctas *= 2;
+  const bool held = K <= ctas * kMostHeld;
+  if (!held) ctas = 2;
+  while (held && ctas < 4 && 2 * (N / kWn) * E * ctas <= 4 * num_sms) ctas *= 2;
+  const WeightsKernel kernel = weights_kernel(ctas, held);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(N / kWn), static_cast<unsigned>(ctas), static_cast<unsigned>(E));
   cfg.blockDim = dim3(kWeightThreads);
+  cfg.dynamicSmemBytes = held ? static_cast<size_t>(held_bytes(K / ctas)) : 0;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -86,7 +86,7 @@ def test_quantize_weights(moe, shape):
     assert torch.equal(codes, q) and same_scales(scales, s)
 
 
-@pytest.mark.parametrize("shape", [(40, 384, 512), (24, 1152, 256), (20, 2176, 1024), (80, 128, 256), (9, 4224, 1280)], ids=str)
+@pytest.mark.parametrize("shape", [(40, 384, 512), (24, 1152, 256), (20, 2176, 1024), (80, 128, 256), (9, 4224, 1280), (3, 8320, 2560), (1, 12416, 256), (2, 12800, 512)], ids=str)
 def test_quantize_weights_of_many_columns(moe, shape):
     """Columns enough to fill the device, where a cluster of fewer CTAs takes them."""
     test_quantize_weights(moe, shape)
