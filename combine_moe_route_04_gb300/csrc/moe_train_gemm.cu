@@ -26,8 +26,8 @@
 //
 // What bounds it (64 experts of 4096 x 1536, 256 rows each): the down and up backward
 // HBM, 1.14 GB in 210 us and 1.85 GB in 321 us (5.4 and 5.8 TB/s; with 8 rows per
-// expert 6.2 and 7.1); the weight backward, 2.4 GB of gradients and 0.6 PFLOP, 521 us,
-// the power cap (1.7 GHz and 1370 W when run on and on); with 8 rows per expert 385
+// expert 6.2 and 7.1); the weight backward, 2.4 GB of gradients and 0.6 PFLOP, 520 to
+// 565 us, the power cap (1.7 GHz and 1370 W when run on and on); with 8 rows per expert 385
 // us, HBM (6.3 TB/s); with 1000 rows 1650 us, 1.50 PFLOP/s.  One dense block of 5003
 // rows, 2176 x 5760: 107 + 167 + 237 us, 1.2, 1.5 and 1.6 PFLOP/s.
 //
