@@ -245,6 +245,11 @@ __device__ __forceinline__ void schedule(const TileRing& ring, const Problem& p,
     later = atomicAdd(sched, 1u);
   }
   bool drew_zero = false;
+  // every draw, of lane 0: a cleared counter gives less than total + 2 clusters
+  auto checked = [&](uint32_t d) {
+    drew_zero |= d == 0u;
+    if (d >= static_cast<uint64_t>(total) + 2u * nclusters) record_status(status, kStatusBounds);
+  };
   int tile = static_cast<int>(cluster);
   for (uint32_t n = 0;;) {
     Tile c{0, 0, 0, 0, 0, 0, 0, false, tile >= total, false, false};
@@ -311,16 +316,15 @@ __device__ __forceinline__ void schedule(const TileRing& ring, const Problem& p,
     if (__any_sync(all, !put) || tile >= total) break;
     n += kMode == kWeightBwd ? static_cast<uint32_t>(__shfl_sync(all, len, owner)) : 1u;
     const uint32_t d = __shfl_sync(all, drawn, 0);
-    drew_zero |= d == 0u;
-    // a cleared counter gives less than total + 3 clusters here
+    if (lane == 0) checked(d);
     const uint64_t next = static_cast<uint64_t>(nclusters) + d;
-    if (next >= static_cast<uint64_t>(total) + 3u * nclusters && lane == 0) record_status(status, kStatusBounds);
     tile = next < static_cast<uint64_t>(total) ? static_cast<int>(next) : total;
     drawn = later;
     if (lane == 0) later = atomicAdd(sched, 1u);
   }
   if (lane == 0) {
-    drew_zero |= drawn == 0u || later == 0u;
+    checked(drawn);
+    checked(later);
     __threadfence();
     const uint32_t mine = stopped(1u, cluster + 1u, drew_zero);
     const uint32_t seen = atomicAdd(sched + 1, mine) + mine;
