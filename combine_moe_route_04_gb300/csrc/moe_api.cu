@@ -132,9 +132,14 @@ moe_status run_up_rows(const moe_shape& s, const uint16_t* Xp, const int32_t* co
       !encode_bf16_2d(&m.b1, Wu, EH, s.I, 32, 64) || !encode_bf16_2d(&m.a64, Xp, mr, s.H, 64, 32) ||
       !encode_bf16_2d(&m.a80, Xp, mr, s.H, 80, 32))
     return MOE_ERR_CUDA;
-  if (g != nullptr)
-    return cuda_status(
-        launch_gemm_up_train(s, m, g, u, h, off_pad, counts, status, ws_sched_up(status), win_done, num_sms, st));
+  if (g != nullptr) {
+    SaveMaps save;
+    const uint16_t* out[3] = {g, u, h};
+    for (int i = 0; i < 3; ++i)
+      if (!encode_bf16_groups(&save.out[i], out[i], mr, s.I, 32)) return MOE_ERR_CUDA;
+    return cuda_status(launch_gemm_up_train(s, m, save, g, u, h, off_pad, counts, status, ws_sched_up(status),
+                                            win_done, num_sms, st));
+  }
   return cuda_status(launch_gemm_up(s, m, h, off_pad, counts, status, ws_sched_up(status), win_done, num_sms, st));
 }
 

@@ -58,8 +58,10 @@
 // are drained (bounded) and TMEM is freed before exit.
 #include <cstdint>
 #include <mutex>
+#include <type_traits>
 
 #include "moe_device.cuh"
+#include "moe_epilogue.cuh"
 #include "moe_internal.h"
 
 namespace moe {
@@ -134,13 +136,16 @@ constexpr int S_TILE_READERS = 1 + S_EPI_WARPS + 1 + S_EPI_WARPS;
 // operand reads) per FLOP that the MMA shape and TMEM allow.  The two
 // accumulators fill TMEM, so there is one accumulator set and the epilogue
 // drain is not overlapped.
-template <bool kUp>
+// Training keeps g and u: pieces of 32 rows of g, u and h are staged for TMA in
+// place of two stages.
+template <bool kUp, bool kSave>
 struct SwapCfg {
   static constexpr int TILE_COLS = kUp ? 256 : 512;      // output columns per tile
   static constexpr int STAGE_BYTES = 2 * S_W_BYTES + S_T_BYTES;  // 24 KB
-  static constexpr int STAGES = 9;
+  static constexpr int STAGES = kSave ? 7 : 9;
   static constexpr int NBUF = 1;                         // accumulator sets in TMEM
-  static constexpr int BAR_OFF = STAGES * STAGE_BYTES;
+  static constexpr int OUT_OFF = STAGES * STAGE_BYTES;
+  static constexpr int BAR_OFF = OUT_OFF + (kSave ? 3 * S_EPI_SPLIT * kPieceBytes : 0);
   static constexpr int NUM_BARS = 2 * STAGES + 2 * NBUF + 1 + 2 * S_TILE_RING;
   static constexpr int WIN_OFF = BAR_OFF + NUM_BARS * 8 + 16;
   static constexpr int TILE_OFF = (WIN_OFF + (MAX_E + 1) * 4 + 15) / 16 * 16;
@@ -150,6 +155,10 @@ struct SwapCfg {
   static constexpr int ALLOC = BYTES + 1024;
   static_assert(ALLOC <= 232448, "shared memory budget (window kernel)");
 };
+
+struct NoMaps {};
+template <bool kSave>
+using SavedMaps = std::conditional_t<kSave, SaveMaps, NoMaps>;
 
 struct WinCoord {
   int e;      // expert
@@ -253,8 +262,9 @@ __global__ void __launch_bounds__(S_THREADS, 1)
                                const int32_t* __restrict__ off_pad, const int32_t* __restrict__ counts, int E,
                                int K, int NT, int N_out, int64_t max_rows, uint32_t* __restrict__ status,
                                uint32_t* __restrict__ sched, uint32_t* __restrict__ win_done, uint32_t win_target,
-                               uint16_t* __restrict__ G, uint16_t* __restrict__ U) {
-  using C = SwapCfg<kUp>;
+                               uint16_t* __restrict__ G, uint16_t* __restrict__ U,
+                               const __grid_constant__ SavedMaps<kSave> save) {
+  using C = SwapCfg<kUp, kSave>;
   static_assert(kUp || !kSave, "only the gate/up GEMM has g and u");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -611,6 +621,8 @@ __global__ void __launch_bounds__(S_THREADS, 1)
     // the quarter's warps take its 32-token chunks in turn (chunk half,
     // half + S_EPI_SPLIT, ...), so a short window still splits evenly
     const int half = (warp - 2) / 4;
+    uint8_t* staging = smem + C::OUT_OFF + half * 3 * kPieceBytes;  // (kSave)
+    const bool leader = q == 0 && lane == 0;                        // of four warps: TMA
     uint32_t tcount = 0;
     for (uint32_t n = 0;; ++n) {
       const int tile = ring_take(ring, n, rank, rempty0, false, abort_flag, status);
@@ -634,28 +646,70 @@ __global__ void __launch_bounds__(S_THREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive_peer(tempty0 + 8u * a);
       };
+      if constexpr (kSave) {
+        // Pieces of 32 rows, the quarter's warps' in turn: g, u and h rounded,
+        // transposed through shared memory and stored by TMA, or where fewer rows
+        // are left by the warps, sixteen lanes a row.  (64 experts of 4096 x 1536, 256
+        // rows each: 326 us, stored straight from registers, with two stages more, 340;
+        // 1024 rows 908 and 1025, 8 rows 252 and 246; one expert of 2176 x 5760, 5003
+        // rows: 183 and 223; 8 of 256 x 512, 32 rows: 8.3 and 10.4.)
+        const int col0 = c.j * C::TILE_COLS + (C::TILE_COLS / 2) * static_cast<int>(rank);
+        const int rows = col0 < N_out ? c.rows : 0;  // (columns are multiples of 128)
+        const uint32_t lanes = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+        if (half * 32 >= rows) release();
+        for (int r = half * 32; r < rows; r += S_EPI_SPLIT * 32) {
+          uint32_t g[32], u[32], pg[16], pu[16], ph[16];
+          load_piece(lanes + r, g);
+          load_piece(lanes + 256 + r, u);
+          tmem_ld_wait();
+          if (r + S_EPI_SPLIT * 32 >= rows) release();
+          round_piece(g, pg);
+          round_piece(u, pu);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float x = __uint_as_float(g[i]);
+            g[i] = __float_as_uint(x * __fdividef(1.0f, 1.0f + __expf(-x)) * __uint_as_float(u[i]));
+          }
+          round_piece(g, ph);
+          if (leader) tma_store_wait_read<0>();
+          __syncwarp();
+          named_barrier_sync(3 + half, 128);  // the last pieces have left
+          stage_piece(smem_u32(staging), q, pg, lane);
+          stage_piece(smem_u32(staging) + kPieceBytes, q, pu, lane);
+          stage_piece(smem_u32(staging) + 2 * kPieceBytes, q, ph, lane);
+          fence_proxy_async_smem();
+          named_barrier_sync(3 + half, 128);
+          const int left = rows - r;
+          if (left >= 32) {
+            if (leader) {
+              for (int i = 0; i < 3; ++i)
+                tma_store_3d(&save.out[i], staging + i * kPieceBytes, 0, c.row0 + r, col0 / 64);
+              tma_store_commit();
+            }
+          } else {
+            for (int i = 0; i < 3; ++i) {
+              uint16_t* dst = i == 0 ? G : i == 1 ? U : D;
+              for (int t = 2 * q + (lane >> 4); t < left; t += 8)
+                *reinterpret_cast<uint4*>(dst + static_cast<int64_t>(c.row0 + r + t) * N_out + col0 + (lane & 15) * 8) =
+                    *reinterpret_cast<const uint4*>(staging + i * kPieceBytes + staged_at(t, lane & 15));
+            }
+          }
+        }
+        ++tcount;
+        if (tracked) {  // count this warp's part, written (its turn's by the leader)
+          if (leader) tma_store_wait_all<0>();
+          __syncwarp();
+          if (lane == 0) {
+            fence_acq_rel_gpu();
+            atomicAdd(win_done + c.wid, 1u);
+          }
+        }
+        continue;
+      }
       if (mine == 0) release();
       uint32_t packed[CH_PER * 16];                 // bf16 pairs (token 2i, 2i+1 of chunk cl) of this column
       uint32_t packed1[kUp ? 1 : CH_PER * 16];      // down: the second accumulator's column
       const uint32_t tbase = tmem_base + a * ACC_COLS + (static_cast<uint32_t>(q * 32) << 16);
-      // Training: g and u of a 32-token chunk leave as bf16 as they are read,
-      // in the store pattern of h below (neighbouring lanes swap tokens).
-      auto save_chunk = [&](uint16_t* S, const uint32_t (&v)[32], int ch) {
-        const int cg = c.j * C::TILE_COLS + (C::TILE_COLS / 2) * static_cast<int>(rank) + col;
-        if (cg >= N_out) return;  // uniform across the warp
-        const int odd = lane & 1;
-        uint32_t* dst = reinterpret_cast<uint32_t*>(S + static_cast<int64_t>(c.row0 + ch * 32 + odd) * N_out + (cg & ~1));
-        const int rem = c.rows - ch * 32;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          if (2 * i < rem) {  // uniform across the warp
-            const uint32_t pair = pack_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-            const uint32_t other = __shfl_xor_sync(0xffffffffu, pair, 1);
-            const uint32_t w = odd ? __byte_perm(other, pair, 0x7632) : __byte_perm(pair, other, 0x5410);
-            if (2 * i + odd < rem) dst[static_cast<int64_t>(i) * N_out] = w;  // two rows = N_out words
-          }
-        }
-      };
 #pragma unroll
       for (int cl = 0; cl < CH_PER; ++cl) {
         const int ch = half + S_EPI_SPLIT * cl;
@@ -666,10 +720,6 @@ __global__ void __launch_bounds__(S_THREADS, 1)
             tmem_ld_32x32b_x32(tbase + 256 + ch * 32, uv);
             tmem_ld_wait();
             if (cl == mine - 1) release();
-            if constexpr (kSave) {
-              save_chunk(G, gv, ch);
-              save_chunk(U, uv, ch);
-            }
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               const float g0 = __uint_as_float(gv[2 * i]), g1 = __uint_as_float(gv[2 * i + 1]);
@@ -756,6 +806,8 @@ __global__ void __launch_bounds__(S_THREADS, 1)
         }
       }
     }
+    if (kSave && leader) tma_store_wait_all<0>();  // this thread's stores are written
+    __syncwarp();
   }
 
   // The down GEMM of a forward skipped griddepcontrol.wait at entry; it waits
@@ -826,8 +878,9 @@ __global__ void scatter_rows_kernel(const uint16_t* __restrict__ X, const int32_
 template <bool kUp, bool kSave = false>
 cudaError_t launch_gemm(const moe_shape& s, const GemmMaps& maps, uint16_t* D, const int32_t* off_pad,
                         const int32_t* counts, uint32_t* status, uint32_t* sched, uint32_t* win_done,
-                        int num_sms, cudaStream_t st, uint16_t* g = nullptr, uint16_t* u = nullptr) {
-  using C = SwapCfg<kUp>;
+                        int num_sms, cudaStream_t st, uint16_t* g = nullptr, uint16_t* u = nullptr,
+                        const SavedMaps<kSave>& save = {}) {
+  using C = SwapCfg<kUp, kSave>;
   // the shared-memory opt-in, once per device (host threads may race here)
   static bool attr_done[64] = {};
   static std::mutex attr_mu;
@@ -871,7 +924,7 @@ cudaError_t launch_gemm(const moe_shape& s, const GemmMaps& maps, uint16_t* D, c
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, grouped_gemm_window_kernel<kUp, kSave>, maps.a, maps.a64, maps.a80, maps.b0, maps.b1, D,
                             off_pad, counts, s.E, K, NT, kUp ? s.I : s.H, max_rows_of(s), status, sched, win_done,
-                            win_target, g, u);
+                            win_target, g, u, save);
 }
 
 }  // namespace
@@ -891,10 +944,10 @@ cudaError_t launch_gemm_up(const moe_shape& s, const GemmMaps& maps, uint16_t* h
   return launch_gemm<true>(s, maps, h, off_pad, counts, status, sched, win_done, num_sms, st);
 }
 
-cudaError_t launch_gemm_up_train(const moe_shape& s, const GemmMaps& maps, uint16_t* g, uint16_t* u, uint16_t* h,
-                                 const int32_t* off_pad, const int32_t* counts, uint32_t* status, uint32_t* sched,
+cudaError_t launch_gemm_up_train(const moe_shape& s, const GemmMaps& maps, const SaveMaps& save, uint16_t* g,
+                                 uint16_t* u, uint16_t* h, const int32_t* off_pad, const int32_t* counts, uint32_t* status, uint32_t* sched,
                                  uint32_t* win_done, int num_sms, cudaStream_t st) {
-  return launch_gemm<true, true>(s, maps, h, off_pad, counts, status, sched, win_done, num_sms, st, g, u);
+  return launch_gemm<true, true>(s, maps, h, off_pad, counts, status, sched, win_done, num_sms, st, g, u, save);
 }
 
 cudaError_t launch_gemm_down(const moe_shape& s, const GemmMaps& maps, uint16_t* Y, const int32_t* off_pad,

@@ -142,6 +142,10 @@ struct GemmMaps {
   CUtensorMap a64;   // the same token rows, box 64 x 32 (windows of <= 128 rows)
   CUtensorMap a80;   // the same token rows, box 80 x 32 (windows of <= 160 rows)
 };
+// g, u and h of the training forward, as encode_bf16_groups makes them, boxes of 32 rows
+struct SaveMaps {
+  CUtensorMap out[3];
+};
 
 // sched: the kernel's tile counter and its done counter (two uint32 in the
 // workspace's first 256 bytes, zero between launches)
@@ -152,8 +156,8 @@ cudaError_t launch_gemm_up(const moe_shape& s, const GemmMaps& maps, uint16_t* h
                            const int32_t* counts, uint32_t* status, uint32_t* sched, uint32_t* win_done,
                            int num_sms, cudaStream_t st);
 // the same that also stores g and u (bf16, [max_rows][I])
-cudaError_t launch_gemm_up_train(const moe_shape& s, const GemmMaps& maps, uint16_t* g, uint16_t* u, uint16_t* h,
-                                 const int32_t* off_pad, const int32_t* counts, uint32_t* status, uint32_t* sched,
+cudaError_t launch_gemm_up_train(const moe_shape& s, const GemmMaps& maps, const SaveMaps& save, uint16_t* g,
+                                 uint16_t* u, uint16_t* h, const int32_t* off_pad, const int32_t* counts, uint32_t* status, uint32_t* sched,
                                  uint32_t* win_done, int num_sms, cudaStream_t st);
 cudaError_t launch_gemm_down(const moe_shape& s, const GemmMaps& maps, uint16_t* Y, const int32_t* off_pad,
                              const int32_t* counts, uint32_t* status, uint32_t* sched, uint32_t* win_done,
