@@ -84,7 +84,8 @@ constexpr int kBarOff = kRingOff + kTileRing * 16;
 // full, empty [kStages]; wide, used [kSteps]; tfull, tempty, drain; the ring's
 constexpr int kNumBars = 2 * kStages + 2 * kSteps + 3 + 2 * kTileRing;
 constexpr int kSlotOff = kBarOff + kNumBars * 8;
-constexpr int kSmem = kSlotOff + 16 + 1024;
+constexpr int kRowsOff = kSlotOff + 16;              // the scheduler's counts and first rows
+constexpr int kSmem = kRowsOff + kMaxExperts * 8 + 1024;
 static_assert(kSmem <= 232448, "shared memory budget");
 
 template <int kRegs>
@@ -183,8 +184,9 @@ __device__ __forceinline__ void ring_release(const TileRing& r, uint32_t n, uint
 }
 
 // Tiles are drawn from a counter in the workspace, in order: cluster b starts on
-// tile b, and a warp of its CTA 0 (a lane knowing eight experts) draws every later
-// index, finds the tile and hands it to all roles of both CTAs.  Tile t: expert,
+// tile b, and a warp of its CTA 0 (lane l knowing the experts l, 32 + l, ...) draws every later
+// index, finds the tile and hands it to all roles of both CTAs (the first one before
+// the first draws, whose latency the release to the readers would wait for).  Tile t: expert,
 // column tile, window, so that the windows sharing a weight tile are neighbours;
 // all of an expert's windows but the last have kTok rows.  The cluster that stops
 // drawing last clears the counter, and knows whether the launch started from a
@@ -199,46 +201,50 @@ __device__ __forceinline__ uint32_t stopped(uint32_t clusters, uint32_t index_su
 __device__ __forceinline__ void schedule(const TileRing& ring, int E, int NT, int64_t max_rows,
                                          const int32_t* off_pad, const int32_t* counts, uint32_t cluster,
                                          uint32_t nclusters, int lane, volatile int* abort, uint32_t* status,
-                                         uint32_t* sched) {
-  constexpr int per = kMaxExperts / 32;
+                                         uint32_t* sched, int2* known) {
+  constexpr int kGroups = kMaxExperts / 32;  // of 32 experts
   const uint32_t all = 0xffffffffu;
-  int cnt[per], off[per];
-  int sum = 0;
+  int cnt[kGroups], off[kGroups], end[kGroups];
+  int incl[kGroups];  // windows up to the expert
 #pragma unroll
-  for (int i = 0; i < per; ++i) {
-    const int e = lane * per + i;
-    cnt[i] = off[i] = 0;
-    if (e < E) {
-      const int c = __ldcg(counts + e);
-      const int64_t first = __ldcg(off_pad + e), end = __ldcg(off_pad + e + 1);
+  for (int i = 0; i < kGroups; ++i) {
+    const int e = 32 * i + lane;
+    cnt[i] = off[i] = end[i] = 0;
+    if (32 * i < E && e < E) {
+      cnt[i] = __ldcg(counts + e);
+      off[i] = __ldcg(off_pad + e);
+      end[i] = __ldcg(off_pad + e + 1);
+    }
+  }
+  int windows = 0;
+#pragma unroll
+  for (int i = 0; i < kGroups; ++i) {
+    incl[i] = windows;
+    if (32 * i < E) {
       // an expert whose rows do not lie inside its 128-row blocks and the buffers
       // gets no tiles
-      if (c >= 0 && first >= 0 && (first & 127) == 0 && (end & 127) == 0 && first + c <= end && end <= max_rows) {
-        cnt[i] = c;
-        off[i] = static_cast<int>(first);
-      } else {
+      if (cnt[i] < 0 || off[i] < 0 || (off[i] & 127) != 0 || (end[i] & 127) != 0 ||
+          static_cast<int64_t>(off[i]) + cnt[i] > end[i] || end[i] > max_rows) {
         record_status(status, kStatusBounds);
+        cnt[i] = 0;
       }
-    }
-    sum += (cnt[i] + kTok - 1) / kTok;
-  }
-  int incl = sum;  // windows up to this lane's last expert
+      known[32 * i + lane] = make_int2(cnt[i], off[i]);
+      int sum = (cnt[i] + kTok - 1) / kTok;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(all, incl, o);
-    if (lane >= o) incl += y;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(all, sum, o);
+        if (lane >= o) sum += y;
+      }
+      incl[i] += sum;
+      windows += __shfl_sync(all, sum, 31);
+    }
   }
-  const int windows = __shfl_sync(all, incl, 31);
   // windows of counts that fit the buffers (an expert has at most one that is not full)
   const bool fits = static_cast<int64_t>(windows - E) * kTok <= max_rows;
   if (!fits && lane == 0) record_status(status, kStatusBounds);
   const int total = fits ? NT * windows : 0;
 
   uint32_t drawn = 0, later = 0;  // two draws on their way
-  if (lane == 0) {
-    drawn = atomicAdd(sched, 1u);
-    later = atomicAdd(sched, 1u);
-  }
   bool drew_zero = false;
   // every draw, of lane 0: a cleared counter gives less than total + 2 clusters
   auto checked = [&](uint32_t d) {
@@ -251,29 +257,39 @@ __device__ __forceinline__ void schedule(const TileRing& ring, int E, int NT, in
     int owner = 0;  // the lane that knows the tile's expert
     if (tile < total) {
       const int q = tile / NT;  // (all column tiles of a window's expert lie together)
-      owner = __ffs(__ballot_sync(all, incl > q)) - 1;
-      int base = incl - sum;  // windows before this lane's first expert
-      int rows = 0, row = 0, nw = 1, local = 0;  // the expert's, and the window's place
+      int upto = 0;
+      bool found = false;
 #pragma unroll
-      for (int i = 0; i < per; ++i) {
-        const int n_windows = (cnt[i] + kTok - 1) / kTok;
-        if (q >= base && q < base + n_windows) {
-          c.e = lane * per + i;
-          rows = cnt[i];
-          row = off[i];
-          nw = n_windows;
-          local = tile - NT * base;
+      for (int i = 0; i < kGroups; ++i) {
+        if (32 * i < E && !found) {
+          const uint32_t behind = __ballot_sync(all, incl[i] > q);
+          found = behind != 0u;
+          if (found) {
+            owner = __ffs(behind) - 1;
+            c.e = 32 * i + lane;
+            upto = incl[i];
+          }
         }
-        base += n_windows;
       }
-      c.j = local / nw;
-      const int w = local - c.j * nw;
-      c.row0 = row + kTok * w;
-      c.rows = min(kTok, rows - kTok * w);
+      const int2 mine = known[c.e];  // as this lane left it
+      const int nw = (mine.x + kTok - 1) / kTok;
+      const int local = tile - NT * (upto - nw);
+      int w = 0;
+      c.j = local;
+      if (nw > 1) {
+        c.j = local / nw;
+        w = local - c.j * nw;
+      }
+      c.row0 = mine.y + kTok * w;
+      c.rows = min(kTok, mine.x - kTok * w);
       c.alone = nw == 1;
     }
     bool put = true;
     if (lane == owner) put = ring_put(ring, n, c, abort, status);
+    if (n == 0 && lane == 0) {
+      drawn = atomicAdd(sched, 1u);
+      later = atomicAdd(sched, 1u);
+    }
     if (__any_sync(all, !put) || tile >= total) break;
     const uint32_t d = __shfl_sync(all, drawn, 0);
     if (lane == 0) checked(d);
@@ -461,7 +477,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     } else if (warp == 2 && rank == 0) {
-      schedule(ring, E, NT, max_rows, off_pad, counts, blockIdx.x >> 1, gridDim.x >> 1, lane, abort_flag, status, sched);
+      schedule(ring, E, NT, max_rows, off_pad, counts, blockIdx.x >> 1, gridDim.x >> 1, lane, abort_flag, status, sched,
+               reinterpret_cast<int2*>(smem + kRowsOff));
       __syncwarp();
     }
   } else if (warp < kFirstWide) {
