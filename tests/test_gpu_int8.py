@@ -174,6 +174,16 @@ def test_products(moe, up, counts, size):
     r.check()
 
 
+# more experts than a warp has lanes: the last of 97, every one of 256, the last of 256
+MANY = [[3] + [0] * 95 + [200], [(37 * e) % 150 for e in range(256)], [0] * 255 + [70]]
+
+
+@pytest.mark.parametrize("up", [True, False], ids=["up", "down"])
+@pytest.mark.parametrize("counts", MANY, ids=["97", "256", "last"])
+def test_products_of_many_experts(moe, up, counts):
+    test_products(moe, up, counts, (128, 256))
+
+
 @pytest.mark.parametrize("up", [True, False], ids=["up", "down"])
 @pytest.mark.parametrize("codes", [127, -128, 1])
 def test_products_of_extreme_codes(moe, up, codes):

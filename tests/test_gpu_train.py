@@ -135,6 +135,16 @@ def test_weight_backward_in_runs(moe, size):
     test_weight_backward(moe, counts, size)
 
 
+# more experts than a warp has lanes: the last of 97, every one of 256, the last of 256
+MANY = [[3] + [0] * 95 + [200], [(37 * e) % 150 for e in range(256)], [0] * 255 + [300]]
+
+
+@pytest.mark.parametrize("counts", MANY, ids=["97", "256", "last"])
+def test_many_experts(moe, counts):
+    for test in (test_down_backward, test_up_backward, test_weight_backward, test_up_train):
+        test(moe, counts, (128, 256))
+
+
 @pytest.mark.parametrize("case", [([1500], 2048, 256), ([3001], 256, 1664), ([2003], 1408, 1408)], ids=str)
 def test_one_expert_of_many_rows(moe, case):
     """A dense block: windows of other sizes than powers of two."""
