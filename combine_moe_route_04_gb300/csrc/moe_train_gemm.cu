@@ -626,13 +626,17 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
         }
         ++asked;
       };
+      // A warp whose wait gave up leaves its turn only by a vote, and a vote comes
+      // before any other barrier of the turn: its four warps have the tile, or all go.
       const bool early = kMode == kDownBwd && turn * 32 < rows;
-      if (early) {  // before the accumulator is waited for
-        staging_free();
-        ask(turn * 32);
+      if constexpr (kMode == kDownBwd) {  // before the accumulator is waited for
+        if (leader) tma_store_wait_read<0>();
+        __syncwarp();
+        if (vote_any(!ok, turn)) break;  // (as a barrier, what staging_free has)
+        if (early) ask(turn * 32);
       }
       if (real && c.k > 0) ok = mbar_wait(&tfull[a], (tcount >> 1) & 1u, abort_flag, status);
-      if (vote_any(!ok, turn)) {  // the turn's warps give up together (they share barriers)
+      if (vote_any(!ok, turn)) {
         if (early) {
           int no_abort = 0;
           mbar_wait(&inbar[turn], (asked - 1) & 1u, &no_abort, status);
@@ -653,13 +657,14 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
       if constexpr (kMode == kDownBwd) {
         // pieces of 32 rows, the turns' in turn
         if (!early) release();
+        bool stop = false;
         for (int r = turn * 32; r < rows; r += kTurns * 32) {
           uint32_t v[32];
           load_piece(tb + a * kTileN + r, v);
           tmem_ld_wait();
           if (r + kTurns * 32 >= rows) release();
-          // (a wait that gives up raises the abort flag: the values are not used)
-          mbar_wait(&inbar[turn], (asked - 1) & 1u, abort_flag, status);
+          // (where the wait gives up, the values are not used)
+          const bool there = mbar_wait(&inbar[turn], (asked - 1) & 1u, abort_flag, status);
           const uint32_t at = smem_u32(staging) + staged_at(lane & 7, 4 * q + (lane >> 3), 32);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -680,7 +685,12 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
             stmatrix_x4_trans(at + kPieceBytes + 8 * j * 128, u[0], u[1], u[2], u[3]);
           }
           fence_proxy_async_smem();
-          named_barrier_sync(3 + turn, 128);
+          if (vote_any(!there, turn)) {
+            int no_abort = 0;
+            mbar_wait(&inbar[turn], (asked - 1) & 1u, &no_abort, status);
+            stop = true;
+            break;
+          }
           leave(staging, out.d[0], &maps.out[0], r, 32);
           leave(staging + kPieceBytes, out.d[1], &maps.out[1], r, 32);
           if (leader) tma_store_commit();
@@ -689,6 +699,7 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
             ask(r + kTurns * 32);
           }
         }
+        if (stop) break;
       } else {
         // a turn's 128 rows: all rounded to registers, the accumulator released,
         // then staged and stored HEIGHT rows at a time
