@@ -301,6 +301,31 @@ __device__ __forceinline__ void linger_after_abort(volatile int* abort) {
   if (*abort != 0) __nanosleep(100000);
 }
 
+// ------------------------------------------------------------ tile counters
+// A product's drawers (clusters, or CTAs) take their tiles from a counter in the
+// workspace, and the one that stops drawing last clears it.  That one also knows
+// whether the launch started from a cleared counter: the word behind it counts the
+// drawers that have stopped (bits 0-9), sums their indexes plus one (bits 10-29), and
+// gets bit 30 from the one that drew 0, the first value of a cleared counter.  With
+// anything else in either word the sum comes out wrong (tiles may have been left out):
+// an error.
+constexpr int kMaxDrawers = 1023;
+__device__ __forceinline__ uint32_t stopped(uint32_t drawers, uint32_t index_sum, bool drew_zero) {
+  return drawers | (index_sum << 10) | (drew_zero ? 1u << 30 : 0u);
+}
+// Drawer `index` of `drawers` has drawn its last tile; `any`: a sound launch draws at all.
+__device__ __forceinline__ void stop_drawing(uint32_t* sched, uint32_t index, uint32_t drawers, bool drew_zero,
+                                             bool any, uint32_t* status) {
+  __threadfence();
+  const uint32_t mine = stopped(1u, index + 1u, drew_zero);
+  const uint32_t seen = atomicAdd(sched + 1, mine) + mine;
+  if ((seen & 0x3FFu) == drawers) {  // every drawer has stopped
+    if (seen != stopped(drawers, drawers * (drawers + 1u) / 2u, any)) record_status(status, kStatusBounds);
+    atomicExch(sched, 0u);
+    atomicExch(sched + 1, 0u);
+  }
+}
+
 // ------------------------------------------------------------------ tcgen05
 // TMEM allocation: executed by one whole warp.  Writes the TMEM base address
 // into shared memory at `dst`.

@@ -216,7 +216,8 @@ __device__ __forceinline__ WinCoord decode_window(int tile, int NT, int E, const
 // next tile when it starts the current one, so the index is in place a whole
 // tile before any role needs it, and clusters that got smaller windows take
 // more tiles.  The cluster that finishes drawing last resets the counter for
-// the next launch.
+// the next launch and checks that it was clear for this one: what is left in it
+// by the size of a few tiles would leave out as many, with every draw in range.
 struct TileRing {
   uint64_t* full;        // [S_TILE_RING], this CTA: one arrival (the scheduler)
   uint64_t* empty;       // [S_TILE_RING], used in CTA 0: S_TILE_READERS arrivals
@@ -396,6 +397,7 @@ __global__ void __launch_bounds__(S_THREADS, 1)
       // each tile's first weight slices are loaded during that wait.
       const int64_t up_tiles = static_cast<int64_t>(s_win_off[E]) * (win_target / (2u * S_EPI_WARPS));
       const bool early_weights = !kUp && tracked && up_tiles <= static_cast<int64_t>(num_sm_ids() / 2);
+      bool drew_zero = false;
       // first ring use retired by the abort path below (left out of the drain)
       uint32_t retired_from = 0xFFFFFFFFu;
       // each cluster's first tile is its cluster index (no draw in front of
@@ -418,6 +420,7 @@ __global__ void __launch_bounds__(S_THREADS, 1)
         int next = total_tiles;
         bool published = rank != 0;
         auto publish = [&]() {
+          drew_zero |= raw_next == 0u;
           const uint64_t t = static_cast<uint64_t>(nclusters) + raw_next;
           next = t < static_cast<uint64_t>(total_tiles + nclusters) ? static_cast<int>(t) : total_tiles;
           if (static_cast<uint64_t>(next) != t) record_status(status, kStatusBounds);
@@ -538,11 +541,7 @@ __global__ void __launch_bounds__(S_THREADS, 1)
       if (rank == 0) {
         // this cluster has drawn its last index; the last cluster to get here
         // clears the counter for the next launch
-        __threadfence();
-        if (atomicAdd(sched + 1, 1u) == static_cast<uint32_t>(nclusters - 1)) {
-          atomicExch(sched, 0u);
-          atomicExch(sched + 1, 0u);
-        }
+        stop_drawing(sched, blockIdx.x >> 1, static_cast<uint32_t>(nclusters), drew_zero, total_tiles > 0, status);
       }
       // down GEMM of a forward: the combine may launch once every producer
       // has issued its last loads (launched at entry, its CTAs would wait on
@@ -906,6 +905,7 @@ cudaError_t launch_gemm(const moe_shape& s, const GemmMaps& maps, uint16_t* D, c
   // counted each of its gate/up tiles
   const uint32_t win_target = 2u * S_EPI_WARPS * static_cast<uint32_t>((s.I + 255) / 256);
   int64_t clusters = num_sms / 2;
+  if (clusters > kMaxDrawers) clusters = kMaxDrawers;
   if (max_tiles < clusters) clusters = max_tiles;
   if (clusters <= 0) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};

@@ -188,16 +188,7 @@ __device__ __forceinline__ void ring_release(const TileRing& r, uint32_t n, uint
 // index, finds the tile and hands it to all roles of both CTAs (the first one before
 // the first draws, whose latency the release to the readers would wait for).  Tile t: expert,
 // column tile, window, so that the windows sharing a weight tile are neighbours;
-// all of an expert's windows but the last have kTok rows.  The cluster that stops
-// drawing last clears the counter, and knows whether the launch started from a
-// cleared one: the word behind it counts the clusters that have stopped (bits
-// 0-9), sums their indexes plus one (bits 10-29), and gets bit 30 from the one
-// that drew 0.  With anything else in either word the sum comes out wrong (tiles
-// may have been left out): an error.
-constexpr int kMaxClusters = 1023;
-__device__ __forceinline__ uint32_t stopped(uint32_t clusters, uint32_t index_sum, bool drew_zero) {
-  return clusters | (index_sum << 10) | (drew_zero ? 1u << 30 : 0u);
-}
+// all of an expert's windows but the last have kTok rows.
 __device__ __forceinline__ void schedule(const TileRing& ring, int E, int NT, int64_t max_rows,
                                          const int32_t* off_pad, const int32_t* counts, uint32_t cluster,
                                          uint32_t nclusters, int lane, volatile int* abort, uint32_t* status,
@@ -301,14 +292,7 @@ __device__ __forceinline__ void schedule(const TileRing& ring, int E, int NT, in
   if (lane == 0) {
     checked(drawn);
     checked(later);
-    __threadfence();
-    const uint32_t mine = stopped(1u, cluster + 1u, drew_zero);
-    const uint32_t seen = atomicAdd(sched + 1, mine) + mine;
-    if ((seen & 0x3FFu) == nclusters) {  // every cluster has drawn its last index
-      if (seen != stopped(nclusters, nclusters * (nclusters + 1u) / 2u, true)) record_status(status, kStatusBounds);
-      atomicExch(sched, 0u);
-      atomicExch(sched + 1, 0u);
-    }
+    stop_drawing(sched, cluster, nclusters, drew_zero, true, status);
   }
 }
 
@@ -710,7 +694,7 @@ cudaError_t launch(const moe_shape& s, const Int8Maps& m, const float* sT, const
   const int64_t R = static_cast<int64_t>(s.T) * s.k;
   const int64_t max_tiles = (R / kTok + (s.E < R ? s.E : R)) * NT;
   int64_t clusters = num_sms / 2;
-  if (clusters > kMaxClusters) clusters = kMaxClusters;
+  if (clusters > kMaxDrawers) clusters = kMaxDrawers;
   if (max_tiles < clusters) clusters = max_tiles;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * clusters));

@@ -133,18 +133,9 @@ __device__ __forceinline__ Tile unpack_tile(const int4& v) {
 
 // Tiles go to the clusters in order: cluster b starts on tile b, and a warp of its
 // CTA 0 draws every later index from a counter in the workspace, finds the tile
-// and hands it to all roles of both CTAs through a ring.  The cluster that stops
-// drawing last clears the counter, and knows whether the launch started from a
-// cleared one: the word behind it counts the clusters that have stopped (bits
-// 0-9), sums their indexes plus one (bits 10-29), and gets bit 30 from the one
-// that drew 0.  With anything else in either word the sum comes out wrong (tiles
-// may have been left out).
+// and hands it to all roles of both CTAs through a ring.
 // (Each role finding its tile from the index by itself, with three divisions and
 // a search, took 860 of the 6800 cycles that a weight tile of 8 rows had.)
-constexpr int kMaxClusters = 1023;
-__device__ __forceinline__ uint32_t stopped(uint32_t clusters, uint32_t index_sum, bool drew_zero) {
-  return clusters | (index_sum << 10) | (drew_zero ? 1u << 30 : 0u);
-}
 struct TileRing {
   uint64_t* full;   // [kTileRing], this CTA: one arrival (the scheduler)
   uint64_t* empty;  // [kTileRing], used in CTA 0: READERS arrivals
@@ -343,14 +334,7 @@ __device__ __forceinline__ void schedule(const TileRing& ring, const Problem& p,
   if (lane == 0) {
     checked(drawn);
     checked(later);
-    __threadfence();
-    const uint32_t mine = stopped(1u, cluster + 1u, drew_zero);
-    const uint32_t seen = atomicAdd(sched + 1, mine) + mine;
-    if ((seen & 0x3FFu) == nclusters) {  // every cluster has drawn its last index
-      if (seen != stopped(nclusters, nclusters * (nclusters + 1u) / 2u, true)) record_status(status, kStatusBounds);
-      atomicExch(sched, 0u);
-      atomicExch(sched + 1, 0u);
-    }
+    stop_drawing(sched, cluster, nclusters, drew_zero, true, status);
   }
 }
 
@@ -816,7 +800,7 @@ cudaError_t launch(const moe_shape& s, const TrainMaps& m, const TrainOut& out, 
   }
   const int64_t ti = (s.I + 255) / 256, th = (s.H + 255) / 256;
   int64_t clusters = num_sms / 2;
-  if (clusters > kMaxClusters) clusters = kMaxClusters;
+  if (clusters > kMaxDrawers) clusters = kMaxDrawers;
   // Windows of 256 rows, or of 128 or 64 as long as every tile has a cluster of its
   // own: a tile then loads its weights for fewer rows, but takes less time (one
   // expert of 3968 x 1408, 500 rows: down 31 us with 256 rows, 19 with 64; where 64
