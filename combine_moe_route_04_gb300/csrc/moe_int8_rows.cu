@@ -1,6 +1,8 @@
-// moe_int8_rows.cu -- the grouped products on 8-bit integers for a few rows per
-// expert (the decoding of single tokens): the same results as moe_int8_gemm.cu
-// gives, from integer dot products.
+// moe_int8_rows.cu -- the grouped products on 8-bit integers for a few rows (the
+// decoding of single tokens), from integer dot products: the same bits as
+// moe_int8_gemm.cu gives while every sum and partial sum is below 2^24 (always for a
+// reduction of up to 1024).  Beyond that the sums here are still exact and rounded
+// once, where float32 sums round on the way.
 //
 // With one row per expert the product is a stream of weight rows against one
 // vector each: 100 MB of gate and up codes for a token of 8 experts of 4096 x 1536,

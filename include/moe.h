@@ -410,8 +410,10 @@ moe_status moe_quantize_permute_int8(const moe_shape *shape, const moe_bf16 *X,
  *   x_codes, x_scales: the matrix [max_rows, H] in expert order
  *   wg_*, wu_*:        the matrices [E*I, H]
  *   ws: any workspace, or at least 256 bytes whose first 256 were cleared
- * Products of codes are exact and their float32 sums too while they are below
- * 2^24 (whatever the codes for H <= 1024). */
+ * Products of codes are exact, and their float32 sums too while every partial sum
+ * is below 2^24 (whatever the codes for H <= 1024).  Few rows (by the shape's T, E
+ * and k) are summed in 32-bit integers, which are always exact: past 2^24 a row's
+ * last bits can therefore differ between a call of few rows and one of many. */
 moe_status moe_grouped_gemm_up_int8(const moe_shape *shape, const int8_t *x_codes,
                                     const float *x_scales, const int32_t *counts,
                                     const int32_t *off_pad, const int8_t *wg_codes,
