@@ -150,12 +150,25 @@ cudaError_t launch(const moe_shape& s, const int8_t* x, const float* sx, const i
 
 }  // namespace
 
-// Up to two rows in any expert, or half a row per expert on average.  Measured (4096
-// x 1536, 64 experts, 8 per token; gate/up | down, us, this way and on the tensor
-// cores): 1 token 17 | 10 and 32 | 19, 2 tokens 41 | 20 and 78 | 37, 4 tokens 75 | 47
-// and 80 | 45, 8 tokens 119 | 77 and 104 | 56.
+// Up to two tokens, or half a row per expert on average, but at most 24 rows in all,
+// and 8 tokens, so that the longest expert's weights are read twice at most.  From
+// memory, us, this way and on the tensor cores, gate/up | down (a rule on the rows
+// serves both, as their limits are near to one another):
+//   4096 x 1536, 64 experts, 8 per token: 8 rows 36 | 23 and 33 | 23 (18 | 10 and 28 |
+//     17 where the weights lie in L2), 16 rows 56 | 38 and 79 | 42, 24 rows 70 | 48 and
+//     79 | 42, 32 rows 85 | 58 and 81 | 44
+//   2048 x 768, 128 experts, 8 per token: 8 rows 16 | 14 and 23 | 19, 16 rows 24 | 19
+//     and 25 | 19, 24 rows 29 | 23 and 27 | 29 (13 | 13 and 20 | 22 in L2), 32 rows
+//     38 | 27 and 48 | 29, 64 rows 58 | 44 and 48 | 30
+//   7168 x 2048, 256 experts, 8 per token: 8 rows 64 | 38 and 56 | 50, 16 rows 107 | 60
+//     and 128 | 54, 24 rows 150 | 83 and 132 | 76, 128 rows 609 | 330 and 480 | 240
+//   2048 x 1024, 256 experts, 1 per token: 4 rows 15 | 11 and 23 | 19; 8 rows 19 | 15
+//     and 25 | 19, all in one expert 23 | 16 and 23 | 19; 16 rows 27 | 19 and 27 | 23,
+//     in one expert 36 | 25 and 23 | 19; 128 rows 117 | 79 and 89 | 54, in one expert
+//     230 | 138 and 25 | 21
 bool int8_few_rows(const moe_shape& s) {
-  return s.T <= 2 || 2 * static_cast<int64_t>(s.T) * s.k <= static_cast<int64_t>(s.E);
+  const int64_t rows = static_cast<int64_t>(s.T) * s.k;
+  return rows <= 24 && s.T <= 2 * kRows && (s.T <= 2 || 2 * rows <= s.E);
 }
 
 cudaError_t launch_int8_up_rows(const moe_shape& s, const int8_t* x, const float* x_scales, const int8_t* wg,

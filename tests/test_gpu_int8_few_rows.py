@@ -8,7 +8,7 @@ from gpu_util import need_gpu
 pytestmark = pytest.mark.gpu
 
 torch = pytest.importorskip("torch")
-from test_gpu_int8 import Rows  # noqa: E402
+from test_gpu_int8 import Rows, test_forward  # noqa: E402
 
 
 @pytest.fixture(scope="module")
@@ -36,6 +36,26 @@ def both_ways(moe, up, K, codes=None):
 def test_the_same_bits_where_sums_are_exact(moe, up, K, codes):
     a, b = both_ways(moe, up, K, codes)
     assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+
+
+# rows up to the most that are taken as few, several in an expert, and one more
+COUNTS = [[8] + [0] * 15, [1] + [0] * 18 + [7], [5, 0, 3] + [0] * 253, [4, 4] + [0] * 30, [1] * 8 + [0] * 8,
+          [9] + [0] * 17]
+
+
+@pytest.mark.parametrize("up", [True, False], ids=["up", "down"])
+@pytest.mark.parametrize("counts", COUNTS, ids=lambda c: "%d-rows-of-%d" % (sum(c), len(c)))
+@pytest.mark.parametrize("size", [(128, 128), (384, 640)], ids=lambda s: "%dx%d" % s)
+def test_rows_of_single_experts(moe, up, counts, size):
+    r = Rows(moe, counts, *size, up)
+    r.run(moe)
+    r.check()
+
+
+def test_the_layer_at_the_most_rows(moe):
+    """Three tokens of eight experts each, as few and one row more as many."""
+    for s in [(3, 256, 384, 64, 8), (5, 256, 384, 64, 5)]:
+        test_forward(moe, s)
 
 
 @pytest.mark.parametrize("up", [True, False], ids=["up", "down"])
