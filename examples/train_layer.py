@@ -24,7 +24,9 @@ class ExpertLayer(torch.autograd.Function):
     """out = layer(logits, x, w_gate, w_up, w_down); logits float32, the rest bf16.
 
     Every forward keeps a workspace (routing, gathered rows, h, Y) and g, u until its
-    backward has run; the backward's scratch is its own."""
+    backward has run; the backward's scratch is its own.  There is no second
+    derivative: a backward that is to be differentiated again (create_graph) is
+    refused.  Every backward forms all five gradients, as the library's call does."""
 
     @staticmethod
     def forward(ctx, s, logits, x, w_gate, w_up, w_down):
@@ -39,6 +41,8 @@ class ExpertLayer(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, dout):
+        if torch.is_grad_enabled():  # create_graph: these gradients would be taken for constants
+            raise RuntimeError("ExpertLayer has no second derivative: its backward does not take create_graph")
         w_gate, w_up, w_down, g, u = ctx.saved_tensors
         s, dout = ctx.s, dout.contiguous()
         bws = moe.alloc_backward_workspace(s)
