@@ -136,7 +136,7 @@ moe_status run_up_rows(const moe_shape& s, const uint16_t* Xp, const int32_t* co
     SaveMaps save;
     const uint16_t* out[3] = {g, u, h};
     for (int i = 0; i < 3; ++i)
-      if (!encode_bf16_groups(&save.out[i], out[i], mr, s.I, 32)) return MOE_ERR_CUDA;
+      if (!encode_bf16_groups(&save.out[i], out[i], mr, s.I, kPieceRows)) return MOE_ERR_CUDA;
     return cuda_status(launch_gemm_up_train(s, m, save, g, u, h, off_pad, counts, status, ws_sched_up(status),
                                             win_done, num_sms, st));
   }
@@ -327,11 +327,14 @@ moe_status run_down_backward(const moe_shape& s, const uint16_t* dY, const int32
   const uint64_t mr = static_cast<uint64_t>(max_rows_of(s));
   TrainMaps m = {};
   bool ok = encode_bf16_2d(&m.a[0], Wd, static_cast<uint64_t>(s.E) * s.I, s.H, 128, 64) &&
-            encode_bf16_groups(&m.in[0], g, mr, s.I, 32) && encode_bf16_groups(&m.in[1], u, mr, s.I, 32) &&
-            encode_bf16_groups(&m.out[0], dg, mr, s.I, 32) && encode_bf16_groups(&m.out[1], du, mr, s.I, 32);
+            encode_bf16_groups(&m.in[0], g, mr, s.I, kPieceRows) &&
+            encode_bf16_groups(&m.in[1], u, mr, s.I, kPieceRows) &&
+            encode_bf16_groups(&m.out[0], dg, mr, s.I, kPieceRows) &&
+            encode_bf16_groups(&m.out[1], du, mr, s.I, kPieceRows);
   for (int i = 0; i < 4; ++i) ok = ok && encode_bf16_2d(&m.b[0][i], dY, mr, s.H, train_token_box(i), 64);
   if (!ok) return MOE_ERR_CUDA;
-  return cuda_status(launch_down_backward(s, m, TrainOut{{dg, du, nullptr}}, off_pad, counts, status, ws_sched_up(status), num_sms, st));
+  return cuda_status(launch_down_backward(s, m, TrainOut{{dg, du, nullptr}}, off_pad, counts, status,
+                                          ws_sched_up(status), num_sms, st));
 }
 
 moe_status run_up_backward(const moe_shape& s, const uint16_t* dg, const uint16_t* du, const int32_t* counts,
@@ -340,12 +343,13 @@ moe_status run_up_backward(const moe_shape& s, const uint16_t* dg, const uint16_
   const uint64_t mr = static_cast<uint64_t>(max_rows_of(s)), EH = static_cast<uint64_t>(s.E) * s.H;
   TrainMaps m = {};
   bool ok = encode_bf16_2d(&m.a[0], Wg, EH, s.I, 128, 64) && encode_bf16_2d(&m.a[1], Wu, EH, s.I, 128, 64) &&
-            encode_bf16_groups(&m.out[0], dXp, mr, s.H, 64);
+            encode_bf16_groups(&m.out[0], dXp, mr, s.H, kTrainStoreRows);
   for (int i = 0; i < 4; ++i)
     ok = ok && encode_bf16_2d(&m.b[0][i], dg, mr, s.I, train_token_box(i), 64) &&
          encode_bf16_2d(&m.b[1][i], du, mr, s.I, train_token_box(i), 64);
   if (!ok) return MOE_ERR_CUDA;
-  return cuda_status(launch_up_backward(s, m, TrainOut{{dXp, nullptr, nullptr}}, off_pad, counts, status, ws_sched_down(status), num_sms, st));
+  return cuda_status(launch_up_backward(s, m, TrainOut{{dXp, nullptr, nullptr}}, off_pad, counts, status,
+                                        ws_sched_down(status), num_sms, st));
 }
 
 moe_status run_weight_backward(const moe_shape& s, const uint16_t* Xp, const uint16_t* h, const uint16_t* dg,
@@ -357,10 +361,13 @@ moe_status run_weight_backward(const moe_shape& s, const uint16_t* Xp, const uin
   TrainMaps m = {};
   if (!encode_bf16_2d(&m.a[0], dg, mr, s.I, 64, 64) || !encode_bf16_2d(&m.a[1], du, mr, s.I, 64, 64) ||
       !encode_bf16_2d(&m.a[2], dY, mr, s.H, 64, 64) || !encode_bf16_2d(&m.b[0][0], Xp, mr, s.H, 64, 64) ||
-      !encode_bf16_2d(&m.b[1][0], h, mr, s.I, 64, 64) || !encode_bf16_groups(&m.out[0], dWg, EH, s.I, 64) ||
-      !encode_bf16_groups(&m.out[1], dWu, EH, s.I, 64) || !encode_bf16_groups(&m.out[2], dWd, EI, s.H, 64))
+      !encode_bf16_2d(&m.b[1][0], h, mr, s.I, 64, 64) ||
+      !encode_bf16_groups(&m.out[0], dWg, EH, s.I, kTrainStoreRows) ||
+      !encode_bf16_groups(&m.out[1], dWu, EH, s.I, kTrainStoreRows) ||
+      !encode_bf16_groups(&m.out[2], dWd, EI, s.H, kTrainStoreRows))
     return MOE_ERR_CUDA;
-  return cuda_status(launch_weight_backward(s, m, TrainOut{{dWg, dWu, dWd}}, off_pad, counts, status, ws_sched_up(status), num_sms, st));
+  return cuda_status(launch_weight_backward(s, m, TrainOut{{dWg, dWu, dWd}}, off_pad, counts, status,
+                                            ws_sched_up(status), num_sms, st));
 }
 
 // moe_forward, or with g and u (both or neither) the training forward.

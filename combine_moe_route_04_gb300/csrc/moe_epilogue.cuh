@@ -13,7 +13,8 @@ namespace moe {
 // Staging of 32 rows x 128 bf16 columns, written by the four warps of a turn:
 // two halves of 64 columns, rows of 128 bytes, in the 128-byte swizzle of the
 // stores' tensor map (which also puts eight rows on different banks).
-constexpr int kPieceBytes = 32 * 128 * 2;
+constexpr int kPieceBytes = kPieceRows * 128 * 2;
+static_assert(kPieceRows == 32, "a warp's piece of TMEM");
 // byte offset of row t, 16-byte chunk c (of 16) in the staging (of `rows` rows)
 __device__ __forceinline__ int staged_at(int t, int c, int rows = 32) {
   return (c >> 3) * (rows * 128) + t * 128 + (((c & 7) ^ (t & 7)) << 4);

@@ -142,7 +142,12 @@ struct GemmMaps {
   CUtensorMap a64;   // the same token rows, box 64 x 32 (windows of <= 128 rows)
   CUtensorMap a80;   // the same token rows, box 80 x 32 (windows of <= 160 rows)
 };
-// g, u and h of the training forward, as encode_bf16_groups makes them, boxes of 32 rows
+// Rows of the boxes in which g and u, and h beside them, dg and du move between memory
+// and the kernels' staging, and of those in which dX and the weights' gradients leave
+// it: the maps' boxes and the staging have to agree.
+constexpr int kPieceRows = 32;
+constexpr int kTrainStoreRows = 64;
+// g, u and h of the training forward, as encode_bf16_groups makes them (kPieceRows)
 struct SaveMaps {
   CUtensorMap out[3];
 };
@@ -208,9 +213,10 @@ __host__ __device__ constexpr int train_token_box(int i) { return 16 << i; }
 struct TrainMaps {
   CUtensorMap a[3];     // down: W_down; up: W_gate, W_up (box 128 x 64); weights: dg, du, dY (box 64 x 64)
   CUtensorMap b[2][4];
-  // as 3-D maps (encode_bf16_groups), for the outputs in boxes of the rows stored at once
-  CUtensorMap in[2];    // down: g, u, 32 rows
-  CUtensorMap out[3];   // down: dg, du, 32 rows; up: dX, 64; weights: dW_gate, dW_up, dW_down, 128
+  // as 3-D maps (encode_bf16_groups), in boxes of the rows that one copy moves
+  CUtensorMap in[2];    // down: g, u (kPieceRows)
+  // down: dg, du (kPieceRows); up: dX, weights: dW_gate, dW_up, dW_down (kTrainStoreRows)
+  CUtensorMap out[3];
 };
 struct TrainOut {
   uint16_t* d[3];  // the outputs

@@ -14,11 +14,11 @@
 // A cluster of two CTAs computes a tile of 256 m x up to 256 n (M = 256 MMAs,
 // cta_group::2; CTA r holds 128 of the m and supplies half of the n) into one
 // of two accumulators of 256 TMEM columns, so that the epilogue of a tile runs
-// under the next one's MMAs.  TMEM lane = m, column = n: a piece of 32 n x 128
+// under the next one's MMAs.  TMEM lane = m, column = n: a piece of 64 n x 128
 // m is rounded to bf16, transposed through shared memory (stmatrix) and stored
-// by TMA.  In the down backward the same piece of g and u is loaded into that
-// staging first and read with ldmatrix, which gives each thread the elements
-// whose dh it holds; dg and du go back to the same places.
+// by TMA.  In the down backward pieces have 32 n, and the same piece of g and u is
+// loaded into that staging first and read with ldmatrix, which gives each thread
+// the elements whose dh it holds; dg and du go back to the same places.
 //
 // In the weight backward a cluster takes a run of column tiles over the same rows of
 // a gradient matrix, and where the reduction's stages of the second operand all have
@@ -72,7 +72,7 @@ struct Cfg {
   // twice, so that one half's store is still being read while the other is written
   // (64 experts of 4096 x 1536, 256 rows each: one buffer of 64 rows and a sixth stage
   // 806 us, one of 128 rows 700; later, with cheaper hand-overs, 588 and with two of 64 560).
-  static constexpr int HEIGHT = 64;
+  static constexpr int HEIGHT = kTrainStoreRows;
   static constexpr int BUFS = kMode == kWeightBwd ? 2 : 1;
   static constexpr int STAGES = kMode == kWeightBwd ? 5 : 6;
   static constexpr int TURN_BYTES = BUFS * HEIGHT * 256;
@@ -86,6 +86,7 @@ struct Cfg {
   static constexpr int SLOT_OFF = BAR_OFF + NUM_BARS * 8;
   static constexpr int SMEM = SLOT_OFF + 16 + 1024;
   static_assert(SMEM <= 232448, "shared memory budget");
+  static_assert(kMode != kDownBwd || 2 * kPieceBytes <= TURN_BYTES, "dg and du of a piece");
 };
 
 struct Problem {
