@@ -817,7 +817,8 @@ def moe_forward_int8(s, logits, X, wg_codes, wg_scales, wu_codes, wu_scales, wd_
     s, d = _plan(s), _dtypes()
     rc = (_lib or load()).moe_forward_int8(
         s.ref, _dev_tensor(logits, d.f32, s.T * s.E, "logits"), _dev_tensor(X, d.bf16, s.T * s.H, "X"),
-        *_int8_ptrs(wg_codes, wg_scales, s.E * s.I, s.H, "wg_"), *_int8_ptrs(wu_codes, wu_scales, s.E * s.I, s.H, "wu_"),
+        *_int8_ptrs(wg_codes, wg_scales, s.E * s.I, s.H, "wg_"),
+        *_int8_ptrs(wu_codes, wu_scales, s.E * s.I, s.H, "wu_"),
         *_int8_ptrs(wd_codes, wd_scales, s.E * s.H, s.I, "wd_"), _dev_tensor(out, d.bf16, s.T * s.H, "out"),
         _dev_tensor(ws, d.u8, s.int8_ws, "ws"), _stream(stream))
     if rc:

@@ -922,8 +922,8 @@ cudaError_t launch_gemm(const moe_shape& s, const GemmMaps& maps, uint16_t* D, c
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, grouped_gemm_window_kernel<kUp, kSave>, maps.a, maps.a64, maps.a80, maps.b0, maps.b1, D,
-                            off_pad, counts, s.E, K, NT, kUp ? s.I : s.H, max_rows_of(s), status, sched, win_done,
+  return cudaLaunchKernelEx(&cfg, grouped_gemm_window_kernel<kUp, kSave>, maps.a, maps.a64, maps.a80, maps.b0, maps.b1,
+                            D, off_pad, counts, s.E, K, NT, kUp ? s.I : s.H, max_rows_of(s), status, sched, win_done,
                             win_target, g, u, save);
 }
 
@@ -945,8 +945,9 @@ cudaError_t launch_gemm_up(const moe_shape& s, const GemmMaps& maps, uint16_t* h
 }
 
 cudaError_t launch_gemm_up_train(const moe_shape& s, const GemmMaps& maps, const SaveMaps& save, uint16_t* g,
-                                 uint16_t* u, uint16_t* h, const int32_t* off_pad, const int32_t* counts, uint32_t* status, uint32_t* sched,
-                                 uint32_t* win_done, int num_sms, cudaStream_t st) {
+                                 uint16_t* u, uint16_t* h, const int32_t* off_pad, const int32_t* counts,
+                                 uint32_t* status, uint32_t* sched, uint32_t* win_done, int num_sms,
+                                 cudaStream_t st) {
   return launch_gemm<true, true>(s, maps, h, off_pad, counts, status, sched, win_done, num_sms, st, g, u, save);
 }
 

@@ -11,7 +11,7 @@
 // The rows' kernel and the inverse move data once: 16384 x 4096 rows take 38 us (5.3
 // TB/s; three quarters of the issue slots are used), their values 30.6 us (6.6 TB/s),
 // the values of 64 weights of 4096 x 1536 171 us (7.1 TB/s).  The weights' kernel
-// reads its columns twice, the second time partly from L2.
+// reads its columns once, up to 12288 rows of them, and longer ones twice.
 // Inputs may be what an earlier kernel of a chain of dependent launches wrote, so
 // they are read past L1 (__ldcg), not through the non-coherent path.
 #include <cstdint>

@@ -57,9 +57,8 @@ constexpr int kWBytes = 128 * kStageK;    // codes of one block of 128 weight ro
 constexpr int kStageBytes = 2 * kWBytes + kHalfTok * kStageK;
 constexpr int kStepBytes = kHalfTok * kStepK * 2;  // widened rows
 // Warps: loads, MMAs and scheduler (both in CTA 0 alone) and an idle one; epilogue;
-// widening: whole groups
-// of four warps, which share out the registers: kLaunchRegs a thread at launch,
-// then what each group asks for.
+// widening: whole groups of four warps, which share out the registers: kLaunchRegs a
+// thread at launch, then what each group asks for.
 constexpr int kFirstEpi = 4;
 constexpr int kEpiWarps = 8;
 constexpr int kTurns = kEpiWarps / 4;
@@ -184,11 +183,11 @@ __device__ __forceinline__ void ring_release(const TileRing& r, uint32_t n, uint
 }
 
 // Tiles are drawn from a counter in the workspace, in order: cluster b starts on
-// tile b, and a warp of its CTA 0 (lane l knowing the experts l, 32 + l, ...) draws every later
-// index, finds the tile and hands it to all roles of both CTAs (the first one before
-// the first draws, whose latency the release to the readers would wait for).  Tile t: expert,
-// column tile, window, so that the windows sharing a weight tile are neighbours;
-// all of an expert's windows but the last have kTok rows.
+// tile b, and a warp of its CTA 0 (lane l knowing the experts l, 32 + l, ...) draws
+// every later index, finds the tile and hands it to all roles of both CTAs (the first
+// one before the first draws, whose latency the release to the readers would wait
+// for).  Tile t: expert, column tile, window, so that the windows sharing a weight
+// tile are neighbours; all of an expert's windows but the last have kTok rows.
 __device__ __forceinline__ void schedule(const TileRing& ring, int E, int NT, int64_t max_rows,
                                          const int32_t* off_pad, const int32_t* counts, uint32_t cluster,
                                          uint32_t nclusters, int lane, volatile int* abort, uint32_t* status,
@@ -430,7 +429,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           ring_release(ring, n, rank, rempty0);
           const bool two = col_of(c.j * kTileCols, 1) < N_out;  // a second block in either CTA
           // fp16 operands, float32 sums, both with k contiguous, M = 256, N
-          const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>((c.rows + 15) / 16 * 2) << 17) | ((256u >> 4) << 24);
+          const uint32_t idesc =
+              (1u << 4) | (static_cast<uint32_t>((c.rows + 15) / 16 * 2) << 17) | ((256u >> 4) << 24);
           if (!mbar_wait(tempty, (tcount & 1u) ^ 1u, abort_flag, status)) break;
           tc_fence_after();
           for (int ks = 0; ks < 2 * KS; ++ks, ++it) {

@@ -152,7 +152,7 @@ cudaError_t launch(const moe_shape& s, const int8_t* x, const float* sx, const i
 
 // Up to two tokens, or half a row per expert on average, but at most 24 rows in all,
 // and 8 tokens, so that the longest expert's weights are read twice at most.  From
-// memory, us, this way and on the tensor cores, gate/up | down (a rule on the rows
+// memory (behind a 256 MB fill), us, this way and on the tensor cores, gate/up | down (a rule on the rows
 // serves both, as their limits are near to one another):
 //   4096 x 1536, 64 experts, 8 per token: 8 rows 36 | 23 and 33 | 23 (18 | 10 and 28 |
 //     17 where the weights lie in L2), 16 rows 56 | 38 and 79 | 42, 24 rows 70 | 48 and

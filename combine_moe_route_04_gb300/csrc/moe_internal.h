@@ -162,8 +162,8 @@ cudaError_t launch_gemm_up(const moe_shape& s, const GemmMaps& maps, uint16_t* h
                            int num_sms, cudaStream_t st);
 // the same that also stores g and u (bf16, [max_rows][I])
 cudaError_t launch_gemm_up_train(const moe_shape& s, const GemmMaps& maps, const SaveMaps& save, uint16_t* g,
-                                 uint16_t* u, uint16_t* h, const int32_t* off_pad, const int32_t* counts, uint32_t* status, uint32_t* sched,
-                                 uint32_t* win_done, int num_sms, cudaStream_t st);
+                                 uint16_t* u, uint16_t* h, const int32_t* off_pad, const int32_t* counts,
+                                 uint32_t* status, uint32_t* sched, uint32_t* win_done, int num_sms, cudaStream_t st);
 cudaError_t launch_gemm_down(const moe_shape& s, const GemmMaps& maps, uint16_t* Y, const int32_t* off_pad,
                              const int32_t* counts, uint32_t* status, uint32_t* sched, uint32_t* win_done,
                              int num_sms, cudaStream_t st);

@@ -25,11 +25,12 @@
 // room (STAGES), they stay for the run's tiles: half the traffic from L2.
 //
 // What bounds it (64 experts of 4096 x 1536, 256 rows each): the down and up backward
-// HBM, 1.14 GB in 210 us and 1.85 GB in 321 us (5.4 and 5.8 TB/s; with 8 rows per
-// expert 6.2 and 7.1); the weight backward, 2.4 GB of gradients and 0.6 PFLOP, 520 to
-// 565 us, the power cap (1.7 GHz and 1370 W when run on and on); with 8 rows per expert 385
-// us, HBM (6.3 TB/s); with 1000 rows 1650 us, 1.50 PFLOP/s.  One dense block of 5003
-// rows, 2176 x 5760: 107 + 167 + 237 us, 1.2, 1.5 and 1.6 PFLOP/s.
+// HBM, 1.14 GB in 215 us and 1.85 GB in 324 us (5.3 and 5.7 TB/s; with 8 rows per
+// expert 6.0 and 7.0); the weight backward, 2.4 GB of gradients and 0.6 PFLOP, 520 to
+// 565 us, the power cap (1.7 GHz and 1370 W when run on and on); with 8 rows per expert
+// 384 us, HBM (6.3 TB/s); with 1000 rows 1650 us, 1.50 PFLOP/s.  One dense block of 5003
+// rows, 2176 x 5760: 93 to 114 + 174 + 243 us, 1.1 to 1.35, 1.4 and 1.55 PFLOP/s (the
+// down backward's pieces: g and u of one are asked for when the one before has left).
 //
 // The reduction of the weight backward ends inside a 16-row step of the MMA when
 // an expert's count is no multiple of 16, and the padding rows behind it may
@@ -112,8 +113,8 @@ struct Tile {
   bool load_b, free_b;  // weight backward: brings the second operand, is the last to use it
 };
 __device__ __forceinline__ int4 pack_tile(const Tile& c) {
-  return make_int4(c.n | (c.ok ? 1 << 9 : 0) | (c.last ? 1 << 10 : 0) | (c.mat << 11) | (c.e << 13) | (c.load_b ? 1 << 21 : 0) |
-                       (c.free_b ? 1 << 22 : 0),
+  return make_int4(c.n | (c.ok ? 1 << 9 : 0) | (c.last ? 1 << 10 : 0) | (c.mat << 11) | (c.e << 13) |
+                       (c.load_b ? 1 << 21 : 0) | (c.free_b ? 1 << 22 : 0),
                    (c.m0 / kTileM) | (c.n0 / kTileN << 16), c.row, c.k);
 }
 __device__ __forceinline__ Tile unpack_tile(const int4& v) {
@@ -178,9 +179,9 @@ __device__ __forceinline__ void ring_release(const TileRing& r, uint32_t n, uint
 
 // The scheduler: one warp, lane l knowing the experts l, 32 + l, ...  The first tile
 // is handed out before the first draws, whose latency the release to the readers
-// would wait for.  (Eight neighbouring experts a lane, and the draws first: 27.6 us
-// for the three products of 128 tokens, 256 x 512, 8 experts, where this takes
-// 24.0.)
+// would wait for.  (Eight neighbouring experts a lane, and the draws first: 28.2 us
+// for the three products of 128 tokens, 256 x 512, 8 experts, in a loop where this
+// takes 24.7.)
 //   down and up backward: an expert's c rows are cut into ceil(c / window) windows of
 //   equal size (rounded up to 16), so that those which share a weight tile run in
 //   step; tiles in the order expert, column tile, window.
@@ -218,7 +219,8 @@ __device__ __forceinline__ void schedule(const TileRing& ring, const Problem& p,
     if (32 * i < p.E) {
       const int e = 32 * i + lane;
       // an expert whose rows do not lie inside its blocks and the buffers gets no rows
-      if (e < p.E && (cnt[i] < 0 || off[i] < 0 || static_cast<int64_t>(off[i]) + cnt[i] > end[i] || end[i] > p.max_rows)) {
+      if (e < p.E && (cnt[i] < 0 || off[i] < 0 || static_cast<int64_t>(off[i]) + cnt[i] > end[i] ||
+                      end[i] > p.max_rows)) {
         record_status(status, kStatusBounds);
         cnt[i] = kMode == kWeightBwd ? -1 : 0;
       }
@@ -719,7 +721,8 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
                 stage_piece(smem_u32(buf) + j * 32 * 128, q, packed[i + j], lane, C::HEIGHT);
             fence_proxy_async_smem();
             named_barrier_sync(3 + turn, 128);
-            leave(buf, out.d[kMode == kWeightBwd ? c.mat : 0], &maps.out[kMode == kWeightBwd ? c.mat : 0], r, C::HEIGHT);
+            const int mat = kMode == kWeightBwd ? c.mat : 0;
+            leave(buf, out.d[mat], &maps.out[mat], r, C::HEIGHT);
           }
           if (leader) tma_store_commit();  // (a group for each buffer, of nothing where r lies behind the rows)
         }
@@ -782,8 +785,8 @@ __global__ void __launch_bounds__(Cfg<kMode>::THREADS, 1)
 }
 
 template <int kMode>
-cudaError_t launch(const moe_shape& s, const TrainMaps& m, const TrainOut& out, const int32_t* off_pad, const int32_t* counts,
-                   uint32_t* status, uint32_t* sched, int num_sms, cudaStream_t st) {
+cudaError_t launch(const moe_shape& s, const TrainMaps& m, const TrainOut& out, const int32_t* off_pad,
+                   const int32_t* counts, uint32_t* status, uint32_t* sched, int num_sms, cudaStream_t st) {
   using C = Cfg<kMode>;
   // the shared-memory opt-in, once per device (host threads may race here)
   static bool done[64] = {};

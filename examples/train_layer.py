@@ -69,7 +69,8 @@ class Balance:
         p = self.picks
         moe.moe_route(self.s, logits, p["topk_ids"], p["topk_w"], p["counts"], p["off_pad"], p["block_expert"],
                       p["num_blocks"], p["gather_idx"], p["scatter_idx"], self.route_ws)
-        moe.moe_balance_loss(self.s, logits, p["topk_ids"], None, self.counts, self.num, self.mean, self.losses, self.ws)
+        moe.moe_balance_loss(self.s, logits, p["topk_ids"], None, self.counts, self.num, self.mean, self.losses,
+                             self.ws)
         moe.moe_balance_loss_backward(self.s, logits, None, self.counts, self.num, weights, self.dlogits)
         return self.dlogits
 
